@@ -15,6 +15,8 @@ KVR_DEVERR_KEY_LENGTH = 0x2
 KVR_DEVERR_BLOCK_CAP = 0x4
 KVR_DEVERR_TIMEOUT = 0x8
 KVR_DEVERR_PAST_BLOCKS = 0x10
+KVR_DEVERR_QUERY = 0x20
+KVR_MAX_AXES = 8
 # kvr_qsa_rope
 QSA_ROPE_LAYOUTS = {"interleave_last": 0, "interleave_first": 1, "half_last": 2, "half_first": 3}
 # kvr_dtype
@@ -67,8 +69,47 @@ class DqArgs(ctypes.Structure):
     ]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", _vp), ("dtype", _int), ("T", _i64), ("H", _i64), ("D", _i64),
+        ("q_token_stride", _i64), ("q_head_stride", _i64),
+        ("positions", _vp), ("axes", _i64), ("sections", ctypes.POINTER(_i64)), ("base", ctypes.c_double),
+        ("half_pairs", ctypes.c_int32),
+        ("out", _vp), ("out_token_stride", _i64), ("out_head_stride", _i64),
+        ("cos_out", _vp), ("sin_out", _vp),
+    ]
+
+
+class ReadArgs(ctypes.Structure):
+    _fields_ = [
+        ("ckv_cache", _vp), ("ckv_dtype", _int), ("ckv_scale", _vp), ("ckv_scale_len", _i64),
+        ("k_cache", _vp), ("k_dtype", _int), ("k_scale", _vp), ("k_scale_len", _i64),
+        ("mode", _int), ("cache_d0", _i64), ("cache_d1", _i64), ("index", _vp),
+        ("B", _i64), ("S", _i64), ("Dv", _i64), ("Dk", _i64),
+        ("out", _vp), ("out_dtype", _int), ("out_row_stride", _i64), ("dev_status", _vp),
+    ]
+
+
+class MlaArgs(ctypes.Structure):
+    _fields_ = [
+        ("q_nope", _vp), ("q_rope", _vp), ("dtype", _int),
+        ("T", _i64), ("H", _i64), ("Dv", _i64), ("Dk", _i64),
+        ("q_nope_token_stride", _i64), ("q_nope_head_stride", _i64),
+        ("q_rope_token_stride", _i64), ("q_rope_head_stride", _i64),
+        ("N", _i64), ("query_start", _vp), ("key_length", _vp),
+        ("mode", _int), ("cache_d0", _i64), ("cache_d1", _i64),
+        ("block_table", _vp), ("max_blocks", _i64),
+        ("ckv_cache", _vp), ("ckv_dtype", _int), ("ckv_scale", _vp), ("ckv_scale_len", _i64),
+        ("k_cache", _vp), ("k_dtype", _int), ("k_scale", _vp), ("k_scale_len", _i64),
+        ("softmax_scale", _f32), ("causal", ctypes.c_int32),
+        ("out", _vp), ("out_token_stride", _i64), ("out_head_stride", _i64),
+        ("lse", _vp), ("workspace", _vp), ("workspace_bytes", _i64), ("dev_status", _vp),
+    ]
+
+
 EXPORTS = ("kv_rmsnorm_rope_cache", "kv_rmsnorm_rope_cache_staged", "kv_rmsnorm_rope_cache_staged_static",
-           "qsa_prepare", "dynamic_quant", "kvr_device_copy",
+           "qsa_prepare", "dynamic_quant", "query_rope", "kv_cache_read", "mla_attention",
+           "kvr_mla_attention_workspace", "kvr_device_copy",
            "kvr_check_bounded_wait", "kvr_store_after_delay", "kvr_set_debug_validate",
            "kvr_status_string", "kvr_abi_version")
 
@@ -98,6 +139,14 @@ def lib():
     L.qsa_prepare.restype = _int
     L.dynamic_quant.argtypes = [ctypes.POINTER(DqArgs), _vp]
     L.dynamic_quant.restype = _int
+    L.query_rope.argtypes = [ctypes.POINTER(RopeArgs), _vp]
+    L.query_rope.restype = _int
+    L.kv_cache_read.argtypes = [ctypes.POINTER(ReadArgs), _vp]
+    L.kv_cache_read.restype = _int
+    L.mla_attention.argtypes = [ctypes.POINTER(MlaArgs), _vp]
+    L.mla_attention.restype = _int
+    L.kvr_mla_attention_workspace.argtypes = [ctypes.POINTER(MlaArgs)]
+    L.kvr_mla_attention_workspace.restype = _i64
     L.kvr_check_bounded_wait.argtypes = [_vp, _i64, _i64, _vp]
     L.kvr_check_bounded_wait.restype = _int
     L.kvr_store_after_delay.argtypes = [_vp, _vp, _i64, _i64, _vp]

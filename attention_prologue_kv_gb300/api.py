@@ -393,6 +393,262 @@ def dynamic_quant(q_nope, q_out, dequant_scale, *, exact=False, stream=None):
         raise KvrError(st, "dynamic_quant")
 
 
+def _one_device(device, tensors):
+    """Every tensor (None allowed) on `device`: the library is handed bare addresses."""
+    for name, t in tensors.items():
+        if t is not None and _cuda(t, name).device != device:
+            raise ValueError("%s is on %s, other arguments are on %s" % (name, t.device, device))
+
+
+def _launch(fn, ref, name, device, stream):
+    """Call fn on `stream` (default: the current stream of `device`) with `device` current, as a launch needs it."""
+    if device.index == torch.cuda.current_device():
+        st = fn(ref, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(ref, _stream(stream))
+    if st != N.KVR_OK:
+        raise KvrError(st, name)
+
+
+class BoundCall(PreparedCall):
+    """PreparedCall of an operator that holds its tensors on one device,
+    which need not be the current one when the call is made."""
+
+    def __init__(self, fn, args, name, keep, device):
+        super().__init__(fn, args, name, keep)
+        self._device = device
+
+    def __call__(self, stream=None):
+        _launch(self._fn, self._ref, self._name, self._device, stream)
+
+
+def _heads(t, name, dtype, T=None, H=None):
+    """(T, H, width, token stride, head stride) of a [T, H, width] tensor with a dense last axis."""
+    if t.dim() != 3 or t.dtype != dtype or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s must be [T, H, width], %s, dense along its last dimension" % (name, dtype))
+    if (T is not None and t.shape[0] != T) or (H is not None and t.shape[1] != H):
+        raise ValueError("%s must be [%d, %d, width], got %s" % (name, T, H, list(t.shape)))
+    return t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+
+
+def _dense(t, name, dtype, shape):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError("%s must be contiguous %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+
+
+def _scale(t, name, width):
+    if t is not None and (t.dtype != torch.float32 or t.numel() not in (1, width) or not t.is_contiguous()):
+        raise ValueError("%s must be contiguous float32 with %d elements or 1" % (name, width))
+    return 0 if t is None else t.numel()
+
+
+def _status_word(t):
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise ValueError("dev_status must be an int32 tensor with one element")
+
+
+def _cache_pair(ckv_cache, k_cache, ckv_scale, k_scale, cache_mode, dtype):
+    """Checks of a cache pair and its scales; the fields that ReadArgs and MlaArgs share."""
+    if cache_mode not in N.CACHE_MODES:
+        raise ValueError("cache_mode must be one of %s" % list(N.CACHE_MODES))
+    d0, d1, Dv = _cache_dims(ckv_cache, "ckv_cache")
+    k0, k1, Dk = _cache_dims(k_cache, "k_cache")
+    if (k0, k1) != (d0, d1):
+        raise ValueError("ckv_cache and k_cache must share their leading dims")
+    for t, name in ((ckv_cache, "ckv_cache"), (k_cache, "k_cache")):
+        if t.dtype in _IN_DTYPES and t.dtype != dtype:
+            raise ValueError("a 16-bit %s must be %s" % (name, dtype))
+    return dict(ckv_cache=ckv_cache.data_ptr(), ckv_dtype=_CACHE_DTYPES[ckv_cache.dtype], ckv_scale=_ptr(ckv_scale, "ckv_scale"),
+                ckv_scale_len=_scale(ckv_scale, "ckv_scale", Dv), k_cache=k_cache.data_ptr(),
+                k_dtype=_CACHE_DTYPES[k_cache.dtype], k_scale=_ptr(k_scale, "k_scale"),
+                k_scale_len=_scale(k_scale, "k_scale", Dk), mode=N.CACHE_MODES[cache_mode], cache_d0=d0, cache_d1=d1,
+                Dv=Dv, Dk=Dk)
+
+
+def prepare_query_rope(q, positions, out, *, sections=None, base=10000.0, rope_layout="interleave", cos_out=None,
+                       sin_out=None):
+    """query_rope with its arguments bound once (see PreparedCall)."""
+    _cuda(q, "q")
+    if q.dtype not in _IN_DTYPES:
+        raise ValueError("q must be bfloat16 or float16")
+    T, H, D, q_ts, q_hs = _heads(q, "q", q.dtype)
+    _one_device(q.device, dict(positions=positions, out=out, cos_out=cos_out, sin_out=sin_out))
+    _, _, Do, o_ts, o_hs = _heads(out, "out", q.dtype, T, H)
+    if Do != D:
+        raise ValueError("out must have q's shape")
+    if positions.dim() == 1:
+        positions = positions.unsqueeze(0)
+    if positions.dim() != 2:
+        raise ValueError("positions must be [axes, T] or [T]")
+    axes = positions.shape[0]
+    _dense(positions, "positions", torch.int64, (axes, T))
+    if rope_layout not in ("interleave", "half"):
+        raise ValueError('rope_layout must be "interleave" or "half"')
+    if sections is None:
+        if axes != 1:
+            raise ValueError("sections is needed with several axes")
+        sections = [D // 2]
+    sections = [int(x) for x in sections]
+    if len(sections) != axes or sum(sections) != D // 2 or D % 2 or min(sections, default=-1) < 0:
+        raise ValueError("sections must be one nonnegative count per axis, in all D/2 = %d" % (D // 2))
+    if (cos_out is None) != (sin_out is None):
+        raise ValueError("cos_out and sin_out go together")
+    for t, name in ((cos_out, "cos_out"), (sin_out, "sin_out")):
+        if t is not None and (t.dtype != q.dtype or t.numel() != T * D or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous %s with T*D = %d elements" % (name, q.dtype, T * D))
+    counts = (ctypes.c_int64 * max(1, axes))(*sections)
+    a = N.RopeArgs(q=q.data_ptr(), dtype=_IN_DTYPES[q.dtype], T=T, H=H, D=D, q_token_stride=q_ts, q_head_stride=q_hs,
+                   positions=positions.data_ptr(), axes=axes, sections=counts, base=float(base),
+                   half_pairs=1 if rope_layout == "half" else 0, out=out.data_ptr(), out_token_stride=o_ts,
+                   out_head_stride=o_hs, cos_out=_ptr(cos_out, "cos_out"), sin_out=_ptr(sin_out, "sin_out"))
+    return BoundCall(N.lib().query_rope, a, "query_rope", (q, positions, out, cos_out, sin_out, counts), q.device)
+
+
+def query_rope(q, positions, out, *, sections=None, base=10000.0, rope_layout="interleave", cos_out=None, sin_out=None,
+               stream=None):
+    """RoPE of the query's rotary part: q [T, H, D] (bf16/f16, last axis
+    dense, other strides free, e.g. a slice of a fused projection) turned into
+    `out` [T, H, D] by positions int64 [axes, T] (or [T]). The first
+    sections[0] of the D/2 pairs turn by the first axis, the next sections[1]
+    by the second (time, height, width, ...); pair i by position *
+    base^(-2i/D). rope_layout "interleave": pair i is (x[2i], x[2i+1]), as the
+    KV prologue takes the key's; "half": (x[i], x[i + D/2]); either way its
+    results go to lanes i and i + D/2. cos_out/sin_out (optional, T*D elements,
+    q's dtype) get the tables of the same positions that
+    kv_rmsnorm_rope_cache takes as cos/sin. `out` must not overlap q."""
+    prepare_query_rope(q, positions, out, sections=sections, base=base, rope_layout=rope_layout, cos_out=cos_out,
+                       sin_out=sin_out)(stream)
+
+
+def prepare_kv_cache_read(ckv_cache, k_cache, index, out, *, cache_mode="PA_BSND", ckv_scale=None, k_scale=None,
+                          dev_status=None):
+    """kv_cache_read with its arguments bound once (see PreparedCall)."""
+    _cuda(out, "out")
+    if out.dtype not in _IN_DTYPES:
+        raise ValueError("out must be bfloat16 or float16")
+    if out.dim() not in (2, 3, 4) or out.numel() == 0 and 0 in out.shape[-1:]:
+        raise ValueError("out must be [B, 1, S, D], [B, S, D] or [T, D]")
+    _one_device(out.device, dict(ckv_cache=ckv_cache, k_cache=k_cache, index=index, ckv_scale=ckv_scale, k_scale=k_scale,
+                                 dev_status=dev_status))
+    pair = _cache_pair(ckv_cache, k_cache, ckv_scale, k_scale, cache_mode, out.dtype)
+    B, S, stride = _kv_rows(out)
+    D = pair["Dv"] + pair["Dk"]
+    if out.shape[-1] != D:
+        raise ValueError("out rows must have Dv + Dk = %d elements, got %d" % (D, out.shape[-1]))
+    if B * S <= 1:
+        stride = 0   # one row: its stride says nothing
+    _status_word(dev_status)
+    if index.dtype != torch.int64:
+        raise ValueError("index must be int64")
+    n_index = B * (-(-S // pair["cache_d1"]) if cache_mode == "PA_BLK_BSND" else S)
+    if index.numel() != n_index:
+        raise ValueError("index must have %d entries for %s (B=%d, S=%d), got %d" % (n_index, cache_mode, B, S, index.numel()))
+    a = N.ReadArgs(index=_ptr(index, "index"), B=B, S=S, out=out.data_ptr(), out_dtype=_IN_DTYPES[out.dtype],
+                   out_row_stride=stride, dev_status=_ptr(dev_status, "dev_status"), **pair)
+    return BoundCall(N.lib().kv_cache_read, a, "kv_cache_read",
+                     (ckv_cache, k_cache, index, out, ckv_scale, k_scale, dev_status), out.device)
+
+
+def kv_cache_read(ckv_cache, k_cache, index, out, *, cache_mode="PA_BSND", ckv_scale=None, k_scale=None, dev_status=None,
+                  stream=None):
+    """Rows of a cache pair read back: out [B, 1, S, Dv + Dk] (or [B, S, D],
+    [T, D]; bf16/f16, rows may be strided) receives, for each token of
+    `index` (layout and meaning as kv_rmsnorm_rope_cache's; entries may
+    repeat), its ckv and its k row side by side, 8-bit codes as code / scale.
+    Rows of entries -1 are left as they were; an entry out of range leaves its
+    row too and sets KVR_DEVERR_INDEX in dev_status."""
+    prepare_kv_cache_read(ckv_cache, k_cache, index, out, cache_mode=cache_mode, ckv_scale=ckv_scale, k_scale=k_scale,
+                          dev_status=dev_status)(stream)
+
+
+def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
+                          cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None,
+                          dev_status=None):
+    """mla_attention with its arguments bound once (see PreparedCall). Without
+    a `workspace` the object keeps one of its own: calls of one object that can
+    run at the same time (two streams, two replayed graphs) need an object, or
+    a workspace, each."""
+    _cuda(q_nope, "q_nope")
+    if q_nope.dtype not in _IN_DTYPES:
+        raise ValueError("q_nope must be bfloat16 or float16")
+    device, dtype = q_nope.device, q_nope.dtype
+    _one_device(device, dict(q_rope=q_rope, ckv_cache=ckv_cache, k_cache=k_cache, block_table=block_table,
+                             query_start=query_start, key_length=key_length, out=out, ckv_scale=ckv_scale, k_scale=k_scale,
+                             lse=lse, workspace=workspace, dev_status=dev_status))
+    pair = _cache_pair(ckv_cache, k_cache, ckv_scale, k_scale, cache_mode, dtype)
+    T, H, Dv, n_ts, n_hs = _heads(q_nope, "q_nope", dtype)
+    _, _, Dk, r_ts, r_hs = _heads(q_rope, "q_rope", dtype, T, H)
+    _, _, Do, o_ts, o_hs = _heads(out, "out", dtype, T, H)
+    if (Dv, Dk, Do) != (pair["Dv"], pair["Dk"], pair["Dv"]):
+        raise ValueError("q_nope and out must be as wide as ckv_cache (%d), q_rope as k_cache (%d)" % (pair["Dv"], pair["Dk"]))
+    if key_length.dim() != 1:
+        raise ValueError("key_length must be [N]")
+    Nn = key_length.shape[0]
+    _dense(key_length, "key_length", torch.int64, (Nn,))
+    _dense(query_start, "query_start", torch.int64, (Nn + 1,))
+    max_blocks = 0
+    if cache_mode == "Norm":
+        if block_table is not None:
+            raise ValueError("Norm mode takes no block_table")
+    else:
+        if block_table is None or block_table.dim() != 2:
+            raise ValueError("block_table must be [N, max_blocks] in the paged modes")
+        max_blocks = block_table.shape[1]
+        _dense(block_table, "block_table", torch.int64, (Nn, max_blocks))
+    _dense(lse, "lse", torch.float32, (T, H))
+    _status_word(dev_status)
+    a = N.MlaArgs(q_nope=q_nope.data_ptr(), q_rope=q_rope.data_ptr(), dtype=_IN_DTYPES[dtype], T=T, H=H,
+                  q_nope_token_stride=n_ts, q_nope_head_stride=n_hs, q_rope_token_stride=r_ts, q_rope_head_stride=r_hs,
+                  N=Nn, query_start=query_start.data_ptr(), key_length=key_length.data_ptr(),
+                  block_table=_ptr(block_table, "block_table"), max_blocks=max_blocks, softmax_scale=float(softmax_scale),
+                  causal=1 if causal else 0, out=out.data_ptr(), out_token_stride=o_ts, out_head_stride=o_hs,
+                  lse=_ptr(lse, "lse"), dev_status=_ptr(dev_status, "dev_status"), **pair)
+    with torch.cuda.device(device):
+        need = N.lib().kvr_mla_attention_workspace(ctypes.byref(a))
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        a.workspace = _ptr(workspace, "workspace")
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, ckv_scale, k_scale, lse, workspace,
+            dev_status)
+    call = BoundCall(N.lib().mla_attention, a, "mla_attention", keep, device)
+    call.workspace = workspace
+    return call
+
+
+def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
+                  cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None, dev_status=None,
+                  stream=None):
+    """Latent attention of new tokens over the caches of kv_rmsnorm_rope_cache:
+    out[t, h] = sum_i softmax_i(softmax_scale * (q_nope[t, h] . c[i] +
+    q_rope[t, h] . k[i])) c[i], the key row shared by all heads.
+
+    q_nope [T, H, Dv], q_rope [T, H, Dk], out [T, H, Dv] (bf16/f16, last axis
+    dense); query_start int64 [N + 1]: sequence n has the tokens
+    [query_start[n], query_start[n + 1]), one for a decode step, a few drafted
+    ones or a chunk; key_length int64 [N]: its keys, the new tokens' among them
+    (they are in the cache already). block_table int64 [N, max_blocks] names
+    the cache block of each block_size keys (-1: those keys are left out);
+    cache_mode "Norm" takes None and reads cache batch n. With causal=True token
+    j of L sees the keys before key_length - L + j + 1. A token that sees no
+    key gets zeros and lse -inf; rows outside every sequence stay as they
+    were. lse: optional float32 [T, H], the natural logarithm of the sum.
+    8-bit caches take their write scales (code / scale).
+    `workspace` (optional, device memory of kvr_mla_attention_workspace
+    bytes) must not be shared by calls that can run at the same time; without
+    it the call takes one from PyTorch's allocator."""
+    call = prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out,
+                                 softmax_scale=softmax_scale, cache_mode=cache_mode, causal=causal, ckv_scale=ckv_scale,
+                                 k_scale=k_scale, lse=lse, workspace=workspace, dev_status=dev_status)
+    call(stream)
+    if workspace is None and stream is not None and call.workspace is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=q_nope.device)
+        call.workspace.record_stream(stream)   # taken on the current stream, used on another
+
+
 def device_copy(dst, src, stream=None):
     """16-byte vectorised device copy of src into dst (same byte size); the
     in-process HBM bandwidth reference."""

@@ -2,6 +2,7 @@
 // Every entry point returns before launching anything when its arguments
 // are invalid; see include/kvr.h for the contract.
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <initializer_list>
 #include <mutex>
@@ -553,6 +554,259 @@ kvr_status kvr_device_copy(void* dst, const void* src, int64_t bytes, cudaStream
     if (overlap(dst, bytes, src, bytes)) return KVR_ERR_ALIAS;
     (void)cudaGetLastError();
     return cuda_status(launch_device_copy(dst, src, bytes, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Elements that [A, B, W] rows at a * sa + b * sb span (A, B >= 1), or -1 where
+// a stride is negative or the span reaches 2^61.
+int64_t span3(int64_t A, int64_t B, int64_t W, int64_t sa, int64_t sb) {
+    if (sa < 0 || sb < 0 || !product_fits({A, sa, 4}) || !product_fits({B, sb, 4})) return -1;
+    return (A - 1) * sa + (B - 1) * sb + W;
+}
+
+// True when those rows do not overlap one another (outputs).
+bool rows_apart(int64_t A, int64_t B, int64_t W, int64_t sa, int64_t sb) {
+    if (A == 1) return B == 1 || sb >= W;
+    if (B == 1) return sa >= W;
+    return (sb >= W && sa >= (B - 1) * sb + W) || (sa >= W && sb >= (A - 1) * sa + W);
+}
+
+// Types, scales and sizes that kv_cache_read and mla_attention take for a cache pair.
+kvr_status check_caches(kvr_dtype dt, kvr_dtype ckv_dtype, kvr_dtype k_dtype, const float* ckv_scale, int64_t ckv_len,
+                        const float* k_scale, int64_t k_len, int64_t d0, int64_t d1, int64_t Dv, int64_t Dk) {
+    if (!is16(dt)) return KVR_ERR_DTYPE;
+    if (!(ckv_dtype == dt || is8(ckv_dtype)) || !(k_dtype == dt || is8(k_dtype))) return KVR_ERR_DTYPE;
+    if (d0 < 1 || d1 < 1 || !product_fits({d0, d1, Dv + Dk, 2})) return KVR_ERR_SHAPE;
+    if (is8(ckv_dtype) != (ckv_scale != nullptr)) return KVR_ERR_NULL;
+    if (Dk > 0 && is8(k_dtype) != (k_scale != nullptr)) return KVR_ERR_NULL;
+    if (ckv_scale != nullptr && ckv_len != Dv && ckv_len != 1) return KVR_ERR_SHAPE;
+    if (Dk > 0 && k_scale != nullptr && k_len != Dk && k_len != 1) return KVR_ERR_SHAPE;
+    if (!aligned(ckv_scale, 4) || !aligned(k_scale, 4)) return KVR_ERR_SHAPE;
+    return KVR_OK;
+}
+
+// Validate the arguments of mla_attention. `*empty`: nothing to launch.
+kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
+    *empty = false;
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (a->mode != KVR_CACHE_NORM && a->mode != KVR_CACHE_PA_BSND && a->mode != KVR_CACHE_PA_BLK_BSND) return KVR_ERR_MODE;
+    if (a->T < 0 || a->H < 0 || a->N < 0 || a->Dv < 1 || a->Dv > 1024 || a->Dk < 1 || a->Dk > 256 || a->max_blocks < 0 ||
+        a->H > 0x7FFFFFFF || a->N > 0x7FFFFFFF || !product_fits({a->T, a->H}) || a->T * a->H > 0x7FFFFFFF)
+        return KVR_ERR_SHAPE;
+    const kvr_status st = check_caches(a->dtype, a->ckv_dtype, a->k_dtype, a->ckv_scale, a->ckv_scale_len, a->k_scale,
+                                       a->k_scale_len, a->cache_d0, a->cache_d1, a->Dv, a->Dk);
+    if (st != KVR_OK) return st;
+    const bool norm = a->mode == KVR_CACHE_NORM;
+    if (norm && a->cache_d0 < a->N) return KVR_ERR_SHAPE;
+    if (!norm && !product_fits({a->max_blocks, a->cache_d1, 8})) return KVR_ERR_SHAPE;
+    if (!norm && !product_fits({a->N, a->max_blocks, 8})) return KVR_ERR_SHAPE;
+    if (!(a->softmax_scale == a->softmax_scale)) return KVR_ERR_SHAPE;
+    if (a->T == 0 || a->H == 0 || a->N == 0) {
+        *empty = true;
+        return KVR_OK;
+    }
+    if (a->q_nope == nullptr || a->q_rope == nullptr || a->out == nullptr || a->query_start == nullptr ||
+        a->key_length == nullptr || a->ckv_cache == nullptr || a->k_cache == nullptr ||
+        (!norm && a->max_blocks > 0 && a->block_table == nullptr))
+        return KVR_ERR_NULL;
+    if (!aligned(a->q_nope, 2) || !aligned(a->q_rope, 2) || !aligned(a->out, 2) || !aligned(a->query_start, 8) ||
+        !aligned(a->key_length, 8) || !aligned(a->block_table, 8) || !aligned(a->lse, 4) || !aligned(a->dev_status, 4) ||
+        (is16(a->ckv_dtype) && !aligned(a->ckv_cache, 2)) || (is16(a->k_dtype) && !aligned(a->k_cache, 2)))
+        return KVR_ERR_SHAPE;
+    const int64_t qn = span3(a->T, a->H, a->Dv, a->q_nope_token_stride, a->q_nope_head_stride);
+    const int64_t qr = span3(a->T, a->H, a->Dk, a->q_rope_token_stride, a->q_rope_head_stride);
+    const int64_t o = span3(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride);
+    if (qn < 0 || qr < 0 || o < 0) return KVR_ERR_SHAPE;
+    if (!rows_apart(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride)) return KVR_ERR_ALIAS;
+    const int64_t rows = a->cache_d0 * a->cache_d1;
+    const struct { const void* p; int64_t n; } in[] = {
+        {a->q_nope, qn * 2}, {a->q_rope, qr * 2}, {a->query_start, (a->N + 1) * 8}, {a->key_length, a->N * 8},
+        {norm ? nullptr : a->block_table, a->N * a->max_blocks * 8},
+        {a->ckv_cache, rows * a->Dv * (is16(a->ckv_dtype) ? 2 : 1)}, {a->k_cache, rows * a->Dk * (is16(a->k_dtype) ? 2 : 1)},
+        {a->ckv_scale, a->ckv_scale_len * 4}, {a->k_scale, a->k_scale_len * 4}};
+    const struct { const void* p; int64_t n; } outs[] = {
+        {a->out, o * 2}, {a->lse, a->T * a->H * 4}, {a->workspace, a->workspace_bytes}, {a->dev_status, 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (const auto& x : in)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
+    }
+    *p = MlaParams{};
+    p->qn = a->q_nope;
+    p->qr = a->q_rope;
+    p->out = a->out;
+    p->lse = a->lse;
+    p->ckv = a->ckv_cache;
+    p->kc = a->k_cache;
+    p->ckv_scale = a->ckv_scale;
+    p->k_scale = a->k_scale;
+    p->query_start = a->query_start;
+    p->key_length = a->key_length;
+    p->table = norm ? nullptr : a->block_table;
+    p->status = a->dev_status;
+    p->workspace = a->workspace;
+    p->T = a->T;
+    p->N = a->N;
+    p->d0 = a->cache_d0;
+    p->d1 = a->cache_d1;
+    p->max_blocks = a->max_blocks;
+    // A table without columns may be NULL, as in Norm mode; it holds 0 keys, so that no key is read.
+    p->max_keys = std::min<int64_t>(norm ? a->cache_d1 : a->max_blocks * a->cache_d1, (int64_t(1) << 30) - 1);
+    p->qn_ts = a->q_nope_token_stride;
+    p->qn_hs = a->q_nope_head_stride;
+    p->qr_ts = a->q_rope_token_stride;
+    p->qr_hs = a->q_rope_head_stride;
+    p->o_ts = a->out_token_stride;
+    p->o_hs = a->out_head_stride;
+    p->H = int(a->H);
+    p->Dv = int(a->Dv);
+    p->Dk = int(a->Dk);
+    p->causal = a->causal != 0;
+    p->ckv_kind = out_kind(a->ckv_dtype);
+    p->k_kind = out_kind(a->k_dtype);
+    p->ckv_scale_per_ch = a->ckv_scale_len == a->Dv && a->Dv > 1;
+    p->k_scale_per_ch = a->k_scale_len == a->Dk && a->Dk > 1;
+    p->scale = a->softmax_scale;
+    return KVR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kvr_mla_attention_workspace(const kvr_mla_args* a) {
+    (void)a;
+    return 0;
+}
+
+kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
+    MlaParams p;
+    bool empty;
+    const kvr_status st = mla_plan(a, &p, &empty);
+    if (st != KVR_OK || empty) return st;
+    (void)cudaGetLastError();
+    return cuda_status(launch_mla_generic(p, a->dtype, stream));
+}
+
+kvr_status kv_cache_read(const kvr_read_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (a->mode != KVR_CACHE_NORM && a->mode != KVR_CACHE_PA_BSND && a->mode != KVR_CACHE_PA_BLK_BSND) return KVR_ERR_MODE;
+    if (a->B < 0 || a->S < 0 || a->Dv < 1 || a->Dk < 0 || a->Dv > (int64_t(1) << 30) || a->Dk > (int64_t(1) << 30))
+        return KVR_ERR_SHAPE;
+    const kvr_status st = check_caches(a->out_dtype, a->ckv_dtype, a->Dk > 0 ? a->k_dtype : a->out_dtype, a->ckv_scale,
+                                       a->ckv_scale_len, a->Dk > 0 ? a->k_scale : nullptr, a->k_scale_len, a->cache_d0,
+                                       a->cache_d1, a->Dv, a->Dk);
+    if (st != KVR_OK) return st;
+    const int64_t D = a->Dv + a->Dk, stride = a->out_row_stride == 0 ? D : a->out_row_stride;
+    if (stride < D || !product_fits({a->B, a->S, stride, 2}) || !product_fits({a->B, a->S, 8})) return KVR_ERR_SHAPE;
+    if (a->mode == KVR_CACHE_NORM && a->cache_d0 < a->B) return KVR_ERR_SHAPE;
+    const int64_t T = a->B * a->S;
+    if (T == 0) return KVR_OK;
+    if (a->ckv_cache == nullptr || (a->Dk > 0 && a->k_cache == nullptr) || a->index == nullptr || a->out == nullptr)
+        return KVR_ERR_NULL;
+    if (!aligned(a->index, 8) || !aligned(a->out, 2) || !aligned(a->dev_status, 4) ||
+        (is16(a->ckv_dtype) && !aligned(a->ckv_cache, 2)) || (a->Dk > 0 && is16(a->k_dtype) && !aligned(a->k_cache, 2)))
+        return KVR_ERR_SHAPE;
+    const int64_t nblk = (a->S + a->cache_d1 - 1) / a->cache_d1;
+    const int64_t rows = a->cache_d0 * a->cache_d1, out_bytes = ((T - 1) * stride + D) * 2;
+    const struct { const void* p; int64_t n; } in[] = {
+        {a->ckv_cache, rows * a->Dv * (is16(a->ckv_dtype) ? 2 : 1)},
+        {a->Dk > 0 ? a->k_cache : nullptr, rows * a->Dk * (is16(a->k_dtype) ? 2 : 1)},
+        {a->index, (a->mode == KVR_CACHE_PA_BLK_BSND ? a->B * nblk : T) * 8},
+        {a->ckv_scale, a->ckv_scale_len * 4}, {a->Dk > 0 ? a->k_scale : nullptr, a->k_scale_len * 4}, {a->dev_status, 4}};
+    for (const auto& x : in)
+        if (overlap(a->out, out_bytes, x.p, x.n)) return KVR_ERR_ALIAS;
+    ReadParams p = {};
+    p.ckv = a->ckv_cache;
+    p.kc = a->k_cache;
+    p.ckv_scale = a->ckv_scale;
+    p.k_scale = a->k_scale;
+    p.index = a->index;
+    p.out = a->out;
+    p.status = a->dev_status;
+    p.T = T;
+    p.S = a->S;
+    p.d0 = a->cache_d0;
+    p.d1 = a->cache_d1;
+    p.nblk = nblk;
+    p.out_stride = stride;
+    p.Dv = int(a->Dv);
+    p.Dk = int(a->Dk);
+    p.mode = int(a->mode);
+    p.ckv_kind = out_kind(a->ckv_dtype);
+    p.k_kind = a->Dk > 0 ? out_kind(a->k_dtype) : OUT16;
+    p.ckv_scale_per_ch = a->ckv_scale_len == a->Dv && a->Dv > 1;
+    p.k_scale_per_ch = a->k_scale_len == a->Dk && a->Dk > 1;
+    const bool vec = a->Dv % 8 == 0 && a->Dk % 8 == 0 && stride % 8 == 0 && aligned(a->out, 16) &&
+                     aligned(a->ckv_cache, is8(a->ckv_dtype) ? 8 : 16) &&
+                     (a->Dk == 0 || aligned(a->k_cache, is8(a->k_dtype) ? 8 : 16));
+    (void)cudaGetLastError();
+    return cuda_status(launch_read(p, a->out_dtype, vec, stream));
+}
+
+kvr_status query_rope(const kvr_rope_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (!is16(a->dtype)) return KVR_ERR_DTYPE;
+    if (a->T < 0 || a->H < 0 || a->D < 2 || a->D > 256 || (a->D & 1) || a->axes < 1 || a->axes > KVR_MAX_AXES ||
+        !product_fits({a->T, a->H, a->D, int64_t(1) << 22}) || !product_fits({a->axes, a->T, 8}))
+        return KVR_ERR_SHAPE;
+    if (!(a->base >= 1.0 && a->base < 0x1p63)) return KVR_ERR_SHAPE;
+    if (a->sections == nullptr) return KVR_ERR_NULL;
+    int64_t pairs = 0;
+    for (int64_t i = 0; i < a->axes; ++i) {
+        if (a->sections[i] < 0 || a->sections[i] > a->D / 2) return KVR_ERR_SHAPE;
+        pairs += a->sections[i];
+    }
+    if (pairs != a->D / 2) return KVR_ERR_SHAPE;
+    if ((a->cos_out != nullptr) != (a->sin_out != nullptr)) return KVR_ERR_NULL;
+    // Without heads only the tables are left to write.
+    if (a->T == 0 || (a->H == 0 && a->cos_out == nullptr)) return KVR_OK;
+    if (a->positions == nullptr || (a->H > 0 && (a->q == nullptr || a->out == nullptr))) return KVR_ERR_NULL;
+    if (!aligned(a->q, 2) || !aligned(a->out, 2) || !aligned(a->positions, 8) || !aligned(a->cos_out, 2) ||
+        !aligned(a->sin_out, 2))
+        return KVR_ERR_SHAPE;
+    const bool any = a->H > 0;
+    const int64_t qb = any ? span3(a->T, a->H, a->D, a->q_token_stride, a->q_head_stride) : 0;
+    const int64_t ob = any ? span3(a->T, a->H, a->D, a->out_token_stride, a->out_head_stride) : 0;
+    if (qb < 0 || ob < 0) return KVR_ERR_SHAPE;
+    if (any && !rows_apart(a->T, a->H, a->D, a->out_token_stride, a->out_head_stride)) return KVR_ERR_ALIAS;
+    const struct { const void* p; int64_t n; } in[] = {{a->q, qb * 2}, {a->positions, a->axes * a->T * 8}};
+    const struct { const void* p; int64_t n; } outs[] = {{a->out, ob * 2}, {a->cos_out, a->T * a->D * 2}, {a->sin_out, a->T * a->D * 2}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
+    }
+    RopeParams p = {};
+    p.q = a->q;
+    p.out = a->out;
+    p.positions = a->positions;
+    p.cos = a->cos_out;
+    p.sin = a->sin_out;
+    p.T = a->T;
+    p.H = a->H;
+    p.q_ts = a->q_token_stride;
+    p.q_hs = a->q_head_stride;
+    p.o_ts = a->out_token_stride;
+    p.o_hs = a->out_head_stride;
+    p.D = int(a->D);
+    int64_t i = 0;
+    for (int64_t x = 0; x < a->axes; ++x)
+        for (int64_t k = 0; k < a->sections[x]; ++k, ++i) {
+            // 2^64 / 2 pi * base^(-2i/D): at most 0.16 * 2^64.
+            p.step[i] = uint64_t(std::pow(a->base, -2.0 * double(i) / double(a->D)) * 2935890503282001226.0);
+            p.axis[i] = uint8_t(x);
+        }
+    const bool vec = a->D % 8 == 0 && aligned(a->q, 16) && aligned(a->out, 8) && aligned(a->cos_out, 8) &&
+                     aligned(a->sin_out, 8) && a->q_token_stride % 8 == 0 && a->q_head_stride % 8 == 0 &&
+                     a->out_token_stride % 4 == 0 && a->out_head_stride % 4 == 0;
+    (void)cudaGetLastError();
+    return cuda_status(launch_rope(p, a->dtype, a->half_pairs != 0, vec, stream));
 }
 
 }  // extern "C"

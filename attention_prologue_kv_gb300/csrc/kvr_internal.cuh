@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -58,6 +59,13 @@ __device__ __forceinline__ uint32_t enc8x2(float lo, float hi) {
         int b = min(max(__float2int_rn(hi), -128), 127);
         return (uint32_t(a) & 0xFFu) | ((uint32_t(b) & 0xFFu) << 8);
     }
+}
+
+// One 8-bit code of a runtime kind to float (exact).
+__device__ __forceinline__ float dec8(int kind, uint8_t c) {
+    if (kind == OUT_I8) return float(int8_t(c));
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, kind == OUT_E4M3 ? __NV_E4M3 : __NV_E5M2);
+    return __half2float(__half(h));
 }
 
 // Runtime-kind variant for the small k-cache part.
@@ -287,6 +295,58 @@ struct DqParams {
     int exact;           // recompute near-tie codes from the exact rational
 };
 
+struct RopeParams {
+    const void* q;
+    void* out;
+    const int64_t* positions;
+    void* cos;           // table outputs, or NULL
+    void* sin;
+    int64_t T, H;
+    int64_t q_ts, q_hs, o_ts, o_hs;   // token and head strides in elements
+    int64_t items;       // (token, head block, chunk of a row) triples
+    int D, hb, nhb;      // row width; heads of a block, blocks of a token
+    uint64_t step[128];  // turns of pair i per position, in units of 2^-64 turn
+    uint8_t axis[128];   // axis of pair i
+};
+
+struct ReadParams {
+    const void* ckv;
+    const void* kc;
+    const float* ckv_scale;
+    const float* k_scale;
+    const int64_t* index;
+    void* out;
+    int32_t* status;
+    int64_t T, S, d0, d1, nblk, out_stride;
+    int Dv, Dk, mode;
+    int ckv_kind, k_kind;
+    int ckv_scale_per_ch, k_scale_per_ch;
+};
+
+struct MlaParams {
+    const void* qn;
+    const void* qr;
+    void* out;
+    float* lse;
+    const void* ckv;
+    const void* kc;
+    const float* ckv_scale;
+    const float* k_scale;
+    const int64_t* query_start;
+    const int64_t* key_length;
+    const int64_t* table;       // NULL: Norm mode
+    int32_t* status;
+    void* workspace;
+    int64_t T, N, d0, d1, max_blocks, max_keys;
+    int64_t qn_ts, qn_hs, qr_ts, qr_hs, o_ts, o_hs;
+    int H, Dv, Dk;
+    int causal;
+    int ckv_kind, k_kind;
+    int ckv_scale_per_ch, k_scale_per_ch;
+    float scale;                // softmax scale
+    int pairs;                  // tensor-core kernel: CTA pairs of the grid
+};
+
 // Launch with programmatic stream serialisation allowed: the grid may be
 // scheduled while the previous kernel on the stream drains; its kernels call
 // pdl_wait() before reading global memory (before it they only issue L2
@@ -317,6 +377,10 @@ cudaError_t launch_qsa(const QsaParams& p, int in_dtype, bool vec, bool bulk, bo
 bool qsa_warp_shape(int64_t Di, int64_t kbs);
 cudaError_t launch_device_copy(void* dst, const void* src, int64_t bytes, cudaStream_t s);
 cudaError_t launch_dq(const DqParams& p, int in_dtype, bool vec, cudaStream_t s);
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool vec, cudaStream_t s);
+cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s);
+cudaError_t launch_mla_generic(const MlaParams& p, int dtype, cudaStream_t s);
 
 int sm_count_current_device();
 

@@ -1,7 +1,7 @@
 /*
  * kvr.h - C ABI of libkvr.so, the GB300 (sm_103a) attention-prologue key path.
  *
- * Three operations:
+ * The operations:
  *
  *   kv_rmsnorm_rope_cache()  the fused KV prologue of the page
  *       "aclnnKvRmsNormRopeCache" (hiascend.com, CANN ops-transformer):
@@ -24,6 +24,17 @@
  *
  *   dynamic_quant()  DynamicQuant of q^N, the query-side step beside this
  *       path on "aclnnMlaPrologV3WeightNz": per-row int8 codes and scales.
+ *
+ *   query_rope()  the rotary positions of the query's rotary part q^R, with one
+ *       position per axis (time, height, width, ...); it can write the cos/sin
+ *       tables that kv_rmsnorm_rope_cache() takes for the same tokens.
+ *
+ *   mla_attention()  attention of new tokens (one per sequence, a few, or a
+ *       chunk) over the caches kv_rmsnorm_rope_cache() fills: every head reads
+ *       the same latent row as key and as value.
+ *
+ *   kv_cache_read()  the cache rows of an index read back into dense rows,
+ *       8-bit codes decoded.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller (the
@@ -99,6 +110,7 @@ typedef enum kvr_status {
                                       (one second); that CTA stopped early, output incomplete */
 #define KVR_DEVERR_PAST_BLOCKS 0x10 /* qsa, concat-output form: past_block_index_keys holds
                                       fewer than floor(P/kbs) rows for a sequence */
+#define KVR_DEVERR_QUERY 0x20      /* attention: query_start decreases or leaves [0, T] at a sequence */
 
 typedef enum kvr_dtype {
     KVR_BF16 = 0,
@@ -410,6 +422,186 @@ typedef struct kvr_dq_args {
 } kvr_dq_args;
 
 kvr_status dynamic_quant(const kvr_dq_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of query_rope(): the RoPE of q^R ("aclnnMlaPrologV3WeightNz",
+ * "Formula", query path) by the interleaved formula of
+ * "aclnnKvRmsNormRopeCache" ("Formulas (1) interleaveRope"), with positions of
+ * several axes, as multimodal prompts have them.
+ *
+ *   q            [T, H, D] input, element type `dtype` (bf16 or f16), the last
+ *                axis dense; row (t, h) starts at t * q_token_stride +
+ *                h * q_head_stride elements.
+ *   positions    int64 [axes, T], any sign and size.
+ *   sections     HOST array of `axes` nonnegative counts that add up to D/2:
+ *                the first sections[0] pairs turn by the position on axis 0,
+ *                the next sections[1] by that on axis 1, and so on.
+ *   base         pair i turns by position * base^(-2i/D); 1 <= base < 2^63.
+ *   half_pairs   0: pair i is (x[2i], x[2i+1]); 1: (x[i], x[i + D/2]). Either way its
+ *                results go to lanes i and i + D/2, as in kvr_qsa_rope.
+ *   out          [T, H, D] `dtype`, strides as for q. Must not overlap q.
+ *   cos_out, sin_out  optional out [T, D] `dtype`, dense (both or neither): the
+ *                full-width tables of these positions, lanes i and i + D/2 equal,
+ *                as kv_rmsnorm_rope_cache takes them.
+ *
+ * The angle's whole turns are dropped in 64-bit fixed point (base^(-2i/D) /
+ * 2 pi is rounded once to a multiple of 2^-64, so that an angle is off by at
+ * most |position| * 2^-52 turns); cos and sin of the rest are float32, each
+ * output is rounded once. Limits: T, H >= 0; D even, 2 <= D <= 256;
+ * 1 <= axes <= 8; T * H * D < 2^40.
+ */
+#define KVR_MAX_AXES 8
+typedef struct kvr_rope_args {
+    const void* q;
+    kvr_dtype dtype;
+    int64_t T, H, D;
+    int64_t q_token_stride, q_head_stride;
+    const int64_t* positions;
+    int64_t axes;
+    const int64_t* sections;
+    double base;
+    int32_t half_pairs;
+    void* out;
+    int64_t out_token_stride, out_head_stride;
+    void* cos_out;
+    void* sin_out;
+} kvr_rope_args;
+
+kvr_status query_rope(const kvr_rope_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of kv_cache_read(): for each token of an index, the two cache rows
+ * that kv_rmsnorm_rope_cache() writes for it, side by side in one dense row.
+ *
+ *   ckv_cache, k_cache, their types, scales and dims, mode, index: as in
+ *                kvr_kv_args. An 8-bit code is read as code / scale[c].
+ *                An index entry may occur several times.
+ *   out          [B, S, >= Dv + Dk] of `out_dtype` (bf16 or f16; a 16-bit cache
+ *                has this type too); row t starts out_row_stride elements after
+ *                row t - 1 (0 means Dv + Dk). The row of an entry -1 is left as
+ *                it was; so is that of an entry out of range, which raises
+ *                KVR_DEVERR_INDEX. Must not overlap an input.
+ *
+ * Decoded in float32 (the code times the correctly rounded 1/scale), rounded
+ * once to out_dtype. Limits as kvr_kv_args, but Dk >= 0 (0: no k part; k_cache
+ * may then be NULL) and odd widths are fine.
+ */
+typedef struct kvr_read_args {
+    const void* ckv_cache;
+    kvr_dtype ckv_dtype;
+    const float* ckv_scale;
+    int64_t ckv_scale_len;
+    const void* k_cache;
+    kvr_dtype k_dtype;
+    const float* k_scale;
+    int64_t k_scale_len;
+    kvr_cache_mode mode;
+    int64_t cache_d0, cache_d1;
+    const int64_t* index;
+    int64_t B, S, Dv, Dk;
+    void* out;
+    kvr_dtype out_dtype;
+    int64_t out_row_stride;
+    int32_t* dev_status;
+} kvr_read_args;
+
+kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of mla_attention(): for token j of sequence n and head h
+ *
+ *   s[i] = softmax_scale * (q_nope . c[i] + q_rope . k[i])      over the keys i it sees
+ *   out  = sum_i softmax(s)[i] c[i]
+ *
+ * with c[i], k[i] the rows of key i of the sequence in ckv_cache and k_cache
+ * (the absorbed form of latent attention: one key row for all heads, its
+ * latent part is the value too).
+ *
+ *   q_nope, q_rope  [T, H, Dv] and [T, H, Dk], element type `dtype` (bf16 or
+ *                f16), last axis dense, row (t, h) at t * token_stride +
+ *                h * head_stride elements.
+ *   query_start  int64 [N + 1]: the new tokens of sequence n are rows
+ *                [query_start[n], query_start[n + 1]) of q and out. Rows outside
+ *                every sequence are left as they were. A sequence where it
+ *                decreases or leaves [0, T] is left out (KVR_DEVERR_QUERY).
+ *   key_length   int64 [N]: keys of the sequence, its new tokens among them (as
+ *                qsa_prepare's). A negative one, or one beyond the block table (the
+ *                cache batch in Norm mode): the sequence is left out
+ *                (KVR_DEVERR_KEY_LENGTH).
+ *   causal       nonzero: with L new tokens and K keys, token j sees keys
+ *                [0, K - L + j + 1), and nothing where that is empty (L > K).
+ *                0: every token sees all K keys.
+ *                Keys at or behind K are never used, whatever they hold.
+ *   mode         KVR_CACHE_NORM: sequence n reads cache batch n (needs
+ *                cache_d0 >= N; no block table). KVR_CACHE_PA_BSND or
+ *                KVR_CACHE_PA_BLK_BSND: key i is in block
+ *                block_table[n, i / d1] at i % d1.
+ *   block_table  int64 [N, max_blocks]. An entry -1 leaves that block's keys out
+ *                (nothing of them is read); so does one out of range, which
+ *                raises KVR_DEVERR_INDEX if a token sees the block. Entries
+ *                behind the last key are not used.
+ *   ckv_dtype, k_dtype, ckv_scale, k_scale  as in kvr_kv_args; an 8-bit code
+ *                stands for code / scale[c].
+ *   out          [T, H, Dv] `dtype`, strides as for q. A token that sees no key
+ *                gets zeros.
+ *   lse          optional out float32 [T, H]: log(sum_i exp(s[i])), -inf for a
+ *                token that sees no key.
+ *   workspace    device memory of kvr_mla_attention_workspace(args) bytes,
+ *                16-byte aligned; it holds nothing between calls. Calls that can
+ *                run at the same time need one each.
+ *   dev_status   optional int32 device word (the bits above and
+ *                KVR_DEVERR_TIMEOUT).
+ *
+ * Limits: T, H, N >= 0; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256; keys of a
+ * sequence < 2^30. Rows of at most 512 + 64 channels, both multiples of 8, on
+ * 16-byte boundaries run on the tensor cores, all others on a plain kernel
+ * that is much slower.
+ * Scores, softmax and sums are float32; the tensor-core kernel rounds each
+ * probability to `dtype` for the second product, and with an 8-bit cache of
+ * per-channel scale q / scale[c] to `dtype` for the first one, which moves a
+ * score by up to one unit in the last place of `dtype` (relative to the terms'
+ * size) and lse with it.
+ * out, lse and workspace must not overlap an input or one another. The result
+ * of a call does not change from run to run on one GPU.
+ */
+typedef struct kvr_mla_args {
+    const void* q_nope;
+    const void* q_rope;
+    kvr_dtype dtype;
+    int64_t T, H, Dv, Dk;
+    int64_t q_nope_token_stride, q_nope_head_stride;
+    int64_t q_rope_token_stride, q_rope_head_stride;
+    int64_t N;
+    const int64_t* query_start;
+    const int64_t* key_length;
+    kvr_cache_mode mode;
+    int64_t cache_d0, cache_d1;
+    const int64_t* block_table;
+    int64_t max_blocks;
+    const void* ckv_cache;
+    kvr_dtype ckv_dtype;
+    const float* ckv_scale;
+    int64_t ckv_scale_len;
+    const void* k_cache;
+    kvr_dtype k_dtype;
+    const float* k_scale;
+    int64_t k_scale_len;
+    float softmax_scale;
+    int32_t causal;
+    void* out;
+    int64_t out_token_stride, out_head_stride;
+    float* lse;
+    void* workspace;
+    int64_t workspace_bytes;
+    int32_t* dev_status;
+} kvr_mla_args;
+
+kvr_status mla_attention(const kvr_mla_args* args, cudaStream_t stream);
+
+/* Bytes of workspace that mla_attention(args) needs on the current device (0
+ * where it needs none). Depends on the widths, types, strides and alignments
+ * in *args, not on the lengths; `workspace` itself is not looked at. */
+int64_t kvr_mla_attention_workspace(const kvr_mla_args* args);
 
 /* Measurement helper (no counterpart on the pages): a 16-byte vectorised
  * device-to-device copy of `bytes` bytes (a multiple of 16, both pointers

@@ -1,0 +1,115 @@
+"""GPU parity of mla_attention against the float64 oracle, within the bounds that check_mla derives."""
+import numpy as np
+import pytest
+import torch
+
+import attention_prologue_kv_gb300 as kvr
+from attention_helpers import SENTINEL, check_mla, mla_case, on_tensor_cores, oracle_mla, rounded_query, run_mla
+
+pytestmark = pytest.mark.gpu
+
+
+def check(c):
+    per_channel = any(s is not None and s.numel() > 1 for s in (c.ckv_scale, c.k_scale))
+    got = run_mla(c)
+    tc = on_tensor_cores(c)
+    q = rounded_query(c) if per_channel and tc else [None, None]
+    check_mla(c, got, oracle_mla(c, *q), p_rounded=tc)
+    if per_channel:   # and near the definition itself
+        want = oracle_mla(c)[0]
+        fin = want != SENTINEL
+        assert np.linalg.norm((got[0] - want)[fin]) <= 4 * torch.finfo(c.q_nope.dtype).eps * np.linalg.norm(want[fin])
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new,keys,H", [
+    ([1], [1], 1), ([1], [64], 16), ([1], [65], 128), ([1], [1000], 16), ([1, 1, 1], [1, 63, 129], 40), ([5], [5], 3),
+    ([130], [130], 1), ([7, 1, 0, 3], [300, 9, 20, 3], 20), ([33], [200], 7), ([2, 2], [700, 64], 130), ([1] * 40, list(range(1, 41)), 2)])
+def test_lengths_and_heads(new, keys, H, dtype):
+    check(mla_case(new, keys, H, dtype=dtype, seed=H))
+
+
+@pytest.mark.parametrize("block_size", [1, 3, 16, 32, 64, 100, 128, 500])
+def test_block_sizes(block_size):
+    check(mla_case([3, 1], [401, 130], 8, block_size=block_size, seed=block_size))
+
+
+@pytest.mark.parametrize("mode", ["Norm", "PA_BLK_BSND"])
+def test_modes(mode):
+    check(mla_case([3, 1, 2], [401, 130, 64], 8, mode=mode, seed=1))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_masks(causal):
+    """More new tokens than keys, no keys at all, rows behind the last sequence."""
+    c = mla_case([9, 4, 1, 1], [5, 0, 0, 70], 6, causal=causal, gap=3, seed=2)
+    out, lse, _ = check(c)
+    assert (out[-3:] == SENTINEL).all() and (lse[-3:] == SENTINEL).all()
+    if causal:
+        assert (out[:4] == 0).all() and np.isneginf(lse[:4]).all()
+
+
+def test_holes_in_the_block_table():
+    check(mla_case([1, 4, 1], [200, 90, 33], 16, holes=[(0, 0), (0, 7), (1, 2), (1, 5), (2, 0), (2, 1), (2, 2)], seed=3))
+
+
+def test_bad_metadata_leaves_sequences_out():
+    c = mla_case([2, 1, 3, 1], [40, 50, 60, 33], 4, gap=4, seed=4)
+    c.key_length[1] = -1
+    c.key_length[2] = 10 ** 7
+    check(c)
+    c = mla_case([2, 1, 3, 1], [40, 50, 60, 33], 4, gap=4, seed=4)
+    c.table[3, 1] = 10 ** 9
+    c.table[0, 0] = -5
+    check(c)
+    c.query_start[4] = 10 ** 6
+    check(c)
+    c.query_start[:] = torch.tensor([2, 1, 3, 8, 8])
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cache", ["int8", "fp8_e4m3fn", "fp8_e5m2"])
+@pytest.mark.parametrize("k8,scale_len", [(False, 1), (True, 1), (False, 0), (True, 0)])
+def test_8_bit_caches(cache, dtype, k8, scale_len):
+    check(mla_case([1, 5, 1], [190, 77, 64], 12, dtype=dtype, cache=cache, k_cache=cache if k8 else None, scale_len=scale_len,
+                   k_scale_len=scale_len, seed=6))
+
+
+@pytest.mark.parametrize("Dv,Dk", [(256, 32), (64, 8), (320, 64), (512, 16), (10, 6), (1, 1), (1000, 130), (504, 56)])
+@pytest.mark.parametrize("cache", [None, "int8"])
+def test_widths(Dv, Dk, cache):
+    check(mla_case([3, 1], [150, 70], 5, Dv, Dk, cache=cache, seed=Dv))
+
+
+@pytest.mark.parametrize("pad", [0, 8, 3])
+def test_strided_queries(pad):
+    check(mla_case([3, 1], [150, 70], 5, pad=pad, seed=pad))
+
+
+@pytest.mark.parametrize("spread", [0.01, 30.0])
+def test_flat_and_sharp_softmax(spread):
+    check(mla_case([2], [700], 16, spread=spread, seed=8))
+
+
+def test_long_context_of_one_token():
+    check(mla_case([1], [20000], 8, block_size=128, seed=9))
+
+
+def test_repeats_are_equal():
+    """One GPU, the same inputs: the same bits."""
+    c = mla_case([40, 1], [2000, 900], 24, block_size=64, seed=10)
+    a, b = run_mla(c), run_mla(c)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_empty_problems():
+    for T, H, n in ((0, 4, 2), (3, 0, 1), (3, 4, 0)):
+        z = lambda *s: torch.full(s, SENTINEL, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+        out = z(T, H, 512)
+        kvr.mla_attention(z(T, H, 512), z(T, H, 64), z(2, 4, 1, 512), z(2, 4, 1, 64), torch.zeros(n, 2, device="cuda", dtype=torch.int64),
+                          torch.zeros(n + 1, device="cuda", dtype=torch.int64), torch.zeros(n, device="cuda", dtype=torch.int64), out,
+                          softmax_scale=1.0)
+        torch.cuda.synchronize()
+        assert (out == SENTINEL).all()
