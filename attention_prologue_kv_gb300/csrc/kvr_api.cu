@@ -588,6 +588,17 @@ kvr_status check_caches(kvr_dtype dt, kvr_dtype ckv_dtype, kvr_dtype k_dtype, co
     return KVR_OK;
 }
 
+// Rows that the tensor-core kernel takes: whole 16-byte chunks (16 codes of an
+// 8-bit cache), at most 512 + 64 channels.
+bool mla_tensor_cores(const kvr_mla_args* a) {
+    const int64_t dv = is8(a->ckv_dtype) ? 16 : 8, dk = is8(a->k_dtype) ? 16 : 8;
+    for (const int64_t s : {a->q_nope_token_stride, a->q_nope_head_stride, a->q_rope_token_stride, a->q_rope_head_stride,
+                            a->out_token_stride, a->out_head_stride})
+        if (s % 8 != 0) return false;
+    return a->Dv <= 512 && a->Dk <= 64 && a->Dv % dv == 0 && a->Dk % dk == 0 && a->H <= 65536 && aligned(a->q_nope, 16) &&
+           aligned(a->q_rope, 16) && aligned(a->out, 16) && aligned(a->ckv_cache, 16) && aligned(a->k_cache, 16);
+}
+
 // Validate the arguments of mla_attention. `*empty`: nothing to launch.
 kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
     *empty = false;
@@ -679,8 +690,7 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
 extern "C" {
 
 int64_t kvr_mla_attention_workspace(const kvr_mla_args* a) {
-    (void)a;
-    return 0;
+    return a != nullptr && mla_tensor_cores(a) ? mla_tc_workspace(int(a->Dv)) : 0;
 }
 
 kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
@@ -688,8 +698,13 @@ kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
     bool empty;
     const kvr_status st = mla_plan(a, &p, &empty);
     if (st != KVR_OK || empty) return st;
+    const bool tc = mla_tensor_cores(a);
+    if (tc) {
+        if (a->workspace == nullptr) return KVR_ERR_NULL;
+        if (!aligned(a->workspace, 16) || a->workspace_bytes < mla_tc_workspace(p.Dv)) return KVR_ERR_SHAPE;
+    }
     (void)cudaGetLastError();
-    return cuda_status(launch_mla_generic(p, a->dtype, stream));
+    return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));
 }
 
 kvr_status kv_cache_read(const kvr_read_args* a, cudaStream_t stream) {

@@ -19,6 +19,7 @@ namespace kvr {
 enum OutKind : int { OUT16 = 0, OUT_I8 = 1, OUT_E4M3 = 2, OUT_E5M2 = 3 };
 
 struct BF16 {
+    static constexpr bool is_bf16 = true;
     static __device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16); }
     static __device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
     static __device__ __forceinline__ float one(uint16_t u) { return __uint_as_float(uint32_t(u) << 16); }
@@ -33,6 +34,7 @@ struct BF16 {
 };
 
 struct F16 {
+    static constexpr bool is_bf16 = false;
     static __device__ __forceinline__ float lo(uint32_t u) { return __half2float(__ushort_as_half(uint16_t(u & 0xFFFFu))); }
     static __device__ __forceinline__ float hi(uint32_t u) { return __half2float(__ushort_as_half(uint16_t(u >> 16))); }
     static __device__ __forceinline__ float one(uint16_t u) { return __half2float(__ushort_as_half(u)); }
@@ -381,6 +383,8 @@ cudaError_t launch_dq(const DqParams& p, int in_dtype, bool vec, cudaStream_t s)
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool vec, cudaStream_t s);
 cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s);
 cudaError_t launch_mla_generic(const MlaParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s);
+int64_t mla_tc_workspace(int Dv);   // bytes on the current device
 
 int sm_count_current_device();
 

@@ -553,9 +553,10 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *                KVR_DEVERR_TIMEOUT).
  *
  * Limits: T, H, N >= 0; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256; keys of a
- * sequence < 2^30. Rows of at most 512 + 64 channels, both multiples of 8, on
- * 16-byte boundaries run on the tensor cores, all others on a plain kernel
- * that is much slower.
+ * sequence < 2^30. Rows of at most 512 + 64 channels, both multiples of 8 (of
+ * 16 in an 8-bit cache), on 16-byte boundaries (q, out, caches; strides
+ * multiples of 8) and with H <= 65536 run on the tensor cores, all others on a
+ * plain kernel that is much slower.
  * Scores, softmax and sums are float32; the tensor-core kernel rounds each
  * probability to `dtype` for the second product, and with an 8-bit cache of
  * per-channel scale q / scale[c] to `dtype` for the first one, which moves a
