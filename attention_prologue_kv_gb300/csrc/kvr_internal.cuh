@@ -347,6 +347,7 @@ struct MlaParams {
     int ckv_scale_per_ch, k_scale_per_ch;
     float scale;                // softmax scale
     int pairs;                  // tensor-core kernel: CTA pairs of the grid
+    int box_rows;               // its TMA boxes' rows (0: none)
 };
 
 // Launch with programmatic stream serialisation allowed: the grid may be

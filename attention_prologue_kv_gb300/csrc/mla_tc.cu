@@ -17,7 +17,7 @@
 // reads only its half of the second operand: S splits the keys between the CTAs,
 // P C splits the channels (CTA r has channels [128 r, 128 r + 128) of each 256).
 //
-// A key step in a CTA, three steps in flight:
+// A key step in a CTA, up to four in flight:
 //   load   its 32 keys, all channels, into 9 boxes [32 keys x 64 channels];
 //   S      128 x 64 by the pair; the other CTA's keys come from its shared memory;
 //   swap   the boxes of channels that the other CTA sums are dead now: they take
@@ -31,6 +31,7 @@
 // its O, m and l in the workspace, and a second kernel joins them in a fixed
 // order, so results do not change from run to run.
 #include <mutex>
+#include <type_traits>
 
 #include "tcgen05.cuh"
 
@@ -40,11 +41,13 @@ namespace {
 
 constexpr int ROWS = 128, CROWS = 64;    // rows of a pair, of a CTA
 constexpr int KEYS = 64, CKEYS = 32;     // keys of a step, of a CTA
-constexpr int STAGES = 3;
 constexpr uint32_t QBOX = CROWS * 128, KBOX = CKEYS * 128;
 constexpr uint32_t STAGE_BYTES = 9 * KBOX, PBUF = CROWS * 128;
-constexpr uint32_t OFF_Q = 0, OFF_K = 9 * QBOX, OFF_P = OFF_K + STAGES * STAGE_BYTES, OFF_MISC = OFF_P + 2 * PBUF;
-constexpr int THREADS = 416;             // 4 softmax, 4 key, 4 swap and query warps, 1 MMA warp
+constexpr uint32_t OFF_Q = 0, OFF_P = 9 * QBOX, OFF_K = OFF_P + PBUF;
+constexpr int MAX_STAGES = 4;
+// Steps in flight: 4 fill the shared memory; with codes 3, which leaves room for the scales.
+template <bool C8>
+constexpr int stages_of() { return C8 ? 3 : 4; }
 constexpr uint32_t TMEM_COLS = 512, COL_S = 256;   // O: columns 0..255, S: two buffers of 32 + 32
 constexpr int64_t ITEM_COST = 128;       // an item's own cost, in keys
 constexpr int64_t MIN_KEYS = 128;        // least work of a pair, in keys
@@ -54,17 +57,24 @@ struct Bound {
 };
 
 struct Misc {
-    uint64_t k_full[STAGES], v_full[STAGES], empty[STAGES];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
+    uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t s_full[2], p_full, pv_done, q_full, q_free, k_fix, v_fix, drain;
     uint32_t tmem;
     int abort;
     Bound begin, end;
     int64_t wsum[16];
-    float red[2][128], lred[128];
-    float inv_v[512], inv_k[64];
-    float lift[2];
+    float red[2][128];
+    float inv_k[64], lift;   // 1 / scale of the rotary channels; a power of two taken out of their queries
 };
-constexpr uint32_t SMEM_BYTES = OFF_MISC + uint32_t(sizeof(Misc)) + 1024;
+struct Scales {              // behind Misc, with codes
+    float inv_v[512];        // 1 / scale of a channel
+    float row_mul[2][64];    // power of two taken out of a row's queries, of this part and the next
+};
+template <bool C8>
+constexpr uint32_t smem_of() {
+    return OFF_K + stages_of<C8>() * STAGE_BYTES + uint32_t(sizeof(Misc)) + (C8 ? uint32_t(sizeof(Scales)) : 0u) + 1024u;
+}
+static_assert(smem_of<false>() <= 232448 && smem_of<true>() <= 232448, "shared memory of a CTA");
 
 // Workspace: header, first bounds of the pairs, (m, l) and O of two parts a pair.
 struct Space {
@@ -164,6 +174,7 @@ struct Walk {
 };
 
 // This pair's share of the work: every CTA scans all sequences' costs.
+template <int THREADS>
 __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (int(p.N) + THREADS - 1) / THREADS;
@@ -268,459 +279,604 @@ __device__ __forceinline__ uint32_t box_at(uint32_t box, int row, int chunk) {
     return box + uint32_t(row) * 128u + (uint32_t(chunk ^ (row & 7)) << 4);
 }
 
+// Cache rows through TMA: R rows a box (0: no TMA, 16-byte copies instead).
+struct Maps {
+    CUtensorMap ckv, kc;
+};
+
+// What every role has.
+struct Ctx {
+    const MlaParams& p;
+    Misc* m;
+    Scales* sc;
+    uint32_t base, tmem, rank;
+    int lane, nb;        // nb: 64-channel boxes of the latent part
+    volatile int* abort;
+    bool ok;
+
+    // A wait that gives up (one second) poisons the CTA: the others give up at their first look, and every role
+    // runs its loops to the end without waiting, so that no barrier is left with threads missing.
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+        if (!mbar_wait_cluster(bar, parity, abort)) {
+            *abort = 1;
+            ok = false;
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ uint32_t stage(int st) const { return base + OFF_K + uint32_t(st) * STAGE_BYTES; }
+    // This warp's shared-memory writes are done: tell the MMA warp of the pair.
+    __device__ __forceinline__ void arrive(uint64_t* bar) {
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(bar, 0);
+    }
+};
+
+// One warp brings a CTA's 16-bit cache rows, step by step: SWAP = false its own
+// 32 keys (all channels, rotary part in box 8), SWAP = true the other CTA's keys
+// (this CTA's channels, into the boxes that the scores are done with).
+// Rows that do not exist become zeros: a NaN there would reach the sum through
+// its zero weight.
+template <class IT, bool K8, bool SWAP>
+__device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
+    constexpr int STAGES = stages_of<false>();
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int lane = c.lane, R = p.box_rows;
+    // Boxes: latent ones first; the place of box b, its 64 channels.
+    const int nl = SWAP ? min(2, max(0, c.nb - 2 * int(c.rank))) + min(2, max(0, c.nb - 4 - 2 * int(c.rank))) : c.nb;
+    const int n = SWAP ? nl : nl + 1;
+    auto place = [&](int b) {
+        if (SWAP) return (b >> 1) * 4 + int(c.rank ^ 1) * 2 + (b & 1);
+        return b < nl ? b : 8;
+    };
+    auto channels = [&](int b) { return SWAP ? (b >> 1) * 4 + int(c.rank) * 2 + (b & 1) : b; };
+    uint64_t* fix = SWAP ? &m->v_fix : &m->k_fix;
+    uint64_t* full = SWAP ? m->v_full : m->k_full;
+    int j = 0, fixed = 0, pend = -1;
+    const int mine = int(SWAP ? c.rank ^ 1 : c.rank) * CKEYS + lane;   // this lane's key of a step
+    Walk w(p, m->begin, m->end);
+    while (w.next()) {
+        int64_t next = key_slot(p, w.n, w.s.K, w.kt0 * KEYS + mine);
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+            const int st = j % STAGES;
+            const uint32_t stage = c.stage(st);
+            const int64_t slot = next;
+            if (kt + 1 < w.kt1) next = key_slot(p, w.n, w.s.K, (kt + 1) * KEYS + mine);
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+            uint2 codes[8];
+            if (K8 && !SWAP) {   // rotary codes: 8 of each row (lane >> 3) + 4 rr, decoded below
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr) {
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, slot, rr * 4 + (lane >> 3));
+                    codes[rr] = row >= 0 && (lane & 7) < p.Dk / 8
+                                    ? ld_stream_v2(static_cast<const uint8_t*>(p.kc) + row * p.Dk + (lane & 7) * 8)
+                                    : make_uint2(0, 0);
+                }
+            }
+            uint64_t* bar = SWAP ? &m->s_full[j & 1] : &m->empty[st];
+            const uint32_t parity = SWAP ? (j >> 1) & 1 : ((j / STAGES) & 1) ^ 1;
+            if (SWAP || j >= STAGES) {
+                if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(bar, parity))) {
+                    cp_async_wait<0>();
+                    c.arrive(&full[pend]);
+                    pend = -1;
+                }
+                c.wait(bar, parity);
+            }
+            if (R > 0) {
+                const bool whole = live == 0xFFFFFFFFu;
+                const int groups = CKEYS / R;
+                if (whole) {
+                    if (lane == 0) mbar_expect_at(&full[st], 0, uint32_t(n) * KBOX);
+                } else if (live != 0) {
+                    // Boxes with a row that exists; their other rows are cleared below.
+                    int some = 0;
+                    for (int g = 0; g < groups; ++g) some += (live >> (g * R) & 1);
+                    if (lane == 0) mbar_arrive_expect_tx(fix, uint32_t(n * some) * uint32_t(R) * 128u);
+                }
+                __syncwarp();
+                for (int q0 = 0; q0 < n * groups; q0 += 32) {
+                    const int q = q0 + lane, g = min(q / n, groups - 1), b = q - g * n;
+                    const int row = __shfl_sync(0xFFFFFFFFu, int(slot), g * R);
+                    if (q < n * groups && row >= 0)
+                        tma_box_at(stage + uint32_t(place(b)) * KBOX + uint32_t(g * R) * 128u, SWAP || b < nl ? &maps.ckv : &maps.kc,
+                                   SWAP || b < nl ? channels(b) * 64 : 0, row, whole ? &full[st] : fix, whole ? 0 : c.rank);
+                }
+                if (!whole) {
+                    if (live != 0) {
+                        c.wait(fix, fixed & 1);
+                        ++fixed;
+                    }
+                    if (slot < 0)
+                        for (int b = 0; b < n; ++b)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                st_shared_v4(stage + uint32_t(place(b)) * KBOX + uint32_t(lane) * 128u + k * 16u, make_uint4(0, 0, 0, 0));
+                    c.arrive(&full[st]);
+                }
+            } else {
+                const int nc = p.Dv / 8, nr = p.Dk / 8, ch = lane & 7;
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr) {
+                    const int r = rr * 4 + (lane >> 3);
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, slot, r);
+                    const uint16_t* v = static_cast<const uint16_t*>(p.ckv) + (row < 0 ? 0 : row) * p.Dv;
+                    for (int b = 0; b < nl; ++b) {
+                        const int q = channels(b) * 8 + ch;
+                        const bool in = row >= 0 && q < nc;
+                        cp_async16(box_at(stage + uint32_t(place(b)) * KBOX, r, ch), in ? v + q * 8 : v, in);
+                    }
+                    if (K8 && !SWAP) {
+                        st_shared_v4(box_at(stage + 8 * KBOX, r, ch), dec8x8<IT>(p.k_kind, codes[rr].x, codes[rr].y));
+                    } else if (!SWAP) {
+                        const uint16_t* k = static_cast<const uint16_t*>(p.kc) + (row < 0 ? 0 : row) * p.Dk;
+                        const bool in = row >= 0 && ch < nr;
+                        cp_async16(box_at(stage + 8 * KBOX, r, ch), in ? k + ch * 8 : k, in);
+                    }
+                }
+                cp_async_commit();
+                if (pend >= 0) {
+                    cp_async_wait<1>();
+                    c.arrive(&full[pend]);
+                }
+                pend = st;
+            }
+        }
+    }
+    if (pend >= 0) {
+        cp_async_wait<0>();
+        c.arrive(&full[pend]);
+    }
+}
+
+// Four warps decode a CTA's 8-bit rows into halves (the rotary part into q's type).
+// Thread (key tk, quarter c4): 16 codes a load, the next step's loads in flight.
+template <class IT, bool SWAP>
+__device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int tk = v >> 2, c4 = v & 3;
+    constexpr int STAGES = stages_of<true>();
+    constexpr int NX = SWAP ? 4 : 8;
+    const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16;
+    uint4 x[NX], y[NX], xr[2], yr[2];
+    auto load = [&](int kt, uint4 (&a)[NX], uint4 (&ar)[2]) {
+        const int64_t slot = key_slot(p, w.n, w.s.K, kt * KEYS + int(SWAP ? c.rank ^ 1 : c.rank) * CKEYS + tk);
+        const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (slot < 0 ? 0 : slot) * p.Dv;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int q = SWAP ? ((i >> 1) * 4 + int(c.rank) * 2 + (i & 1)) * 4 + c4 : c4 + 4 * i;
+            a[i] = slot >= 0 && q < nc ? ld_stream_v4(src + q * 16) : make_uint4(0, 0, 0, 0);
+        }
+        if (!SWAP) {
+            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + (slot < 0 ? 0 : slot) * p.Dk * (p.k_kind == OUT16 ? 2 : 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int q = c4 + 4 * i;
+                ar[i] = slot >= 0 && q < nr ? ld_stream_v4(k + q * 16) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    load(w.kt0, x, xr);
+    for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+        if (kt + 1 < w.kt1) load(kt + 1, y, yr);
+        const int st = j % STAGES;
+        const uint32_t stage = c.stage(st);
+        if (SWAP) c.wait(&m->s_full[j & 1], (j >> 1) & 1);
+        else if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int b = SWAP ? (i >> 1) * 4 + int(c.rank ^ 1) * 2 + (i & 1) : i;
+            if ((SWAP ? (i >> 1) * 4 + int(c.rank) * 2 + (i & 1) : i) >= c.nb) continue;
+            const uint32_t box = stage + uint32_t(b) * KBOX;
+            st_shared_v4(box_at(box, tk, 2 * c4), dec8x8<F16>(p.ckv_kind, x[i].x, x[i].y));
+            st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<F16>(p.ckv_kind, x[i].z, x[i].w));
+        }
+        if (!SWAP) {
+            const uint32_t box = stage + 8 * KBOX;
+            if (p.k_kind == OUT16) {
+                st_shared_v4(box_at(box, tk, c4), xr[0]);
+                st_shared_v4(box_at(box, tk, c4 + 4), xr[1]);
+            } else {
+                st_shared_v4(box_at(box, tk, 2 * c4), dec8x8<IT>(p.k_kind, xr[0].x, xr[0].y));
+                st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<IT>(p.k_kind, xr[0].z, xr[0].w));
+            }
+        }
+        c.arrive(SWAP ? &m->v_full[st] : &m->k_full[st]);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) x[i] = y[i];
+        xr[0] = yr[0];
+        xr[1] = yr[1];
+    }
+}
+
+// Four warps bring the queries of a part: lane v & 7 has chunk v & 7 of each box of row v / 8.
 template <class IT, bool C8>
-__global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1) mla_tc_kernel(const __grid_constant__ MlaParams p) {
+__device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int part) {
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int nc = p.Dv / 8, nr = p.Dk / 8, ch = v & 7;
+    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+#pragma unroll 1
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + (v >> 3);
+        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
+        const bool live = row < unsigned(w.s.L) * unsigned(p.H);
+        const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
+        const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
+        const uint16_t* qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
+        if constexpr (!C8) {
+            const bool scaled = p.k_kind != OUT16 && p.k_scale_per_ch;
+            for (int b = 0; b < 8; ++b) {
+                const int q = b * 8 + ch;
+                if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), live && q < nc ? qn + q * 8 : qn, live && q < nc);
+            }
+            if (!scaled) cp_async16(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), live && ch < nr ? qr + ch * 8 : qr, live && ch < nr);
+        } else {
+            // Halves of q / scale: 11 bits keep the rounding of the one product that has to be rounded small. A power
+            // of two per row, put back into its scores, brings the largest to [2^13, 2^14): float16's range then
+            // reaches 2^-38 below it.
+            const bool per = p.ckv_scale_per_ch;
+            uint4 x[8];
+            float top = 0.f;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const int q = b * 8 + ch;
+                x[b] = live && q < nc ? ld_stream_v4(qn + q * 8) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
+                const float* f = c.sc->inv_v + b * 64 + ch * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = fmaxf(top, fmaxf(fabsf(IT::lo(u[k]) * (per ? f[2 * k] : 1.f)), fabsf(IT::hi(u[k]) * (per ? f[2 * k + 1] : 1.f))));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const int e = top > 0.f && top <= 3.0e38f ? max(ilogbf(top), -100) - 13 : 0;
+            const float g = ldexpf(1.f, -e);
+            if (ch == 0) c.sc->row_mul[part & 1][r] = ldexpf(1.f, e);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
+                const float* f = c.sc->inv_v + b * 64 + ch * 8;
+                uint32_t z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) z[k] = F16::pack(IT::lo(u[k]) * (per ? f[2 * k] : 1.f) * g, IT::hi(u[k]) * (per ? f[2 * k + 1] : 1.f) * g);
+                if (b < c.nb) st_shared_v4(box_at(c.base + OFF_Q + b * QBOX, r, ch), make_uint4(z[0], z[1], z[2], z[3]));
+            }
+        }
+        if (C8 || (p.k_kind != OUT16 && p.k_scale_per_ch)) {
+            // The rotary part keeps q's type; a scale per channel goes in with one rounding, over the largest
+            // 1 / scale (as a power of two, put back into the scores).
+            uint4 x = live && ch < nr ? ld_stream_v4(qr + ch * 8) : make_uint4(0, 0, 0, 0);
+            if (p.k_kind != OUT16 && p.k_scale_per_ch) {
+                uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                const float* f = m->inv_k + ch * 8;
+                const float g = 1.f / m->lift;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) u[k] = IT::pack(IT::lo(u[k]) * (f[2 * k] * g), IT::hi(u[k]) * (f[2 * k + 1] * g));
+            }
+            st_shared_v4(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), x);
+        }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    c.arrive(&m->q_full);
+}
+
+// Softmax and output of 128 threads: thread (row r, half h of the keys and channels).
+template <class IT, bool C8, bool K8>
+__device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
+    using PT = typename std::conditional<C8, F16, IT>::type;   // type of the weights and the decoded codes
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int lane = c.lane, r = tid & 63, h = tid >> 6, na = p.Dv > 256 ? 2 : 1;
+    const uint32_t lanes = c.tmem + (uint32_t(tid >> 5) << 21);
+    constexpr bool split = C8 || K8;
+    // Score = fn * (latent product) + fr * (rotary product), in powers of two.
+    const float l2 = p.scale * 1.4426950408889634f;
+    float fn = l2, fr = l2;
+    if (K8) fr = l2 * (p.k_scale_per_ch ? m->lift : m->inv_k[0]);
+    int j = 0, part = 0;
+    Walk w(p, m->begin, m->end);
+    while (w.next()) {
+        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
+        const bool live = row < unsigned(w.s.L) * unsigned(p.H);
+        const int t = int(row / unsigned(p.H)), head = int(row % unsigned(p.H));
+        const int vis = live ? seen(p, w.s.L, w.s.K, t) : 0;
+        int wmin = live ? vis : 0x7FFFFFFF;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
+        float mx = -INFINITY, sum = 0.f;
+        int64_t next = key_slot(p, w.n, w.s.K, w.kt0 * KEYS + h * CKEYS + lane);
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+            const int key0 = kt * KEYS + h * CKEYS;
+            // Keys that exist: bit i for key0 + i.
+            const uint32_t held = __ballot_sync(0xFFFFFFFFu, next >= 0);
+            if (kt + 1 < w.kt1) next = key_slot(p, w.n, w.s.K, key0 + KEYS + lane);
+            c.wait(&m->s_full[j & 1], (j >> 1) & 1);
+            tc_fence_after();
+            if (C8 && kt == w.kt0) fn = l2 * (p.ckv_scale_per_ch ? 1.f : c.sc->inv_v[0]) * c.sc->row_mul[part & 1][r];
+            float s[32];
+            tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64, s);
+            if (split) {
+                float s2[32];
+                tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64 + 32, s2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = fmaf(s2[i], fr, s[i] * fn);
+            } else {
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] *= fn;
+            }
+            if (held != 0xFFFFFFFFu || key0 + CKEYS > wmin) {
+                const int left = vis - key0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i >= left || !(held >> i & 1)) s[i] = -INFINITY;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
+            m->red[j & 1][tid] = top;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            top = fmaxf(fmaxf(top, m->red[j & 1][tid ^ 64]), mx);
+            // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
+            // and the 16-bit rounding of a weight is relative.
+            const bool grow = top > mx + 8.f;
+            const float f = grow ? exp2_approx(mx - top) : 1.f;
+            if (grow) {
+                mx = top;
+                sum *= f;
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float a = exp2_approx(s[2 * i] - ref), b = exp2_approx(s[2 * i + 1] - ref);
+                sum += a + b;
+                pk[i] = PT::pack(a, b);
+            }
+            // The product before this one is done: P's buffer is free and O at rest.
+            if (j > 0) c.wait(&m->pv_done, (j - 1) & 1);
+            if (__any_sync(0xFFFFFFFFu, grow) && kt > w.kt0) {
+                tc_fence_after();
+                for (int q = 0; q < na * 128; q += 32) {
+                    float o[32];
+                    tmem_ld32(lanes + q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= f;
+                    tmem_st32(lanes + q, o);
+                }
+                tmem_wait_st();
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                st_shared_v4(box_at(c.base + OFF_P, r, h * 4 + q), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+            tc_fence_before();
+            c.arrive(&m->p_full);
+        }
+        // Output of the part.
+        c.wait(&m->pv_done, (j - 1) & 1);
+        tc_fence_after();
+        m->red[j & 1][tid] = sum;   // the next step's buffer: its own maximum comes after this read
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const float l = m->red[j & 1][tid & 63] + m->red[j & 1][(tid & 63) + 64];
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const bool none = l == 0.f;
+        const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
+        uint16_t* out = nullptr;
+        float* po = nullptr;
+        if (w.whole) {
+            out = static_cast<uint16_t*>(p.out) + (w.s.q0 + t) * p.o_ts + int64_t(head) * p.o_hs;
+            if (live && h == 0 && p.lse != nullptr)
+                p.lse[(w.s.q0 + t) * p.H + head] = none ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+        } else {
+            const Space ws = ws_space(p);
+            const int64_t at = (int64_t(pair) * 2 + (part ? 1 : 0)) * ROWS + c.rank * CROWS + r;
+            po = ws.o + at * p.Dv;
+            if (live && h == 0) ws.ml[at] = make_float2(mx, l);
+        }
+        for (int q = 0; q < na * 128; q += 32) {
+            float o[32];
+            tmem_ld32(lanes + q, o);
+            tmem_wait_ld();
+            const int ch = (q >> 7) * 256 + h * 128 + (q & 127);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                o[i] = none ? 0.f : o[i] * inv;
+                if (C8) o[i] *= c.sc->inv_v[ch + i];
+            }
+            if (!live) continue;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                if (ch + k >= p.Dv) break;
+                if (w.whole) {
+                    *reinterpret_cast<uint4*>(out + ch + k) = make_uint4(IT::pack(o[k], o[k + 1]), IT::pack(o[k + 2], o[k + 3]),
+                                                                         IT::pack(o[k + 4], o[k + 5]), IT::pack(o[k + 6], o[k + 7]));
+                } else {
+                    *reinterpret_cast<float4*>(po + ch + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    *reinterpret_cast<float4*>(po + ch + k + 4) = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+                }
+            }
+        }
+        tc_fence_before();
+        ++part;
+    }
+}
+
+// The MMA warp of CTA 0: S of a step is issued before O of the one before, which waits for its softmax.
+template <class IT, bool C8, bool K8>
+__device__ __forceinline__ void mma_warp(Ctx& c) {
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    constexpr int STAGES = stages_of<C8>();
+    constexpr bool half = C8 || !IT::is_bf16;   // type of the latent operands
+    constexpr uint32_t id_n = tc_idesc(ROWS, KEYS, !half, false), id_r = tc_idesc(ROWS, KEYS, IT::is_bf16, false),
+                       id_o = tc_idesc(ROWS, 256, !half, true);
+    constexpr bool split = C8 || K8;
+    const bool leader = elect_one(), two = p.Dv > 256;
+    const uint64_t qd = tc_desc(c.base + OFF_Q, 16, 1024), pd = tc_desc(c.base + OFF_P, 16, 1024);
+    int j = 0, parts = 0;
+    bool prev = false, prev_first = false;
+    auto issue_o = [&](int i, bool first) {
+        c.wait(&m->p_full, i & 1);
+        c.wait(&m->v_full[i % STAGES], (i / STAGES) & 1);
+        tc_fence_after();
+        const uint64_t vd = tc_desc(c.stage(i % STAGES), KBOX, 1024);
+        if (leader) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                if (a == 0 || two)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        tc_mma_pair(c.tmem + a * 128, pd + s * 2, vd + ((a * 4 + (s >> 1) * 2) * KBOX + (s & 1) * 2048) / 16, id_o,
+                                    !(first && s == 0));
+            tc_commit_pair(&m->pv_done);
+            tc_commit_pair(&m->empty[i % STAGES]);
+        }
+        __syncwarp();
+    };
+    Walk w(p, m->begin, m->end);
+    while (w.next()) {
+        if (prev) issue_o(j - 1, prev_first);
+        prev = false;
+        c.wait(&m->q_full, parts & 1);
+        ++parts;
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+            const int st = j % STAGES;
+            c.wait(&m->k_full[st], (j / STAGES) & 1);
+            tc_fence_after();
+            const uint64_t kd = tc_desc(c.stage(st), 16, 1024);
+            const uint32_t d = c.tmem + COL_S + uint32_t(j & 1) * 64;
+            if (leader) {
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < c.nb)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            tc_mma_pair(d, qd + (b * QBOX) / 16 + s * 2, kd + (b * KBOX) / 16 + s * 2, id_n, b > 0 || s > 0);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    tc_mma_pair(d + (split ? 32 : 0), qd + (8 * QBOX) / 16 + s * 2, kd + (8 * KBOX) / 16 + s * 2, id_r, !split || s > 0);
+                tc_commit_pair(&m->s_full[j & 1]);
+                if (kt + 1 == w.kt1) tc_commit_pair(&m->q_free);
+            }
+            __syncwarp();
+            if (prev) issue_o(j - 1, prev_first);
+            prev = true;
+            prev_first = kt == w.kt0;
+        }
+    }
+    if (prev) issue_o(j - 1, prev_first);
+    if (!c.ok) {   // let what was issued finish before TMEM goes
+        if (leader) {
+            tc_commit_pair(&m->drain);
+            mbar_wait(&m->drain, 0, nullptr);
+        }
+        __syncwarp();
+    }
+}
+
+// Warps: 0-3 softmax. 16-bit latent rows: 4 keys, 5 swap, 6 MMA, 8-11 queries. Codes: 4-7 keys, 8-11 swap and queries,
+// 12 MMA.
+template <bool C8>
+constexpr int threads_of() { return C8 ? 416 : 384; }
+
+template <class IT, bool C8, bool K8>
+__global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
+    mla_tc_kernel(const __grid_constant__ MlaParams p, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t smem_raw[];
+    constexpr int NT = threads_of<C8>();
+    constexpr int MMA_WARP = C8 ? 12 : 6;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    Misc* m = reinterpret_cast<Misc*>(smem_raw + (base - smem_u32(smem_raw)) + OFF_MISC);
+    constexpr int STAGES = stages_of<C8>();
+    Misc* m = reinterpret_cast<Misc*>(smem_raw + (base - smem_u32(smem_raw)) + OFF_K + STAGES * STAGE_BYTES);
+    Scales* sc = reinterpret_cast<Scales*>(m + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
-    const int na = p.Dv > 256 ? 2 : 1, nb = (p.Dv + 63) / 64;
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&m->k_full[s], 8);
-            mbar_init(&m->v_full[s], 8);
+            mbar_init(&m->k_full[s], C8 ? 8 : 2);
+            mbar_init(&m->v_full[s], C8 ? 8 : 2);
             mbar_init(&m->empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&m->s_full[s], 1);
-            mbar_init(&m->p_full[s], 8);
-            mbar_init(&m->pv_done[s], 1);
-        }
+        mbar_init(&m->s_full[0], 1);
+        mbar_init(&m->s_full[1], 1);
+        mbar_init(&m->p_full, 8);
+        mbar_init(&m->pv_done, 1);
         mbar_init(&m->q_full, 8);
+        mbar_init(&m->q_free, 1);
+        mbar_init(&m->k_fix, 1);
+        mbar_init(&m->v_fix, 1);
         mbar_init(&m->drain, 1);
         m->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc_pair(&m->tmem, TMEM_COLS);
+    if (warp == MMA_WARP) tmem_alloc_pair(&m->tmem, TMEM_COLS);
     pdl_wait();
     pdl_launch_dependents();
-    schedule(p, m, pair);
-    // 1 / scale of each channel, and per part the power of two that the query is divided by (below).
-    if (C8 || p.k_kind != OUT16) {
-        for (int c = tid; c < 512; c += THREADS)
-            m->inv_v[c] = p.ckv_kind == OUT16 || c >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? c : 0];
-        if (tid < 64) m->inv_k[tid] = p.k_kind == OUT16 || tid >= p.Dk ? 1.f : 1.f / p.k_scale[p.k_scale_per_ch ? tid : 0];
-        __syncthreads();
-        if (warp < 2) {
-            float v = 0.f;
-            for (int c = lane; c < (warp ? p.Dk : p.Dv); c += 32) v = fmaxf(v, fabsf(warp ? m->inv_k[c] : m->inv_v[c]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-            if (lane == 0) m->lift[warp] = exp2f(ceilf(log2f(v)));
+    schedule<NT>(p, m, pair);
+    if (C8) {
+        for (int ch = tid; ch < 512; ch += NT) sc->inv_v[ch] = ch >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? ch : 0];
+    }
+    if (K8 && warp == 0) {
+        float v = 0.f;
+        for (int ch = lane; ch < 64; ch += 32) {
+            const float x = ch >= p.Dk ? 0.f : 1.f / p.k_scale[p.k_scale_per_ch ? ch : 0];
+            m->inv_k[ch] = x;
+            v = fmaxf(v, fabsf(x));
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        if (lane == 0) m->lift = exp2f(ceilf(log2f(v)));
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    volatile int* abort = &m->abort;
-    bool ok = true;
-    // A wait that gives up (one second) poisons the CTA: the others give up at their first look, and every role
-    // runs its loops to the end without waiting, so that no barrier is left with threads missing.
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!mbar_wait_cluster(bar, parity, abort)) {
-            *abort = 1;
-            ok = false;
-        }
-    };
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-        wait(bar, parity);
-        __syncwarp();
-    };
+    Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
 
     if (warp < 4) {
-        // ------------------------------------------------------------------
-        // Softmax and output: thread (row r, half h of the keys and channels).
-        // ------------------------------------------------------------------
-        const int r = tid & 63, h = tid >> 6;
-        const uint32_t lanes = tmem + (uint32_t(warp) << 21);
-        // Score = fn * (latent product) + fr * (rotary product), in powers of two.
-        const float l2 = p.scale * 1.4426950408889634f;
-        float fn = l2, fr = l2;
-        const bool split = C8 || p.k_kind != OUT16;
-        if (split) {
-            fn = l2 * (p.ckv_scale_per_ch ? m->lift[0] : m->inv_v[0]);
-            fr = l2 * (p.k_scale_per_ch ? m->lift[1] : m->inv_k[0]);
-        }
-        int j = 0, part = 0;
+        softmax_warps<IT, C8, K8>(c, tid, pair);
+    } else if (warp == MMA_WARP) {
+        if (rank == 0) mma_warp<IT, C8, K8>(c);
+    } else if constexpr (C8) {
         Walk w(p, m->begin, m->end);
-        while (w.next()) {
-            const unsigned row = unsigned(w.i) * ROWS + rank * CROWS + r;
-            const bool live = row < unsigned(w.s.L) * unsigned(p.H);
-            const int t = int(row / unsigned(p.H)), head = int(row % unsigned(p.H));
-            const int vis = live ? seen(p, w.s.L, w.s.K, t) : 0;
-            int wmin = live ? vis : 0x7FFFFFFF;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
-            float mx = -INFINITY, sum = 0.f;
-            for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-                const int key0 = kt * KEYS + h * CKEYS;
-                // Keys that exist: bit i for key0 + i.
-                const uint32_t held = __ballot_sync(0xFFFFFFFFu, key_slot(p, w.n, w.s.K, key0 + lane) >= 0);
-                wait_warp(&m->s_full[j & 1], (j >> 1) & 1);
-                tc_fence_after();
-                float s[32];
-                tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64, s);
-                if (split) {
-                    float s2[32];
-                    tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64 + 32, s2);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = fmaf(s2[i], fr, s[i] * fn);
-                } else {
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] *= fn;
-                }
-                if (held != 0xFFFFFFFFu || key0 + CKEYS > wmin) {
-                    const int left = vis - key0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i >= left || !(held >> i & 1)) s[i] = -INFINITY;
-                }
-                float top = s[0];
-#pragma unroll
-                for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
-                m->red[j & 1][tid] = top;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                top = fmaxf(fmaxf(top, m->red[j & 1][tid ^ 64]), mx);
-                // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
-                // and the 16-bit rounding of a weight is relative.
-                const bool grow = top > mx + 8.f;
-                const float f = grow ? exp2f(mx - top) : 1.f;
-                if (grow) {
-                    mx = top;
-                    sum *= f;
-                }
-                if (__any_sync(0xFFFFFFFFu, grow) && kt > w.kt0) {
-                    wait_warp(&m->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
-                    tc_fence_after();
-                    for (int c = 0; c < na * 128; c += 32) {
-                        float o[32];
-                        tmem_ld32(lanes + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= f;
-                        tmem_st32(lanes + c, o);
-                    }
-                    tmem_wait_st();
-                }
-                const float ref = mx == -INFINITY ? 0.f : mx;
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = exp2f(s[2 * i] - ref), b = exp2f(s[2 * i + 1] - ref);
-                    sum += a + b;
-                    pk[i] = IT::pack(a, b);
-                }
-                if (j >= 2) wait_warp(&m->pv_done[j & 1], ((j - 2) >> 1) & 1);
-                const uint32_t pb = base + OFF_P + uint32_t(j & 1) * PBUF;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st_shared_v4(box_at(pb, r, h * 4 + q), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-                fence_async_proxy();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(&m->p_full[j & 1], 0);
-            }
-            // Output of the part.
-            wait_warp(&m->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
-            tc_fence_after();
-            m->lred[tid] = sum;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            const float l = m->lred[tid & 63] + m->lred[(tid & 63) + 64];
-            const bool none = l == 0.f;
-            const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
-            uint16_t* out = nullptr;
-            float* po = nullptr;
-            if (w.whole) {
-                out = static_cast<uint16_t*>(p.out) + (w.s.q0 + t) * p.o_ts + int64_t(head) * p.o_hs;
-                if (live && h == 0 && p.lse != nullptr)
-                    p.lse[(w.s.q0 + t) * p.H + head] = none ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+        int j = 0;
+        for (int part = 0; w.next(); ++part) {
+            if (warp < 8) {
+                code_warps<IT, false>(c, tid - 128, w, j);
             } else {
-                const Space ws = ws_space(p);
-                const int64_t at = (int64_t(pair) * 2 + (part ? 1 : 0)) * ROWS + rank * CROWS + r;
-                po = ws.o + at * p.Dv;
-                if (live && h == 0) ws.ml[at] = make_float2(mx, l);
-            }
-            for (int c = 0; c < na * 128; c += 32) {
-                float o[32];
-                tmem_ld32(lanes + c, o);
-                tmem_wait_ld();
-                const int ch = (c >> 7) * 256 + h * 128 + (c & 127);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    o[i] = none ? 0.f : o[i] * inv;
-                    if (C8) o[i] *= m->inv_v[ch + i];
-                }
-                if (!live) continue;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (ch + 8 * q >= p.Dv) break;
-                    if (w.whole) {
-                        *reinterpret_cast<uint4*>(out + ch + 8 * q) =
-                            make_uint4(IT::pack(o[8 * q], o[8 * q + 1]), IT::pack(o[8 * q + 2], o[8 * q + 3]),
-                                       IT::pack(o[8 * q + 4], o[8 * q + 5]), IT::pack(o[8 * q + 6], o[8 * q + 7]));
-                    } else {
-                        *reinterpret_cast<float4*>(po + ch + 8 * q) = make_float4(o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3]);
-                        *reinterpret_cast<float4*>(po + ch + 8 * q + 4) =
-                            make_float4(o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]);
-                    }
-                }
-            }
-            tc_fence_before();
-            ++part;
-        }
-    } else if (warp < 8) {
-        // ------------------------------------------------------------------
-        // Keys: thread (key tk, quarter c4 of each 64-byte group).
-        // ------------------------------------------------------------------
-        const int tk = (tid - 128) >> 2, c4 = tid & 3;
-        int j = 0, pend = -1;
-        const int nc = p.Dv / 8, nr = p.Dk / 8;
-        Walk w(p, m->begin, m->end);
-        while (w.next()) {
-            for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-                const int st = j % STAGES;
-                const uint32_t stage = base + OFF_K + st * STAGE_BYTES;
-                const int64_t slot = key_slot(p, w.n, w.s.K, kt * KEYS + int(rank) * CKEYS + tk);
-                const bool have = slot >= 0;
-                const int64_t row = have ? slot : 0;
-                uint4 x[8], xr = make_uint4(0, 0, 0, 0);
-                if constexpr (C8) {
-                    const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + row * p.Dv;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int q = c4 + 4 * i;   // 16 codes
-                        x[i] = have && q * 2 < nc ? ld_stream_v4(src + q * 16) : make_uint4(0, 0, 0, 0);
-                    }
-                }
-                if (p.k_kind != OUT16 && have && c4 * 2 < nr) xr = ld_stream_v4(static_cast<const uint8_t*>(p.kc) + row * p.Dk + c4 * 16);
-                if (j >= STAGES) {
-                    const uint32_t ph = ((j / STAGES) & 1) ^ 1;
-                    if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(&m->empty[st], ph))) {
-                        cp_async_wait<0>();
-                        fence_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_at(&m->k_full[pend], 0);
-                        pend = -1;
-                    }
-                    wait(&m->empty[st], ph);
-                    __syncwarp();
-                }
-                if constexpr (C8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int q = 2 * (c4 + 4 * i);
-                        if (q >= nb * 8) continue;
-                        const uint32_t box = stage + uint32_t(q >> 3) * KBOX;
-                        st_shared_v4(box_at(box, tk, q & 7), dec8x8<IT>(p.ckv_kind, x[i].x, x[i].y));
-                        st_shared_v4(box_at(box, tk, (q & 7) + 1), dec8x8<IT>(p.ckv_kind, x[i].z, x[i].w));
-                    }
-                } else {
-                    const uint16_t* src = static_cast<const uint16_t*>(p.ckv) + row * p.Dv;
-                    for (int q = c4; q < nb * 8; q += 4) {
-                        const bool in = have && q < nc;
-                        cp_async16(box_at(stage + uint32_t(q >> 3) * KBOX, tk, q & 7), in ? src + q * 8 : src, in);
-                    }
-                }
-                if (p.k_kind != OUT16) {
-                    st_shared_v4(box_at(stage + 8 * KBOX, tk, 2 * c4), dec8x8<IT>(p.k_kind, xr.x, xr.y));
-                    st_shared_v4(box_at(stage + 8 * KBOX, tk, 2 * c4 + 1), dec8x8<IT>(p.k_kind, xr.z, xr.w));
-                } else {
-                    const uint16_t* src = static_cast<const uint16_t*>(p.kc) + row * p.Dk;
-                    for (int q = c4; q < 8; q += 4) {
-                        const bool in = have && q < nr;
-                        cp_async16(box_at(stage + 8 * KBOX, tk, q), in ? src + q * 8 : src, in);
-                    }
-                }
-                cp_async_commit();
-                if (pend >= 0) {
-                    cp_async_wait<1>();
-                    fence_async_proxy();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(&m->k_full[pend], 0);
-                }
-                pend = st;
+                load_queries<IT, true>(c, tid - 256, w, part);
+                code_warps<IT, true>(c, tid - 256, w, j);
             }
         }
-        cp_async_wait<0>();
-        fence_async_proxy();
-        __syncwarp();
-        if (pend >= 0 && lane == 0) mbar_arrive_at(&m->k_full[pend], 0);
-    } else if (warp < 12) {
-        // ------------------------------------------------------------------
-        // Queries of a part, then for each step the other CTA's keys.
-        // ------------------------------------------------------------------
-        const int v = tid - 256, tk = v >> 2, c4 = v & 3;
-        int j = 0, pend = -1;
-        const int nc = p.Dv / 8, nr = p.Dk / 8;
-        Walk w(p, m->begin, m->end);
-        while (w.next()) {
-            // The last product with the old queries is done: the loop below has waited for its S.
-            if (pend >= 0) {
-                cp_async_wait<0>();
-                fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(&m->v_full[pend], 0);
-                pend = -1;
-            }
-            const int c = v & 7;
-#pragma unroll 1
-            for (int it = 0; it < 4; ++it) {
-                const int r = it * 16 + (v >> 3);
-                const unsigned row = unsigned(w.i) * ROWS + rank * CROWS + r;
-                const bool live = row < unsigned(w.s.L) * unsigned(p.H);
-                const int64_t t = w.s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
-                const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
-                const uint16_t* qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
-                uint4 x[9];
-#pragma unroll
-                for (int b = 0; b < 9; ++b) {
-                    const int q = b < 8 ? b * 8 + c : c;
-                    x[b] = live && q < (b < 8 ? nc : nr) ? ld_stream_v4((b < 8 ? qn : qr) + q * 8) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int b = 0; b < 9; ++b) {
-                    // A scale per channel goes into the query, rounded once; over the part's largest 1 / scale
-                    // (as a power of two, put back into the score), so that float16 neither overflows nor loses bits.
-                    if (b < 8 ? C8 && p.ckv_scale_per_ch : p.k_scale_per_ch && p.k_kind != OUT16) {
-                        const float* f = b < 8 ? m->inv_v + b * 64 + c * 8 : m->inv_k + c * 8;
-                        const float g = 1.f / m->lift[b < 8 ? 0 : 1];
-                        uint32_t* u = reinterpret_cast<uint32_t*>(&x[b]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = IT::pack(IT::lo(u[k]) * (f[2 * k] * g), IT::hi(u[k]) * (f[2 * k + 1] * g));
-                    }
-                    st_shared_v4(box_at(base + OFF_Q + b * QBOX, r, c), x[b]);
-                }
-            }
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(&m->q_full, 0);
-            for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-                const int st = j % STAGES;
-                const uint32_t stage = base + OFF_K + st * STAGE_BYTES;
-                const int64_t slot = key_slot(p, w.n, w.s.K, kt * KEYS + int(rank ^ 1) * CKEYS + tk);
-                const bool have = slot >= 0;
-                const int64_t row = have ? slot : 0;
-                uint4 x[4];
-                if constexpr (C8) {
-                    const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + row * p.Dv;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int cb = (i >> 1) * 4 + int(rank) * 2 + (i & 1), q = cb * 4 + c4;
-                        x[i] = have && q * 2 < nc ? ld_stream_v4(src + q * 16) : make_uint4(0, 0, 0, 0);
-                    }
-                }
-                if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(&m->s_full[j & 1], (j >> 1) & 1))) {
-                    cp_async_wait<0>();
-                    fence_async_proxy();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(&m->v_full[pend], 0);
-                    pend = -1;
-                }
-                wait(&m->s_full[j & 1], (j >> 1) & 1);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int cb = (i >> 1) * 4 + int(rank) * 2 + (i & 1), db = (i >> 1) * 4 + int(rank ^ 1) * 2 + (i & 1);
-                    if (cb * 8 >= nc) continue;
-                    const uint32_t box = stage + uint32_t(db) * KBOX;
-                    if constexpr (C8) {
-                        st_shared_v4(box_at(box, tk, 2 * c4), dec8x8<IT>(p.ckv_kind, x[i].x, x[i].y));
-                        st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<IT>(p.ckv_kind, x[i].z, x[i].w));
-                    } else {
-                        const uint16_t* src = static_cast<const uint16_t*>(p.ckv) + row * p.Dv;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int q = cb * 8 + c4 + 4 * k;
-                            const bool in = have && q < nc;
-                            cp_async16(box_at(box, tk, c4 + 4 * k), in ? src + q * 8 : src, in);
-                        }
-                    }
-                }
-                cp_async_commit();
-                if (pend >= 0) {
-                    cp_async_wait<1>();
-                    fence_async_proxy();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(&m->v_full[pend], 0);
-                }
-                pend = st;
-            }
-        }
-        cp_async_wait<0>();
-        fence_async_proxy();
-        __syncwarp();
-        if (pend >= 0 && lane == 0) mbar_arrive_at(&m->v_full[pend], 0);
-    } else if (rank == 0 && lane == 0) {
-        // ------------------------------------------------------------------
-        // MMA: S of a step is issued before O of the one before, which waits for its softmax.
-        // ------------------------------------------------------------------
-        constexpr uint32_t id_s = tc_idesc(ROWS, KEYS, IT::is_bf16, false), id_o = tc_idesc(ROWS, 256, IT::is_bf16, true);
-        const bool split = C8 || p.k_kind != OUT16;
-        int j = 0, parts = 0;
-        bool prev = false, prev_first = false;
-        auto issue_o = [&](int i, bool first) {
-            wait(&m->p_full[i & 1], (i >> 1) & 1);
-            wait(&m->v_full[i % STAGES], (i / STAGES) & 1);
-            tc_fence_after();
-            const uint64_t pd = tc_desc(base + OFF_P + uint32_t(i & 1) * PBUF, 16, 1024);
-            const uint64_t vd = tc_desc(base + OFF_K + (i % STAGES) * STAGE_BYTES, KBOX, 1024);
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                if (a >= na) break;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    tc_mma_pair(tmem + a * 128, pd + s * 2, vd + ((a * 4 + (s >> 1) * 2) * KBOX + (s & 1) * 2048) / 16, id_o,
-                                !(first && s == 0));
-            }
-            tc_commit_pair(&m->pv_done[i & 1]);
-            tc_commit_pair(&m->empty[i % STAGES]);
-        };
-        Walk w(p, m->begin, m->end);
-        while (w.next()) {
-            if (prev) issue_o(j - 1, prev_first);
-            prev = false;
-            wait(&m->q_full, parts & 1);
-            ++parts;
-            for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-                const int st = j % STAGES;
-                wait(&m->k_full[st], (j / STAGES) & 1);
-                tc_fence_after();
-                const uint64_t qd = tc_desc(base + OFF_Q, 16, 1024), kd = tc_desc(base + OFF_K + st * STAGE_BYTES, 16, 1024);
-                const uint32_t d = tmem + COL_S + uint32_t(j & 1) * 64;
-                for (int b = 0; b < nb; ++b)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        tc_mma_pair(d, qd + (b * QBOX) / 16 + s * 2, kd + (b * KBOX) / 16 + s * 2, id_s, b > 0 || s > 0);
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    tc_mma_pair(d + (split ? 32 : 0), qd + (8 * QBOX) / 16 + s * 2, kd + (8 * KBOX) / 16 + s * 2, id_s, !split || s > 0);
-                tc_commit_pair(&m->s_full[j & 1]);
-                if (prev) issue_o(j - 1, prev_first);
-                prev = true;
-                prev_first = kt == w.kt0;
-            }
-        }
-        if (prev) issue_o(j - 1, prev_first);
-        if (!ok) {   // let what was issued finish before TMEM goes
-            tc_commit_pair(&m->drain);
-            mbar_wait(&m->drain, 0, nullptr);
+    } else {
+        if (warp == 4) {
+            key_warp<IT, K8, false>(c, maps);
+        } else if (warp == 5) {
+            key_warp<IT, K8, true>(c, maps);
+        } else if (warp >= 8) {
+            Walk w(p, m->begin, m->end);
+            for (int part = 0; w.next(); ++part) load_queries<IT, false>(c, tid - 256, w, part);
         }
     }
-    if (!ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
+    if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
-    if (warp == 12) tmem_free_pair(tmem, TMEM_COLS);
+    if (warp == MMA_WARP) tmem_free_pair(tmem, TMEM_COLS);
 }
 
 // Joins the parts of the items that were cut: block x takes the item at the
@@ -783,7 +939,14 @@ __global__ void __launch_bounds__(128) mla_join_kernel(const __grid_constant__ M
 
 }  // namespace
 
-int mla_tc_pairs() {
+template <class IT, bool C8, bool K8>
+static cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(mla_tc_kernel<IT, C8, K8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<C8>());
+}
+
+// CTA pairs that fit on the current device at once (a GPC with an odd number of
+// SMs leaves one over); looked up once per device, as is the shared memory allowed.
+static int mla_tc_pairs() {
     static std::mutex mu;
     static int cache[64] = {0};
     int dev = 0;
@@ -793,22 +956,23 @@ int mla_tc_pairs() {
     }
     std::lock_guard<std::mutex> lock(mu);
     if (cache[dev] == 0) {
-        // Pairs that fit on the GPU at once (a GPC with an odd number of SMs leaves one over).
         int n = 0;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(unsigned(sm_count_current_device()));
-        cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.gridDim = dim3(unsigned(sm_count_current_device()) / 2 * 2);
+        cfg.blockDim = dim3(threads_of<false>());
+        cfg.dynamicSmemBytes = smem_of<false>();
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
+        const cudaError_t e[] = {allow_smem<BF16, false, false>(), allow_smem<BF16, false, true>(), allow_smem<BF16, true, false>(),
+                                 allow_smem<BF16, true, true>(), allow_smem<F16, false, false>(), allow_smem<F16, false, true>(),
+                                 allow_smem<F16, true, false>(), allow_smem<F16, true, true>()};
         bool good = true;
-        for (auto f : {mla_tc_kernel<BF16, false>, mla_tc_kernel<BF16, true>, mla_tc_kernel<F16, false>, mla_tc_kernel<F16, true>})
-            good = good && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) == cudaSuccess;
-        good = good && cudaOccupancyMaxActiveClusters(&n, mla_tc_kernel<BF16, false>, &cfg) == cudaSuccess && n > 0;
+        for (const cudaError_t x : e) good = good && x == cudaSuccess;
+        good = good && cudaOccupancyMaxActiveClusters(&n, mla_tc_kernel<BF16, false, false>, &cfg) == cudaSuccess && n > 0;
         if (!good) {
             (void)cudaGetLastError();
             return 1;
@@ -820,18 +984,59 @@ int mla_tc_pairs() {
 
 int64_t mla_tc_workspace(int Dv) { return ws_bytes(mla_tc_pairs(), Dv); }
 
+// The driver's tensor-map encoder, found through the runtime (no link to libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+static bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int width, int box_rows) {
+    const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)}, strides[1] = {cuuint64_t(width) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, one[2] = {1, 1};
+    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
+                     dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class IT>
-static cudaError_t launch_mla_tc_t(const MlaParams& p, cudaStream_t s) {
-    const dim3 g(unsigned(p.pairs * 2)), b(THREADS);
-    cudaError_t e = p.ckv_kind == OUT16 ? launch_pdl(mla_tc_kernel<IT, false>, g, b, SMEM_BYTES, s, p)
-                                        : launch_pdl(mla_tc_kernel<IT, true>, g, b, SMEM_BYTES, s, p);
+static cudaError_t launch_mla_tc_t(const MlaParams& p, const Maps& maps, cudaStream_t s) {
+    const bool c8 = p.ckv_kind != OUT16, k8 = p.k_kind != OUT16;
+    const dim3 g(unsigned(p.pairs * 2)), b16(threads_of<false>()), b8(threads_of<true>());
+    const cudaError_t e =
+        c8 ? (k8 ? launch_pdl(mla_tc_kernel<IT, true, true>, g, b8, smem_of<true>(), s, p, maps)
+                 : launch_pdl(mla_tc_kernel<IT, true, false>, g, b8, smem_of<true>(), s, p, maps))
+           : (k8 ? launch_pdl(mla_tc_kernel<IT, false, true>, g, b16, smem_of<false>(), s, p, maps)
+                 : launch_pdl(mla_tc_kernel<IT, false, false>, g, b16, smem_of<false>(), s, p, maps));
     if (e != cudaSuccess || p.pairs == 1) return e;
     return launch_pdl(mla_join_kernel<IT>, dim3(unsigned(p.pairs - 1), ROWS / 16), dim3(128), 0, s, p);
 }
 
 cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     p.pairs = mla_tc_pairs();
-    return dtype == KVR_BF16 ? launch_mla_tc_t<BF16>(p, s) : launch_mla_tc_t<F16>(p, s);
+    // TMA boxes of R rows, R the largest power of two (8 to 32) that divides the block: a box never crosses one, and
+    // its rows keep their place in the 8-row swizzle. Other blocks, codes and narrow rows take 16-byte copies.
+    Maps maps = {};
+    p.box_rows = 0;
+    const int64_t rows = p.d0 * p.d1;
+    if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv >= 64 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
+        int r = 32;
+        while (p.table != nullptr && r > 1 && p.d1 % r != 0) r /= 2;
+        if (r >= 8 && encoder() != nullptr && encode_rows(&maps.ckv, p.ckv, dtype == KVR_BF16, rows, p.Dv, r) &&
+            encode_rows(&maps.kc, p.kc, dtype == KVR_BF16, rows, p.Dk, r))
+            p.box_rows = r;
+    }
+    return dtype == KVR_BF16 ? launch_mla_tc_t<BF16>(p, maps, s) : launch_mla_tc_t<F16>(p, maps, s);
 }
 
 }  // namespace kvr

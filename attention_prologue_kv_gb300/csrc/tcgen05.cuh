@@ -2,6 +2,8 @@
 // (cta_group::2), and the cluster-scope barriers around it.
 #pragma once
 
+#include <cuda.h>
+
 #include "kvr_internal.cuh"
 
 namespace kvr {
@@ -43,6 +45,36 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
         if (*abort) return false;
         if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) return false;
     }
+}
+
+// The same, announcing `bytes` of copies that complete on that barrier.
+__device__ __forceinline__ void mbar_expect_at(uint64_t* bar, uint32_t rank, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [a], %2;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(rank), "r"(bytes)
+        : "memory");
+}
+// TMA box of a 2-D tensor into this CTA's shared memory; its bytes complete
+// on the barrier at the same place in CTA `rank` of the pair.
+__device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [a];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(rank)
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Make shared-memory writes of this thread visible to the tensor cores and TMA.

@@ -139,17 +139,21 @@ def oracle_mla(c, q_nope=None, q_rope=None):
 
 def rounded_query(c):
     """q as the tensor-core kernel multiplies it where a cache has a scale per
-    channel: q / scale rounded to q's type (one rounding; a power of two taken out
-    first changes nothing here), times scale again."""
-    out = []
-    for q, s in ((c.q_nope, c.ckv_scale), (c.q_rope, c.k_scale)):
-        q64 = f64(q)
-        if s is not None and s.numel() > 1:
-            inv = (1.0 / s).to(torch.float32)
-            lift = 2.0 ** torch.ceil(torch.log2(inv.max()))
-            q64 = f64((q.to(torch.float32) * (inv / lift)).to(q.dtype)) * f64(s) * float(lift)
-        out.append(q64)
-    return out
+    channel, in float64: the latent part as halves of q / scale, with a power of
+    two per row that brings the largest to [2^13, 2^14); the rotary part as q /
+    scale in q's type, a power of two over the largest 1 / scale taken out."""
+    def inverse(s):
+        return (1.0 / s).to(torch.float32)
+
+    n64, r64 = f64(c.q_nope), f64(c.q_rope)
+    if c.ckv_scale is not None and c.ckv_scale.numel() > 1:
+        x = c.q_nope.to(torch.float32) * inverse(c.ckv_scale)
+        g = 2.0 ** (13 - torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))))
+        n64 = f64((x * g).to(torch.float16)) / f64(g) * f64(c.ckv_scale)
+    if c.k_scale is not None and c.k_scale.numel() > 1:
+        lift = 2.0 ** torch.ceil(torch.log2(inverse(c.k_scale).max()))
+        r64 = f64((c.q_rope.to(torch.float32) * (inverse(c.k_scale) / lift)).to(c.q_rope.dtype)) * f64(c.k_scale) * float(lift)
+    return n64, r64
 
 
 def check_mla(c, gpu, ref, p_rounded=True):
