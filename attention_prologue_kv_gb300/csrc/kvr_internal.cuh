@@ -347,6 +347,7 @@ struct MlaParams {
     int ckv_scale_per_ch, k_scale_per_ch;
     float scale;                // softmax scale
     int pairs;                  // tensor-core kernel: CTA pairs of the grid
+    int out_wide;               // its output rows lie on 32-byte boundaries
     int box_rows;               // its TMA boxes' rows (0: none)
 };
 

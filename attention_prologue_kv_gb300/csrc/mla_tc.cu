@@ -56,12 +56,18 @@ struct Bound {
     int n, i, kt, pad;   // sequence, row tile, key tile
 };
 
+struct Seq {
+    int64_t q0;
+    int L, K;   // L = 0: nothing to do
+};
+
 struct Misc {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t s_full[2], p_full, pv_done, q_full, q_free, k_fix, v_fix, drain;
     uint32_t tmem;
     int abort;
     Bound begin, end;
+    Seq first;               // the sequence of `begin`
     int64_t wsum[16];
     float red[2][128];
     float inv_k[64], lift;   // 1 / scale of the rotary channels; a power of two taken out of their queries
@@ -91,11 +97,6 @@ __device__ __forceinline__ Space ws_space(const MlaParams& p) {
     return {reinterpret_cast<int32_t*>(w), reinterpret_cast<Bound*>(w + 256), reinterpret_cast<float2*>(w + ws_ml(p.pairs)),
             reinterpret_cast<float*>(w + ws_o(p.pairs))};
 }
-
-struct Seq {
-    int64_t q0;
-    int L, K;   // L = 0: nothing to do
-};
 
 __device__ __forceinline__ Seq load_seq(const MlaParams& p, int n, int* bits = nullptr) {
     const int64_t a = p.query_start[n], b = p.query_start[n + 1], K = p.key_length[n];
@@ -136,7 +137,7 @@ __device__ Bound locate(const MlaParams& p, int n, const Seq& s, int64_t off) {
     }
     const int64_t c0 = cost(p, s.L, s.K, lo), c1 = cost(p, s.L, s.K, lo + 1);
     const int kn = key_tiles(p, s.L, s.K, lo);
-    const int kt = int(double(off - c0) / double(c1 - c0) * double(kn));   // monotonic in off: shares neither overlap nor leave gaps
+    const int kt = int(float(off - c0) / float(c1 - c0) * float(kn));   // monotonic in off: shares neither overlap nor leave gaps
     return {n, lo, min(kt, kn - 1), 0};
 }
 
@@ -144,12 +145,12 @@ __device__ Bound locate(const MlaParams& p, int n, const Seq& s, int64_t off) {
 struct Walk {
     const MlaParams& p;
     Bound at, end;
-    int loaded = -1;
+    int loaded;
     Seq s;
     // the current part
     int n, i, kt0, kt1;
     bool whole;
-    __device__ Walk(const MlaParams& q, const Bound& b, const Bound& e) : p(q), at(b), end(e) {}
+    __device__ Walk(const MlaParams& q, const Misc* m) : p(q), at(m->begin), end(m->end), loaded(m->begin.n), s(m->first) {}
     __device__ bool next() {
         for (;;) {
             if (at.n >= p.N || at.n > end.n || (at.n == end.n && (at.i > end.i || (at.i == end.i && at.kt >= end.kt)))) return false;
@@ -200,9 +201,19 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
         if (w < warp) base += m->wsum[w];
         total += m->wsum[w];
     }
-    const int64_t most = total / (p.H * MIN_KEYS);
-    const int active = most < 1 ? 1 : (most < p.pairs ? int(most) : p.pairs);
-    const int64_t u0 = pair < active ? total * pair / active : total, u1 = pair < active ? total * (pair + 1) / active : total;
+    // Equal shares, but none below MIN_KEYS (64-bit divisions only where they are needed: they take about 100 cycles).
+    const int64_t least = int64_t(p.H) * MIN_KEYS;
+    const int active = total >= least * p.pairs ? p.pairs : max(1, int(unsigned(total) / unsigned(least)));
+    int64_t u0 = total, u1 = total;
+    if (pair < active) {
+        if (total < (int64_t(1) << 31) / 128) {
+            u0 = unsigned(total) * unsigned(pair) / unsigned(active);
+            u1 = unsigned(total) * unsigned(pair + 1) / unsigned(active);
+        } else {
+            u0 = total * pair / active;
+            u1 = total * (pair + 1) / active;
+        }
+    }
     if (sum > 0) {
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
@@ -214,6 +225,7 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
                 const int64_t c = s.L > 0 ? cost(p, s.L, s.K, row_tiles(p, s.L)) : 0;
                 if (u < b + c) {
                     (e ? m->end : m->begin) = locate(p, n, s, u - b);
+                    if (e == 0) m->first = s;
                     break;
                 }
                 b += c;
@@ -297,7 +309,7 @@ struct Ctx {
     // A wait that gives up (one second) poisons the CTA: the others give up at their first look, and every role
     // runs its loops to the end without waiting, so that no barrier is left with threads missing.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!mbar_wait_cluster(bar, parity, abort)) {
+        if (!mbar_wait(bar, parity, abort)) {
             *abort = 1;
             ok = false;
         }
@@ -335,7 +347,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     uint64_t* full = SWAP ? m->v_full : m->k_full;
     int j = 0, fixed = 0, pend = -1;
     const int mine = int(SWAP ? c.rank ^ 1 : c.rank) * CKEYS + lane;   // this lane's key of a step
-    Walk w(p, m->begin, m->end);
+    Walk w(p, m);
     while (w.next()) {
         int64_t next = key_slot(p, w.n, w.s.K, w.kt0 * KEYS + mine);
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
@@ -357,7 +369,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
             uint64_t* bar = SWAP ? &m->s_full[j & 1] : &m->empty[st];
             const uint32_t parity = SWAP ? (j >> 1) & 1 : ((j / STAGES) & 1) ^ 1;
             if (SWAP || j >= STAGES) {
-                if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(bar, parity))) {
+                if (pend >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) {
                     cp_async_wait<0>();
                     c.arrive(&full[pend]);
                     pend = -1;
@@ -581,7 +593,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     float fn = l2, fr = l2;
     if (K8) fr = l2 * (p.k_scale_per_ch ? m->lift : m->inv_k[0]);
     int j = 0, part = 0;
-    Walk w(p, m->begin, m->end);
+    Walk w(p, m);
     while (w.next()) {
         const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
         const bool live = row < unsigned(w.s.L) * unsigned(p.H);
@@ -672,6 +684,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
         uint16_t* out = nullptr;
         float* po = nullptr;
+        const bool wide = p.out_wide;
         if (w.whole) {
             out = static_cast<uint16_t*>(p.out) + (w.s.q0 + t) * p.o_ts + int64_t(head) * p.o_hs;
             if (live && h == 0 && p.lse != nullptr)
@@ -693,16 +706,23 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
                 if (C8) o[i] *= c.sc->inv_v[ch + i];
             }
             if (!live) continue;
+            if (w.whole) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                if (ch + k >= p.Dv) break;
-                if (w.whole) {
-                    *reinterpret_cast<uint4*>(out + ch + k) = make_uint4(IT::pack(o[k], o[k + 1]), IT::pack(o[k + 2], o[k + 3]),
-                                                                         IT::pack(o[k + 4], o[k + 5]), IT::pack(o[k + 6], o[k + 7]));
-                } else {
-                    *reinterpret_cast<float4*>(po + ch + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                    *reinterpret_cast<float4*>(po + ch + k + 4) = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+                for (int k = 0; k < 32; k += 16) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = IT::pack(o[k + 2 * i], o[k + 2 * i + 1]);
+                    if (wide && ch + k + 16 <= p.Dv) {
+                        st_global_v8(out + ch + k, u);
+                    } else {
+                        if (ch + k < p.Dv) *reinterpret_cast<uint4*>(out + ch + k) = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (ch + k + 8 < p.Dv) *reinterpret_cast<uint4*>(out + ch + k + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                    if (ch + k < p.Dv) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t(&)[8]>(o[k]));
             }
         }
         tc_fence_before();
@@ -742,7 +762,7 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
         }
         __syncwarp();
     };
-    Walk w(p, m->begin, m->end);
+    Walk w(p, m);
     while (w.next()) {
         if (prev) issue_o(j - 1, prev_first);
         prev = false;
@@ -850,7 +870,7 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     } else if (warp == MMA_WARP) {
         if (rank == 0) mma_warp<IT, C8, K8>(c);
     } else if constexpr (C8) {
-        Walk w(p, m->begin, m->end);
+        Walk w(p, m);
         int j = 0;
         for (int part = 0; w.next(); ++part) {
             if (warp < 8) {
@@ -866,7 +886,7 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
         } else if (warp == 5) {
             key_warp<IT, K8, true>(c, maps);
         } else if (warp >= 8) {
-            Walk w(p, m->begin, m->end);
+            Walk w(p, m);
             for (int part = 0; w.next(); ++part) load_queries<IT, false>(c, tid - 256, w, part);
         }
     }
@@ -879,62 +899,80 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     if (warp == MMA_WARP) tmem_free_pair(tmem, TMEM_COLS);
 }
 
-// Joins the parts of the items that were cut: block x takes the item at the
-// first bound inside it, if bound x + 1 is that one; 16 rows a block, 4 a warp.
+// Joins the parts of the items that were cut: the blocks x take the item that
+// bound x + 1 is in, if that is the first bound inside it. One warp a row.
+constexpr int JOIN_ROWS = 4;
 template <class IT>
-__global__ void __launch_bounds__(128) mla_join_kernel(const __grid_constant__ MlaParams p) {
+__global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_constant__ MlaParams p) {
     pdl_wait();
     pdl_launch_dependents();
     const Space ws = ws_space(p);
-    const int active = *ws.active, b = blockIdx.x + 1;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
+    const int b = blockIdx.x + 1;
+    const int active = *ws.active;
     if (b >= active) return;
-    const Bound at = ws.bounds[b], before = ws.bounds[b - 1];
+    const Bound before = ws.bounds[b - 1], at = ws.bounds[b];
     const bool same = before.n == at.n && before.i == at.i;
     if (at.n >= p.N || at.kt == 0 || (same && before.kt > 0)) return;
     const Seq s = load_seq(p, at.n);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Parts: the last of pair b - 1, then the first of each pair whose bound is inside the item.
-    int last = b;
-    while (last + 1 < active && ws.bounds[last + 1].n == at.n && ws.bounds[last + 1].i == at.i && ws.bounds[last + 1].kt > 0) ++last;
-    for (int k = 0; k < 4; ++k) {
-        const int r = blockIdx.y * 16 + warp * 4 + k;
-        const unsigned row = unsigned(at.i) * ROWS + r;
-        if (row >= unsigned(s.L) * unsigned(p.H)) break;
-        float mx = -INFINITY;
-        for (int q = b - 1; q <= last; ++q) {
-            if (q < last && ws.bounds[q].n == ws.bounds[q + 1].n && ws.bounds[q].i == ws.bounds[q + 1].i && ws.bounds[q].kt == ws.bounds[q + 1].kt) continue;
-            mx = fmaxf(mx, ws.ml[(int64_t(q) * 2 + (q == b - 1 && !same ? 1 : 0)) * ROWS + r].x);
-        }
-        float l = 0.f;
-        float4 o[4];
+    const unsigned row = unsigned(at.i) * ROWS + r;
+    if (row >= unsigned(s.L) * unsigned(p.H)) return;
+    // Parts: the last of pair b - 1, then the first of each pair whose bound is inside the item, but for pairs without
+    // work (the next bound is their own). Lane q has part b - 1 + q0 + q.
+    float mx = -INFINITY, l = 0.f;
+    float4 o[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = b - 1; q <= last; ++q) {
-            if (q < last && ws.bounds[q].n == ws.bounds[q + 1].n && ws.bounds[q].i == ws.bounds[q + 1].i && ws.bounds[q].kt == ws.bounds[q + 1].kt) continue;
-            const int64_t slot = (int64_t(q) * 2 + (q == b - 1 && !same ? 1 : 0)) * ROWS + r;
-            const float2 ml = ws.ml[slot];
-            if (ml.y == 0.f) continue;
-            const float f = exp2f(ml.x - mx);
-            l += ml.y * f;
+    for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool more = true;
+    for (int q0 = 0; more; q0 += 32) {
+        const int q = b - 1 + q0 + lane;
+        Bound me = {-1, 0, 0, 0}, nx = {-1, 0, 0, 0};
+        if (q < active) me = ws.bounds[q];
+        if (q + 1 < active) nx = ws.bounds[q + 1];
+        const bool in = q == b - 1 || (me.n == at.n && me.i == at.i && me.kt > 0);
+        const uint32_t run = __ballot_sync(0xFFFFFFFFu, in);
+        const int count = run == 0xFFFFFFFFu ? 32 : __ffs(~run) - 1;
+        more = count == 32;
+        const bool work = lane < count && !(me.n == nx.n && me.i == nx.i && me.kt == nx.kt);
+        const int64_t slot = (int64_t(q) * 2 + (q == b - 1 && !same ? 1 : 0)) * ROWS + r;
+        const float2 ml = work ? ws.ml[slot] : make_float2(-INFINITY, 0.f);
+        float top = ml.y == 0.f ? -INFINITY : ml.x;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int ch = (c * 32 + lane) * 4;
-                if (ch >= p.Dv) break;
-                const float4 x = *reinterpret_cast<const float4*>(ws.o + slot * p.Dv + ch);
-                o[c].x += x.x * f, o[c].y += x.y * f, o[c].z += x.z * f, o[c].w += x.w * f;
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+        top = fmaxf(top, mx);
+        const float back = mx == -INFINITY ? 0.f : exp2_approx(mx - top);
+        const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - top);
+        mx = top;
+        l *= back;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c].x *= back, o[c].y *= back, o[c].z *= back, o[c].w *= back;
+        const float add = ml.y * f;
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {   // in order
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            const int64_t sk = __shfl_sync(0xFFFFFFFFu, slot, k);
+            l += __shfl_sync(0xFFFFFFFFu, add, k);
+            if (fk != 0.f) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int ch = (c * 32 + lane) * 4;
+                    if (ch < p.Dv) {
+                        const float4 x = *reinterpret_cast<const float4*>(ws.o + sk * p.Dv + ch);
+                        o[c].x += x.x * fk, o[c].y += x.y * fk, o[c].z += x.z * fk, o[c].w += x.w * fk;
+                    }
+                }
             }
         }
-        const int64_t t = s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int ch = (c * 32 + lane) * 4;
-            if (ch >= p.Dv) break;
-            *reinterpret_cast<uint2*>(out + ch) = make_uint2(IT::pack(o[c].x * inv, o[c].y * inv), IT::pack(o[c].z * inv, o[c].w * inv));
-        }
-        if (lane == 0 && p.lse != nullptr) p.lse[t * p.H + head] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
     }
+    const int64_t t = s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int ch = (c * 32 + lane) * 4;
+        if (ch < p.Dv) *reinterpret_cast<uint2*>(out + ch) = make_uint2(IT::pack(o[c].x * inv, o[c].y * inv), IT::pack(o[c].z * inv, o[c].w * inv));
+    }
+    if (lane == 0 && p.lse != nullptr) p.lse[t * p.H + head] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
@@ -1019,11 +1057,12 @@ static cudaError_t launch_mla_tc_t(const MlaParams& p, const Maps& maps, cudaStr
            : (k8 ? launch_pdl(mla_tc_kernel<IT, false, true>, g, b16, smem_of<false>(), s, p, maps)
                  : launch_pdl(mla_tc_kernel<IT, false, false>, g, b16, smem_of<false>(), s, p, maps));
     if (e != cudaSuccess || p.pairs == 1) return e;
-    return launch_pdl(mla_join_kernel<IT>, dim3(unsigned(p.pairs - 1), ROWS / 16), dim3(128), 0, s, p);
+    return launch_pdl(mla_join_kernel<IT>, dim3(unsigned(p.pairs - 1), ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, s, p);
 }
 
 cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     p.pairs = mla_tc_pairs();
+    p.out_wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.o_ts % 16 == 0 && p.o_hs % 16 == 0;
     // TMA boxes of R rows, R the largest power of two (8 to 32) that divides the block: a box never crosses one, and
     // its rows keep their place in the 8-row swizzle. Other blocks, codes and narrow rows take 16-byte copies.
     Maps maps = {};

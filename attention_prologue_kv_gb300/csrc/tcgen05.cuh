@@ -16,35 +16,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Arrive on the barrier at the same place in CTA `rank` of the cluster.
+// Arrive on the barrier at the same place in CTA `rank` of the cluster. What the
+// arrivals of these kernels publish is operands in the arriving CTA's own shared
+// memory, for the tensor core of that CTA (after fence_async_proxy): no data
+// crosses over with them, so CTA scope does (a release at cluster scope cost about
+// 1000 cycles an arrival).
 __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
         "r"(rank)
         : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
-        : "memory");
-    return ok != 0;
-}
-// As mbar_wait, for barriers that the other CTA or the tensor cores arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) return false;
-    }
 }
 
 // The same, announcing `bytes` of copies that complete on that barrier.
@@ -52,7 +35,7 @@ __device__ __forceinline__ void mbar_expect_at(uint64_t* bar, uint32_t rank, uin
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [a], %2;\n\t}" ::"r"(smem_u32(bar)),
+        "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [a], %2;\n\t}" ::"r"(smem_u32(bar)),
         "r"(rank), "r"(bytes)
         : "memory");
 }
@@ -65,6 +48,12 @@ __device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map,
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [a];\n\t}" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(rank)
         : "memory");
+}
+// 32 bytes to global memory, 32-byte aligned: a whole sector from one thread.
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
