@@ -291,9 +291,11 @@ __device__ __forceinline__ uint32_t box_at(uint32_t box, int row, int chunk) {
     return box + uint32_t(row) * 128u + (uint32_t(chunk ^ (row & 7)) << 4);
 }
 
-// Cache rows through TMA: R rows a box (0: no TMA, 16-byte copies instead).
+// Cache rows through TMA, seen as [64-channel box][row][channel], so that one copy brings 32 rows of several
+// boxes: all boxes of the latent part, two of them (the swap), the rotary part. Where a block ends inside 32 rows, a
+// copy brings R rows of one box. One copy a box took the key warp 2200 cycles a step (32 rows of all: 2 copies).
 struct Maps {
-    CUtensorMap ckv, kc;
+    CUtensorMap all, two, rope;
 };
 
 // What every role has.
@@ -337,7 +339,6 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     const int lane = c.lane, R = p.box_rows;
     // Boxes: latent ones first; the place of box b, its 64 channels.
     const int nl = SWAP ? min(2, max(0, c.nb - 2 * int(c.rank))) + min(2, max(0, c.nb - 4 - 2 * int(c.rank))) : c.nb;
-    const int n = SWAP ? nl : nl + 1;
     auto place = [&](int b) {
         if (SWAP) return (b >> 1) * 4 + int(c.rank ^ 1) * 2 + (b & 1);
         return b < nl ? b : 8;
@@ -379,21 +380,37 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
             if (R > 0) {
                 const bool whole = live == 0xFFFFFFFFu;
                 const int groups = CKEYS / R;
+                const int boxes = SWAP ? 2 * ((c.nb + 3) / 4) : c.nb + 1;   // a pair that lies behind the row is zeros
+                uint64_t* done = whole ? &full[st] : fix;
+                const uint32_t to = whole ? 0 : c.rank;
                 if (whole) {
-                    if (lane == 0) mbar_expect_at(&full[st], 0, uint32_t(n) * KBOX);
+                    if (lane == 0) mbar_expect_at(done, 0, uint32_t(boxes) * KBOX);
                 } else if (live != 0) {
-                    // Boxes with a row that exists; their other rows are cleared below.
-                    int some = 0;
-                    for (int g = 0; g < groups; ++g) some += (live >> (g * R) & 1);
-                    if (lane == 0) mbar_arrive_expect_tx(fix, uint32_t(n * some) * uint32_t(R) * 128u);
+                    // Groups of R rows with one that exists; their other rows are cleared below.
+                    uint32_t some = 0;
+                    for (int g = 0; g < groups; ++g) some += live >> (g * R) & 1;
+                    if (lane == 0) mbar_arrive_expect_tx(fix, uint32_t(boxes) * some * uint32_t(R) * 128u);
                 }
                 __syncwarp();
-                for (int q0 = 0; q0 < n * groups; q0 += 32) {
-                    const int q = q0 + lane, g = min(q / n, groups - 1), b = q - g * n;
-                    const int row = __shfl_sync(0xFFFFFFFFu, int(slot), g * R);
-                    if (q < n * groups && row >= 0)
-                        tma_box_at(stage + uint32_t(place(b)) * KBOX + uint32_t(g * R) * 128u, SWAP || b < nl ? &maps.ckv : &maps.kc,
-                                   SWAP || b < nl ? channels(b) * 64 : 0, row, whole ? &full[st] : fix, whole ? 0 : c.rank);
+                if (R == CKEYS) {
+                    if (lane == 0 && slot >= 0) {
+                        if (SWAP) {
+                            for (int b = 0; b < boxes; b += 2)
+                                tma_box_at(stage + uint32_t(place(b)) * KBOX, &maps.two, 0, int(slot), channels(b), done, to);
+                        } else {
+                            tma_box_at(stage, &maps.all, 0, int(slot), 0, done, to);
+                            tma_box_at(stage + 8 * KBOX, &maps.rope, 0, int(slot), 0, done, to);
+                        }
+                    }
+                } else {   // a box at a time: a copy of several would put them R rows apart
+                    for (int q0 = 0; q0 < boxes * groups; q0 += 32) {
+                        const int q = q0 + lane, g = min(q / boxes, groups - 1), b = q - g * boxes;
+                        const int row = __shfl_sync(0xFFFFFFFFu, int(slot), g * R);
+                        const bool rope = !SWAP && b == c.nb;
+                        if (q < boxes * groups && row >= 0)
+                            tma_box_at(stage + uint32_t(place(b)) * KBOX + uint32_t(g * R) * 128u, rope ? &maps.rope : &maps.all, 0, row,
+                                       rope ? 0 : channels(b), done, to);
+                    }
                 }
                 if (!whole) {
                     if (live != 0) {
@@ -401,7 +418,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                         ++fixed;
                     }
                     if (slot < 0)
-                        for (int b = 0; b < n; ++b)
+                        for (int b = 0; b < boxes; ++b)
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 st_shared_v4(stage + uint32_t(place(b)) * KBOX + uint32_t(lane) * 128u + k * 16u, make_uint4(0, 0, 0, 0));
@@ -577,6 +594,17 @@ __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int p
     cp_async_commit();
     cp_async_wait<0>();
     c.arrive(&m->q_full);
+}
+
+// Brings the queries of the next part into L2 meanwhile.
+__device__ __forceinline__ void prefetch_queries(Ctx& c, int v, const Walk& w) {
+    const MlaParams& p = c.p;
+    const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + (v >> 1);
+    if (row >= unsigned(w.s.L) * unsigned(p.H)) return;
+    const int64_t t = w.s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
+    const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
+    for (int ch = (v & 1) * 64; ch < p.Dv; ch += 128) prefetch_l2(qn + ch);
+    if ((v & 1) == 0) prefetch_l2(static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs);
 }
 
 // Softmax and output of 128 threads: thread (row r, half h of the keys and channels).
@@ -841,6 +869,9 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
         fence_mbar_init();
     }
     if (warp == MMA_WARP) tmem_alloc_pair(&m->tmem, TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();   // barriers and TMEM are set up; the other half is below, behind the schedule
     pdl_wait();
     pdl_launch_dependents();
     schedule<NT>(p, m, pair);
@@ -858,9 +889,8 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
         for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
         if (lane == 0) m->lift = exp2f(ceilf(log2f(v)));
     }
-    tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
     Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
@@ -887,7 +917,12 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
             key_warp<IT, K8, true>(c, maps);
         } else if (warp >= 8) {
             Walk w(p, m);
-            for (int part = 0; w.next(); ++part) load_queries<IT, false>(c, tid - 256, w, part);
+            bool more = w.next();
+            for (int part = 0; more; ++part) {
+                load_queries<IT, false>(c, tid - 256, w, part);
+                more = w.next();
+                if (more) prefetch_queries(c, tid - 256, w);
+            }
         }
     }
     if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
@@ -1039,10 +1074,10 @@ static EncodeTiled encoder() {
     }();
     return fn;
 }
-static bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int width, int box_rows) {
-    const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)}, strides[1] = {cuuint64_t(width) * 2};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, one[2] = {1, 1};
-    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
+static bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int width, int box_rows, int boxes) {
+    const cuuint64_t dims[3] = {64, cuuint64_t(rows), cuuint64_t(width) / 64}, strides[2] = {cuuint64_t(width) * 2, 128};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(boxes)}, one[3] = {1, 1, 1};
+    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
                      dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1068,11 +1103,12 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     Maps maps = {};
     p.box_rows = 0;
     const int64_t rows = p.d0 * p.d1;
-    if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv >= 64 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
+    if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv % 64 == 0 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
         int r = 32;
         while (p.table != nullptr && r > 1 && p.d1 % r != 0) r /= 2;
-        if (r >= 8 && encoder() != nullptr && encode_rows(&maps.ckv, p.ckv, dtype == KVR_BF16, rows, p.Dv, r) &&
-            encode_rows(&maps.kc, p.kc, dtype == KVR_BF16, rows, p.Dk, r))
+        const bool bf = dtype == KVR_BF16;
+        if (r >= 8 && encoder() != nullptr && encode_rows(&maps.all, p.ckv, bf, rows, p.Dv, r, r == 32 ? p.Dv / 64 : 1) &&
+            encode_rows(&maps.two, p.ckv, bf, rows, p.Dv, r, 2) && encode_rows(&maps.rope, p.kc, bf, rows, p.Dk, r, 1))
             p.box_rows = r;
     }
     return dtype == KVR_BF16 ? launch_mla_tc_t<BF16>(p, maps, s) : launch_mla_tc_t<F16>(p, maps, s);

@@ -13,6 +13,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -39,14 +41,14 @@ __device__ __forceinline__ void mbar_expect_at(uint64_t* bar, uint32_t rank, uin
         "r"(rank), "r"(bytes)
         : "memory");
 }
-// TMA box of a 2-D tensor into this CTA's shared memory; its bytes complete
+// TMA box of a 3-D tensor into this CTA's shared memory; its bytes complete
 // on the barrier at the same place in CTA `rank` of the pair.
-__device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint32_t rank) {
+__device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [a];\n\t}" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(rank)
+        "mapa.shared::cluster.u32 a, %5, %6;\n\t"
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [a];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "r"(rank)
         : "memory");
 }
 // 32 bytes to global memory, 32-byte aligned: a whole sector from one thread.
