@@ -348,6 +348,7 @@ struct MlaParams {
     float scale;                // softmax scale
     int pairs;                  // tensor-core kernel: CTA pairs of the grid
     int out_wide;               // its output rows lie on 32-byte boundaries
+    int runs;                   // its blocks hold whole halves of a step
     int box_rows;               // its TMA boxes' rows (0: none)
 };
 

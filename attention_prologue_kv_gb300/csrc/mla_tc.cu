@@ -68,8 +68,9 @@ struct Misc {
     int abort;
     Bound begin, end;
     Seq first;               // the sequence of `begin`
-    int64_t wsum[16];
-    float red[2][128];
+    int64_t wsum[17];
+    float red[2][256];
+    uint32_t held[MAX_STAGES][2];   // keys of a step that exist: bit i of a half for its key i
     float inv_k[64], lift;   // 1 / scale of the rotary channels; a power of two taken out of their queries
 };
 struct Scales {              // behind Misc, with codes
@@ -78,7 +79,7 @@ struct Scales {              // behind Misc, with codes
 };
 template <bool C8>
 constexpr uint32_t smem_of() {
-    return OFF_K + stages_of<C8>() * STAGE_BYTES + uint32_t(sizeof(Misc)) + (C8 ? uint32_t(sizeof(Scales)) : 0u) + 1024u;
+    return OFF_K + stages_of<C8>() * STAGE_BYTES + uint32_t(sizeof(Misc)) + (C8 ? uint32_t(sizeof(Scales)) : 0u);
 }
 static_assert(smem_of<false>() <= 232448 && smem_of<true>() <= 232448, "shared memory of a CTA");
 
@@ -130,7 +131,8 @@ __device__ __forceinline__ int64_t cost(const MlaParams& p, int L, int K, int64_
 // Where the share that begins at `off` of a sequence's cost begins.
 __device__ Bound locate(const MlaParams& p, int n, const Seq& s, int64_t off) {
     int lo = 0, hi = row_tiles(p, s.L) - 1;
-    while (lo < hi) {
+#pragma unroll 1
+    while (lo < hi) {   // (one row tile, as in a decode step, needs no search)
         const int mid = (lo + hi + 1) / 2;
         if (cost(p, s.L, s.K, mid) <= off) lo = mid;
         else hi = mid - 1;
@@ -174,19 +176,25 @@ struct Walk {
     }
 };
 
-// This pair's share of the work: every CTA scans all sequences' costs.
+// This pair's share of the work: every CTA scans all sequences' costs, twice side by side: the first half of the warps
+// for the share's begin, the second for its end.
 template <int THREADS>
 __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
+    constexpr int HALF = THREADS / 64;   // warps of a half (one may be left over)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (int(p.N) + THREADS - 1) / THREADS;
-    const int n0 = min(tid * per, int(p.N)), n1 = min(n0 + per, int(p.N));
+    const int half = warp < HALF ? 0 : 1, first = half * HALF, id = tid - first * 32;
+    const bool works = warp < 2 * HALF;
+    const int N = int(p.N), per = (N + HALF * 32 - 1) / (HALF * 32);
+    const int n0 = works ? min(id * per, N) : N, n1 = works ? min(n0 + per, N) : N;
     int64_t sum = 0;
     int bits = 0;
+    Seq s = {0, 0, 0};
+#pragma unroll 1
     for (int n = n0; n < n1; ++n) {
-        const Seq s = load_seq(p, n, &bits);
+        s = load_seq(p, n, &bits);
         if (s.L > 0) sum += cost(p, s.L, s.K, row_tiles(p, s.L));
     }
-    if (bits != 0 && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bits);
+    if (bits != 0 && blockIdx.x == 0 && half == 0 && p.status != nullptr) atomicOr(p.status, bits);
     int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -194,50 +202,48 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
         if (lane >= o) scan += v;
     }
     if (lane == 31) m->wsum[warp] = scan;
-    if (tid == 0) m->begin = m->end = {int(p.N), 0, 0, 0};
+    if (tid == 0) m->begin = m->end = {N, 0, 0, 0};
     __syncthreads();
-    int64_t base = scan - sum, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) base += m->wsum[w];
-        total += m->wsum[w];
-    }
-    // Equal shares, but none below MIN_KEYS (64-bit divisions only where they are needed: they take about 100 cycles).
-    const int64_t least = int64_t(p.H) * MIN_KEYS;
-    const int active = total >= least * p.pairs ? p.pairs : max(1, int(unsigned(total) / unsigned(least)));
-    int64_t u0 = total, u1 = total;
-    if (pair < active) {
-        if (total < (int64_t(1) << 31) / 128) {
-            u0 = unsigned(total) * unsigned(pair) / unsigned(active);
-            u1 = unsigned(total) * unsigned(pair + 1) / unsigned(active);
-        } else {
-            u0 = total * pair / active;
-            u1 = total * (pair + 1) / active;
+    if (works) {
+        // Sums of the warps before this one and of all: lane i has warp i's.
+        int64_t of = lane < HALF ? m->wsum[first + lane] : 0, before = lane < warp - first ? of : 0;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            of += __shfl_xor_sync(0xFFFFFFFFu, of, o);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
         }
-    }
-    if (sum > 0) {
+        const int64_t total = __shfl_sync(0xFFFFFFFFu, of, 0);
+        int64_t base = scan - sum + __shfl_sync(0xFFFFFFFFu, before, 0);
+        // Equal shares, but none below MIN_KEYS (64-bit divisions only where they are needed: they take about 100 cycles).
+        const int64_t least = int64_t(p.H) * MIN_KEYS;
+        const int active = total >= least * p.pairs ? p.pairs : max(1, int(unsigned(total) / unsigned(least)));
+        int64_t u = total;
+        if (pair + half < active) {
+            if (total < (int64_t(1) << 31) / 256) u = unsigned(total) * unsigned(pair + half) / unsigned(active);
+            else u = total * (pair + half) / active;
+        }
+        if (u >= base && u < base + sum) {
+            int n = n0;
+            if (per > 1)
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const int64_t u = e ? u1 : u0;
-            if (u < base || u >= base + sum) continue;
-            int64_t b = base;
-            for (int n = n0; n < n1; ++n) {
-                const Seq s = load_seq(p, n);
-                const int64_t c = s.L > 0 ? cost(p, s.L, s.K, row_tiles(p, s.L)) : 0;
-                if (u < b + c) {
-                    (e ? m->end : m->begin) = locate(p, n, s, u - b);
-                    if (e == 0) m->first = s;
-                    break;
+                for (; n < n1; ++n) {
+                    s = load_seq(p, n);
+                    const int64_t c = s.L > 0 ? cost(p, s.L, s.K, row_tiles(p, s.L)) : 0;
+                    if (u < base + c) break;
+                    base += c;
                 }
-                b += c;
+            const Bound b = locate(p, n, s, u - base);
+            if (half) {
+                m->end = b;
+            } else {
+                m->begin = b;
+                m->first = s;
             }
         }
+        if (tid == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
     }
     __syncthreads();
-    if (tid == 0 && cluster_rank() == 0) {
-        const Space w = ws_space(p);
-        w.bounds[pair] = m->begin;
-        if (pair == 0) *w.active = active;
-    }
+    if (tid == 0 && cluster_rank() == 0) ws_space(p).bounds[pair] = m->begin;
 }
 
 // Four 8-bit codes to packed 16-bit values (exact in either type).
@@ -274,7 +280,7 @@ __device__ __forceinline__ uint4 dec8x8(int kind, uint32_t a, uint32_t b) {
 }
 
 // Cache row of a key, or -1 where there is none to read.
-__device__ __forceinline__ int64_t key_slot(const MlaParams& p, int n, int K, int key) {
+__device__ __forceinline__ int64_t key_row(const MlaParams& p, int n, int K, int key) {
     if (key >= K) return -1;
     if (p.table == nullptr) return n * p.d1 + key;
     const unsigned d1 = unsigned(p.d1 < (1 << 30) ? p.d1 : (1 << 30));   // keys stay below 2^30
@@ -287,6 +293,42 @@ __device__ __forceinline__ int64_t key_slot(const MlaParams& p, int n, int K, in
     return e * p.d1 + (unsigned(key) - q * d1);
 }
 
+// Cache rows of the keys of a part, for one warp. Where blocks hold whole halves of a step (a multiple of 32 keys, or
+// Norm mode) lane i looks up the first row of steps base + i, once for 32 steps: a lookup and its division a step, even
+// one step ahead, cost the lone warp that brings the keys about 1000 cycles. Else each lane looks up its key k, one
+// step ahead.
+struct Rows {
+    const MlaParams& p;
+    int n = 0, K = 0, base = 0;
+    int64_t r[2];        // of the halves: first row of step base + lane, or this lane's row of the step asked for next
+    __device__ __forceinline__ explicit Rows(const MlaParams& q) : p(q) {}
+    __device__ __forceinline__ void look(int step, int k, int halves) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) r[h] = halves >> h & 1 ? key_row(p, n, K, step * KEYS + h * CKEYS + k) : -1;
+    }
+    __device__ __forceinline__ void begin(const Walk& w, int lane, int k, int halves) {
+        n = w.n;
+        K = w.s.K;
+        base = w.kt0;
+        look(p.runs ? base + lane : base, p.runs ? 0 : k, halves);
+    }
+    // This lane's row of key k in a half of step kt, -1 where there is none; next() before going on to step kt + 1.
+    template <int H>
+    __device__ __forceinline__ int64_t row(int kt, int k) const {
+        if (!p.runs) return r[H];
+        const int64_t f = __shfl_sync(0xFFFFFFFFu, r[H], kt - base);
+        return f >= 0 && kt * KEYS + H * CKEYS + k < K ? f + k : -1;
+    }
+    __device__ __forceinline__ void next(int kt, int lane, int k, int halves) {
+        if (!p.runs) {
+            look(kt + 1, k, halves);
+        } else if (kt + 1 - base >= 32) {
+            base = kt + 1;
+            look(base + lane, 0, halves);
+        }
+    }
+};
+
 __device__ __forceinline__ uint32_t box_at(uint32_t box, int row, int chunk) {
     return box + uint32_t(row) * 128u + (uint32_t(chunk ^ (row & 7)) << 4);
 }
@@ -297,6 +339,13 @@ __device__ __forceinline__ uint32_t box_at(uint32_t box, int row, int chunk) {
 struct Maps {
     CUtensorMap all, two, rope;
 };
+
+// The rest of a wait, out of line: the roles' loops have to stay in the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_wait(bar, parity, abort)) return true;
+    *abort = 1;
+    return false;
+}
 
 // What every role has.
 struct Ctx {
@@ -311,10 +360,7 @@ struct Ctx {
     // A wait that gives up (one second) poisons the CTA: the others give up at their first look, and every role
     // runs its loops to the end without waiting, so that no barrier is left with threads missing.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!mbar_wait(bar, parity, abort)) {
-            *abort = 1;
-            ok = false;
-        }
+        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort) && ok;
         __syncwarp();
     }
     __device__ __forceinline__ uint32_t stage(int st) const { return base + OFF_K + uint32_t(st) * STAGE_BYTES; }
@@ -347,15 +393,18 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     uint64_t* fix = SWAP ? &m->v_fix : &m->k_fix;
     uint64_t* full = SWAP ? m->v_full : m->k_full;
     int j = 0, fixed = 0, pend = -1;
-    const int mine = int(SWAP ? c.rank ^ 1 : c.rank) * CKEYS + lane;   // this lane's key of a step
+    const int mine = int(SWAP ? c.rank ^ 1 : c.rank), halves = SWAP ? 1 << mine : 3;
+    Rows rows(p);
     Walk w(p, m);
+#pragma unroll 1
     while (w.next()) {
-        int64_t next = key_slot(p, w.n, w.s.K, w.kt0 * KEYS + mine);
+        rows.begin(w, lane, lane, halves);
+#pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int st = j % STAGES;
             const uint32_t stage = c.stage(st);
-            const int64_t slot = next;
-            if (kt + 1 < w.kt1) next = key_slot(p, w.n, w.s.K, (kt + 1) * KEYS + mine);
+            const int64_t lo = rows.row<0>(kt, lane), hi = rows.row<1>(kt, lane), slot = mine ? hi : lo;
+            rows.next(kt, lane, lane, halves);
             const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
             uint2 codes[8];
             if (K8 && !SWAP) {   // rotary codes: 8 of each row (lane >> 3) + 4 rr, decoded below
@@ -377,6 +426,13 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                 }
                 c.wait(bar, parity);
             }
+            if (!SWAP) {
+                const uint32_t theirs = __ballot_sync(0xFFFFFFFFu, (mine ? lo : hi) >= 0);
+                if (lane == 0) {
+                    m->held[st][mine] = live;
+                    m->held[st][mine ^ 1] = theirs;
+                }
+            }
             if (R > 0) {
                 const bool whole = live == 0xFFFFFFFFu;
                 const int groups = CKEYS / R;
@@ -388,29 +444,20 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                 } else if (live != 0) {
                     // Groups of R rows with one that exists; their other rows are cleared below.
                     uint32_t some = 0;
+#pragma unroll 1
                     for (int g = 0; g < groups; ++g) some += live >> (g * R) & 1;
                     if (lane == 0) mbar_arrive_expect_tx(fix, uint32_t(boxes) * some * uint32_t(R) * 128u);
                 }
                 __syncwarp();
-                if (R == CKEYS) {
-                    if (lane == 0 && slot >= 0) {
-                        if (SWAP) {
-                            for (int b = 0; b < boxes; b += 2)
-                                tma_box_at(stage + uint32_t(place(b)) * KBOX, &maps.two, 0, int(slot), channels(b), done, to);
-                        } else {
-                            tma_box_at(stage, &maps.all, 0, int(slot), 0, done, to);
-                            tma_box_at(stage + 8 * KBOX, &maps.rope, 0, int(slot), 0, done, to);
-                        }
-                    }
-                } else {   // a box at a time: a copy of several would put them R rows apart
-                    for (int q0 = 0; q0 < boxes * groups; q0 += 32) {
-                        const int q = q0 + lane, g = min(q / boxes, groups - 1), b = q - g * boxes;
-                        const int row = __shfl_sync(0xFFFFFFFFu, int(slot), g * R);
-                        const bool rope = !SWAP && b == c.nb;
-                        if (q < boxes * groups && row >= 0)
-                            tma_box_at(stage + uint32_t(place(b)) * KBOX + uint32_t(g * R) * 128u, rope ? &maps.rope : &maps.all, 0, row,
-                                       rope ? 0 : channels(b), done, to);
-                    }
+                // A box at a time: a copy of several would put them R rows apart.
+#pragma unroll 1
+                for (int q0 = 0; q0 < boxes * groups; q0 += 32) {
+                    const int q = q0 + lane, g = min(q / boxes, groups - 1), b = q - g * boxes;
+                    const int row = __shfl_sync(0xFFFFFFFFu, int(slot), g * R);
+                    const bool rope = !SWAP && b == c.nb;
+                    if (q < boxes * groups && row >= 0)
+                        tma_box_at(stage + uint32_t(place(b)) * KBOX + uint32_t(g * R) * 128u, rope ? &maps.rope : &maps.all, 0, row,
+                                   rope ? 0 : channels(b), done, to);
                 }
                 if (!whole) {
                     if (live != 0) {
@@ -418,6 +465,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                         ++fixed;
                     }
                     if (slot < 0)
+#pragma unroll 1
                         for (int b = 0; b < boxes; ++b)
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
@@ -431,6 +479,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                     const int r = rr * 4 + (lane >> 3);
                     const int64_t row = __shfl_sync(0xFFFFFFFFu, slot, r);
                     const uint16_t* v = static_cast<const uint16_t*>(p.ckv) + (row < 0 ? 0 : row) * p.Dv;
+#pragma unroll 1
                     for (int b = 0; b < nl; ++b) {
                         const int q = channels(b) * 8 + ch;
                         const bool in = row >= 0 && q < nc;
@@ -459,6 +508,82 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     }
 }
 
+// key_warp where a TMA copy takes the whole half of a step. One thread's instructions set the pace here (about 5 cycles
+// each): the step's path is kept short.
+template <bool SWAP>
+__device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
+    constexpr int STAGES = stages_of<false>();
+    static_assert((STAGES & (STAGES - 1)) == 0, "stages are counted by masks");
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int lane = c.lane;
+    const int mine = int(SWAP ? c.rank ^ 1 : c.rank);
+    const int boxes = SWAP ? 2 * ((c.nb + 3) / 4) : c.nb + 1;   // a pair that lies behind the row is zeros
+    const uint32_t place = (SWAP ? uint32_t(c.rank ^ 1) * 2 : 0) * KBOX;
+    uint64_t* fix = SWAP ? &m->v_fix : &m->k_fix;
+    uint64_t* full = SWAP ? m->v_full : m->k_full;
+    auto copy = [&](uint32_t stage, int row, uint64_t* done, uint32_t to) {
+        if (SWAP) {
+            tma_box_at(stage + place, &maps.two, 0, row, int(c.rank) * 2, done, to);
+            if (boxes > 2) tma_box_at(stage + place + 4 * KBOX, &maps.two, 0, row, int(c.rank) * 2 + 4, done, to);
+        } else {
+            tma_box_at(stage, &maps.all, 0, row, 0, done, to);
+            tma_box_at(stage + 8 * KBOX, &maps.rope, 0, row, 0, done, to);
+        }
+    };
+    int j = 0, fixed = 0;
+    Walk w(p, m);
+#pragma unroll 1
+    while (w.next()) {
+        const int n = w.n, K = w.s.K;
+        int base = w.kt0 - 32, own = -1, other = -1;   // first rows of this lane's step, base + lane
+#pragma unroll 1
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+            if (kt - base >= 32) {
+                base = kt;
+                own = int(key_row(p, n, K, (base + lane) * KEYS + mine * CKEYS));
+                if (!SWAP) other = int(key_row(p, n, K, (base + lane) * KEYS + (mine ^ 1) * CKEYS));
+            }
+            const int row = __shfl_sync(0xFFFFFFFFu, own, kt - base), row2 = SWAP ? 0 : __shfl_sync(0xFFFFFFFFu, other, kt - base);
+            const int left = K - kt * KEYS - mine * CKEYS, left2 = K - kt * KEYS - (mine ^ 1) * CKEYS;
+            const uint32_t live = row < 0 ? 0u : (left >= CKEYS ? 0xFFFFFFFFu : (1u << left) - 1u);
+            const int st = j & (STAGES - 1);
+            const uint32_t stage = c.stage(st);
+            if (SWAP) c.wait(&m->s_full[j & 1], (j >> 1) & 1);
+            else if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+            if (!SWAP && lane == 0) {
+                m->held[st][mine] = live;
+                m->held[st][mine ^ 1] = row2 < 0 ? 0u : (left2 >= CKEYS ? 0xFFFFFFFFu : (1u << left2) - 1u);
+            }
+            if (live == 0xFFFFFFFFu) {
+                if (lane == 0) {
+                    mbar_expect_at(&full[st], 0, uint32_t(boxes) * KBOX);
+                    copy(stage, row, &full[st], 0);
+                }
+                __syncwarp();
+            } else {   // the last keys of a sequence, or a hole: clear the rows that do not exist
+                if (live != 0) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(fix, uint32_t(boxes) * KBOX);
+                        copy(stage, row, fix, c.rank);
+                    }
+                    __syncwarp();
+                    c.wait(fix, fixed & 1);
+                    ++fixed;
+                }
+                if (!(live >> lane & 1))
+#pragma unroll 1
+                    for (int b = 0; b < boxes; ++b) {
+                        const uint32_t box = stage + (SWAP ? place + uint32_t((b >> 1) * 4 + (b & 1)) * KBOX : uint32_t(b < c.nb ? b : 8) * KBOX);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) st_shared_v4(box + uint32_t(lane) * 128u + k * 16u, make_uint4(0, 0, 0, 0));
+                    }
+                c.arrive(&full[st]);
+            }
+        }
+    }
+}
+
 // Four warps decode a CTA's 8-bit rows into halves (the rotary part into q's type).
 // Thread (key tk, quarter c4): 16 codes a load, the next step's loads in flight.
 template <class IT, bool SWAP>
@@ -470,8 +595,20 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
     constexpr int NX = SWAP ? 4 : 8;
     const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16;
     uint4 x[NX], y[NX], xr[2], yr[2];
+    const int mine = int(SWAP ? c.rank ^ 1 : c.rank), halves = SWAP ? 1 << mine : 3;
+    Rows rows(p);
+    rows.begin(w, c.lane, tk, halves);
+    uint32_t held = 0, next = 0;   // this warp's 8 keys of this CTA (byte 0) and of the other (byte 1) that exist: this step, the next
+    auto bits = [](uint32_t b) {   // every fourth bit
+        b &= 0x11111111u;
+        b = (b | b >> 3) & 0x03030303u;
+        b = (b | b >> 6) & 0x000F000Fu;
+        return (b | b >> 12) & 0xFFu;
+    };
     auto load = [&](int kt, uint4 (&a)[NX], uint4 (&ar)[2]) {
-        const int64_t slot = key_slot(p, w.n, w.s.K, kt * KEYS + int(SWAP ? c.rank ^ 1 : c.rank) * CKEYS + tk);
+        const int64_t lo = rows.row<0>(kt, tk), hi = rows.row<1>(kt, tk), slot = mine ? hi : lo;
+        rows.next(kt, c.lane, tk, halves);
+        if (!SWAP) next = bits(__ballot_sync(0xFFFFFFFFu, slot >= 0)) | bits(__ballot_sync(0xFFFFFFFFu, (mine ? lo : hi) >= 0)) << 8;
         const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (slot < 0 ? 0 : slot) * p.Dv;
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
@@ -488,6 +625,8 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
         }
     };
     load(w.kt0, x, xr);
+    held = next;
+#pragma unroll 1
     for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
         if (kt + 1 < w.kt1) load(kt + 1, y, yr);
         const int st = j % STAGES;
@@ -503,6 +642,10 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
             st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<F16>(p.ckv_kind, x[i].z, x[i].w));
         }
         if (!SWAP) {
+            if (c.lane == 0) {
+                reinterpret_cast<uint8_t*>(&m->held[st][mine])[v >> 5] = uint8_t(held);
+                reinterpret_cast<uint8_t*>(&m->held[st][mine ^ 1])[v >> 5] = uint8_t(held >> 8);
+            }
             const uint32_t box = stage + 8 * KBOX;
             if (p.k_kind == OUT16) {
                 st_shared_v4(box_at(box, tk, c4), xr[0]);
@@ -517,6 +660,7 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
         for (int i = 0; i < NX; ++i) x[i] = y[i];
         xr[0] = yr[0];
         xr[1] = yr[1];
+        held = next;
     }
 }
 
@@ -526,17 +670,26 @@ __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int p
     const MlaParams& p = c.p;
     Misc* m = c.m;
     const int nc = p.Dv / 8, nr = p.Dk / 8, ch = v & 7;
-    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
-#pragma unroll 1
+    const uint16_t *qns[4], *qrs[4];
+    uint32_t lives = 0;
+#pragma unroll
     for (int it = 0; it < 4; ++it) {
-        const int r = it * 16 + (v >> 3);
-        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
+        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + it * 16 + (v >> 3);
         const bool live = row < unsigned(w.s.L) * unsigned(p.H);
         const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
-        const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
-        const uint16_t* qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
+        qns[it] = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
+        qrs[it] = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
+        lives |= uint32_t(live) << it;
+    }
+    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + (v >> 3);
+        const bool live = lives >> it & 1;
+        const uint16_t *qn = qns[it], *qr = qrs[it];
         if constexpr (!C8) {
             const bool scaled = p.k_kind != OUT16 && p.k_scale_per_ch;
+#pragma unroll
             for (int b = 0; b < 8; ++b) {
                 const int q = b * 8 + ch;
                 if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), live && q < nc ? qn + q * 8 : qn, live && q < nc);
@@ -603,18 +756,118 @@ __device__ __forceinline__ void prefetch_queries(Ctx& c, int v, const Walk& w) {
     if (row >= unsigned(w.s.L) * unsigned(p.H)) return;
     const int64_t t = w.s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
     const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
+#pragma unroll 1
     for (int ch = (v & 1) * 64; ch < p.Dv; ch += 128) prefetch_l2(qn + ch);
     if ((v & 1) == 0) prefetch_l2(static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs);
 }
 
-// Softmax and output of 128 threads: thread (row r, half h of the keys and channels).
+// Groups of four softmax warps: two where registers allow (16-bit rows). A lone warp of a scheduler goes at about 5
+// cycles an instruction, so what a warp has to do sets the time of a step's softmax and of a part's output.
+template <bool C8>
+constexpr int groups_of() { return C8 ? 1 : 2; }
+template <bool C8>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(128 * groups_of<C8>()) : "memory");
+}
+
+// Output of a part (a row tile of a sequence), by the softmax warps: thread (row r, half h of the channels; group g has
+// half of the 256 columns). Each thread writes its row's sectors itself, with few instructions: through shared memory, for
+// whole lines, took more of them and longer (7000 cycles a part against 5000).
+template <class IT, bool C8>
+__device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part, const Walk& w, unsigned row, bool live, float2 ml) {
+    constexpr int G = groups_of<C8>();
+    const MlaParams& p = c.p;
+    const int r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
+    const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
+    const bool none = ml.y == 0.f;
+    const int64_t t = w.s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
+    const int q0 = g * 128, q1 = min(q0 + 256 / G, p.Dv > 256 ? 256 : 128);
+    if (!w.whole) {
+        const Space ws = ws_space(p);
+        const int64_t at = (int64_t(pair) * 2 + (part ? 1 : 0)) * ROWS + c.rank * CROWS + r;
+        if (live && h == 0 && g == 0) ws.ml[at] = ml;
+        float* po = ws.o + at * p.Dv;
+#pragma unroll 1
+        for (int q = q0; q < q1; q += 32) {   // (a row without keys leaves what it may: the join skips it)
+            float o[32];
+            __syncwarp();
+            tmem_ld32(lanes + q, o);
+            tmem_wait_ld();
+            const int ch = (q >> 7) * 256 + h * 128 + (q & 127);
+            if (C8) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= c.sc->inv_v[ch + k];
+            }
+            if (live && ch + 32 <= p.Dv) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t*>(o) + k);
+            } else if (live) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                    if (ch + k < p.Dv) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t*>(o) + k);
+            }
+        }
+    } else {
+        if (live && h == 0 && g == 0 && p.lse != nullptr)
+            p.lse[t * p.H + head] = none ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs;
+        const float inv = none ? 0.f : 1.f / ml.y;
+        const bool zero = __any_sync(0xFFFFFFFFu, none);   // a row without keys: zeros, whatever the others' keys hold
+#pragma unroll 1
+        for (int q = q0; q < q1; q += 32) {
+            float o[32];
+            __syncwarp();
+            tmem_ld32(lanes + q, o);
+            tmem_wait_ld();
+            const int ch = (q >> 7) * 256 + h * 128 + (q & 127);
+            if (C8) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= c.sc->inv_v[ch + k];
+            }
+            uint32_t u[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float2 x = __fmul2_rn(make_float2(o[2 * k], o[2 * k + 1]), make_float2(inv, inv));
+                u[k] = IT::pack(x.x, x.y);
+            }
+            if (zero) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) u[k] = none ? 0u : u[k];
+            }
+            if (live && p.out_wide && ch + 32 <= p.Dv) {
+                st_global_v8(out + ch, u);
+                st_global_v8(out + ch + 16, u + 8);
+            } else if (live) {
+#pragma unroll
+                for (int k = 0; k < 16; k += 4)
+                    if (ch + 2 * k < p.Dv) *reinterpret_cast<uint4*>(out + ch + 2 * k) = make_uint4(u[k], u[k + 1], u[k + 2], u[k + 3]);
+            }
+        }
+    }
+    tc_fence_before();
+}
+
+// Over the threads of row r, always in this order.
+template <int G>
+__device__ __forceinline__ float row_max(const float* x, int r) {
+    const float v = fmaxf(x[r], x[r + 64]);
+    return G == 1 ? v : fmaxf(v, fmaxf(x[r + 128], x[r + 192]));
+}
+template <int G>
+__device__ __forceinline__ float row_sum(const float* x, int r) {
+    const float v = x[r] + x[r + 64];
+    return G == 1 ? v : v + (x[r + 128] + x[r + 192]);
+}
+
+// Softmax: thread (row r, half h of the keys, group g: half of that half).
 template <class IT, bool C8, bool K8>
 __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     using PT = typename std::conditional<C8, F16, IT>::type;   // type of the weights and the decoded codes
+    constexpr int G = groups_of<C8>(), NK = CKEYS / G;          // keys of a thread
     const MlaParams& p = c.p;
     Misc* m = c.m;
-    const int lane = c.lane, r = tid & 63, h = tid >> 6, na = p.Dv > 256 ? 2 : 1;
-    const uint32_t lanes = c.tmem + (uint32_t(tid >> 5) << 21);
+    const int lane = c.lane, r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
+    const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
     constexpr bool split = C8 || K8;
     // Score = fn * (latent product) + fr * (rotary product), in powers of two.
     const float l2 = p.scale * 1.4426950408889634f;
@@ -622,49 +875,50 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     if (K8) fr = l2 * (p.k_scale_per_ch ? m->lift : m->inv_k[0]);
     int j = 0, part = 0;
     Walk w(p, m);
+#pragma unroll 1
     while (w.next()) {
         const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
         const bool live = row < unsigned(w.s.L) * unsigned(p.H);
-        const int t = int(row / unsigned(p.H)), head = int(row % unsigned(p.H));
-        const int vis = live ? seen(p, w.s.L, w.s.K, t) : 0;
+        const int vis = live ? seen(p, w.s.L, w.s.K, int(row / unsigned(p.H))) : 0;
         int wmin = live ? vis : 0x7FFFFFFF;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
         float mx = -INFINITY, sum = 0.f;
-        int64_t next = key_slot(p, w.n, w.s.K, w.kt0 * KEYS + h * CKEYS + lane);
+#pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-            const int key0 = kt * KEYS + h * CKEYS;
-            // Keys that exist: bit i for key0 + i.
-            const uint32_t held = __ballot_sync(0xFFFFFFFFu, next >= 0);
-            if (kt + 1 < w.kt1) next = key_slot(p, w.n, w.s.K, key0 + KEYS + lane);
+            const int key0 = kt * KEYS + h * CKEYS + g * NK;
+            float* red = m->red[j & 1];
             c.wait(&m->s_full[j & 1], (j >> 1) & 1);
             tc_fence_after();
+            // Keys that exist: bit i for key0 + i.
+            const uint32_t held = m->held[j % stages_of<C8>()][h] >> (g * NK);
             if (C8 && kt == w.kt0) fn = l2 * (p.ckv_scale_per_ch ? 1.f : c.sc->inv_v[0]) * c.sc->row_mul[part & 1][r];
-            float s[32];
-            tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64, s);
+            float s[NK];
+            tmem_ld(lanes + COL_S + uint32_t(j & 1) * 64 + g * NK, s);
             if (split) {
-                float s2[32];
-                tmem_ld32(lanes + COL_S + uint32_t(j & 1) * 64 + 32, s2);
+                float s2[NK];
+                tmem_ld(lanes + COL_S + uint32_t(j & 1) * 64 + 32 + g * NK, s2);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = fmaf(s2[i], fr, s[i] * fn);
+                for (int i = 0; i < NK; ++i) s[i] = fmaf(s2[i], fr, s[i] * fn);
             } else {
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] *= fn;
+                for (int i = 0; i < NK; ++i) s[i] *= fn;
             }
-            if (held != 0xFFFFFFFFu || key0 + CKEYS > wmin) {
+            constexpr uint32_t all = NK == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+            if ((held & all) != all || key0 + NK > wmin) {
                 const int left = vis - key0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < NK; ++i)
                     if (i >= left || !(held >> i & 1)) s[i] = -INFINITY;
             }
             float top = s[0];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) top = fmaxf(top, s[i]);
-            m->red[j & 1][tid] = top;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            top = fmaxf(fmaxf(top, m->red[j & 1][tid ^ 64]), mx);
+            for (int i = 1; i < NK; ++i) top = fmaxf(top, s[i]);
+            red[tid] = top;
+            softmax_sync<C8>();
+            top = fmaxf(row_max<G>(red, r), mx);
             // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
             // and the 16-bit rounding of a weight is relative.
             const bool grow = top > mx + 8.f;
@@ -674,9 +928,9 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
                 sum *= f;
             }
             const float ref = mx == -INFINITY ? 0.f : mx;
-            uint32_t pk[16];
+            uint32_t pk[NK / 2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < NK / 2; ++i) {
                 const float a = exp2_approx(s[2 * i] - ref), b = exp2_approx(s[2 * i + 1] - ref);
                 sum += a + b;
                 pk[i] = PT::pack(a, b);
@@ -685,7 +939,9 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             if (j > 0) c.wait(&m->pv_done, (j - 1) & 1);
             if (__any_sync(0xFFFFFFFFu, grow) && kt > w.kt0) {
                 tc_fence_after();
-                for (int q = 0; q < na * 128; q += 32) {
+                const int q1 = min(g * 128 + 256 / G, p.Dv > 256 ? 256 : 128);
+#pragma unroll 1
+                for (int q = g * 128; q < q1; q += 32) {
                     float o[32];
                     tmem_ld32(lanes + q, o);
                     tmem_wait_ld();
@@ -696,65 +952,37 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
                 tmem_wait_st();
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                st_shared_v4(box_at(c.base + OFF_P, r, h * 4 + q), make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+            for (int q = 0; q < NK / 8; ++q)
+                st_shared_v4(box_at(c.base + OFF_P, r, h * 4 + g * (NK / 8) + q),
+                             make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
             tc_fence_before();
             c.arrive(&m->p_full);
         }
-        // Output of the part.
+        // The rows' m and l for the output.
+        float* red = m->red[j & 1];
+        red[tid] = sum;   // the next step's buffer: its own maxima come after the second barrier
+        softmax_sync<C8>();
+        const float2 ml = make_float2(mx, row_sum<G>(red, r));
+        softmax_sync<C8>();
         c.wait(&m->pv_done, (j - 1) & 1);
         tc_fence_after();
-        m->red[j & 1][tid] = sum;   // the next step's buffer: its own maximum comes after this read
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const float l = m->red[j & 1][tid & 63] + m->red[j & 1][(tid & 63) + 64];
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const bool none = l == 0.f;
-        const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
-        uint16_t* out = nullptr;
-        float* po = nullptr;
-        const bool wide = p.out_wide;
-        if (w.whole) {
-            out = static_cast<uint16_t*>(p.out) + (w.s.q0 + t) * p.o_ts + int64_t(head) * p.o_hs;
-            if (live && h == 0 && p.lse != nullptr)
-                p.lse[(w.s.q0 + t) * p.H + head] = none ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
-        } else {
-            const Space ws = ws_space(p);
-            const int64_t at = (int64_t(pair) * 2 + (part ? 1 : 0)) * ROWS + c.rank * CROWS + r;
-            po = ws.o + at * p.Dv;
-            if (live && h == 0) ws.ml[at] = make_float2(mx, l);
-        }
-        for (int q = 0; q < na * 128; q += 32) {
-            float o[32];
-            tmem_ld32(lanes + q, o);
-            tmem_wait_ld();
-            const int ch = (q >> 7) * 256 + h * 128 + (q & 127);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                o[i] = none ? 0.f : o[i] * inv;
-                if (C8) o[i] *= c.sc->inv_v[ch + i];
-            }
-            if (!live) continue;
-            if (w.whole) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 16) {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = IT::pack(o[k + 2 * i], o[k + 2 * i + 1]);
-                    if (wide && ch + k + 16 <= p.Dv) {
-                        st_global_v8(out + ch + k, u);
-                    } else {
-                        if (ch + k < p.Dv) *reinterpret_cast<uint4*>(out + ch + k) = make_uint4(u[0], u[1], u[2], u[3]);
-                        if (ch + k + 8 < p.Dv) *reinterpret_cast<uint4*>(out + ch + k + 8) = make_uint4(u[4], u[5], u[6], u[7]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                    if (ch + k < p.Dv) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t(&)[8]>(o[k]));
-            }
-        }
-        tc_fence_before();
+        output_part<IT, C8>(c, tid, pair, part, w, row, live, ml);
         ++part;
+    }
+}
+
+// Four warps: queries of a part (and, with codes, its swaps).
+template <class IT, bool C8>
+__device__ __forceinline__ void query_warps(Ctx& c, int v) {
+    Walk w(c.p, c.m);
+    int j = 0;
+    bool more = w.next();
+#pragma unroll 1
+    for (int part = 0; more; ++part) {
+        load_queries<IT, C8>(c, v, w, part);
+        if (C8) code_warps<IT, true>(c, v, w, j);
+        more = w.next();
+        if (!C8 && more) prefetch_queries(c, v, w);
     }
 }
 
@@ -791,11 +1019,13 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
         __syncwarp();
     };
     Walk w(p, m);
+#pragma unroll 1
     while (w.next()) {
         if (prev) issue_o(j - 1, prev_first);
         prev = false;
         c.wait(&m->q_full, parts & 1);
         ++parts;
+#pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int st = j % STAGES;
             c.wait(&m->k_full[st], (j / STAGES) & 1);
@@ -831,26 +1061,31 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
     }
 }
 
-// Warps: 0-3 softmax. 16-bit latent rows: 4 keys, 5 swap, 6 MMA, 8-11 queries. Codes: 4-7 keys, 8-11 swap and queries,
-// 12 MMA.
+// Warps: first the softmax's (8; 4 with codes). Then, 16-bit latent rows: 8 keys, 9 swap, 10 MMA, 12-15 queries; codes: 4-7
+// keys, 8-11 queries and swap, 12 MMA.
 template <bool C8>
-constexpr int threads_of() { return C8 ? 416 : 384; }
+constexpr int threads_of() { return C8 ? 416 : 512; }
 
 template <class IT, bool C8, bool K8>
 __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     mla_tc_kernel(const __grid_constant__ MlaParams p, const __grid_constant__ Maps maps) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];   // the swizzle repeats every 1024 bytes
     constexpr int NT = threads_of<C8>();
-    constexpr int MMA_WARP = C8 ? 12 : 6;
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    constexpr int MMA_WARP = C8 ? 12 : 10;
+    const uint32_t base = smem_u32(smem_raw);
     constexpr int STAGES = stages_of<C8>();
-    Misc* m = reinterpret_cast<Misc*>(smem_raw + (base - smem_u32(smem_raw)) + OFF_K + STAGES * STAGE_BYTES);
+    Misc* m = reinterpret_cast<Misc*>(smem_raw + OFF_K + STAGES * STAGE_BYTES);
     Scales* sc = reinterpret_cast<Scales*>(m + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
 
+    if (base % 1024 != 0) {   // the declaration's alignment was not kept: nothing below would be right
+        if (tid == 0 && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
+        return;
+    }
     if (tid == 0) {
+#pragma unroll 1
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&m->k_full[s], C8 ? 8 : 2);
             mbar_init(&m->v_full[s], C8 ? 8 : 2);
@@ -858,7 +1093,7 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
         }
         mbar_init(&m->s_full[0], 1);
         mbar_init(&m->s_full[1], 1);
-        mbar_init(&m->p_full, 8);
+        mbar_init(&m->p_full, 8 * groups_of<C8>());
         mbar_init(&m->pv_done, 1);
         mbar_init(&m->q_full, 8);
         mbar_init(&m->q_free, 1);
@@ -876,10 +1111,12 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     pdl_launch_dependents();
     schedule<NT>(p, m, pair);
     if (C8) {
+#pragma unroll 1
         for (int ch = tid; ch < 512; ch += NT) sc->inv_v[ch] = ch >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? ch : 0];
     }
     if (K8 && warp == 0) {
         float v = 0.f;
+#pragma unroll 1
         for (int ch = lane; ch < 64; ch += 32) {
             const float x = ch >= p.Dk ? 0.f : 1.f / p.k_scale[p.k_scale_per_ch ? ch : 0];
             m->inv_k[ch] = x;
@@ -895,34 +1132,28 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = m->tmem;
     Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
 
-    if (warp < 4) {
+    if (warp < 4 * groups_of<C8>()) {
         softmax_warps<IT, C8, K8>(c, tid, pair);
     } else if (warp == MMA_WARP) {
         if (rank == 0) mma_warp<IT, C8, K8>(c);
     } else if constexpr (C8) {
-        Walk w(p, m);
-        int j = 0;
-        for (int part = 0; w.next(); ++part) {
-            if (warp < 8) {
-                code_warps<IT, false>(c, tid - 128, w, j);
-            } else {
-                load_queries<IT, true>(c, tid - 256, w, part);
-                code_warps<IT, true>(c, tid - 256, w, j);
-            }
+        if (warp < 8) {
+            Walk w(p, m);
+            int j = 0;
+#pragma unroll 1
+            while (w.next()) code_warps<IT, false>(c, tid - 128, w, j);
+        } else {
+            query_warps<IT, true>(c, tid - 256);
         }
     } else {
-        if (warp == 4) {
-            key_warp<IT, K8, false>(c, maps);
-        } else if (warp == 5) {
-            key_warp<IT, K8, true>(c, maps);
-        } else if (warp >= 8) {
-            Walk w(p, m);
-            bool more = w.next();
-            for (int part = 0; more; ++part) {
-                load_queries<IT, false>(c, tid - 256, w, part);
-                more = w.next();
-                if (more) prefetch_queries(c, tid - 256, w);
-            }
+        if (warp == 8) {
+            if (!K8 && p.box_rows == CKEYS) key_warp_tma<false>(c, maps);
+            else key_warp<IT, K8, false>(c, maps);
+        } else if (warp == 9) {
+            if (!K8 && p.box_rows == CKEYS) key_warp_tma<true>(c, maps);
+            else key_warp<IT, K8, true>(c, maps);
+        } else if (warp >= 12) {
+            query_warps<IT, false>(c, tid - 384);
         }
     }
     if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
@@ -959,6 +1190,7 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_c
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     bool more = true;
+#pragma unroll 1
     for (int q0 = 0; more; q0 += 32) {
         const int q = b - 1 + q0 + lane;
         Bound me = {-1, 0, 0, 0}, nx = {-1, 0, 0, 0};
@@ -1102,6 +1334,7 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     // its rows keep their place in the 8-row swizzle. Other blocks, codes and narrow rows take 16-byte copies.
     Maps maps = {};
     p.box_rows = 0;
+    p.runs = p.table == nullptr || p.d1 % CKEYS == 0;
     const int64_t rows = p.d0 * p.d1;
     if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv % 64 == 0 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
         int r = 32;

@@ -52,7 +52,7 @@ __device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map,
         : "memory");
 }
 // 32 bytes to global memory, 32-byte aligned: a whole sector from one thread.
-__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
@@ -121,6 +121,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) { tmem_ld16(addr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) { tmem_ld32(addr, v); }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
     asm volatile(
@@ -146,6 +157,12 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t src) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+    return v;
 }
 
 }  // namespace kvr
