@@ -415,12 +415,20 @@ class BoundCall(PreparedCall):
     """PreparedCall of an operator that holds its tensors on one device,
     which need not be the current one when the call is made."""
 
+    workspace = None
+
     def __init__(self, fn, args, name, keep, device):
         super().__init__(fn, args, name, keep)
         self._device = device
+        self._index = device.index
 
     def __call__(self, stream=None):
-        _launch(self._fn, self._ref, self._name, self._device, stream)
+        if stream is None and torch._C._cuda_getDevice() == self._index:   # the serving loop's call, kept short
+            st = self._fn(self._ref, torch._C._cuda_getCurrentRawStream(self._index))
+            if st != N.KVR_OK:
+                raise KvrError(st, self._name)
+        else:
+            _launch(self._fn, self._ref, self._name, self._device, stream)
 
 
 def _heads(t, name, dtype, T=None, H=None):

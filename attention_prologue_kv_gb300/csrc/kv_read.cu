@@ -3,35 +3,33 @@
 // Operation: out[t] = [ckv_cache[slot(t)] / ckv_scale | k_cache[slot(t)] / k_scale]
 // with the slots of "aclnnKvRmsNormRopeCache" ("Restrictions on index").
 //
-// A stream, bound by HBM: one warp per row, each lane moves 8-channel chunks
-// (a 16-byte or 8-byte load, a 16-byte store).
+// A stream, bound by HBM. Rows of 512 + 64 channels: a warp takes four rows at
+// a time, their loads in flight together: a lane has 16 channels of each latent
+// row, whose 1 / scale it keeps in registers, and an eighth of one rotary row.
+// Other widths on 16-byte boundaries: one warp per row, chunks of 8 channels.
 #include "kvr_internal.cuh"
 
 namespace kvr {
 
 constexpr int READ_THREADS = 128;
 
-// Cache row of token t, or -1.
-__device__ __forceinline__ int64_t read_row(const ReadParams& p, int64_t t) {
-    const int64_t b = t / p.S, s = t - b * p.S;
-    if (p.mode == KVR_CACHE_PA_BLK_BSND) {
-        const int64_t q = s / p.d1, r = s - q * p.d1;
-        const int64_t e = p.index[b * p.nblk + q];
-        if (e == -1) return -1;
-        if (e < 0 || e >= p.d0 * p.d1 || e % p.d1 + r >= p.d1) {
-            if (p.status != nullptr) atomicOr(p.status, KVR_DEVERR_INDEX);
-            return -1;
-        }
-        return e + r;
-    }
-    const int64_t e = p.index[t];
+// Cache row of token t, or -1. I: 32-bit arithmetic where everything fits, as 64-bit divisions take about 100 instructions.
+template <class I>
+__device__ __forceinline__ int64_t read_row_t(const ReadParams& p, int64_t token) {
+    const I t = I(token), S = I(p.S), d1 = I(p.d1), rows = I(p.d0) * d1;
+    const I b = t / S, s = t - b * S;
+    const bool blocks = p.mode == KVR_CACHE_PA_BLK_BSND, norm = p.mode == KVR_CACHE_NORM;
+    const I q = blocks ? s / d1 : 0, r = blocks ? s - q * d1 : 0;
+    const int64_t e = p.index[blocks ? int64_t(b) * p.nblk + q : token];
     if (e == -1) return -1;
-    const int64_t range = p.mode == KVR_CACHE_NORM ? p.d1 : p.d0 * p.d1;
-    if (e < 0 || e >= range) {
+    if (e < 0 || e >= int64_t(norm ? d1 : rows) || (blocks && I(e) % d1 + r >= d1)) {
         if (p.status != nullptr) atomicOr(p.status, KVR_DEVERR_INDEX);
         return -1;
     }
-    return p.mode == KVR_CACHE_NORM ? b * p.d1 + e : e;
+    return norm ? int64_t(b) * p.d1 + e : e + int64_t(r);
+}
+__device__ __forceinline__ int64_t read_row(const ReadParams& p, int64_t t) {
+    return p.small ? read_row_t<uint32_t>(p, t) : read_row_t<uint64_t>(p, t);
 }
 
 // Eight values of a row, from channel c0 on.
@@ -65,6 +63,110 @@ __global__ void __launch_bounds__(READ_THREADS) read_vec_kernel(const __grid_con
     }
 }
 
+// 16 codes of kind K to 16 values.
+template <int K>
+__device__ __forceinline__ void codes16(const uint4& w, float (&v)[16]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (K == OUT_I8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = float(int8_t(u[i] >> (8 * k)));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(uint16_t(u[i] >> (16 * k)), K == OUT_E4M3 ? __NV_E4M3 : __NV_E5M2);
+                v[4 * i + 2 * k] = __half2float(__ushort_as_half(h.x));
+                v[4 * i + 2 * k + 1] = __half2float(__ushort_as_half(h.y));
+            }
+        }
+    }
+}
+
+constexpr int READ_ROWS = 4;   // rows of a warp at a time
+constexpr int READ_ROWS_THREADS = 256;
+template <class OT, int K>
+__global__ void __launch_bounds__(READ_ROWS_THREADS) read_rows_kernel(const __grid_constant__ ReadParams p) {
+    constexpr int Dv = 512, Dk = 64;
+    // 1 / scale, once a CTA: read by every warp of the grid from global memory it took as long as the rows.
+    __shared__ __align__(16) float inv_s[Dv];
+    __shared__ __align__(16) float invk_s[Dk];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, eighth = lane & 7, sub = lane >> 3;
+    const int64_t warps = int64_t(gridDim.x) * (READ_ROWS_THREADS / 32);
+    int64_t t = (int64_t(blockIdx.x) * (READ_ROWS_THREADS / 32) + (threadIdx.x >> 5)) * READ_ROWS;
+    int64_t mine = -1;
+    if (lane < READ_ROWS && t + lane < p.T) mine = read_row(p, t + lane);
+    float inv[16], invk[8];
+    if (K != OUT16 || p.k_kind != OUT16) {
+        if constexpr (K != OUT16)
+            for (int c = threadIdx.x; c < Dv; c += READ_ROWS_THREADS) inv_s[c] = __frcp_rn(p.ckv_scale[p.ckv_scale_per_ch ? c : 0]);
+        if (p.k_kind != OUT16 && threadIdx.x < Dk) invk_s[threadIdx.x] = __frcp_rn(p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0]);
+        __syncthreads();
+        if constexpr (K != OUT16) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(inv + i) = *reinterpret_cast<const float4*>(inv_s + lane * 16 + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(invk + i) = *reinterpret_cast<const float4*>(invk_s + eighth * 8 + i);
+    }
+    for (; t < p.T; t += warps * READ_ROWS) {
+        int64_t row[READ_ROWS];
+#pragma unroll
+        for (int k = 0; k < READ_ROWS; ++k) row[k] = __shfl_sync(0xFFFFFFFFu, mine, k);
+        const int64_t krow = __shfl_sync(0xFFFFFFFFu, mine, sub);
+        const int64_t after = t + warps * READ_ROWS + lane;
+        mine = lane < READ_ROWS && after < p.T ? read_row(p, after) : -1;
+        constexpr int NW = K == OUT16 ? 2 : 1;
+        uint4 x[READ_ROWS][NW], y = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < READ_ROWS; ++k)
+            if (row[k] >= 0) {
+                if constexpr (K == OUT16) {   // lane's halves of the row: 8 channels each
+                    x[k][0] = ld_stream_v4(static_cast<const uint16_t*>(p.ckv) + row[k] * Dv + lane * 8);
+                    x[k][1] = ld_stream_v4(static_cast<const uint16_t*>(p.ckv) + row[k] * Dv + 256 + lane * 8);
+                } else {
+                    x[k][0] = ld_stream_v4(static_cast<const uint8_t*>(p.ckv) + row[k] * Dv + lane * 16);
+                }
+            }
+        if (krow >= 0) {
+            if (p.k_kind == OUT16) {
+                y = ld_stream_v4(static_cast<const uint16_t*>(p.kc) + krow * Dk + eighth * 8);
+            } else {
+                const uint2 w = ld_stream_v2(static_cast<const uint8_t*>(p.kc) + krow * Dk + eighth * 8);
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = dec8(p.k_kind, uint8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3)))) * invk[i];
+                y = make_uint4(OT::pack(v[0], v[1]), OT::pack(v[2], v[3]), OT::pack(v[4], v[5]), OT::pack(v[6], v[7]));
+            }
+        }
+        uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride;
+#pragma unroll
+        for (int k = 0; k < READ_ROWS; ++k)
+            if (row[k] >= 0) {
+                uint16_t* o = out + k * p.out_stride;
+                if constexpr (K == OUT16) {
+                    *reinterpret_cast<uint4*>(o + lane * 8) = x[k][0];
+                    *reinterpret_cast<uint4*>(o + 256 + lane * 8) = x[k][1];
+                } else {
+                    float v[16];
+                    codes16<K>(x[k][0], v);
+                    uint32_t u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = OT::pack(v[2 * i] * inv[2 * i], v[2 * i + 1] * inv[2 * i + 1]);
+                    if (p.out_wide) {
+                        st_global_v8(o + lane * 16, u);
+                    } else {
+                        *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(o + lane * 16 + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+                    }
+                }
+            }
+        if (krow >= 0) *reinterpret_cast<uint4*>(out + sub * p.out_stride + Dv + eighth * 8) = y;
+    }
+}
+
 // Any width and alignment, element by element.
 template <class OT>
 __device__ __forceinline__ uint16_t read_one(const void* cache, int kind, int64_t at, const float* scale, bool per_ch, int c) {
@@ -89,15 +191,27 @@ __global__ void __launch_bounds__(READ_THREADS) read_generic_kernel(const __grid
     }
 }
 
-cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s) {
-    const int per = READ_THREADS / 32;
-    const int64_t cap = int64_t(sm_count_current_device()) * 16;
+template <class OT>
+static cudaError_t launch_read_t(const ReadParams& p, bool vec, cudaStream_t s) {
+    // 16 codes a load need rows on 16-byte boundaries; 8-byte ones take the narrower chunks.
+    const bool rows = vec && p.Dv == 512 && p.Dk == 64 && reinterpret_cast<uintptr_t>(p.ckv) % 16 == 0;
+    const int threads = rows ? READ_ROWS_THREADS : READ_THREADS;
+    const int64_t per = threads / 32 * (rows ? READ_ROWS : 1);
+    const int64_t cap = int64_t(sm_count_current_device()) * (rows ? 4 : 16);
     int64_t grid = (p.T + per - 1) / per;
     if (grid > cap) grid = cap;
-    const dim3 g{unsigned(grid)}, b{unsigned(READ_THREADS)};
-    if (out_dtype == KVR_BF16)
-        return vec ? launch_pdl(read_vec_kernel<BF16>, g, b, 0, s, p) : launch_pdl(read_generic_kernel<BF16>, g, b, 0, s, p);
-    return vec ? launch_pdl(read_vec_kernel<F16>, g, b, 0, s, p) : launch_pdl(read_generic_kernel<F16>, g, b, 0, s, p);
+    const dim3 g{unsigned(grid)}, b{unsigned(threads)};
+    if (rows) switch (p.ckv_kind) {
+            case OUT_I8: return launch_pdl(read_rows_kernel<OT, OUT_I8>, g, b, 0, s, p);
+            case OUT_E4M3: return launch_pdl(read_rows_kernel<OT, OUT_E4M3>, g, b, 0, s, p);
+            case OUT_E5M2: return launch_pdl(read_rows_kernel<OT, OUT_E5M2>, g, b, 0, s, p);
+            default: return launch_pdl(read_rows_kernel<OT, OUT16>, g, b, 0, s, p);
+        }
+    return vec ? launch_pdl(read_vec_kernel<OT>, g, b, 0, s, p) : launch_pdl(read_generic_kernel<OT>, g, b, 0, s, p);
+}
+
+cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s) {
+    return out_dtype == KVR_BF16 ? launch_read_t<BF16>(p, vec, s) : launch_read_t<F16>(p, vec, s);
 }
 
 }  // namespace kvr

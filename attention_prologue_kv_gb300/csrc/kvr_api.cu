@@ -756,6 +756,9 @@ kvr_status kv_cache_read(const kvr_read_args* a, cudaStream_t stream) {
     p.k_kind = a->Dk > 0 ? out_kind(a->k_dtype) : OUT16;
     p.ckv_scale_per_ch = a->ckv_scale_len == a->Dv && a->Dv > 1;
     p.k_scale_per_ch = a->k_scale_len == a->Dk && a->Dk > 1;
+    const int64_t fits = int64_t(1) << 31;
+    p.small = T < fits && a->cache_d1 < fits && rows < fits;
+    p.out_wide = aligned(a->out, 32) && stride % 16 == 0;
     const bool vec = a->Dv % 8 == 0 && a->Dk % 8 == 0 && stride % 8 == 0 && aligned(a->out, 16) &&
                      aligned(a->ckv_cache, is8(a->ckv_dtype) ? 8 : 16) &&
                      (a->Dk == 0 || aligned(a->k_cache, is8(a->k_dtype) ? 8 : 16));
@@ -811,10 +814,11 @@ kvr_status query_rope(const kvr_rope_args* a, cudaStream_t stream) {
     p.o_hs = a->out_head_stride;
     p.D = int(a->D);
     int64_t i = 0;
+    const double octaves = -2.0 * std::log2(a->base) / double(a->D);
     for (int64_t x = 0; x < a->axes; ++x)
         for (int64_t k = 0; k < a->sections[x]; ++k, ++i) {
-            // 2^64 / 2 pi * base^(-2i/D): at most 0.16 * 2^64.
-            p.step[i] = uint64_t(std::pow(a->base, -2.0 * double(i) / double(a->D)) * 2935890503282001226.0);
+            // 2^64 / 2 pi * base^(-2i/D): at most 0.16 * 2^64. (exp2 takes a third of pow's time.)
+            p.step[i] = uint64_t(std::exp2(octaves * double(i)) * 2935890503282001226.0);
             p.axis[i] = uint8_t(x);
         }
     const bool vec = a->D % 8 == 0 && aligned(a->q, 16) && aligned(a->out, 8) && aligned(a->cos_out, 8) &&

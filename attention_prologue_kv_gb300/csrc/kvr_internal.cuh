@@ -110,6 +110,13 @@ __device__ __forceinline__ int64_t ld_stream_s64(const int64_t* p) {
     return r;
 }
 
+// 32 bytes to global memory, 32-byte aligned: a whole sector from one thread.
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // mbarrier, bulk async copy (TMA engine), programmatic dependent launch
 // ---------------------------------------------------------------------------
@@ -305,8 +312,8 @@ struct RopeParams {
     void* sin;
     int64_t T, H;
     int64_t q_ts, q_hs, o_ts, o_hs;   // token and head strides in elements
-    int64_t items;       // (token, head block, chunk of a row) triples
-    int D, hb, nhb;      // row width; heads of a block, blocks of a token
+    int D;               // row width
+    int tokens;          // tokens a CTA takes at a time
     uint64_t step[128];  // turns of pair i per position, in units of 2^-64 turn
     uint8_t axis[128];   // axis of pair i
 };
@@ -323,6 +330,8 @@ struct ReadParams {
     int Dv, Dk, mode;
     int ckv_kind, k_kind;
     int ckv_scale_per_ch, k_scale_per_ch;
+    int small;           // T, S, d1 and the cache's rows fit 31 bits
+    int out_wide;        // the output's rows lie on 32-byte boundaries
 };
 
 struct MlaParams {

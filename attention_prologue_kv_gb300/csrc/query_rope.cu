@@ -11,96 +11,128 @@
 // so far positions lose nothing; read as a signed integer it is the rest in
 // [-1/2, 1/2) turn, and sincospif takes it from there.
 //
-// A stream, bound by HBM: each thread keeps one 8-channel chunk of a token's
-// row (4 angles in registers) and walks a block of heads with it: 16-byte
-// loads, two 8-byte stores a row.
+// A stream, bound by HBM. A CTA takes a few tokens at a time: one thread a
+// (token, pair) turns the angle into shared memory, then the threads take the
+// tokens' rows in order, 8 channels each: 16-byte loads, two 8-byte stores. The
+// first rows are loaded before the angles are waited for.
 #include "kvr_internal.cuh"
 
 namespace kvr {
 
-constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_BATCH = 4;      // rows of a thread in flight
+constexpr int ROPE_TOKENS = 8;     // most tokens of a CTA at a time
 
-__device__ __forceinline__ void turn(const RopeParams& p, int64_t t, int i, float& c, float& s) {
+__device__ __forceinline__ float2 turn(const RopeParams& p, int64_t t, int i) {
     const uint64_t r = uint64_t(p.positions[int64_t(p.axis[i]) * p.T + t]) * p.step[i];
-    sincospif(__ll2float_rn(int64_t(r)) * 0x1p-63f, &s, &c);   // r * 2^-64 turns = r * 2^-63 half turns
+    float2 cs;
+    sincospif(__ll2float_rn(int64_t(r)) * 0x1p-63f, &cs.y, &cs.x);   // r * 2^-64 turns = r * 2^-63 half turns
+    return cs;
 }
+
+// Where a thread is in the rows (token, head) of a batch of tokens.
+struct RopeRow {
+    int t;
+    int64_t h;
+    __device__ __forceinline__ void next(int dt, int64_t dh, int64_t H) {
+        t += dt;
+        h += dh;
+        if (h >= H) {
+            h -= H;
+            ++t;
+        }
+    }
+};
 
 // V pairs (2V channels) a thread: 4 for rows on 16-byte boundaries, 1 otherwise.
 template <class IT, bool HALF, int V>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ float2 cs[ROPE_TOKENS][128];
+    const int half = p.D / 2, nc = half / V, tid = threadIdx.x;
+    const int slots = ROPE_THREADS / nc;               // rows at a time
+    const int chunk = tid % nc, i0 = chunk * V;
+    const bool works = tid < slots * nc;
+    const int dt = int(p.H > 0 ? slots / p.H : 0);
+    const int64_t dh = p.H > 0 ? slots % p.H : 0;
     pdl_wait();
     pdl_launch_dependents();
-    const int half = p.D / 2, nc = half / V;
-    const int64_t stride = int64_t(gridDim.x) * ROPE_THREADS;
-    for (int64_t it = int64_t(blockIdx.x) * ROPE_THREADS + threadIdx.x; it < p.items; it += stride) {
-        const int64_t row = it / nc;
-        const int i0 = int(it - row * nc) * V;
-        const int64_t t = row / p.nhb;
-        const int64_t h0 = (row - t * p.nhb) * p.hb;
-        const int64_t h1 = h0 + p.hb < p.H ? h0 + p.hb : p.H;
-        float c[V], s[V];
+    for (int64_t t0 = int64_t(blockIdx.x) * p.tokens; t0 < p.T; t0 += int64_t(gridDim.x) * p.tokens) {
+        const int n = int(p.T - t0 < p.tokens ? p.T - t0 : p.tokens);
+        RopeRow at = {n, 0};
+        if (works && p.H > 0) at = {int((tid / nc) / p.H), (tid / nc) % p.H};
+        uint32_t x[ROPE_BATCH][V];   // V = 4: a row's 16 bytes (HALF: 8 and 8); V = 1: its two values
+        auto load = [&](RopeRow r) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) turn(p, t, i0 + j, c[j], s[j]);
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.q_ts;
-        uint16_t* o = static_cast<uint16_t*>(p.out) + t * p.o_ts + i0;
-        if constexpr (V == 4) {
-            if (p.cos != nullptr && h0 == 0) {
-                const uint2 cc = make_uint2(IT::pack(c[0], c[1]), IT::pack(c[2], c[3]));
-                const uint2 ss = make_uint2(IT::pack(s[0], s[1]), IT::pack(s[2], s[3]));
-                uint16_t* pc = static_cast<uint16_t*>(p.cos) + t * p.D + i0;
-                uint16_t* ps = static_cast<uint16_t*>(p.sin) + t * p.D + i0;
-                *reinterpret_cast<uint2*>(pc) = cc;
-                *reinterpret_cast<uint2*>(pc + half) = cc;
-                *reinterpret_cast<uint2*>(ps) = ss;
-                *reinterpret_cast<uint2*>(ps + half) = ss;
-            }
-#pragma unroll 4
-            for (int64_t h = h0; h < h1; ++h) {
-                float a[4], b[4];
-                if constexpr (HALF) {
-                    const uint2 x = ld_stream_v2(q + h * p.q_hs + i0), y = ld_stream_v2(q + h * p.q_hs + half + i0);
-                    a[0] = IT::lo(x.x), a[1] = IT::hi(x.x), a[2] = IT::lo(x.y), a[3] = IT::hi(x.y);
-                    b[0] = IT::lo(y.x), b[1] = IT::hi(y.x), b[2] = IT::lo(y.y), b[3] = IT::hi(y.y);
-                } else {
-                    const uint4 x = ld_stream_v4(q + h * p.q_hs + 2 * i0);
-                    a[0] = IT::lo(x.x), b[0] = IT::hi(x.x), a[1] = IT::lo(x.y), b[1] = IT::hi(x.y);
-                    a[2] = IT::lo(x.z), b[2] = IT::hi(x.z), a[3] = IT::lo(x.w), b[3] = IT::hi(x.w);
+            for (int k = 0; k < ROPE_BATCH; ++k) {
+                if (r.t < n) {
+                    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (t0 + r.t) * p.q_ts + r.h * p.q_hs;
+                    if constexpr (V == 4 && HALF) {
+                        const uint2 a = ld_stream_v2(q + i0), b = ld_stream_v2(q + half + i0);
+                        x[k][0] = a.x, x[k][1] = a.y, x[k][2] = b.x, x[k][3] = b.y;
+                    } else if constexpr (V == 4) {
+                        const uint4 a = ld_stream_v4(q + 2 * i0);
+                        x[k][0] = a.x, x[k][1] = a.y, x[k][2] = a.z, x[k][3] = a.w;
+                    } else {
+                        x[k][0] = uint32_t(q[HALF ? i0 : 2 * i0]) | uint32_t(q[HALF ? i0 + half : 2 * i0 + 1]) << 16;
+                    }
                 }
-                float u[4], v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u[j] = a[j] * c[j] - b[j] * s[j];
-                    v[j] = b[j] * c[j] + a[j] * s[j];
-                }
-                *reinterpret_cast<uint2*>(o + h * p.o_hs) = make_uint2(IT::pack(u[0], u[1]), IT::pack(u[2], u[3]));
-                *reinterpret_cast<uint2*>(o + h * p.o_hs + half) = make_uint2(IT::pack(v[0], v[1]), IT::pack(v[2], v[3]));
+                r.next(dt, dh, p.H);
             }
-        } else {
-            if (p.cos != nullptr && h0 == 0) {
-                uint16_t* pc = static_cast<uint16_t*>(p.cos) + t * p.D + i0;
-                uint16_t* ps = static_cast<uint16_t*>(p.sin) + t * p.D + i0;
-                pc[0] = pc[half] = IT::one_out(c[0]);
-                ps[0] = ps[half] = IT::one_out(s[0]);
-            }
-            for (int64_t h = h0; h < h1; ++h) {
-                const uint16_t* x = q + h * p.q_hs;
-                const float a = IT::one(x[HALF ? i0 : 2 * i0]), b = IT::one(x[HALF ? i0 + half : 2 * i0 + 1]);
-                o[h * p.o_hs] = IT::one_out(a * c[0] - b * s[0]);
-                o[h * p.o_hs + half] = IT::one_out(b * c[0] + a * s[0]);
+        };
+        load(at);
+        for (int e = tid; e < n * half; e += ROPE_THREADS) {
+            const int t = e / half, i = e - t * half;
+            const float2 v = turn(p, t0 + t, i);
+            cs[t][i] = v;
+            if (p.cos != nullptr) {
+                uint16_t* pc = static_cast<uint16_t*>(p.cos) + (t0 + t) * p.D + i;
+                uint16_t* ps = static_cast<uint16_t*>(p.sin) + (t0 + t) * p.D + i;
+                pc[0] = pc[half] = IT::one_out(v.x);
+                ps[0] = ps[half] = IT::one_out(v.y);
             }
         }
+        __syncthreads();
+        while (at.t < n) {
+#pragma unroll
+            for (int k = 0; k < ROPE_BATCH; ++k) {
+                if (at.t < n) {
+                    uint16_t* o = static_cast<uint16_t*>(p.out) + (t0 + at.t) * p.o_ts + at.h * p.o_hs + i0;
+                    if constexpr (V == 4) {
+                        float u[4], v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 c = cs[at.t][i0 + j];
+                            const float a = HALF ? ((j & 1) ? IT::hi(x[k][j >> 1]) : IT::lo(x[k][j >> 1])) : IT::lo(x[k][j]);
+                            const float b = HALF ? ((j & 1) ? IT::hi(x[k][2 + (j >> 1)]) : IT::lo(x[k][2 + (j >> 1)])) : IT::hi(x[k][j]);
+                            u[j] = a * c.x - b * c.y;
+                            v[j] = b * c.x + a * c.y;
+                        }
+                        *reinterpret_cast<uint2*>(o) = make_uint2(IT::pack(u[0], u[1]), IT::pack(u[2], u[3]));
+                        *reinterpret_cast<uint2*>(o + half) = make_uint2(IT::pack(v[0], v[1]), IT::pack(v[2], v[3]));
+                    } else {
+                        const float2 c = cs[at.t][i0];
+                        const float a = IT::lo(x[k][0]), b = IT::hi(x[k][0]);
+                        o[0] = IT::one_out(a * c.x - b * c.y);
+                        o[half] = IT::one_out(b * c.x + a * c.y);
+                    }
+                }
+                at.next(dt, dh, p.H);
+            }
+            load(at);
+        }
+        __syncthreads();   // the angles are read
     }
 }
 
 template <class IT, bool HALF, int V>
 static cudaError_t launch_rope_t(RopeParams p, cudaStream_t s) {
-    p.hb = 8;
-    p.nhb = p.H > 0 ? int((p.H + p.hb - 1) / p.hb) : 1;   // without heads: the tables alone
-    p.items = p.T * p.nhb * (p.D / 2 / V);
-    const int64_t cap = int64_t(sm_count_current_device()) * 16;
-    int64_t grid = (p.items + ROPE_THREADS - 1) / ROPE_THREADS;
-    if (grid > cap) grid = cap;
-    return launch_pdl(rope_kernel<IT, HALF, V>, dim3(unsigned(grid)), dim3(ROPE_THREADS), 0, s, p);
+    // Tokens a CTA takes at a time: 8 make one (token, pair) a thread at 64 channels; fewer where that would leave SMs
+    // without two CTAs each.
+    const int64_t sms = sm_count_current_device();
+    const int64_t t = p.T / (sms * 2);
+    p.tokens = int(t < 1 ? 1 : (t < ROPE_TOKENS ? t : ROPE_TOKENS));
+    const int64_t need = (p.T + p.tokens - 1) / p.tokens, cap = sms * 8;
+    return launch_pdl(rope_kernel<IT, HALF, V>, dim3(unsigned(need < cap ? need : cap)), dim3(ROPE_THREADS), 0, s, p);
 }
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool vec, cudaStream_t s) {

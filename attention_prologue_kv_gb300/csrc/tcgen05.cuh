@@ -51,12 +51,6 @@ __device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map,
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "r"(rank)
         : "memory");
 }
-// 32 bytes to global memory, 32-byte aligned: a whole sector from one thread.
-__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));

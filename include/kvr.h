@@ -445,8 +445,8 @@ kvr_status dynamic_quant(const kvr_dq_args* args, cudaStream_t stream);
  *                as kv_rmsnorm_rope_cache takes them.
  *
  * The angle's whole turns are dropped in 64-bit fixed point (base^(-2i/D) /
- * 2 pi is rounded once to a multiple of 2^-64, so that an angle is off by at
- * most |position| * 2^-52 turns); cos and sin of the rest are float32, each
+ * 2 pi is good to a multiple of 2^-50, so that an angle is off by at most
+ * |position| * 2^-50 turns); cos and sin of the rest are float32, each
  * output is rounded once. Limits: T, H >= 0; D even, 2 <= D <= 256;
  * 1 <= axes <= 8; T * H * D < 2^40.
  */
