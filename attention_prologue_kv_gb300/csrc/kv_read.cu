@@ -5,7 +5,7 @@
 //
 // A stream, bound by HBM. Rows of 512 + 64 channels: a warp takes four rows at
 // a time, their loads in flight together: a lane has 16 channels of each latent
-// row, whose 1 / scale it keeps in registers, and an eighth of one rotary row.
+// row and an eighth of one rotary row.
 // Other widths on 16-byte boundaries: one warp per row, chunks of 8 channels.
 #include "kvr_internal.cuh"
 
@@ -63,107 +63,120 @@ __global__ void __launch_bounds__(READ_THREADS) read_vec_kernel(const __grid_con
     }
 }
 
-// 16 codes of kind K to 16 values.
-template <int K>
-__device__ __forceinline__ void codes16(const uint4& w, float (&v)[16]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Four codes of kind K, times four factors, to two packed values.
+template <class OT, int K>
+__device__ __forceinline__ uint2 codes4(uint32_t u, const float4& f) {
+    float v[4];
+    if constexpr (K == OUT_I8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (K == OUT_I8) {
+        for (int k = 0; k < 4; ++k) v[k] = float(int8_t(u >> (8 * k)));
+    } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * i + k] = float(int8_t(u[i] >> (8 * k)));
-        } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(uint16_t(u[i] >> (16 * k)), K == OUT_E4M3 ? __NV_E4M3 : __NV_E5M2);
-                v[4 * i + 2 * k] = __half2float(__ushort_as_half(h.x));
-                v[4 * i + 2 * k + 1] = __half2float(__ushort_as_half(h.y));
-            }
+        for (int k = 0; k < 2; ++k) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(uint16_t(u >> (16 * k)), K == OUT_E4M3 ? __NV_E4M3 : __NV_E5M2);
+            v[2 * k] = __half2float(__ushort_as_half(h.x));
+            v[2 * k + 1] = __half2float(__ushort_as_half(h.y));
         }
     }
+    return make_uint2(OT::pack(v[0] * f.x, v[1] * f.y), OT::pack(v[2] * f.z, v[3] * f.w));
 }
 
 constexpr int READ_ROWS = 4;   // rows of a warp at a time
 constexpr int READ_ROWS_THREADS = 256;
 template <class OT, int K>
-__global__ void __launch_bounds__(READ_ROWS_THREADS) read_rows_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(READ_ROWS_THREADS, K == OUT16 ? 3 : 4) read_rows_kernel(const __grid_constant__ ReadParams p) {
     constexpr int Dv = 512, Dk = 64;
-    // 1 / scale, once a CTA: read by every warp of the grid from global memory it took as long as the rows.
-    __shared__ __align__(16) float inv_s[Dv];
-    __shared__ __align__(16) float invk_s[Dk];
+    // 1 / scale, once a CTA (read by every warp of the grid from global memory it took as long as the rows), four
+    // channels of lane l's 16 at [i][l]: registers for it would leave a quarter of the warps.
+    __shared__ float4 inv_s[4][32];
+    __shared__ float4 invk_s[2][8];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, eighth = lane & 7, sub = lane >> 3;
-    const int64_t warps = int64_t(gridDim.x) * (READ_ROWS_THREADS / 32);
+    const int64_t step = int64_t(gridDim.x) * (READ_ROWS_THREADS / 32) * READ_ROWS;
     int64_t t = (int64_t(blockIdx.x) * (READ_ROWS_THREADS / 32) + (threadIdx.x >> 5)) * READ_ROWS;
     int64_t mine = -1;
     if (lane < READ_ROWS && t + lane < p.T) mine = read_row(p, t + lane);
-    float inv[16], invk[8];
     if (K != OUT16 || p.k_kind != OUT16) {
         if constexpr (K != OUT16)
-            for (int c = threadIdx.x; c < Dv; c += READ_ROWS_THREADS) inv_s[c] = __frcp_rn(p.ckv_scale[p.ckv_scale_per_ch ? c : 0]);
-        if (p.k_kind != OUT16 && threadIdx.x < Dk) invk_s[threadIdx.x] = __frcp_rn(p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0]);
+            for (int c = threadIdx.x; c < Dv; c += READ_ROWS_THREADS)
+                reinterpret_cast<float*>(&inv_s[c >> 2 & 3][c >> 4])[c & 3] = __frcp_rn(p.ckv_scale[p.ckv_scale_per_ch ? c : 0]);
+        if (p.k_kind != OUT16 && threadIdx.x < Dk)
+            reinterpret_cast<float*>(&invk_s[threadIdx.x >> 2 & 1][threadIdx.x >> 3])[threadIdx.x & 3] =
+                __frcp_rn(p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0]);
         __syncthreads();
-        if constexpr (K != OUT16) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(inv + i) = *reinterpret_cast<const float4*>(inv_s + lane * 16 + i);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(invk + i) = *reinterpret_cast<const float4*>(invk_s + eighth * 8 + i);
     }
-    for (; t < p.T; t += warps * READ_ROWS) {
-        int64_t row[READ_ROWS];
-#pragma unroll
-        for (int k = 0; k < READ_ROWS; ++k) row[k] = __shfl_sync(0xFFFFFFFFu, mine, k);
-        const int64_t krow = __shfl_sync(0xFFFFFFFFu, mine, sub);
-        const int64_t after = t + warps * READ_ROWS + lane;
-        mine = lane < READ_ROWS && after < p.T ? read_row(p, after) : -1;
+#pragma unroll 1
+    for (; t < p.T; t += step) {
         constexpr int NW = K == OUT16 ? 2 : 1;
         uint4 x[READ_ROWS][NW], y = make_uint4(0, 0, 0, 0);
+        uint32_t live = 0;
 #pragma unroll
-        for (int k = 0; k < READ_ROWS; ++k)
-            if (row[k] >= 0) {
-                if constexpr (K == OUT16) {   // lane's halves of the row: 8 channels each
-                    x[k][0] = ld_stream_v4(static_cast<const uint16_t*>(p.ckv) + row[k] * Dv + lane * 8);
-                    x[k][1] = ld_stream_v4(static_cast<const uint16_t*>(p.ckv) + row[k] * Dv + 256 + lane * 8);
-                } else {
-                    x[k][0] = ld_stream_v4(static_cast<const uint8_t*>(p.ckv) + row[k] * Dv + lane * 16);
-                }
+        for (int k = 0; k < READ_ROWS; ++k) {
+            const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, k);
+            if (row < 0) continue;
+            live |= 1u << k;
+            if constexpr (K == OUT16) {   // 8 channels of each half of the row
+                const uint16_t* src = static_cast<const uint16_t*>(p.ckv) + row * Dv + lane * 8;
+                x[k][0] = ld_stream_v4(src);
+                x[k][1] = ld_stream_v4(src + 256);
+            } else {
+                x[k][0] = ld_stream_v4(static_cast<const uint8_t*>(p.ckv) + row * Dv + lane * 16);
             }
+        }
+        const int64_t krow = __shfl_sync(0xFFFFFFFFu, mine, sub);
         if (krow >= 0) {
             if (p.k_kind == OUT16) {
                 y = ld_stream_v4(static_cast<const uint16_t*>(p.kc) + krow * Dk + eighth * 8);
             } else {
                 const uint2 w = ld_stream_v2(static_cast<const uint8_t*>(p.kc) + krow * Dk + eighth * 8);
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = dec8(p.k_kind, uint8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3)))) * invk[i];
-                y = make_uint4(OT::pack(v[0], v[1]), OT::pack(v[2], v[3]), OT::pack(v[4], v[5]), OT::pack(v[6], v[7]));
+                y.x = w.x;
+                y.y = w.y;
             }
         }
+        // The next rows' index entries, while these rows come.
+        const int64_t after = t + step + lane;
+        mine = lane < READ_ROWS && after < p.T ? read_row(p, after) : -1;
         uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride;
+        if constexpr (K == OUT16) {
 #pragma unroll
-        for (int k = 0; k < READ_ROWS; ++k)
-            if (row[k] >= 0) {
-                uint16_t* o = out + k * p.out_stride;
-                if constexpr (K == OUT16) {
-                    *reinterpret_cast<uint4*>(o + lane * 8) = x[k][0];
-                    *reinterpret_cast<uint4*>(o + 256 + lane * 8) = x[k][1];
-                } else {
-                    float v[16];
-                    codes16<K>(x[k][0], v);
+            for (int k = 0; k < READ_ROWS; ++k)
+                if (live >> k & 1) {
+                    *reinterpret_cast<uint4*>(out + k * p.out_stride + lane * 8) = x[k][0];
+                    *reinterpret_cast<uint4*>(out + k * p.out_stride + 256 + lane * 8) = x[k][1];
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < READ_ROWS; ++k)
+                if (live >> k & 1) {
+                    uint16_t* o = out + k * p.out_stride + lane * 16;
+                    const uint32_t w[4] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w};
                     uint32_t u[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = OT::pack(v[2 * i] * inv[2 * i], v[2 * i + 1] * inv[2 * i + 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 z = codes4<OT, K>(w[i], inv_s[i][lane]);
+                        u[2 * i] = z.x;
+                        u[2 * i + 1] = z.y;
+                    }
                     if (p.out_wide) {
-                        st_global_v8(o + lane * 16, u);
+                        st_global_v8(o, u);
                     } else {
-                        *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(u[0], u[1], u[2], u[3]);
-                        *reinterpret_cast<uint4*>(o + lane * 16 + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+                        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(o + 8) = make_uint4(u[4], u[5], u[6], u[7]);
                     }
                 }
+        }
+        if (krow >= 0) {
+            if (p.k_kind != OUT16) {
+                uint2 a, b;
+                const float4 f = invk_s[0][eighth], g = invk_s[1][eighth];
+                if (p.k_kind == OUT_I8) a = codes4<OT, OUT_I8>(y.x, f), b = codes4<OT, OUT_I8>(y.y, g);
+                else if (p.k_kind == OUT_E4M3) a = codes4<OT, OUT_E4M3>(y.x, f), b = codes4<OT, OUT_E4M3>(y.y, g);
+                else a = codes4<OT, OUT_E5M2>(y.x, f), b = codes4<OT, OUT_E5M2>(y.y, g);
+                y = make_uint4(a.x, a.y, b.x, b.y);
             }
-        if (krow >= 0) *reinterpret_cast<uint4*>(out + sub * p.out_stride + Dv + eighth * 8) = y;
+            *reinterpret_cast<uint4*>(out + sub * p.out_stride + Dv + eighth * 8) = y;
+        }
     }
 }
 
