@@ -61,7 +61,7 @@ struct Seq {
     int L, K;   // L = 0: nothing to do
 };
 
-struct Misc {
+struct alignas(16) Misc {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t s_full[2], p_full, pv_done, q_full, q_free, k_fix, v_fix, drain;
     uint32_t tmem;
@@ -73,7 +73,7 @@ struct Misc {
     uint32_t held[MAX_STAGES][2];   // keys of a step that exist: bit i of a half for its key i
     float inv_k[64], lift;   // 1 / scale of the rotary channels; a power of two taken out of their queries
 };
-struct Scales {              // behind Misc, with codes
+struct alignas(16) Scales {              // behind Misc, with codes
     float inv_v[512];        // 1 / scale of a channel
     float row_mul[2][64];    // power of two taken out of a row's queries, of this part and the next
 };
@@ -246,11 +246,11 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
     if (tid == 0 && cluster_rank() == 0) ws_space(p).bounds[pair] = m->begin;
 }
 
-// Four 8-bit codes to packed 16-bit values (exact in either type).
-template <class IT>
-__device__ __forceinline__ uint2 dec8x4(int kind, uint32_t u) {
+// Four 8-bit codes of kind K to halves, exactly.
+template <int K>
+__device__ __forceinline__ uint2 codes_to_halves(uint32_t u) {
     uint32_t h[2];
-    if (kind == OUT_I8) {   // 1024 + (code + 128) as a half, less 1152
+    if constexpr (K == OUT_I8) {   // 1024 + (code + 128) as a half, less 1152
         u ^= 0x80808080u;
         const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
 #pragma unroll
@@ -259,7 +259,7 @@ __device__ __forceinline__ uint2 dec8x4(int kind, uint32_t u) {
             __half2 r = __hsub2(*reinterpret_cast<__half2*>(&x), off);
             h[k] = *reinterpret_cast<uint32_t*>(&r);
         }
-    } else if (kind == OUT_E5M2) {   // the upper byte of a half
+    } else if constexpr (K == OUT_E5M2) {   // the upper byte of a half
         h[0] = __byte_perm(u, 0, 0x1404);
         h[1] = __byte_perm(u, 0, 0x3424);
     } else {
@@ -267,16 +267,21 @@ __device__ __forceinline__ uint2 dec8x4(int kind, uint32_t u) {
             : "=r"(h[0]), "=r"(h[1])
             : "r"(u));
     }
-    if constexpr (IT::is_bf16) {
-        return make_uint2(BF16::pack(F16::lo(h[0]), F16::hi(h[0])), BF16::pack(F16::lo(h[1]), F16::hi(h[1])));
-    } else {
-        return make_uint2(h[0], h[1]);
-    }
+    return make_uint2(h[0], h[1]);
 }
+template <int K>
+__device__ __forceinline__ uint4 codes_to_halves(uint32_t a, uint32_t b) {
+    const uint2 x = codes_to_halves<K>(a), y = codes_to_halves<K>(b);
+    return make_uint4(x.x, x.y, y.x, y.y);
+}
+// Eight codes of a runtime kind to values of type IT (the rotary part's).
 template <class IT>
 __device__ __forceinline__ uint4 dec8x8(int kind, uint32_t a, uint32_t b) {
-    const uint2 x = dec8x4<IT>(kind, a), y = dec8x4<IT>(kind, b);
-    return make_uint4(x.x, x.y, y.x, y.y);
+    const uint4 h = kind == OUT_I8 ? codes_to_halves<OUT_I8>(a, b)
+                                   : (kind == OUT_E5M2 ? codes_to_halves<OUT_E5M2>(a, b) : codes_to_halves<OUT_E4M3>(a, b));
+    if constexpr (!IT::is_bf16) return h;
+    return make_uint4(BF16::pack(F16::lo(h.x), F16::hi(h.x)), BF16::pack(F16::lo(h.y), F16::hi(h.y)),
+                      BF16::pack(F16::lo(h.z), F16::hi(h.z)), BF16::pack(F16::lo(h.w), F16::hi(h.w)));
 }
 
 // Cache row of a key, or -1 where there is none to read.
@@ -584,136 +589,203 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
     }
 }
 
-// Four warps decode a CTA's 8-bit rows into halves (the rotary part into q's type).
-// Thread (key tk, quarter c4): 16 codes a load, the next step's loads in flight.
-template <class IT, bool SWAP>
-__device__ __forceinline__ void code_warps(Ctx& c, int v, Walk& w, int& j) {
+// 8-bit latent rows, decoded into halves (the rotary part into q's type): a lane has 16 codes, a quarter of a box, of one
+// of 8 rows, so that a warp's stores fill the banks. The next step's loads are in flight meanwhile.
+// Four warps bring a CTA's own 32 keys.
+template <class IT, int CK>
+__device__ __forceinline__ void code_keys(Ctx& c, int v) {
+    constexpr int STAGES = stages_of<true>();
     const MlaParams& p = c.p;
     Misc* m = c.m;
-    const int tk = v >> 2, c4 = v & 3;
-    constexpr int STAGES = stages_of<true>();
-    constexpr int NX = SWAP ? 4 : 8;
+    const int lane = c.lane, tk = v >> 2, c4 = v & 3;
     const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16;
-    uint4 x[NX], y[NX], xr[2], yr[2];
-    const int mine = int(SWAP ? c.rank ^ 1 : c.rank), halves = SWAP ? 1 << mine : 3;
+    const uint32_t at0 = box_at(0, tk, 2 * c4), at1 = box_at(0, tk, 2 * c4 + 1);   // this lane's places in a box
+    int j = 0;
     Rows rows(p);
-    rows.begin(w, c.lane, tk, halves);
-    uint32_t held = 0, next = 0;   // this warp's 8 keys of this CTA (byte 0) and of the other (byte 1) that exist: this step, the next
-    auto bits = [](uint32_t b) {   // every fourth bit
-        b &= 0x11111111u;
-        b = (b | b >> 3) & 0x03030303u;
-        b = (b | b >> 6) & 0x000F000Fu;
-        return (b | b >> 12) & 0xFFu;
-    };
-    auto load = [&](int kt, uint4 (&a)[NX], uint4 (&ar)[2]) {
-        const int64_t lo = rows.row<0>(kt, tk), hi = rows.row<1>(kt, tk), slot = mine ? hi : lo;
-        rows.next(kt, c.lane, tk, halves);
-        if (!SWAP) next = bits(__ballot_sync(0xFFFFFFFFu, slot >= 0)) | bits(__ballot_sync(0xFFFFFFFFu, (mine ? lo : hi) >= 0)) << 8;
-        const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (slot < 0 ? 0 : slot) * p.Dv;
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int q = SWAP ? ((i >> 1) * 4 + int(c.rank) * 2 + (i & 1)) * 4 + c4 : c4 + 4 * i;
-            a[i] = slot >= 0 && q < nc ? ld_stream_v4(src + q * 16) : make_uint4(0, 0, 0, 0);
-        }
-        if (!SWAP) {
-            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + (slot < 0 ? 0 : slot) * p.Dk * (p.k_kind == OUT16 ? 2 : 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int q = c4 + 4 * i;
-                ar[i] = slot >= 0 && q < nr ? ld_stream_v4(k + q * 16) : make_uint4(0, 0, 0, 0);
-            }
-        }
-    };
-    load(w.kt0, x, xr);
-    held = next;
+    Walk w(p, m);
 #pragma unroll 1
-    for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-        if (kt + 1 < w.kt1) load(kt + 1, y, yr);
-        const int st = j % STAGES;
-        const uint32_t stage = c.stage(st);
-        if (SWAP) c.wait(&m->s_full[j & 1], (j >> 1) & 1);
-        else if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+    while (w.next()) {
+        uint4 x[8], y[8], xr[2], yr[2];
+        const int kt1 = w.kt1;
+        rows.begin(w, lane, tk, 3);
+        uint32_t held = 0, next = 0;   // this warp's 8 keys of this CTA (byte 0) and of the other (byte 1) that exist
+        auto bits = [](uint32_t b) {   // every fourth bit
+            b &= 0x11111111u;
+            b = (b | b >> 3) & 0x03030303u;
+            b = (b | b >> 6) & 0x000F000Fu;
+            return (b | b >> 12) & 0xFFu;
+        };
+        auto load = [&](int kt, uint4 (&a)[8], uint4 (&ar)[2]) {
+            const int64_t lo = rows.row<0>(kt, tk), hi = rows.row<1>(kt, tk), slot = c.rank ? hi : lo;
+            rows.next(kt, lane, tk, 3);
+            next = bits(__ballot_sync(0xFFFFFFFFu, slot >= 0)) | bits(__ballot_sync(0xFFFFFFFFu, (c.rank ? lo : hi) >= 0)) << 8;
+            const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (slot < 0 ? 0 : slot) * p.Dv + c4 * 16;
+            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + (slot < 0 ? 0 : slot) * p.Dk * (p.k_kind == OUT16 ? 2 : 1) + c4 * 16;
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int b = SWAP ? (i >> 1) * 4 + int(c.rank ^ 1) * 2 + (i & 1) : i;
-            if ((SWAP ? (i >> 1) * 4 + int(c.rank) * 2 + (i & 1) : i) >= c.nb) continue;
-            const uint32_t box = stage + uint32_t(b) * KBOX;
-            st_shared_v4(box_at(box, tk, 2 * c4), dec8x8<F16>(p.ckv_kind, x[i].x, x[i].y));
-            st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<F16>(p.ckv_kind, x[i].z, x[i].w));
-        }
-        if (!SWAP) {
-            if (c.lane == 0) {
-                reinterpret_cast<uint8_t*>(&m->held[st][mine])[v >> 5] = uint8_t(held);
-                reinterpret_cast<uint8_t*>(&m->held[st][mine ^ 1])[v >> 5] = uint8_t(held >> 8);
+            for (int i = 0; i < 8; ++i) a[i] = slot >= 0 && c4 + 4 * i < nc ? ld_stream_v4(src + 64 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ar[i] = slot >= 0 && c4 + 4 * i < nr ? ld_stream_v4(k + 64 * i) : make_uint4(0, 0, 0, 0);
+        };
+        load(w.kt0, x, xr);
+        held = next;
+#pragma unroll 1
+        for (int kt = w.kt0; kt < kt1; ++kt, ++j) {
+            if (kt + 1 < kt1) load(kt + 1, y, yr);
+            const int st = j % STAGES;
+            const uint32_t stage = c.stage(st);
+            if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i >= c.nb) break;
+                st_shared_v4(stage + i * KBOX + at0, codes_to_halves<CK>(x[i].x, x[i].y));
+                st_shared_v4(stage + i * KBOX + at1, codes_to_halves<CK>(x[i].z, x[i].w));
             }
             const uint32_t box = stage + 8 * KBOX;
             if (p.k_kind == OUT16) {
                 st_shared_v4(box_at(box, tk, c4), xr[0]);
                 st_shared_v4(box_at(box, tk, c4 + 4), xr[1]);
             } else {
-                st_shared_v4(box_at(box, tk, 2 * c4), dec8x8<IT>(p.k_kind, xr[0].x, xr[0].y));
-                st_shared_v4(box_at(box, tk, 2 * c4 + 1), dec8x8<IT>(p.k_kind, xr[0].z, xr[0].w));
+                st_shared_v4(box + at0, dec8x8<IT>(p.k_kind, xr[0].x, xr[0].y));
+                st_shared_v4(box + at1, dec8x8<IT>(p.k_kind, xr[0].z, xr[0].w));
             }
-        }
-        c.arrive(SWAP ? &m->v_full[st] : &m->k_full[st]);
+            if (lane == 0) {
+                reinterpret_cast<uint8_t*>(&m->held[st][c.rank])[v >> 5] = uint8_t(held);
+                reinterpret_cast<uint8_t*>(&m->held[st][c.rank ^ 1])[v >> 5] = uint8_t(held >> 8);
+            }
+            c.arrive(&m->k_full[st]);
 #pragma unroll
-        for (int i = 0; i < NX; ++i) x[i] = y[i];
-        xr[0] = yr[0];
-        xr[1] = yr[1];
-        held = next;
+            for (int i = 0; i < 8; ++i) x[i] = y[i];
+            xr[0] = yr[0];
+            xr[1] = yr[1];
+            held = next;
+        }
     }
 }
 
-// Four warps bring the queries of a part: lane v & 7 has chunk v & 7 of each box of row v / 8.
+// Three warps bring the other CTA's keys of a part (this CTA's channels): 16 pieces of 8 rows of a box, in turn.
+template <int CK>
+__device__ __forceinline__ void code_swaps(Ctx& c, int v, const Walk& w, int& j) {
+    constexpr int STAGES = stages_of<true>(), TURNS = 6;
+    const MlaParams& p = c.p;
+    Misc* m = c.m;
+    const int lane = c.lane, wp = v >> 5, theirs = int(c.rank ^ 1);
+    uint4 x[TURNS], y[TURNS];
+    Rows rows(p);
+    rows.begin(w, lane, lane, 1 << theirs);
+    auto load = [&](int kt, uint4 (&a)[TURNS]) {
+        const int64_t slot = theirs ? rows.row<1>(kt, lane) : rows.row<0>(kt, lane);
+        rows.next(kt, lane, lane, 1 << theirs);
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int piece = wp + 3 * i, b = piece & 3, row = (piece >> 2) * 8 + (lane >> 2);
+            const int64_t r = __shfl_sync(0xFFFFFFFFu, slot, row & 31);
+            const int q = ((b >> 1) * 4 + int(c.rank) * 2 + (b & 1)) * 64 + (lane & 3) * 16;   // first channel
+            a[i] = piece < 16 && r >= 0 && q < p.Dv ? ld_stream_v4(static_cast<const uint8_t*>(p.ckv) + r * p.Dv + q) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(w.kt0, x);
+#pragma unroll 1
+    for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
+        if (kt + 1 < w.kt1) load(kt + 1, y);
+        const int st = j % STAGES;
+        const uint32_t stage = c.stage(st);
+        c.wait(&m->s_full[j & 1], (j >> 1) & 1);
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int piece = wp + 3 * i, b = piece & 3, row = (piece >> 2) * 8 + (lane >> 2);
+            if (piece >= 16) break;
+            const uint32_t box = stage + uint32_t((b >> 1) * 4 + theirs * 2 + (b & 1)) * KBOX;
+            st_shared_v4(box_at(box, row, 2 * (lane & 3)), codes_to_halves<CK>(x[i].x, x[i].y));
+            st_shared_v4(box_at(box, row, 2 * (lane & 3) + 1), codes_to_halves<CK>(x[i].z, x[i].w));
+        }
+        c.arrive(&m->v_full[st]);
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) x[i] = y[i];
+    }
+}
+
+// The query warps (four; three with codes) bring the queries of a part: lane v & 7 has chunk v & 7 of each box of a row.
 template <class IT, bool C8>
 __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int part) {
+    constexpr int AT_ONCE = C8 ? 12 : 16, TURNS = C8 ? 6 : 4;   // rows of a turn
     const MlaParams& p = c.p;
     Misc* m = c.m;
     const int nc = p.Dv / 8, nr = p.Dk / 8, ch = v & 7;
-    const uint16_t *qns[4], *qrs[4];
-    uint32_t lives = 0;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + it * 16 + (v >> 3);
-        const bool live = row < unsigned(w.s.L) * unsigned(p.H);
+    const bool per_rope = p.k_kind != OUT16 && p.k_scale_per_ch;
+    auto row_of = [&](int turn, const uint16_t*& qn, const uint16_t*& qr) {
+        const int r = turn * AT_ONCE + (v >> 3);
+        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
+        const bool live = r < CROWS && row < unsigned(w.s.L) * unsigned(p.H);
         const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
-        qns[it] = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
-        qrs[it] = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
-        lives |= uint32_t(live) << it;
-    }
-    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+        qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs + ch * 8;
+        qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + ch * 8;
+        return live;
+    };
+    // The rotary part keeps q's type; a scale per channel goes in with one rounding, over the largest 1 / scale (as a
+    // power of two, put back into the scores).
+    auto rope = [&](const uint16_t* qr, bool live, int r) {
+        uint4 x = live && ch < nr ? ld_stream_v4(qr) : make_uint4(0, 0, 0, 0);
+        if (per_rope) {
+            uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+            const float* f = m->inv_k + ch * 8;
+            const float g = 1.f / m->lift;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int r = it * 16 + (v >> 3);
-        const bool live = lives >> it & 1;
-        const uint16_t *qn = qns[it], *qr = qrs[it];
-        if constexpr (!C8) {
-            const bool scaled = p.k_kind != OUT16 && p.k_scale_per_ch;
+            for (int k = 0; k < 4; ++k) u[k] = IT::pack(IT::lo(u[k]) * (f[2 * k] * g), IT::hi(u[k]) * (f[2 * k + 1] * g));
+        }
+        st_shared_v4(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), x);
+    };
+    if constexpr (!C8) {
+        const uint16_t *qn[TURNS], *qr[TURNS];
+        uint32_t lives = 0;
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) lives |= uint32_t(row_of(i, qn[i], qr[i])) << i;
+        if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int r = i * AT_ONCE + (v >> 3);
+            const bool live = lives >> i & 1;
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-                const int q = b * 8 + ch;
-                if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), live && q < nc ? qn + q * 8 : qn, live && q < nc);
+                const bool in = live && b * 8 + ch < nc;
+                if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), in ? qn[i] + b * 64 : qn[i], in);
             }
-            if (!scaled) cp_async16(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), live && ch < nr ? qr + ch * 8 : qr, live && ch < nr);
-        } else {
-            // Halves of q / scale: 11 bits keep the rounding of the one product that has to be rounded small. A power
-            // of two per row, put back into its scores, brings the largest to [2^13, 2^14): float16's range then
-            // reaches 2^-38 below it.
-            const bool per = p.ckv_scale_per_ch;
+            if (!per_rope) cp_async16(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), qr[i], live && ch < nr);
+        }
+        cp_async_commit();
+        if (per_rope) {
+#pragma unroll 1
+            for (int i = 0; i < TURNS; ++i) {
+                const bool live = row_of(i, qn[0], qr[0]);
+                rope(qr[0], live, i * AT_ONCE + (v >> 3));
+            }
+        }
+        cp_async_wait<0>();
+    } else {
+        // Halves of q / scale: 11 bits keep the rounding of the one product that has to be rounded small. A power of two
+        // per row, put back into its scores, brings the largest to [2^13, 2^14): float16's range then reaches 2^-38
+        // below it.
+        const bool per = p.ckv_scale_per_ch;
+        if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+#pragma unroll 1
+        for (int i = 0; i < TURNS; ++i) {
+            const int r = i * AT_ONCE + (v >> 3);
+            if (i * AT_ONCE + (v >> 5) * 4 >= CROWS) break;   // the warp's rows end (they do together: 4 a warp)
+            const uint16_t *qn, *qr;
+            const bool live = row_of(i, qn, qr);
             uint4 x[8];
             float top = 0.f;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const int q = b * 8 + ch;
-                x[b] = live && q < nc ? ld_stream_v4(qn + q * 8) : make_uint4(0, 0, 0, 0);
-            }
+            for (int b = 0; b < 8; ++b) x[b] = live && b * 8 + ch < nc ? ld_stream_v4(qn + b * 64) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
                 const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
-                const float* f = c.sc->inv_v + b * 64 + ch * 8;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top = fmaxf(top, fmaxf(fabsf(IT::lo(u[k]) * (per ? f[2 * k] : 1.f)), fabsf(IT::hi(u[k]) * (per ? f[2 * k + 1] : 1.f))));
+                float4 f0 = make_float4(1.f, 1.f, 1.f, 1.f), f1 = f0;
+                if (per) {
+                    f0 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8);
+                    f1 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8 + 4);
+                }
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(IT::lo(u[0]) * f0.x), fabsf(IT::hi(u[0]) * f0.y)), fmaxf(fabsf(IT::lo(u[1]) * f0.z), fabsf(IT::hi(u[1]) * f0.w))));
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(IT::lo(u[2]) * f1.x), fabsf(IT::hi(u[2]) * f1.y)), fmaxf(fabsf(IT::lo(u[3]) * f1.z), fabsf(IT::hi(u[3]) * f1.w))));
             }
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -723,29 +795,19 @@ __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int p
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
                 const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
-                const float* f = c.sc->inv_v + b * 64 + ch * 8;
-                uint32_t z[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) z[k] = F16::pack(IT::lo(u[k]) * (per ? f[2 * k] : 1.f) * g, IT::hi(u[k]) * (per ? f[2 * k + 1] : 1.f) * g);
-                if (b < c.nb) st_shared_v4(box_at(c.base + OFF_Q + b * QBOX, r, ch), make_uint4(z[0], z[1], z[2], z[3]));
+                float4 f0 = make_float4(1.f, 1.f, 1.f, 1.f), f1 = f0;
+                if (per) {
+                    f0 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8);
+                    f1 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8 + 4);
+                }
+                if (b < c.nb)
+                    st_shared_v4(box_at(c.base + OFF_Q + b * QBOX, r, ch),
+                                 make_uint4(F16::pack(IT::lo(u[0]) * f0.x * g, IT::hi(u[0]) * f0.y * g), F16::pack(IT::lo(u[1]) * f0.z * g, IT::hi(u[1]) * f0.w * g),
+                                            F16::pack(IT::lo(u[2]) * f1.x * g, IT::hi(u[2]) * f1.y * g), F16::pack(IT::lo(u[3]) * f1.z * g, IT::hi(u[3]) * f1.w * g)));
             }
-        }
-        if (C8 || (p.k_kind != OUT16 && p.k_scale_per_ch)) {
-            // The rotary part keeps q's type; a scale per channel goes in with one rounding, over the largest
-            // 1 / scale (as a power of two, put back into the scores).
-            uint4 x = live && ch < nr ? ld_stream_v4(qr + ch * 8) : make_uint4(0, 0, 0, 0);
-            if (p.k_kind != OUT16 && p.k_scale_per_ch) {
-                uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-                const float* f = m->inv_k + ch * 8;
-                const float g = 1.f / m->lift;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) u[k] = IT::pack(IT::lo(u[k]) * (f[2 * k] * g), IT::hi(u[k]) * (f[2 * k + 1] * g));
-            }
-            st_shared_v4(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), x);
+            rope(qr, live, r);
         }
     }
-    cp_async_commit();
-    cp_async_wait<0>();
     c.arrive(&m->q_full);
 }
 
@@ -761,21 +823,17 @@ __device__ __forceinline__ void prefetch_queries(Ctx& c, int v, const Walk& w) {
     if ((v & 1) == 0) prefetch_l2(static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs);
 }
 
-// Groups of four softmax warps: two where registers allow (16-bit rows). A lone warp of a scheduler goes at about 5
-// cycles an instruction, so what a warp has to do sets the time of a step's softmax and of a part's output.
-template <bool C8>
-constexpr int groups_of() { return C8 ? 1 : 2; }
-template <bool C8>
-__device__ __forceinline__ void softmax_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(128 * groups_of<C8>()) : "memory");
-}
+// Two groups of four softmax warps: a lone warp of a scheduler goes at about 5 cycles an instruction, so what a warp has
+// to do sets the time of a step's softmax and of a part's output.
+constexpr int GROUPS = 2;
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(128 * GROUPS) : "memory"); }
 
 // Output of a part (a row tile of a sequence), by the softmax warps: thread (row r, half h of the channels; group g has
 // half of the 256 columns). Each thread writes its row's sectors itself, with few instructions: through shared memory, for
 // whole lines, took more of them and longer (7000 cycles a part against 5000).
 template <class IT, bool C8>
 __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part, const Walk& w, unsigned row, bool live, float2 ml) {
-    constexpr int G = groups_of<C8>();
+    constexpr int G = GROUPS;
     const MlaParams& p = c.p;
     const int r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
     const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
@@ -847,26 +905,18 @@ __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part,
     tc_fence_before();
 }
 
-// Over the threads of row r, always in this order.
-template <int G>
-__device__ __forceinline__ float row_max(const float* x, int r) {
-    const float v = fmaxf(x[r], x[r + 64]);
-    return G == 1 ? v : fmaxf(v, fmaxf(x[r + 128], x[r + 192]));
-}
-template <int G>
-__device__ __forceinline__ float row_sum(const float* x, int r) {
-    const float v = x[r] + x[r + 64];
-    return G == 1 ? v : v + (x[r + 128] + x[r + 192]);
-}
+// Over the four threads of row r, always in this order.
+__device__ __forceinline__ float row_max(const float* x, int r) { return fmaxf(fmaxf(x[r], x[r + 64]), fmaxf(x[r + 128], x[r + 192])); }
+__device__ __forceinline__ float row_sum(const float* x, int r) { return (x[r] + x[r + 64]) + (x[r + 128] + x[r + 192]); }
 
 // Softmax: thread (row r, half h of the keys, group g: half of that half).
 template <class IT, bool C8, bool K8>
 __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     using PT = typename std::conditional<C8, F16, IT>::type;   // type of the weights and the decoded codes
-    constexpr int G = groups_of<C8>(), NK = CKEYS / G;          // keys of a thread
+    constexpr int G = GROUPS, NK = CKEYS / G;          // keys of a thread
     const MlaParams& p = c.p;
     Misc* m = c.m;
-    const int lane = c.lane, r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
+    const int r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
     const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
     constexpr bool split = C8 || K8;
     // Score = fn * (latent product) + fr * (rotary product), in powers of two.
@@ -917,8 +967,8 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
 #pragma unroll
             for (int i = 1; i < NK; ++i) top = fmaxf(top, s[i]);
             red[tid] = top;
-            softmax_sync<C8>();
-            top = fmaxf(row_max<G>(red, r), mx);
+            softmax_sync();
+            top = fmaxf(row_max(red, r), mx);
             // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
             // and the 16-bit rounding of a weight is relative.
             const bool grow = top > mx + 8.f;
@@ -961,9 +1011,9 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         // The rows' m and l for the output.
         float* red = m->red[j & 1];
         red[tid] = sum;   // the next step's buffer: its own maxima come after the second barrier
-        softmax_sync<C8>();
-        const float2 ml = make_float2(mx, row_sum<G>(red, r));
-        softmax_sync<C8>();
+        softmax_sync();
+        const float2 ml = make_float2(mx, row_sum(red, r));
+        softmax_sync();
         c.wait(&m->pv_done, (j - 1) & 1);
         tc_fence_after();
         output_part<IT, C8>(c, tid, pair, part, w, row, live, ml);
@@ -971,16 +1021,17 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     }
 }
 
-// Four warps: queries of a part (and, with codes, its swaps).
-template <class IT, bool C8>
+// The query warps: queries of a part and, with codes, its swaps.
+template <class IT, int CK>
 __device__ __forceinline__ void query_warps(Ctx& c, int v) {
+    constexpr bool C8 = CK != OUT16;
     Walk w(c.p, c.m);
     int j = 0;
     bool more = w.next();
 #pragma unroll 1
     for (int part = 0; more; ++part) {
         load_queries<IT, C8>(c, v, w, part);
-        if (C8) code_warps<IT, true>(c, v, w, j);
+        if constexpr (C8) code_swaps<CK>(c, v, w, j);
         more = w.next();
         if (!C8 && more) prefetch_queries(c, v, w);
     }
@@ -1061,17 +1112,17 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
     }
 }
 
-// Warps: first the softmax's (8; 4 with codes). Then, 16-bit latent rows: 8 keys, 9 swap, 10 MMA, 12-15 queries; codes: 4-7
-// keys, 8-11 queries and swap, 12 MMA.
-template <bool C8>
-constexpr int threads_of() { return C8 ? 416 : 512; }
+// Warps: 0-7 softmax. 16-bit latent rows: 8 keys, 9 swap, 10 MMA, 12-15 queries; codes: 8-11 keys, 12-14 queries and
+// swap, 15 MMA.
+constexpr int NT = 512;
 
-template <class IT, bool C8, bool K8>
-__global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
+// CK: OutKind of the latent rows; K8: the rotary ones are codes.
+template <class IT, int CK, bool K8>
+__global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     mla_tc_kernel(const __grid_constant__ MlaParams p, const __grid_constant__ Maps maps) {
+    constexpr bool C8 = CK != OUT16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];   // the swizzle repeats every 1024 bytes
-    constexpr int NT = threads_of<C8>();
-    constexpr int MMA_WARP = C8 ? 12 : 10;
+    constexpr int MMA_WARP = C8 ? 15 : 10;
     const uint32_t base = smem_u32(smem_raw);
     constexpr int STAGES = stages_of<C8>();
     Misc* m = reinterpret_cast<Misc*>(smem_raw + OFF_K + STAGES * STAGE_BYTES);
@@ -1088,14 +1139,14 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&m->k_full[s], C8 ? 8 : 2);
-            mbar_init(&m->v_full[s], C8 ? 8 : 2);
+            mbar_init(&m->v_full[s], C8 ? 6 : 2);
             mbar_init(&m->empty[s], 1);
         }
         mbar_init(&m->s_full[0], 1);
         mbar_init(&m->s_full[1], 1);
-        mbar_init(&m->p_full, 8 * groups_of<C8>());
+        mbar_init(&m->p_full, 8 * GROUPS);
         mbar_init(&m->pv_done, 1);
-        mbar_init(&m->q_full, 8);
+        mbar_init(&m->q_full, C8 ? 6 : 8);
         mbar_init(&m->q_free, 1);
         mbar_init(&m->k_fix, 1);
         mbar_init(&m->v_fix, 1);
@@ -1132,19 +1183,13 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = m->tmem;
     Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
 
-    if (warp < 4 * groups_of<C8>()) {
+    if (warp < 4 * GROUPS) {
         softmax_warps<IT, C8, K8>(c, tid, pair);
     } else if (warp == MMA_WARP) {
         if (rank == 0) mma_warp<IT, C8, K8>(c);
     } else if constexpr (C8) {
-        if (warp < 8) {
-            Walk w(p, m);
-            int j = 0;
-#pragma unroll 1
-            while (w.next()) code_warps<IT, false>(c, tid - 128, w, j);
-        } else {
-            query_warps<IT, true>(c, tid - 256);
-        }
+        if (warp < 12) code_keys<IT, CK>(c, tid - 256);
+        else query_warps<IT, CK>(c, tid - 384);
     } else {
         if (warp == 8) {
             if (!K8 && p.box_rows == CKEYS) key_warp_tma<false>(c, maps);
@@ -1153,7 +1198,7 @@ __global__ void __launch_bounds__(threads_of<C8>(), 1) __cluster_dims__(2, 1, 1)
             if (!K8 && p.box_rows == CKEYS) key_warp_tma<true>(c, maps);
             else key_warp<IT, K8, true>(c, maps);
         } else if (warp >= 12) {
-            query_warps<IT, false>(c, tid - 384);
+            query_warps<IT, CK>(c, tid - 384);
         }
     }
     if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
@@ -1244,10 +1289,21 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_c
 
 }  // namespace
 
-template <class IT, bool C8, bool K8>
-static cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(mla_tc_kernel<IT, C8, K8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<C8>());
+// The kernel for a type and cache kinds, as a launch takes it.
+using MlaKernel = void (*)(MlaParams, Maps);
+template <class IT, int CK>
+static MlaKernel kernel_of_k(bool k8) { return k8 ? MlaKernel(mla_tc_kernel<IT, CK, true>) : MlaKernel(mla_tc_kernel<IT, CK, false>); }
+template <class IT>
+static MlaKernel kernel_of_ck(int ck, bool k8) {
+    switch (ck) {
+        case OUT_I8: return kernel_of_k<IT, OUT_I8>(k8);
+        case OUT_E4M3: return kernel_of_k<IT, OUT_E4M3>(k8);
+        case OUT_E5M2: return kernel_of_k<IT, OUT_E5M2>(k8);
+        default: return kernel_of_k<IT, OUT16>(k8);
+    }
 }
+static MlaKernel kernel_of(int dtype, int ck, bool k8) { return dtype == KVR_BF16 ? kernel_of_ck<BF16>(ck, k8) : kernel_of_ck<F16>(ck, k8); }
+static uint32_t smem_for(int ck) { return ck == OUT16 ? smem_of<false>() : smem_of<true>(); }
 
 // CTA pairs that fit on the current device at once (a GPC with an odd number of
 // SMs leaves one over); looked up once per device, as is the shared memory allowed.
@@ -1264,20 +1320,21 @@ static int mla_tc_pairs() {
         int n = 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(sm_count_current_device()) / 2 * 2);
-        cfg.blockDim = dim3(threads_of<false>());
-        cfg.dynamicSmemBytes = smem_of<false>();
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = smem_for(OUT16);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e[] = {allow_smem<BF16, false, false>(), allow_smem<BF16, false, true>(), allow_smem<BF16, true, false>(),
-                                 allow_smem<BF16, true, true>(), allow_smem<F16, false, false>(), allow_smem<F16, false, true>(),
-                                 allow_smem<F16, true, false>(), allow_smem<F16, true, true>()};
         bool good = true;
-        for (const cudaError_t x : e) good = good && x == cudaSuccess;
-        good = good && cudaOccupancyMaxActiveClusters(&n, mla_tc_kernel<BF16, false, false>, &cfg) == cudaSuccess && n > 0;
+        for (int dtype : {KVR_BF16, KVR_F16})
+            for (int ck : {OUT16, OUT_I8, OUT_E4M3, OUT_E5M2})
+                for (bool k8 : {false, true})
+                    good = good && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_of(dtype, ck, k8)),
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_for(ck))) == cudaSuccess;
+        good = good && cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kernel_of(KVR_BF16, OUT16, false)), &cfg) == cudaSuccess && n > 0;
         if (!good) {
             (void)cudaGetLastError();
             return 1;
@@ -1314,19 +1371,6 @@ static bool encode_rows(CUtensorMap* map, const void* base, bool bf16, int64_t r
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class IT>
-static cudaError_t launch_mla_tc_t(const MlaParams& p, const Maps& maps, cudaStream_t s) {
-    const bool c8 = p.ckv_kind != OUT16, k8 = p.k_kind != OUT16;
-    const dim3 g(unsigned(p.pairs * 2)), b16(threads_of<false>()), b8(threads_of<true>());
-    const cudaError_t e =
-        c8 ? (k8 ? launch_pdl(mla_tc_kernel<IT, true, true>, g, b8, smem_of<true>(), s, p, maps)
-                 : launch_pdl(mla_tc_kernel<IT, true, false>, g, b8, smem_of<true>(), s, p, maps))
-           : (k8 ? launch_pdl(mla_tc_kernel<IT, false, true>, g, b16, smem_of<false>(), s, p, maps)
-                 : launch_pdl(mla_tc_kernel<IT, false, false>, g, b16, smem_of<false>(), s, p, maps));
-    if (e != cudaSuccess || p.pairs == 1) return e;
-    return launch_pdl(mla_join_kernel<IT>, dim3(unsigned(p.pairs - 1), ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, s, p);
-}
-
 cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     p.pairs = mla_tc_pairs();
     p.out_wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.o_ts % 16 == 0 && p.o_hs % 16 == 0;
@@ -1344,7 +1388,11 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
             encode_rows(&maps.two, p.ckv, bf, rows, p.Dv, r, 2) && encode_rows(&maps.rope, p.kc, bf, rows, p.Dk, r, 1))
             p.box_rows = r;
     }
-    return dtype == KVR_BF16 ? launch_mla_tc_t<BF16>(p, maps, s) : launch_mla_tc_t<F16>(p, maps, s);
+    const cudaError_t e = launch_pdl(kernel_of(dtype, p.ckv_kind, p.k_kind != OUT16), dim3(unsigned(p.pairs * 2)), dim3(NT),
+                                     smem_for(p.ckv_kind), s, p, maps);
+    if (e != cudaSuccess || p.pairs == 1) return e;
+    const dim3 grid(unsigned(p.pairs - 1), ROWS / JOIN_ROWS), block(32 * JOIN_ROWS);
+    return dtype == KVR_BF16 ? launch_pdl(mla_join_kernel<BF16>, grid, block, 0, s, p) : launch_pdl(mla_join_kernel<F16>, grid, block, 0, s, p);
 }
 
 }  // namespace kvr
