@@ -49,7 +49,7 @@ constexpr int MAX_STAGES = 4;
 template <bool C8>
 constexpr int stages_of() { return C8 ? 3 : 4; }
 constexpr uint32_t TMEM_COLS = 512, COL_S = 256;   // O: columns 0..255, S: two buffers of 32 + 32
-constexpr int64_t ITEM_COST = 128;       // an item's own cost, in keys
+constexpr int64_t ITEM_COST = 448;       // an item's own cost, in keys (its queries, first scores and output: about 7 steps)
 constexpr int64_t MIN_KEYS = 128;        // least work of a pair, in keys
 
 struct Bound {
