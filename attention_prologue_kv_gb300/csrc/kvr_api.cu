@@ -690,7 +690,10 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
 extern "C" {
 
 int64_t kvr_mla_attention_workspace(const kvr_mla_args* a) {
-    return a != nullptr && mla_tensor_cores(a) ? mla_tc_workspace(int(a->Dv)) : 0;
+    MlaParams p;
+    bool empty;
+    if (mla_plan(a, &p, &empty) != KVR_OK || empty || !mla_tensor_cores(a)) return 0;
+    return mla_tc_workspace(p, a->dtype);
 }
 
 kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
@@ -701,7 +704,7 @@ kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
     const bool tc = mla_tensor_cores(a);
     if (tc) {
         if (a->workspace == nullptr) return KVR_ERR_NULL;
-        if (!aligned(a->workspace, 16) || a->workspace_bytes < mla_tc_workspace(p.Dv)) return KVR_ERR_SHAPE;
+        if (!aligned(a->workspace, 16) || a->workspace_bytes < mla_tc_workspace(p, a->dtype)) return KVR_ERR_SHAPE;
     }
     (void)cudaGetLastError();
     return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));

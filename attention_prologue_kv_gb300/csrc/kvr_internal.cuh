@@ -357,7 +357,8 @@ struct MlaParams {
     float scale;                // softmax scale
     int pairs;                  // tensor-core kernel: CTA pairs of the grid
     int out_wide;               // its output rows lie on 32-byte boundaries
-    int runs;                   // its blocks hold whole halves of a step
+    const float* row_mul;       // power of two per row that its prepared queries lack, or NULL
+    int runs, groups;           // its blocks hold whole halves of a step, whole groups of 8 keys
     int box_rows;               // its TMA boxes' rows (0: none)
 };
 
@@ -396,7 +397,7 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool ve
 cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s);
 cudaError_t launch_mla_generic(const MlaParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s);
-int64_t mla_tc_workspace(int Dv);   // bytes on the current device
+int64_t mla_tc_workspace(const MlaParams& p, int dtype);   // bytes on the current device
 
 int sm_count_current_device();
 

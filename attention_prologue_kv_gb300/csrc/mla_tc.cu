@@ -73,9 +73,8 @@ struct alignas(16) Misc {
     uint32_t held[MAX_STAGES][2];   // keys of a step that exist: bit i of a half for its key i
     float inv_k[64], lift;   // 1 / scale of the rotary channels; a power of two taken out of their queries
 };
-struct alignas(16) Scales {              // behind Misc, with codes
-    float inv_v[512];        // 1 / scale of a channel
-    float row_mul[2][64];    // power of two taken out of a row's queries, of this part and the next
+struct alignas(16) Scales {   // behind Misc, with codes
+    float inv_v[512];         // 1 / scale of a channel
 };
 template <bool C8>
 constexpr uint32_t smem_of() {
@@ -590,224 +589,212 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
 }
 
 // 8-bit latent rows, decoded into halves (the rotary part into q's type): a lane has 16 codes, a quarter of a box, of one
-// of 8 rows, so that a warp's stores fill the banks. The next step's loads are in flight meanwhile.
-// Four warps bring a CTA's own 32 keys.
+// of 8 rows, so that a warp's stores fill the banks. The next step's loads are in flight meanwhile. Where blocks hold whole
+// groups of 8 keys, lane i looks up a group's first row for step base + i, once for 32 steps.
+struct Group {
+    int64_t first;   // of step base + lane
+    __device__ __forceinline__ void look(const MlaParams& p, int n, int K, int step, int key) { first = key_row(p, n, K, step * KEYS + key); }
+    __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(0xFFFFFFFFu, first, i); }
+};
+// Of 8 keys from `key` on, which exist, given the first one's row.
+__device__ __forceinline__ uint32_t group_bits(int64_t first, int K, int key) {
+    const int left = K - key;
+    return first < 0 ? 0u : (left >= 8 ? 0xFFu : (1u << max(left, 0)) - 1u);
+}
+
+// Eight warps bring a CTA's own 32 keys: warp & 3 has 8 of them, warp >> 2 half of the channels.
 template <class IT, int CK>
 __device__ __forceinline__ void code_keys(Ctx& c, int v) {
     constexpr int STAGES = stages_of<true>();
     const MlaParams& p = c.p;
     Misc* m = c.m;
-    const int lane = c.lane, tk = v >> 2, c4 = v & 3;
-    const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16;
+    const int lane = c.lane, wp = v >> 5 & 3, half = v >> 7, sub = lane >> 2, tk = wp * 8 + sub, c4 = lane & 3;
+    const int mine = int(c.rank) * CKEYS + wp * 8, theirs = mine ^ CKEYS;   // first keys of the groups
+    const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16, nb = c.nb - half * 4;
     const uint32_t at0 = box_at(0, tk, 2 * c4), at1 = box_at(0, tk, 2 * c4 + 1);   // this lane's places in a box
     int j = 0;
-    Rows rows(p);
     Walk w(p, m);
 #pragma unroll 1
     while (w.next()) {
-        uint4 x[8], y[8], xr[2], yr[2];
-        const int kt1 = w.kt1;
-        rows.begin(w, lane, tk, 3);
-        uint32_t held = 0, next = 0;   // this warp's 8 keys of this CTA (byte 0) and of the other (byte 1) that exist
-        auto bits = [](uint32_t b) {   // every fourth bit
-            b &= 0x11111111u;
-            b = (b | b >> 3) & 0x03030303u;
-            b = (b | b >> 6) & 0x000F000Fu;
-            return (b | b >> 12) & 0xFFu;
+        const int n = w.n, K = w.s.K, kt0 = w.kt0, kt1 = w.kt1;
+        int base = kt0 - 32;
+        Group own, other;
+        struct Load {
+            uint4 x[4], rope;
+            uint32_t held;   // the groups' keys that exist: of this CTA (byte 0) and the other (byte 1)
         };
-        auto load = [&](int kt, uint4 (&a)[8], uint4 (&ar)[2]) {
-            const int64_t lo = rows.row<0>(kt, tk), hi = rows.row<1>(kt, tk), slot = c.rank ? hi : lo;
-            rows.next(kt, lane, tk, 3);
-            next = bits(__ballot_sync(0xFFFFFFFFu, slot >= 0)) | bits(__ballot_sync(0xFFFFFFFFu, (c.rank ? lo : hi) >= 0)) << 8;
-            const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (slot < 0 ? 0 : slot) * p.Dv + c4 * 16;
-            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + (slot < 0 ? 0 : slot) * p.Dk * (p.k_kind == OUT16 ? 2 : 1) + c4 * 16;
+        auto load = [&](int kt, Load& a) {
+            int64_t slot;
+            if (p.groups) {
+                if (kt - base >= 32) {
+                    base = kt;
+                    own.look(p, n, K, base + lane, mine);
+                    other.look(p, n, K, base + lane, theirs);
+                }
+                const int64_t f = own.of(kt - base), g = other.of(kt - base);
+                a.held = group_bits(f, K, kt * KEYS + mine) | group_bits(g, K, kt * KEYS + theirs) << 8;
+                slot = a.held >> sub & 1 ? f + sub : -1;
+            } else {
+                slot = key_row(p, n, K, kt * KEYS + mine + sub);
+                auto bits = [](uint32_t b) {   // every fourth bit
+                    b &= 0x11111111u;
+                    b = (b | b >> 3) & 0x03030303u;
+                    b = (b | b >> 6) & 0x000F000Fu;
+                    return (b | b >> 12) & 0xFFu;
+                };
+                const uint32_t l = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+                const uint32_t o = __ballot_sync(0xFFFFFFFFu, key_row(p, n, K, kt * KEYS + theirs + sub) >= 0);
+                a.held = bits(l) | bits(o) << 8;
+            }
+            const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + slot * p.Dv + half * 256 + c4 * 16;
+            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + slot * p.Dk * (p.k_kind == OUT16 ? 2 : 1) + (half * 4 + c4) * 16;
+            if (slot >= 0 && half * 16 + 16 <= nc && half * 4 + 4 <= nr) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = slot >= 0 && c4 + 4 * i < nc ? ld_stream_v4(src + 64 * i) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) a.x[i] = ld_stream_v4(src + 64 * i);
+                a.rope = ld_stream_v4(k);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) ar[i] = slot >= 0 && c4 + 4 * i < nr ? ld_stream_v4(k + 64 * i) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) a.x[i] = slot >= 0 && half * 16 + c4 + 4 * i < nc ? ld_stream_v4(src + 64 * i) : make_uint4(0, 0, 0, 0);
+                a.rope = slot >= 0 && half * 4 + c4 < nr ? ld_stream_v4(k) : make_uint4(0, 0, 0, 0);
+            }
         };
-        load(w.kt0, x, xr);
-        held = next;
-#pragma unroll 1
-        for (int kt = w.kt0; kt < kt1; ++kt, ++j) {
-            if (kt + 1 < kt1) load(kt + 1, y, yr);
+        auto store = [&](int kt, const Load& a) {
             const int st = j % STAGES;
             const uint32_t stage = c.stage(st);
             if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i >= c.nb) break;
-                st_shared_v4(stage + i * KBOX + at0, codes_to_halves<CK>(x[i].x, x[i].y));
-                st_shared_v4(stage + i * KBOX + at1, codes_to_halves<CK>(x[i].z, x[i].w));
-            }
+            for (int i = 0; i < 4; ++i)
+                if (i < nb) {
+                    st_shared_v4(stage + (half * 4 + i) * KBOX + at0, codes_to_halves<CK>(a.x[i].x, a.x[i].y));
+                    st_shared_v4(stage + (half * 4 + i) * KBOX + at1, codes_to_halves<CK>(a.x[i].z, a.x[i].w));
+                }
             const uint32_t box = stage + 8 * KBOX;
-            if (p.k_kind == OUT16) {
-                st_shared_v4(box_at(box, tk, c4), xr[0]);
-                st_shared_v4(box_at(box, tk, c4 + 4), xr[1]);
-            } else {
-                st_shared_v4(box + at0, dec8x8<IT>(p.k_kind, xr[0].x, xr[0].y));
-                st_shared_v4(box + at1, dec8x8<IT>(p.k_kind, xr[0].z, xr[0].w));
+            if (p.k_kind == OUT16) {   // eight pieces a row: four of each half
+                st_shared_v4(box_at(box, tk, half * 4 + c4), a.rope);
+            } else if (half == 0) {    // four pieces a row
+                st_shared_v4(box + at0, dec8x8<IT>(p.k_kind, a.rope.x, a.rope.y));
+                st_shared_v4(box + at1, dec8x8<IT>(p.k_kind, a.rope.z, a.rope.w));
             }
-            if (lane == 0) {
-                reinterpret_cast<uint8_t*>(&m->held[st][c.rank])[v >> 5] = uint8_t(held);
-                reinterpret_cast<uint8_t*>(&m->held[st][c.rank ^ 1])[v >> 5] = uint8_t(held >> 8);
+            if (lane == 0 && half == 0) {
+                reinterpret_cast<uint8_t*>(&m->held[st][c.rank])[wp] = uint8_t(a.held);
+                reinterpret_cast<uint8_t*>(&m->held[st][c.rank ^ 1])[wp] = uint8_t(a.held >> 8);
             }
             c.arrive(&m->k_full[st]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = y[i];
-            xr[0] = yr[0];
-            xr[1] = yr[1];
-            held = next;
+            ++j;
+        };
+        Load x, y;
+        load(kt0, x);
+#pragma unroll 1
+        for (int kt = kt0; kt < kt1; kt += 2) {   // two steps a turn: the loads in flight need no copies
+            if (kt + 1 < kt1) load(kt + 1, y);
+            store(kt, x);
+            if (kt + 1 == kt1) break;
+            if (kt + 2 < kt1) load(kt + 2, x);
+            store(kt + 1, y);
         }
     }
 }
 
-// Three warps bring the other CTA's keys of a part (this CTA's channels): 16 pieces of 8 rows of a box, in turn.
+// Three warps bring the other CTA's keys of a part (this CTA's four boxes of channels): warp w has box w of the four
+// groups of 8 rows and, in turn, their box 3 (groups 0 and 3, group 1, group 2).
 template <int CK>
 __device__ __forceinline__ void code_swaps(Ctx& c, int v, const Walk& w, int& j) {
-    constexpr int STAGES = stages_of<true>(), TURNS = 6;
+    constexpr int STAGES = stages_of<true>();
     const MlaParams& p = c.p;
     Misc* m = c.m;
-    const int lane = c.lane, wp = v >> 5, theirs = int(c.rank ^ 1);
-    uint4 x[TURNS], y[TURNS];
-    Rows rows(p);
-    rows.begin(w, lane, lane, 1 << theirs);
-    auto load = [&](int kt, uint4 (&a)[TURNS]) {
-        const int64_t slot = theirs ? rows.row<1>(kt, lane) : rows.row<0>(kt, lane);
-        rows.next(kt, lane, lane, 1 << theirs);
+    const int lane = c.lane, wp = v >> 5, theirs = int(c.rank ^ 1), sub = lane >> 2;
+    const int n = w.n, K = w.s.K, kt0 = w.kt0, kt1 = w.kt1;
+    int base = kt0 - 32;
+    Group group[4];
+    auto channel = [&](int b) { return ((b >> 1) * 4 + int(c.rank) * 2 + (b & 1)) * 64; };
+    const int qa = channel(wp), qb = channel(3);
+    const uint32_t boxa = uint32_t((wp >> 1) * 4 + theirs * 2 + (wp & 1)) * KBOX, boxb = uint32_t(4 + theirs * 2 + 1) * KBOX;
+    auto load = [&](int kt, uint4 (&a)[6]) {
+        int64_t slot[4];
+        if (p.groups) {
+            if (kt - base >= 32) {
+                base = kt;
 #pragma unroll
-        for (int i = 0; i < TURNS; ++i) {
-            const int piece = wp + 3 * i, b = piece & 3, row = (piece >> 2) * 8 + (lane >> 2);
-            const int64_t r = __shfl_sync(0xFFFFFFFFu, slot, row & 31);
-            const int q = ((b >> 1) * 4 + int(c.rank) * 2 + (b & 1)) * 64 + (lane & 3) * 16;   // first channel
-            a[i] = piece < 16 && r >= 0 && q < p.Dv ? ld_stream_v4(static_cast<const uint8_t*>(p.ckv) + r * p.Dv + q) : make_uint4(0, 0, 0, 0);
+                for (int g = 0; g < 4; ++g) group[g].look(p, n, K, base + lane, theirs * CKEYS + g * 8);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t f = group[g].of(kt - base);
+                slot[g] = f >= 0 && kt * KEYS + theirs * CKEYS + g * 8 + sub < K ? f + sub : -1;
+            }
+        } else {
+            const int64_t s = key_row(p, n, K, kt * KEYS + theirs * CKEYS + lane);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) slot[g] = __shfl_sync(0xFFFFFFFFu, s, g * 8 + sub);
         }
+        const int64_t extra = wp == 0 ? slot[0] : (wp == 1 ? slot[1] : slot[2]);
+        const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (lane & 3) * 16;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) a[g] = slot[g] >= 0 && qa + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + slot[g] * p.Dv + qa) : make_uint4(0, 0, 0, 0);
+        a[4] = extra >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + extra * p.Dv + qb) : make_uint4(0, 0, 0, 0);
+        a[5] = wp == 0 && slot[3] >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + slot[3] * p.Dv + qb) : make_uint4(0, 0, 0, 0);
     };
-    load(w.kt0, x);
-#pragma unroll 1
-    for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
-        if (kt + 1 < w.kt1) load(kt + 1, y);
+    auto put = [&](uint32_t box, int g, const uint4& x) {
+        st_shared_v4(box_at(box, g * 8 + sub, 2 * (lane & 3)), codes_to_halves<CK>(x.x, x.y));
+        st_shared_v4(box_at(box, g * 8 + sub, 2 * (lane & 3) + 1), codes_to_halves<CK>(x.z, x.w));
+    };
+    auto store = [&](const uint4 (&a)[6]) {
         const int st = j % STAGES;
         const uint32_t stage = c.stage(st);
         c.wait(&m->s_full[j & 1], (j >> 1) & 1);
 #pragma unroll
-        for (int i = 0; i < TURNS; ++i) {
-            const int piece = wp + 3 * i, b = piece & 3, row = (piece >> 2) * 8 + (lane >> 2);
-            if (piece >= 16) break;
-            const uint32_t box = stage + uint32_t((b >> 1) * 4 + theirs * 2 + (b & 1)) * KBOX;
-            st_shared_v4(box_at(box, row, 2 * (lane & 3)), codes_to_halves<CK>(x[i].x, x[i].y));
-            st_shared_v4(box_at(box, row, 2 * (lane & 3) + 1), codes_to_halves<CK>(x[i].z, x[i].w));
-        }
+        for (int g = 0; g < 4; ++g) put(stage + boxa, g, a[g]);
+        put(stage + boxb, wp, a[4]);
+        if (wp == 0) put(stage + boxb, 3, a[5]);
         c.arrive(&m->v_full[st]);
-#pragma unroll
-        for (int i = 0; i < TURNS; ++i) x[i] = y[i];
+        ++j;
+    };
+    uint4 x[6], y[6];
+    load(kt0, x);
+#pragma unroll 1
+    for (int kt = kt0; kt < kt1; kt += 2) {
+        if (kt + 1 < kt1) load(kt + 1, y);
+        store(x);
+        if (kt + 1 == kt1) break;
+        if (kt + 2 < kt1) load(kt + 2, x);
+        store(y);
     }
 }
 
 // The query warps (four; three with codes) bring the queries of a part: lane v & 7 has chunk v & 7 of each box of a row.
-template <class IT, bool C8>
+template <bool C8>
 __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int part) {
     constexpr int AT_ONCE = C8 ? 12 : 16, TURNS = C8 ? 6 : 4;   // rows of a turn
     const MlaParams& p = c.p;
     Misc* m = c.m;
     const int nc = p.Dv / 8, nr = p.Dk / 8, ch = v & 7;
-    const bool per_rope = p.k_kind != OUT16 && p.k_scale_per_ch;
-    auto row_of = [&](int turn, const uint16_t*& qn, const uint16_t*& qr) {
-        const int r = turn * AT_ONCE + (v >> 3);
+    const uint16_t *qn[TURNS], *qr[TURNS];
+    uint32_t lives = 0;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int r = i * AT_ONCE + (v >> 3);
         const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
         const bool live = r < CROWS && row < unsigned(w.s.L) * unsigned(p.H);
         const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
-        qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs + ch * 8;
-        qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + ch * 8;
-        return live;
-    };
-    // The rotary part keeps q's type; a scale per channel goes in with one rounding, over the largest 1 / scale (as a
-    // power of two, put back into the scores).
-    auto rope = [&](const uint16_t* qr, bool live, int r) {
-        uint4 x = live && ch < nr ? ld_stream_v4(qr) : make_uint4(0, 0, 0, 0);
-        if (per_rope) {
-            uint32_t* u = reinterpret_cast<uint32_t*>(&x);
-            const float* f = m->inv_k + ch * 8;
-            const float g = 1.f / m->lift;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = IT::pack(IT::lo(u[k]) * (f[2 * k] * g), IT::hi(u[k]) * (f[2 * k + 1] * g));
-        }
-        st_shared_v4(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), x);
-    };
-    if constexpr (!C8) {
-        const uint16_t *qn[TURNS], *qr[TURNS];
-        uint32_t lives = 0;
-#pragma unroll
-        for (int i = 0; i < TURNS; ++i) lives |= uint32_t(row_of(i, qn[i], qr[i])) << i;
-        if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
-#pragma unroll
-        for (int i = 0; i < TURNS; ++i) {
-            const int r = i * AT_ONCE + (v >> 3);
-            const bool live = lives >> i & 1;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const bool in = live && b * 8 + ch < nc;
-                if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), in ? qn[i] + b * 64 : qn[i], in);
-            }
-            if (!per_rope) cp_async16(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), qr[i], live && ch < nr);
-        }
-        cp_async_commit();
-        if (per_rope) {
-#pragma unroll 1
-            for (int i = 0; i < TURNS; ++i) {
-                const bool live = row_of(i, qn[0], qr[0]);
-                rope(qr[0], live, i * AT_ONCE + (v >> 3));
-            }
-        }
-        cp_async_wait<0>();
-    } else {
-        // Halves of q / scale: 11 bits keep the rounding of the one product that has to be rounded small. A power of two
-        // per row, put back into its scores, brings the largest to [2^13, 2^14): float16's range then reaches 2^-38
-        // below it.
-        const bool per = p.ckv_scale_per_ch;
-        if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
-#pragma unroll 1
-        for (int i = 0; i < TURNS; ++i) {
-            const int r = i * AT_ONCE + (v >> 3);
-            if (i * AT_ONCE + (v >> 5) * 4 >= CROWS) break;   // the warp's rows end (they do together: 4 a warp)
-            const uint16_t *qn, *qr;
-            const bool live = row_of(i, qn, qr);
-            uint4 x[8];
-            float top = 0.f;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) x[b] = live && b * 8 + ch < nc ? ld_stream_v4(qn + b * 64) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
-                float4 f0 = make_float4(1.f, 1.f, 1.f, 1.f), f1 = f0;
-                if (per) {
-                    f0 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8);
-                    f1 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8 + 4);
-                }
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(IT::lo(u[0]) * f0.x), fabsf(IT::hi(u[0]) * f0.y)), fmaxf(fabsf(IT::lo(u[1]) * f0.z), fabsf(IT::hi(u[1]) * f0.w))));
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(IT::lo(u[2]) * f1.x), fabsf(IT::hi(u[2]) * f1.y)), fmaxf(fabsf(IT::lo(u[3]) * f1.z), fabsf(IT::hi(u[3]) * f1.w))));
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const int e = top > 0.f && top <= 3.0e38f ? max(ilogbf(top), -100) - 13 : 0;
-            const float g = ldexpf(1.f, -e);
-            if (ch == 0) c.sc->row_mul[part & 1][r] = ldexpf(1.f, e);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[b]);
-                float4 f0 = make_float4(1.f, 1.f, 1.f, 1.f), f1 = f0;
-                if (per) {
-                    f0 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8);
-                    f1 = *reinterpret_cast<const float4*>(c.sc->inv_v + b * 64 + ch * 8 + 4);
-                }
-                if (b < c.nb)
-                    st_shared_v4(box_at(c.base + OFF_Q + b * QBOX, r, ch),
-                                 make_uint4(F16::pack(IT::lo(u[0]) * f0.x * g, IT::hi(u[0]) * f0.y * g), F16::pack(IT::lo(u[1]) * f0.z * g, IT::hi(u[1]) * f0.w * g),
-                                            F16::pack(IT::lo(u[2]) * f1.x * g, IT::hi(u[2]) * f1.y * g), F16::pack(IT::lo(u[3]) * f1.z * g, IT::hi(u[3]) * f1.w * g)));
-            }
-            rope(qr, live, r);
-        }
+        qn[i] = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs + ch * 8;
+        qr[i] = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + ch * 8;
+        lives |= uint32_t(live) << i;
     }
+    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int r = i * AT_ONCE + (v >> 3);
+        const bool live = lives >> i & 1;
+        if (C8 && r >= CROWS) break;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const bool in = live && b * 8 + ch < nc;
+            if (b < c.nb) cp_async16(box_at(c.base + OFF_Q + b * QBOX, r, ch), in ? qn[i] + b * 64 : qn[i], in);
+        }
+        cp_async16(box_at(c.base + OFF_Q + 8 * QBOX, r, ch), qr[i], live && ch < nr);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
     c.arrive(&m->q_full);
 }
 
@@ -823,17 +810,21 @@ __device__ __forceinline__ void prefetch_queries(Ctx& c, int v, const Walk& w) {
     if ((v & 1) == 0) prefetch_l2(static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs);
 }
 
-// Two groups of four softmax warps: a lone warp of a scheduler goes at about 5 cycles an instruction, so what a warp has
-// to do sets the time of a step's softmax and of a part's output.
-constexpr int GROUPS = 2;
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(128 * GROUPS) : "memory"); }
+// Groups of four softmax warps: a lone warp of a scheduler goes at about 5 cycles an instruction, so what a warp has to do
+// sets the time of a step's softmax and of a part's output. With codes the warps are needed more for decoding.
+template <bool C8>
+constexpr int groups_of() { return C8 ? 1 : 2; }
+template <bool C8>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(128 * groups_of<C8>()) : "memory");
+}
 
 // Output of a part (a row tile of a sequence), by the softmax warps: thread (row r, half h of the channels; group g has
 // half of the 256 columns). Each thread writes its row's sectors itself, with few instructions: through shared memory, for
 // whole lines, took more of them and longer (7000 cycles a part against 5000).
 template <class IT, bool C8>
 __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part, const Walk& w, unsigned row, bool live, float2 ml) {
-    constexpr int G = GROUPS;
+    constexpr int G = groups_of<C8>();
     const MlaParams& p = c.p;
     const int r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
     const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
@@ -905,15 +896,23 @@ __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part,
     tc_fence_before();
 }
 
-// Over the four threads of row r, always in this order.
-__device__ __forceinline__ float row_max(const float* x, int r) { return fmaxf(fmaxf(x[r], x[r + 64]), fmaxf(x[r + 128], x[r + 192])); }
-__device__ __forceinline__ float row_sum(const float* x, int r) { return (x[r] + x[r + 64]) + (x[r + 128] + x[r + 192]); }
+// Over the threads of row r (two a group), always in this order.
+template <int G>
+__device__ __forceinline__ float row_max(const float* x, int r) {
+    const float v = fmaxf(x[r], x[r + 64]);
+    return G == 1 ? v : fmaxf(v, fmaxf(x[r + 128], x[r + 192]));
+}
+template <int G>
+__device__ __forceinline__ float row_sum(const float* x, int r) {
+    const float v = x[r] + x[r + 64];
+    return G == 1 ? v : v + (x[r + 128] + x[r + 192]);
+}
 
 // Softmax: thread (row r, half h of the keys, group g: half of that half).
 template <class IT, bool C8, bool K8>
 __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     using PT = typename std::conditional<C8, F16, IT>::type;   // type of the weights and the decoded codes
-    constexpr int G = GROUPS, NK = CKEYS / G;          // keys of a thread
+    constexpr int G = groups_of<C8>(), NK = CKEYS / G;          // keys of a thread
     const MlaParams& p = c.p;
     Misc* m = c.m;
     const int r = tid & 63, h = tid >> 6 & 1, g = tid >> 7;
@@ -933,6 +932,10 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         int wmin = live ? vis : 0x7FFFFFFF;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
+        if (C8) {
+            fn = l2 * (p.ckv_scale_per_ch ? 1.f : c.sc->inv_v[0]);
+            if (p.row_mul != nullptr && live) fn *= p.row_mul[(w.s.q0 + row / unsigned(p.H)) * p.H + row % unsigned(p.H)];
+        }
         float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
@@ -942,7 +945,6 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             tc_fence_after();
             // Keys that exist: bit i for key0 + i.
             const uint32_t held = m->held[j % stages_of<C8>()][h] >> (g * NK);
-            if (C8 && kt == w.kt0) fn = l2 * (p.ckv_scale_per_ch ? 1.f : c.sc->inv_v[0]) * c.sc->row_mul[part & 1][r];
             float s[NK];
             tmem_ld(lanes + COL_S + uint32_t(j & 1) * 64 + g * NK, s);
             if (split) {
@@ -967,8 +969,8 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
 #pragma unroll
             for (int i = 1; i < NK; ++i) top = fmaxf(top, s[i]);
             red[tid] = top;
-            softmax_sync();
-            top = fmaxf(row_max(red, r), mx);
+            softmax_sync<C8>();
+            top = fmaxf(row_max<G>(red, r), mx);
             // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
             // and the 16-bit rounding of a weight is relative.
             const bool grow = top > mx + 8.f;
@@ -1011,9 +1013,9 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         // The rows' m and l for the output.
         float* red = m->red[j & 1];
         red[tid] = sum;   // the next step's buffer: its own maxima come after the second barrier
-        softmax_sync();
-        const float2 ml = make_float2(mx, row_sum(red, r));
-        softmax_sync();
+        softmax_sync<C8>();
+        const float2 ml = make_float2(mx, row_sum<G>(red, r));
+        softmax_sync<C8>();
         c.wait(&m->pv_done, (j - 1) & 1);
         tc_fence_after();
         output_part<IT, C8>(c, tid, pair, part, w, row, live, ml);
@@ -1022,7 +1024,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
 }
 
 // The query warps: queries of a part and, with codes, its swaps.
-template <class IT, int CK>
+template <int CK>
 __device__ __forceinline__ void query_warps(Ctx& c, int v) {
     constexpr bool C8 = CK != OUT16;
     Walk w(c.p, c.m);
@@ -1030,10 +1032,10 @@ __device__ __forceinline__ void query_warps(Ctx& c, int v) {
     bool more = w.next();
 #pragma unroll 1
     for (int part = 0; more; ++part) {
-        load_queries<IT, C8>(c, v, w, part);
+        load_queries<C8>(c, v, w, part);
         if constexpr (C8) code_swaps<CK>(c, v, w, j);
         more = w.next();
-        if (!C8 && more) prefetch_queries(c, v, w);
+        if (!C8 && more) prefetch_queries(c, v, w);   // (with codes they were just written)
     }
 }
 
@@ -1112,8 +1114,8 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
     }
 }
 
-// Warps: 0-7 softmax. 16-bit latent rows: 8 keys, 9 swap, 10 MMA, 12-15 queries; codes: 8-11 keys, 12-14 queries and
-// swap, 15 MMA.
+// Warps. 16-bit latent rows: 0-7 softmax, 8 keys, 9 swap, 10 MMA, 12-15 queries; codes: 0-3 softmax, 4-11 keys, 12-14
+// queries and swap, 15 MMA.
 constexpr int NT = 512;
 
 // CK: OutKind of the latent rows; K8: the rotary ones are codes.
@@ -1138,13 +1140,13 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     if (tid == 0) {
 #pragma unroll 1
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&m->k_full[s], C8 ? 8 : 2);
+            mbar_init(&m->k_full[s], C8 ? 16 : 2);
             mbar_init(&m->v_full[s], C8 ? 6 : 2);
             mbar_init(&m->empty[s], 1);
         }
         mbar_init(&m->s_full[0], 1);
         mbar_init(&m->s_full[1], 1);
-        mbar_init(&m->p_full, 8 * GROUPS);
+        mbar_init(&m->p_full, 8 * groups_of<C8>());
         mbar_init(&m->pv_done, 1);
         mbar_init(&m->q_full, C8 ? 6 : 8);
         mbar_init(&m->q_free, 1);
@@ -1183,13 +1185,13 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = m->tmem;
     Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
 
-    if (warp < 4 * GROUPS) {
+    if (warp < 4 * groups_of<C8>()) {
         softmax_warps<IT, C8, K8>(c, tid, pair);
     } else if (warp == MMA_WARP) {
         if (rank == 0) mma_warp<IT, C8, K8>(c);
     } else if constexpr (C8) {
-        if (warp < 12) code_keys<IT, CK>(c, tid - 256);
-        else query_warps<IT, CK>(c, tid - 384);
+        if (warp < 12) code_keys<IT, CK>(c, tid - 128);
+        else query_warps<CK>(c, tid - 384);
     } else {
         if (warp == 8) {
             if (!K8 && p.box_rows == CKEYS) key_warp_tma<false>(c, maps);
@@ -1198,7 +1200,7 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
             if (!K8 && p.box_rows == CKEYS) key_warp_tma<true>(c, maps);
             else key_warp<IT, K8, true>(c, maps);
         } else if (warp >= 12) {
-            query_warps<IT, CK>(c, tid - 384);
+            query_warps<CK>(c, tid - 384);
         }
     }
     if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
@@ -1208,6 +1210,76 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     cluster_sync_all();
     tc_fence_after();
     if (warp == MMA_WARP) tmem_free_pair(tmem, TMEM_COLS);
+}
+
+// Queries for a cache of codes. A scale per channel goes into the query, q / scale, rounded once: to halves, whose 11 bits
+// keep that rounding small (the products with the codes, exact as halves, then run on halves whatever q's type). A power
+// of two per row, put back into its scores, keeps q / scale below 2^14: it comes from the row's largest |q| and the largest
+// 1 / scale, and float16's range then reaches 2^-38 below. The rotary part keeps q's type, with the scale per channel
+// over a power of two of the largest 1 / scale. One warp a row.
+template <class IT>
+__global__ void __launch_bounds__(256) mla_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn_out, float* mul_out, uint16_t* qr_out) {
+    __shared__ float inv[512], invk[64], most[2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (qn_out != nullptr)
+        for (int c = threadIdx.x; c < p.Dv; c += 256) inv[c] = p.ckv_scale_per_ch ? 1.f / p.ckv_scale[c] : 1.f;
+    if (qr_out != nullptr && threadIdx.x < p.Dk) invk[threadIdx.x] = 1.f / p.k_scale[threadIdx.x];
+    __syncthreads();
+    if (warp < 2) {
+        float v = 0.f;
+        if (warp == 0 && qn_out != nullptr)
+            for (int c = lane; c < p.Dv; c += 32) v = fmaxf(v, fabsf(inv[c]));
+        if (warp == 1 && qr_out != nullptr)
+            for (int c = lane; c < p.Dk; c += 32) v = fmaxf(v, fabsf(invk[c]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        if (lane == 0) most[warp] = exp2f(ceilf(log2f(v)));
+    }
+    __syncthreads();
+    const float lift = most[0], g_rope = 1.f / most[1];
+    const int64_t rows = p.T * p.H;
+    for (int64_t row = int64_t(blockIdx.x) * 8 + warp; row < rows; row += int64_t(gridDim.x) * 8) {
+        const int64_t t = row / p.H, head = row - t * p.H;
+        if (qn_out != nullptr) {
+            const uint16_t* q = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
+            uint4 x[2];
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int ch = (k * 32 + lane) * 8;
+                x[k] = ch < p.Dv ? ld_stream_v4(q + ch) : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(IT::lo(u[i])), fabsf(IT::hi(u[i]))));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const int e = top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) + ilogbf(lift) - 13, -113), 113) : 0;
+            const float g = ldexpf(1.f, -e);
+            if (lane == 0) mul_out[row] = ldexpf(1.f, e);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int ch = (k * 32 + lane) * 8;
+                if (ch >= p.Dv) break;
+                const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                uint32_t z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = F16::pack(IT::lo(u[i]) * inv[ch + 2 * i] * g, IT::hi(u[i]) * inv[ch + 2 * i + 1] * g);
+                *reinterpret_cast<uint4*>(qn_out + row * p.Dv + ch) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+        }
+        if (qr_out != nullptr && lane * 8 < p.Dk) {
+            const uint4 x = ld_stream_v4(static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + lane * 8);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                z[i] = IT::pack(IT::lo(u[i]) * (invk[lane * 8 + 2 * i] * g_rope), IT::hi(u[i]) * (invk[lane * 8 + 2 * i + 1] * g_rope));
+            *reinterpret_cast<uint4*>(qr_out + row * p.Dk + lane * 8) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+    }
 }
 
 // Joins the parts of the items that were cut: the blocks x take the item that
@@ -1344,7 +1416,18 @@ static int mla_tc_pairs() {
     return cache[dev];
 }
 
-int64_t mla_tc_workspace(int Dv) { return ws_bytes(mla_tc_pairs(), Dv); }
+// Queries that a cache of codes needs prepared: the latent part unless q has halves and the scale is one, the rotary
+// part where its scale is per channel.
+static bool prepares_nope(const MlaParams& p, int dtype) { return p.ckv_kind != OUT16 && (p.ckv_scale_per_ch || dtype != KVR_F16); }
+static bool prepares_rope(const MlaParams& p) { return p.k_kind != OUT16 && p.k_scale_per_ch; }
+static int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
+
+int64_t mla_tc_workspace(const MlaParams& p, int dtype) {
+    int64_t n = round_up(ws_bytes(mla_tc_pairs(), p.Dv));
+    if (prepares_nope(p, dtype)) n += round_up(p.T * p.H * p.Dv * 2) + round_up(p.T * p.H * 4);
+    if (prepares_rope(p)) n += round_up(p.T * p.H * p.Dk * 2);
+    return n;
+}
 
 // The driver's tensor-map encoder, found through the runtime (no link to libcuda).
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1379,6 +1462,7 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     Maps maps = {};
     p.box_rows = 0;
     p.runs = p.table == nullptr || p.d1 % CKEYS == 0;
+    p.groups = p.table == nullptr || p.d1 % 8 == 0;
     const int64_t rows = p.d0 * p.d1;
     if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv % 64 == 0 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
         int r = 32;
@@ -1387,6 +1471,34 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
         if (r >= 8 && encoder() != nullptr && encode_rows(&maps.all, p.ckv, bf, rows, p.Dv, r, r == 32 ? p.Dv / 64 : 1) &&
             encode_rows(&maps.two, p.ckv, bf, rows, p.Dv, r, 2) && encode_rows(&maps.rope, p.kc, bf, rows, p.Dk, r, 1))
             p.box_rows = r;
+    }
+    const bool nope = prepares_nope(p, dtype), rope = prepares_rope(p);
+    if (nope || rope) {
+        char* at = static_cast<char*>(p.workspace) + round_up(ws_bytes(p.pairs, p.Dv));
+        uint16_t *qn = nullptr, *qr = nullptr;
+        float* mul = nullptr;
+        if (nope) {
+            qn = reinterpret_cast<uint16_t*>(at);
+            mul = reinterpret_cast<float*>(at + round_up(p.T * p.H * p.Dv * 2));
+            at += round_up(p.T * p.H * p.Dv * 2) + round_up(p.T * p.H * 4);
+        }
+        if (rope) qr = reinterpret_cast<uint16_t*>(at);
+        const int64_t cap = int64_t(sm_count_current_device()) * 8, need = (p.T * p.H + 7) / 8;
+        const dim3 grid(unsigned(need < cap ? need : cap));
+        const cudaError_t e = dtype == KVR_BF16 ? launch_pdl(mla_queries_kernel<BF16>, grid, dim3(256), 0, s, p, qn, mul, qr)
+                                                : launch_pdl(mla_queries_kernel<F16>, grid, dim3(256), 0, s, p, qn, mul, qr);
+        if (e != cudaSuccess) return e;
+        if (nope) {
+            p.qn = qn;
+            p.row_mul = mul;
+            p.qn_ts = int64_t(p.H) * p.Dv;
+            p.qn_hs = p.Dv;
+        }
+        if (rope) {
+            p.qr = qr;
+            p.qr_ts = int64_t(p.H) * p.Dk;
+            p.qr_hs = p.Dk;
+        }
     }
     const cudaError_t e = launch_pdl(kernel_of(dtype, p.ckv_kind, p.k_kind != OUT16), dim3(unsigned(p.pairs * 2)), dim3(NT),
                                      smem_for(p.ckv_kind), s, p, maps);

@@ -600,8 +600,9 @@ typedef struct kvr_mla_args {
 kvr_status mla_attention(const kvr_mla_args* args, cudaStream_t stream);
 
 /* Bytes of workspace that mla_attention(args) needs on the current device (0
- * where it needs none). Depends on the widths, types, strides and alignments
- * in *args, not on the lengths; `workspace` itself is not looked at. */
+ * where it needs none, or where args are not valid). Depends on T, H, the
+ * widths, types, scale lengths, strides and alignments in *args, not on what
+ * the device arrays hold; `workspace` itself is not looked at. */
 int64_t kvr_mla_attention_workspace(const kvr_mla_args* args);
 
 /* Measurement helper (no counterpart on the pages): a 16-byte vectorised

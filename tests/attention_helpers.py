@@ -139,16 +139,19 @@ def oracle_mla(c, q_nope=None, q_rope=None):
 
 def rounded_query(c):
     """q as the tensor-core kernel multiplies it where a cache has a scale per
-    channel, in float64: the latent part as halves of q / scale, with a power of
-    two per row that brings the largest to [2^13, 2^14); the rotary part as q /
-    scale in q's type, a power of two over the largest 1 / scale taken out."""
+    channel, in float64: the latent part as halves of q / scale, over a power of two
+    per row (of its largest |q| and the largest 1 / scale) that keeps them below
+    2^14; the rotary part as q / scale in q's type, a power of two over the
+    largest 1 / scale taken out."""
     def inverse(s):
         return (1.0 / s).to(torch.float32)
 
     n64, r64 = f64(c.q_nope), f64(c.q_rope)
     if c.ckv_scale is not None and c.ckv_scale.numel() > 1:
-        x = c.q_nope.to(torch.float32) * inverse(c.ckv_scale)
-        g = 2.0 ** (13 - torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))))
+        inv = inverse(c.ckv_scale)
+        q = c.q_nope.to(torch.float32)
+        x = q * inv
+        g = 2.0 ** (13 - torch.floor(torch.log2(q.abs().amax(-1, keepdim=True))) - torch.ceil(torch.log2(inv.max())))
         n64 = f64((x * g).to(torch.float16)) / f64(g) * f64(c.ckv_scale)
     if c.k_scale is not None and c.k_scale.numel() > 1:
         lift = 2.0 ** torch.ceil(torch.log2(inverse(c.k_scale).max()))
