@@ -523,7 +523,8 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *   query_start  int64 [N + 1]: the new tokens of sequence n are rows
  *                [query_start[n], query_start[n + 1]) of q and out. Rows outside
  *                every sequence are left as they were. A sequence where it
- *                decreases or leaves [0, T] is left out (KVR_DEVERR_QUERY).
+ *                decreases or leaves [0, T] is left out (KVR_DEVERR_QUERY); rows
+ *                that two of the others then share get one of the two results.
  *   key_length   int64 [N]: keys of the sequence, its new tokens among them (as
  *                qsa_prepare's). A negative one, or one beyond the block table (the
  *                cache batch in Norm mode): the sequence is left out
@@ -531,7 +532,10 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *   causal       nonzero: with L new tokens and K keys, token j sees keys
  *                [0, K - L + j + 1), and nothing where that is empty (L > K).
  *                0: every token sees all K keys.
- *                Keys at or behind K are never used, whatever they hold.
+ *                Keys at or behind K are never used, whatever they hold. Those
+ *                before K are taken to be finite: a NaN or an infinity in one may
+ *                reach every token of its sequence, also one that does not see it
+ *                (its weight there is zero, and zero times it is NaN).
  *   mode         KVR_CACHE_NORM: sequence n reads cache batch n (needs
  *                cache_d0 >= N; no block table). KVR_CACHE_PA_BSND or
  *                KVR_CACHE_PA_BLK_BSND: key i is in block
