@@ -50,10 +50,14 @@ template <bool C8>
 constexpr int stages_of() { return C8 ? 3 : 4; }
 constexpr uint32_t TMEM_COLS = 512, COL_S = 256;   // O: columns 0..255, S: two buffers of 32 + 32
 constexpr int64_t ITEM_COST = 448;       // an item's own cost, in keys (its queries, first scores and output: about 7 steps)
-constexpr int64_t MIN_KEYS = 128;        // least work of a pair, in keys
+constexpr int64_t MIN_KEYS = 320;        // least work of a pair, in keys: the join of more parts then costs more than they save
 
 struct Bound {
     int n, i, kt, pad;   // sequence, row tile, key tile
+};
+struct alignas(16) Start {   // a pair's begin, as the join reads it: with its sequence's first row and its tokens
+    int n, i, kt, L;
+    int64_t q0, pad;
 };
 
 struct Seq {
@@ -65,7 +69,7 @@ struct alignas(16) Misc {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t s_full[2], p_full, pv_done, q_full, q_free, k_fix, v_fix, drain;
     uint32_t tmem;
-    int abort;
+    int abort, large;
     Bound begin, end;
     Seq first;               // the sequence of `begin`
     int64_t wsum[17];
@@ -82,19 +86,19 @@ constexpr uint32_t smem_of() {
 }
 static_assert(smem_of<false>() <= 232448 && smem_of<true>() <= 232448, "shared memory of a CTA");
 
-// Workspace: header, first bounds of the pairs, (m, l) and O of two parts a pair.
+// Workspace: header, the pairs' begins, (m, l) and O of two parts a pair.
 struct Space {
     int32_t* active;
-    Bound* bounds;
+    Start* starts;
     float2* ml;
     float* o;
 };
-__host__ __device__ inline int64_t ws_ml(int pairs) { return 256 + (int64_t(pairs) * 16 + 255) / 256 * 256; }
+__host__ __device__ inline int64_t ws_ml(int pairs) { return 256 + (int64_t(pairs) * 32 + 255) / 256 * 256; }
 __host__ __device__ inline int64_t ws_o(int pairs) { return ws_ml(pairs) + int64_t(pairs) * 2 * ROWS * 8; }
 __host__ __device__ inline int64_t ws_bytes(int pairs, int Dv) { return ws_o(pairs) + int64_t(pairs) * 2 * ROWS * Dv * 4; }
 __device__ __forceinline__ Space ws_space(const MlaParams& p) {
     char* w = static_cast<char*>(p.workspace);
-    return {reinterpret_cast<int32_t*>(w), reinterpret_cast<Bound*>(w + 256), reinterpret_cast<float2*>(w + ws_ml(p.pairs)),
+    return {reinterpret_cast<int32_t*>(w), reinterpret_cast<Start*>(w + 256), reinterpret_cast<float2*>(w + ws_ml(p.pairs)),
             reinterpret_cast<float*>(w + ws_o(p.pairs))};
 }
 
@@ -175,6 +179,54 @@ struct Walk {
     }
 };
 
+// Where share `which` of `active` begins, in cost.
+__device__ __forceinline__ int64_t share(int64_t total, int which, int active) {
+    if (which >= active) return total;
+    if (total < (int64_t(1) << 31) / 256) return unsigned(total) * unsigned(which) / unsigned(active);   // 64-bit divisions take about 100 instructions
+    return total * which / active;
+}
+// Pairs that get work: equal shares, but none below MIN_KEYS.
+__device__ __forceinline__ int active_pairs(const MlaParams& p, int64_t total) {
+    const int64_t least = int64_t(p.H) * MIN_KEYS;
+    return total >= least * p.pairs ? p.pairs : max(1, int(unsigned(total) / unsigned(least)));
+}
+
+// A pair's share where a warp holds all sequences and their cost is small (a few conversations: latency counts): one warp
+// for its begin, one for its end, without a word between warps. A kernel's first instructions come from far, up to 100
+// cycles each, so the few steps here took 9800 cycles by the way below. False: that way is to be taken.
+__device__ __forceinline__ bool schedule_small(const MlaParams& p, Misc* m, int pair) {
+    const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+    Seq s = {0, 0, 0};
+    int bits = 0;
+    if (lane < p.N) s = load_seq(p, lane, &bits);
+    const int64_t mine = s.L > 0 ? cost(p, s.L, s.K, row_tiles(p, s.L)) : 0;
+    if (__any_sync(0xFFFFFFFFu, mine >= 1 << 18)) return false;
+    int scan = int(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    const int total = __shfl_sync(0xFFFFFFFFu, scan, 31), active = active_pairs(p, total);
+    const int u = int(share(total, pair + half, active)), base = scan - int(mine);
+    if (u >= base && u < scan) {
+        const Bound b = locate(p, lane, s, u - base);
+        if (half) {
+            m->end = b;
+        } else {
+            m->begin = b;
+            m->first = s;
+        }
+    } else if (u == total && lane == 0) {
+        (half ? m->end : m->begin) = {int(p.N), 0, 0, 0};
+    }
+    if (half == 0) {
+        if (bits != 0 && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bits);
+        if (lane == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
+    }
+    return true;
+}
+
 // This pair's share of the work: every CTA scans all sequences' costs, twice side by side: the first half of the warps
 // for the share's begin, the second for its end.
 template <int THREADS>
@@ -213,14 +265,8 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
         }
         const int64_t total = __shfl_sync(0xFFFFFFFFu, of, 0);
         int64_t base = scan - sum + __shfl_sync(0xFFFFFFFFu, before, 0);
-        // Equal shares, but none below MIN_KEYS (64-bit divisions only where they are needed: they take about 100 cycles).
-        const int64_t least = int64_t(p.H) * MIN_KEYS;
-        const int active = total >= least * p.pairs ? p.pairs : max(1, int(unsigned(total) / unsigned(least)));
-        int64_t u = total;
-        if (pair + half < active) {
-            if (total < (int64_t(1) << 31) / 256) u = unsigned(total) * unsigned(pair + half) / unsigned(active);
-            else u = total * (pair + half) / active;
-        }
+        const int active = active_pairs(p, total);
+        const int64_t u = share(total, pair + half, active);
         if (u >= base && u < base + sum) {
             int n = n0;
             if (per > 1)
@@ -241,8 +287,6 @@ __device__ void schedule(const MlaParams& p, Misc* m, int pair) {
         }
         if (tid == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
     }
-    __syncthreads();
-    if (tid == 0 && cluster_rank() == 0) ws_space(p).bounds[pair] = m->begin;
 }
 
 // Four 8-bit codes of kind K to halves, exactly.
@@ -1154,6 +1198,7 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
         mbar_init(&m->v_fix, 1);
         mbar_init(&m->drain, 1);
         m->abort = 0;
+        m->large = 0;
         fence_mbar_init();
     }
     if (warp == MMA_WARP) tmem_alloc_pair(&m->tmem, TMEM_COLS);
@@ -1162,7 +1207,15 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     cluster_arrive();   // barriers and TMEM are set up; the other half is below, behind the schedule
     pdl_wait();
     pdl_launch_dependents();
-    schedule<NT>(p, m, pair);
+    if (p.N <= 32) {
+        if (warp < 2 && !schedule_small(p, m, pair) && lane == 0) m->large = 1;
+        __syncthreads();
+    }
+    if (p.N > 32 || m->large) {
+        schedule<NT>(p, m, pair);
+        __syncthreads();
+    }
+    if (tid == 0 && rank == 0) ws_space(p).starts[pair] = {m->begin.n, m->begin.i, m->begin.kt, m->first.L, m->first.q0, 0};
     if (C8) {
 #pragma unroll 1
         for (int ch = tid; ch < 512; ch += NT) sc->inv_v[ch] = ch >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? ch : 0];
@@ -1282,44 +1335,46 @@ __global__ void __launch_bounds__(256) mla_queries_kernel(const __grid_constant_
     }
 }
 
-// Joins the parts of the items that were cut: the blocks x take the item that
-// bound x + 1 is in, if that is the first bound inside it. One warp a row.
+// Joins the parts of the items that were cut: the blocks x take the item that the begin of pair x + 1 is in, if that is
+// the first one inside it. One warp a row. Latency is what it costs (three rounds of loads; 6 us before the begins were
+// loaded together and came with their sequence): it follows the last part.
 constexpr int JOIN_ROWS = 4;
 template <class IT>
 __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_constant__ MlaParams p) {
+    const Space ws = ws_space(p);
+    const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), b = blockIdx.x + 1;
+    auto start = [&](int q) {
+        Start v = {-1, 0, 0, 0, 0, 0};
+        if (q < p.pairs) v = ws.starts[q];
+        return v;
+    };
     pdl_wait();
     pdl_launch_dependents();
-    const Space ws = ws_space(p);
-    const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
-    const int b = blockIdx.x + 1;
+    // Lane q has pair b - 1 + q and the one after it.
     const int active = *ws.active;
-    if (b >= active) return;
-    const Bound before = ws.bounds[b - 1], at = ws.bounds[b];
-    const bool same = before.n == at.n && before.i == at.i;
-    if (at.n >= p.N || at.kt == 0 || (same && before.kt > 0)) return;
-    const Seq s = load_seq(p, at.n);
-    const unsigned row = unsigned(at.i) * ROWS + r;
-    if (row >= unsigned(s.L) * unsigned(p.H)) return;
-    // Parts: the last of pair b - 1, then the first of each pair whose bound is inside the item, but for pairs without
-    // work (the next bound is their own). Lane q has part b - 1 + q0 + q.
+    Start me = start(b - 1 + lane), nx = start(b + lane);
+    const int n = __shfl_sync(0xFFFFFFFFu, nx.n, 0), i = __shfl_sync(0xFFFFFFFFu, nx.i, 0), kt = __shfl_sync(0xFFFFFFFFu, nx.kt, 0);
+    const unsigned L = __shfl_sync(0xFFFFFFFFu, nx.L, 0);
+    const int64_t q0 = __shfl_sync(0xFFFFFFFFu, nx.q0, 0);
+    const bool same = __shfl_sync(0xFFFFFFFFu, me.n == n && me.i == i, 0), cut = __shfl_sync(0xFFFFFFFFu, me.kt > 0, 0);
+    const unsigned row = unsigned(i) * ROWS + r;
+    if (b >= active || n >= p.N || kt == 0 || (same && cut) || row >= L * unsigned(p.H)) return;
+    // Parts: the last of pair b - 1, then the first of each pair that begins inside the item, but for pairs without
+    // work (the next one begins where they do).
     float mx = -INFINITY, l = 0.f;
     float4 o[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool more = true;
 #pragma unroll 1
-    for (int q0 = 0; more; q0 += 32) {
-        const int q = b - 1 + q0 + lane;
-        Bound me = {-1, 0, 0, 0}, nx = {-1, 0, 0, 0};
-        if (q < active) me = ws.bounds[q];
-        if (q + 1 < active) nx = ws.bounds[q + 1];
-        const bool in = q == b - 1 || (me.n == at.n && me.i == at.i && me.kt > 0);
+    for (int at = b - 1;; at += 32) {
+        const int q = at + lane;
+        const bool in = q == b - 1 || (q < active && me.n == n && me.i == i && me.kt > 0);
         const uint32_t run = __ballot_sync(0xFFFFFFFFu, in);
         const int count = run == 0xFFFFFFFFu ? 32 : __ffs(~run) - 1;
-        more = count == 32;
-        const bool work = lane < count && !(me.n == nx.n && me.i == nx.i && me.kt == nx.kt);
+        const bool work = lane < count && !(q + 1 < active && me.n == nx.n && me.i == nx.i && me.kt == nx.kt);
         const int64_t slot = (int64_t(q) * 2 + (q == b - 1 && !same ? 1 : 0)) * ROWS + r;
         const float2 ml = work ? ws.ml[slot] : make_float2(-INFINITY, 0.f);
+        const float* from = ws.o + slot * p.Dv;
         float top = ml.y == 0.f ? -INFINITY : ml.x;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
@@ -1331,24 +1386,36 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c].x *= back, o[c].y *= back, o[c].z *= back, o[c].w *= back;
         const float add = ml.y * f;
-#pragma unroll 4
-        for (int k = 0; k < count; ++k) {   // in order
-            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-            const int64_t sk = __shfl_sync(0xFFFFFFFFu, slot, k);
-            l += __shfl_sync(0xFFFFFFFFu, add, k);
-            if (fk != 0.f) {
+        float4 x[2][4];   // a part's row, the next one on its way
+        auto fetch = [&](int k, float4 (&y)[4]) {
+            const float* src = reinterpret_cast<const float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(from), k));
+            const bool has = __shfl_sync(0xFFFFFFFFu, f, k) != 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int ch = (c * 32 + lane) * 4;
-                    if (ch < p.Dv) {
-                        const float4 x = *reinterpret_cast<const float4*>(ws.o + sk * p.Dv + ch);
-                        o[c].x += x.x * fk, o[c].y += x.y * fk, o[c].z += x.z * fk, o[c].w += x.w * fk;
-                    }
-                }
+            for (int c = 0; c < 4; ++c) {
+                const int ch = (c * 32 + lane) * 4;
+                y[c] = has && ch < p.Dv ? __ldcg(reinterpret_cast<const float4*>(src + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
+        };
+        auto take = [&](int k, const float4 (&y)[4]) {   // in order
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            l += __shfl_sync(0xFFFFFFFFu, add, k);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c].x += y[c].x * fk, o[c].y += y[c].y * fk, o[c].z += y[c].z * fk, o[c].w += y[c].w * fk;
+        };
+        fetch(0, x[0]);
+#pragma unroll 1
+        for (int k = 0; k < count; k += 2) {
+            if (k + 1 < count) fetch(k + 1, x[1]);
+            take(k, x[0]);
+            if (k + 1 == count) break;
+            if (k + 2 < count) fetch(k + 2, x[0]);
+            take(k + 1, x[1]);
         }
+        if (count < 32) break;
+        me = start(at + 32 + lane);
+        nx = start(at + 33 + lane);
     }
-    const int64_t t = s.q0 + row / unsigned(p.H), head = row % unsigned(p.H);
+    const int64_t t = q0 + row / unsigned(p.H), head = row % unsigned(p.H);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs;
 #pragma unroll
