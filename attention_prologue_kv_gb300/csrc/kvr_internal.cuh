@@ -356,6 +356,7 @@ struct MlaParams {
     int ckv_scale_per_ch, k_scale_per_ch;
     float scale;                // softmax scale
     int pairs;                  // tensor-core kernel: CTA pairs of the grid
+    int q_flat;                 // its query rows are evenly spaced over heads and tokens
     int out_wide;               // its output rows lie on 32-byte boundaries
     const float* row_mul;       // power of two per row that its prepared queries lack, or NULL
     int runs, groups;           // its blocks hold whole halves of a step, whole groups of 8 keys

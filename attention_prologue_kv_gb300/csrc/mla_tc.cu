@@ -694,12 +694,12 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
             const uint8_t* k = static_cast<const uint8_t*>(p.kc) + slot * p.Dk * (p.k_kind == OUT16 ? 2 : 1) + (half * 4 + c4) * 16;
             if (slot >= 0 && half * 16 + 16 <= nc && half * 4 + 4 <= nr) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a.x[i] = ld_stream_v4(src + 64 * i);
-                a.rope = ld_stream_v4(k);
+                for (int i = 0; i < 4; ++i) a.x[i] = ld_ahead_v4(src + 64 * i);
+                a.rope = ld_ahead_v4(k);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a.x[i] = slot >= 0 && half * 16 + c4 + 4 * i < nc ? ld_stream_v4(src + 64 * i) : make_uint4(0, 0, 0, 0);
-                a.rope = slot >= 0 && half * 4 + c4 < nr ? ld_stream_v4(k) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) a.x[i] = slot >= 0 && half * 16 + c4 + 4 * i < nc ? ld_ahead_v4(src + 64 * i) : make_uint4(0, 0, 0, 0);
+                a.rope = slot >= 0 && half * 4 + c4 < nr ? ld_ahead_v4(k) : make_uint4(0, 0, 0, 0);
             }
         };
         auto store = [&](int kt, const Load& a) {
@@ -774,9 +774,9 @@ __device__ __forceinline__ void code_swaps(Ctx& c, int v, const Walk& w, int& j)
         const int64_t extra = wp == 0 ? slot[0] : (wp == 1 ? slot[1] : slot[2]);
         const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + (lane & 3) * 16;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) a[g] = slot[g] >= 0 && qa + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + slot[g] * p.Dv + qa) : make_uint4(0, 0, 0, 0);
-        a[4] = extra >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + extra * p.Dv + qb) : make_uint4(0, 0, 0, 0);
-        a[5] = wp == 0 && slot[3] >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_stream_v4(src + slot[3] * p.Dv + qb) : make_uint4(0, 0, 0, 0);
+        for (int g = 0; g < 4; ++g) a[g] = slot[g] >= 0 && qa + (lane & 3) * 16 < p.Dv ? ld_ahead_v4(src + slot[g] * p.Dv + qa) : make_uint4(0, 0, 0, 0);
+        a[4] = extra >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_ahead_v4(src + extra * p.Dv + qb) : make_uint4(0, 0, 0, 0);
+        a[5] = wp == 0 && slot[3] >= 0 && qb + (lane & 3) * 16 < p.Dv ? ld_ahead_v4(src + slot[3] * p.Dv + qb) : make_uint4(0, 0, 0, 0);
     };
     auto put = [&](uint32_t box, int g, const uint4& x) {
         st_shared_v4(box_at(box, g * 8 + sub, 2 * (lane & 3)), codes_to_halves<CK>(x.x, x.y));
@@ -814,14 +814,20 @@ __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int p
     const int nc = p.Dv / 8, nr = p.Dk / 8, ch = v & 7;
     const uint16_t *qn[TURNS], *qr[TURNS];
     uint32_t lives = 0;
+    const unsigned rows = unsigned(w.s.L) * unsigned(p.H), row0 = unsigned(w.i) * ROWS + c.rank * CROWS + (v >> 3);
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
-        const int r = i * AT_ONCE + (v >> 3);
-        const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
-        const bool live = r < CROWS && row < unsigned(w.s.L) * unsigned(p.H);
-        const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
-        qn[i] = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs + ch * 8;
-        qr[i] = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + ch * 8;
+        const unsigned row = row0 + i * AT_ONCE;
+        const bool live = i * AT_ONCE + (v >> 3) < CROWS && row < rows;
+        if (p.q_flat) {   // head after head, token after token
+            const int64_t at = live ? w.s.q0 * p.H + row : 0;
+            qn[i] = static_cast<const uint16_t*>(p.qn) + at * p.qn_hs + ch * 8;
+            qr[i] = static_cast<const uint16_t*>(p.qr) + at * p.qr_hs + ch * 8;
+        } else {
+            const int64_t t = live ? w.s.q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
+            qn[i] = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs + ch * 8;
+            qr[i] = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs + ch * 8;
+        }
         lives |= uint32_t(live) << i;
     }
     if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
@@ -1567,6 +1573,7 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
             p.qr_hs = p.Dk;
         }
     }
+    p.q_flat = p.qn_ts == p.H * p.qn_hs && p.qr_ts == p.H * p.qr_hs;
     const cudaError_t e = launch_pdl(kernel_of(dtype, p.ckv_kind, p.k_kind != OUT16), dim3(unsigned(p.pairs * 2)), dim3(NT),
                                      smem_for(p.ckv_kind), s, p, maps);
     if (e != cudaSuccess || p.pairs == 1) return e;
