@@ -561,11 +561,13 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  * 16 in an 8-bit cache), on 16-byte boundaries (q, out, caches; strides
  * multiples of 8) and with H <= 65536 run on the tensor cores, all others on a
  * plain kernel that is much slower.
- * Scores, softmax and sums are float32; the tensor-core kernel rounds each
- * probability to `dtype` for the second product, and with an 8-bit cache of
- * per-channel scale q / scale[c] to `dtype` for the first one, which moves a
- * score by up to one unit in the last place of `dtype` (relative to the terms'
- * size) and lse with it.
+ * Scores, softmax and sums are float32. The tensor-core kernel rounds each
+ * probability for the second product, to `dtype`, or to float16 with an 8-bit
+ * latent cache, whose products run on float16 (every code is exact there). A
+ * scale per channel goes into the query: q / scale[c] is rounded once, to
+ * float16 for the latent part and to `dtype` for the rotary part, which moves a
+ * score by up to one unit in the last place of that type (relative to the
+ * terms' size) and lse with it; one scale for all channels rounds nothing more.
  * out, lse and workspace must not overlap an input or one another. The result
  * of a call does not change from run to run on one GPU.
  */
