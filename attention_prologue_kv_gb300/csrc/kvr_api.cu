@@ -704,7 +704,7 @@ kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
     const bool tc = mla_tensor_cores(a);
     if (tc) {
         if (a->workspace == nullptr) return KVR_ERR_NULL;
-        if (!aligned(a->workspace, 16) || a->workspace_bytes < mla_tc_workspace(p, a->dtype)) return KVR_ERR_SHAPE;
+        if (!aligned(a->workspace, 32) || a->workspace_bytes < mla_tc_workspace(p, a->dtype)) return KVR_ERR_SHAPE;
     }
     (void)cudaGetLastError();
     return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));

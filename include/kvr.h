@@ -551,7 +551,7 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *   lse          optional out float32 [T, H]: log(sum_i exp(s[i])), -inf for a
  *                token that sees no key.
  *   workspace    device memory of kvr_mla_attention_workspace(args) bytes,
- *                16-byte aligned; it holds nothing between calls. Calls that can
+ *                32-byte aligned; it holds nothing between calls. Calls that can
  *                run at the same time need one each.
  *   dev_status   optional int32 device word (the bits above and
  *                KVR_DEVERR_TIMEOUT).

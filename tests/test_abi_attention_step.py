@@ -113,6 +113,7 @@ def mla_args(**kw):
     (dict(out=6 * M), N.KVR_ERR_ALIAS), (dict(lse=16 * M), N.KVR_ERR_ALIAS), (dict(workspace=16 * M, workspace_bytes=4096), N.KVR_ERR_ALIAS),
     (dict(workspace=None), N.KVR_ERR_NULL), (dict(), N.KVR_ERR_SHAPE),   # no room in the workspace
     (dict(workspace=64 * M + 8, workspace_bytes=1 << 40), N.KVR_ERR_SHAPE),
+    (dict(workspace=64 * M + 16, workspace_bytes=1 << 24), N.KVR_ERR_SHAPE),   # its rows are written 32 bytes at a time
     (dict(cache_d0=1 << 40, cache_d1=1 << 20), N.KVR_ERR_SHAPE),
     (dict(T=0, q_nope=None), N.KVR_OK), (dict(H=0, q_nope=None), N.KVR_OK), (dict(N=0, query_start=None), N.KVR_OK)])
 def test_mla_refusals(lib, kw, want):
