@@ -117,6 +117,13 @@ __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void ld_global_v8(const float* src, float* v) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(src)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // mbarrier, bulk async copy (TMA engine), programmatic dependent launch
 // ---------------------------------------------------------------------------

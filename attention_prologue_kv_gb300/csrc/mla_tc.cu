@@ -883,9 +883,10 @@ __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part,
     const int q0 = g * 128, q1 = min(q0 + 256 / G, p.Dv > 256 ? 256 : 128);
     if (!w.whole) {
         const Space ws = ws_space(p);
-        const int64_t at = (int64_t(pair) * 2 + (part ? 1 : 0)) * ROWS + c.rank * CROWS + r;
-        if (live && h == 0 && g == 0) ws.ml[at] = ml;
-        float* po = ws.o + at * p.Dv;
+        const int64_t slot = int64_t(pair) * 2 + (part ? 1 : 0);
+        const int in = c.rank * CROWS + r;
+        if (live && h == 0 && g == 0) ws.ml[slot * ROWS + in] = ml;
+        float* po = ws.o + slot * ROWS * p.Dv + in * 8;   // [8 channels of all rows]: a warp's stores are whole lines
 #pragma unroll 1
         for (int q = q0; q < q1; q += 32) {   // (a row without keys leaves what it may: the join skips it)
             float o[32];
@@ -899,11 +900,11 @@ __device__ __forceinline__ void output_part(Ctx& c, int tid, int pair, int part,
             }
             if (live && ch + 32 <= p.Dv) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t*>(o) + k);
+                for (int k = 0; k < 32; k += 8) st_global_v8(po + (ch + k) * ROWS, reinterpret_cast<const uint32_t*>(o) + k);
             } else if (live) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
-                    if (ch + k < p.Dv) st_global_v8(po + ch + k, reinterpret_cast<const uint32_t*>(o) + k);
+                    if (ch + k < p.Dv) st_global_v8(po + (ch + k) * ROWS, reinterpret_cast<const uint32_t*>(o) + k);
             }
         }
     } else {
@@ -1342,13 +1343,14 @@ __global__ void __launch_bounds__(256) mla_queries_kernel(const __grid_constant_
 }
 
 // Joins the parts of the items that were cut: the blocks x take the item that the begin of pair x + 1 is in, if that is
-// the first one inside it. One warp a row. Latency is what it costs (three rounds of loads; 6 us before the begins were
-// loaded together and came with their sequence): it follows the last part.
-constexpr int JOIN_ROWS = 4;
+// the first one inside it. A warp has 32 rows, a lane 16 channels of its row. Latency is what it costs, of two rounds of
+// loads: it follows the last part.
+constexpr int JOIN_WARPS = 4;   // of a block: 32 rows, 64 channels
 template <class IT>
-__global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_constant__ MlaParams p) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) mla_join_kernel(const __grid_constant__ MlaParams p) {
     const Space ws = ws_space(p);
-    const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), b = blockIdx.x + 1;
+    const int lane = threadIdx.x & 31, b = blockIdx.x + 1;
+    const int r = blockIdx.z * 32 + lane, ch = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * 16;
     auto start = [&](int q) {
         Start v = {-1, 0, 0, 0, 0, 0};
         if (q < p.pairs) v = ws.starts[q];
@@ -1363,14 +1365,36 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_c
     const unsigned L = __shfl_sync(0xFFFFFFFFu, nx.L, 0);
     const int64_t q0 = __shfl_sync(0xFFFFFFFFu, nx.q0, 0);
     const bool same = __shfl_sync(0xFFFFFFFFu, me.n == n && me.i == i, 0), cut = __shfl_sync(0xFFFFFFFFu, me.kt > 0, 0);
-    const unsigned row = unsigned(i) * ROWS + r;
-    if (b >= active || n >= p.N || kt == 0 || (same && cut) || row >= L * unsigned(p.H)) return;
+    const unsigned row = unsigned(i) * ROWS + r, rows = L * unsigned(p.H);
+    if (b >= active || n >= p.N || kt == 0 || (same && cut) || ch >= p.Dv || unsigned(i) * ROWS + (r & ~31) >= rows) return;
+    const bool live = row < rows, two = ch + 8 < p.Dv;
     // Parts: the last of pair b - 1, then the first of each pair that begins inside the item, but for pairs without
     // work (the next one begins where they do).
-    float mx = -INFINITY, l = 0.f;
-    float4 o[4];
+    struct Part {
+        float2 ml;
+        float o[16];
+    };
+    float mx = -INFINITY, l = 0.f, o[16];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < 16; ++c) o[c] = 0.f;
+    auto fetch = [&](int slot, Part& x) {
+        x.ml = make_float2(-INFINITY, 0.f);
+        if (live && slot >= 0) {
+            x.ml = ws.ml[int64_t(slot) * ROWS + r];
+            const float* from = ws.o + int64_t(slot) * ROWS * p.Dv + (ch * ROWS + r * 8);
+            ld_global_v8(from, x.o);
+            if (two) ld_global_v8(from + 8 * ROWS, x.o + 8);
+        }
+    };
+    auto take = [&](const Part& x) {   // in order; a part whose keys the row does not see has left nothing
+        if (x.ml.y == 0.f) return;
+        const float top = fmaxf(mx, x.ml.x);
+        const float back = mx == top ? 1.f : exp2_approx(mx - top), f = x.ml.x == top ? 1.f : exp2_approx(x.ml.x - top);
+        mx = top;
+        l = l * back + x.ml.y * f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[c] = o[c] * back + x.o[c] * f;
+    };
 #pragma unroll 1
     for (int at = b - 1;; at += 32) {
         const int q = at + lane;
@@ -1378,58 +1402,31 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS) mla_join_kernel(const __grid_c
         const uint32_t run = __ballot_sync(0xFFFFFFFFu, in);
         const int count = run == 0xFFFFFFFFu ? 32 : __ffs(~run) - 1;
         const bool work = lane < count && !(q + 1 < active && me.n == nx.n && me.i == nx.i && me.kt == nx.kt);
-        const int64_t slot = (int64_t(q) * 2 + (q == b - 1 && !same ? 1 : 0)) * ROWS + r;
-        const float2 ml = work ? ws.ml[slot] : make_float2(-INFINITY, 0.f);
-        const float* from = ws.o + slot * p.Dv;
-        float top = ml.y == 0.f ? -INFINITY : ml.x;
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-        top = fmaxf(top, mx);
-        const float back = mx == -INFINITY ? 0.f : exp2_approx(mx - top);
-        const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - top);
-        mx = top;
-        l *= back;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c].x *= back, o[c].y *= back, o[c].z *= back, o[c].w *= back;
-        const float add = ml.y * f;
-        float4 x[2][4];   // a part's row, the next one on its way
-        auto fetch = [&](int k, float4 (&y)[4]) {
-            const float* src = reinterpret_cast<const float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(from), k));
-            const bool has = __shfl_sync(0xFFFFFFFFu, f, k) != 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int ch = (c * 32 + lane) * 4;
-                y[c] = has && ch < p.Dv ? __ldcg(reinterpret_cast<const float4*>(src + ch)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        };
-        auto take = [&](int k, const float4 (&y)[4]) {   // in order
-            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-            l += __shfl_sync(0xFFFFFFFFu, add, k);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c].x += y[c].x * fk, o[c].y += y[c].y * fk, o[c].z += y[c].z * fk, o[c].w += y[c].w * fk;
-        };
-        fetch(0, x[0]);
+        const int slot = work ? q * 2 + (q == b - 1 && !same ? 1 : 0) : -1;
+        Part x[2];   // a part, the next one on its way
+        fetch(__shfl_sync(0xFFFFFFFFu, slot, 0), x[0]);
 #pragma unroll 1
         for (int k = 0; k < count; k += 2) {
-            if (k + 1 < count) fetch(k + 1, x[1]);
-            take(k, x[0]);
+            if (k + 1 < count) fetch(__shfl_sync(0xFFFFFFFFu, slot, k + 1), x[1]);
+            take(x[0]);
             if (k + 1 == count) break;
-            if (k + 2 < count) fetch(k + 2, x[0]);
-            take(k + 1, x[1]);
+            if (k + 2 < count) fetch(__shfl_sync(0xFFFFFFFFu, slot, k + 2), x[0]);
+            take(x[1]);
         }
         if (count < 32) break;
         me = start(at + 32 + lane);
         nx = start(at + 33 + lane);
     }
+    if (!live) return;
     const int64_t t = q0 + row / unsigned(p.H), head = row % unsigned(p.H);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + head * p.o_hs + ch;
+    uint32_t u[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int ch = (c * 32 + lane) * 4;
-        if (ch < p.Dv) *reinterpret_cast<uint2*>(out + ch) = make_uint2(IT::pack(o[c].x * inv, o[c].y * inv), IT::pack(o[c].z * inv, o[c].w * inv));
-    }
-    if (lane == 0 && p.lse != nullptr) p.lse[t * p.H + head] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+    for (int c = 0; c < 8; ++c) u[c] = IT::pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+    *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (two) *reinterpret_cast<uint4*>(out + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+    if (ch == 0 && p.lse != nullptr) p.lse[t * p.H + head] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
@@ -1577,7 +1574,9 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     const cudaError_t e = launch_pdl(kernel_of(dtype, p.ckv_kind, p.k_kind != OUT16), dim3(unsigned(p.pairs * 2)), dim3(NT),
                                      smem_for(p.ckv_kind), s, p, maps);
     if (e != cudaSuccess || p.pairs == 1) return e;
-    const dim3 grid(unsigned(p.pairs - 1), ROWS / JOIN_ROWS), block(32 * JOIN_ROWS);
+    // (no item has more rows than the call)
+    const int64_t groups = (p.T * p.H + 31) / 32;
+    const dim3 grid(unsigned(p.pairs - 1), unsigned(p.Dv + 63) / 64, unsigned(groups < ROWS / 32 ? groups : ROWS / 32)), block(32 * JOIN_WARPS);
     return dtype == KVR_BF16 ? launch_pdl(mla_join_kernel<BF16>, grid, block, 0, s, p) : launch_pdl(mla_join_kernel<F16>, grid, block, 0, s, p);
 }
 
