@@ -47,14 +47,14 @@ def _stream(stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _kv_rows(kv):
+def _kv_rows(kv, name="kv"):
     """(Bkv, Skv, row stride in elements) of a [Bkv,1,Skv,D] / [Bkv,Skv,D] / [T,D]
     tensor whose rows are uniformly strided and whose last dim is dense."""
     if kv.stride(-1) != 1:
-        raise ValueError("kv must be dense along its last dimension")
+        raise ValueError("%s must be dense along its last dimension" % name)
     if kv.dim() == 4:
         if kv.shape[1] != 1:
-            raise ValueError("kv must be [Bkv, 1, Skv, D]: the head axis N is 1")
+            raise ValueError("%s must be [Bkv, 1, Skv, D]: the head axis N is 1" % name)
         B, S = kv.shape[0], kv.shape[2]
         sb, ss = kv.stride(0), kv.stride(2)
     elif kv.dim() == 3:
@@ -64,10 +64,10 @@ def _kv_rows(kv):
         B, S = kv.shape[0], 1
         sb, ss = kv.stride(0), kv.stride(0)
     else:
-        raise ValueError("kv must be 2-D, 3-D or 4-D")
+        raise ValueError("%s must be 2-D, 3-D or 4-D" % name)
     stride = ss if S > 1 else sb
     if B > 1 and S > 0 and sb != S * stride:
-        raise ValueError("kv rows must be uniformly strided")
+        raise ValueError("%s rows must be uniformly strided" % name)
     return B, S, stride
 
 
@@ -540,7 +540,7 @@ def prepare_kv_cache_read(ckv_cache, k_cache, index, out, *, cache_mode="PA_BSND
     _one_device(out.device, dict(ckv_cache=ckv_cache, k_cache=k_cache, index=index, ckv_scale=ckv_scale, k_scale=k_scale,
                                  dev_status=dev_status))
     pair = _cache_pair(ckv_cache, k_cache, ckv_scale, k_scale, cache_mode, out.dtype)
-    B, S, stride = _kv_rows(out)
+    B, S, stride = _kv_rows(out, "out")
     D = pair["Dv"] + pair["Dk"]
     if out.shape[-1] != D:
         raise ValueError("out rows must have Dv + Dk = %d elements, got %d" % (D, out.shape[-1]))
