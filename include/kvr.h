@@ -524,7 +524,7 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *                [query_start[n], query_start[n + 1]) of q and out. Rows outside
  *                every sequence are left as they were. A sequence where it
  *                decreases or leaves [0, T] is left out (KVR_DEVERR_QUERY); rows
- *                that two of the others then share get one of the two results.
+ *                that two of the others then share get elements of either result.
  *   key_length   int64 [N]: keys of the sequence, its new tokens among them (as
  *                qsa_prepare's). A negative one, or one beyond the block table (the
  *                cache batch in Norm mode): the sequence is left out
@@ -557,7 +557,7 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *                KVR_DEVERR_TIMEOUT).
  *
  * Limits: T, H, N >= 0; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256; keys of a
- * sequence < 2^30. Rows of at most 512 + 64 channels, both multiples of 8 (of
+ * sequence <= 2^24 (one that has more is left out, KVR_DEVERR_KEY_LENGTH). Rows of at most 512 + 64 channels, both multiples of 8 (of
  * 16 in an 8-bit cache), on 16-byte boundaries (q, out, caches; strides
  * multiples of 8) and with H <= 65536 run on the tensor cores, all others on a
  * plain kernel that is much slower.

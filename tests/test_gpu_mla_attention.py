@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import attention_prologue_kv_gb300 as kvr
-from attention_helpers import SENTINEL, check_mla, mla_case, on_tensor_cores, oracle_mla, rounded_query, run_mla
+from attention_prologue_kv_gb300 import _native as N
+from attention_helpers import SENTINEL, check_mla, half_step, mla_case, on_tensor_cores, oracle_mla, rounded_query, run_mla
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,23 @@ def test_empty_problems():
                           softmax_scale=1.0)
         torch.cuda.synchronize()
         assert (out == SENTINEL).all()
+
+
+def test_most_keys():
+    """2^24 keys (a table that names one block over and over: the softmax is that of the block alone) and one more.
+
+    A part sums 2^24 / 76 keys, 16 an instruction into the output's sum and two at a time into a thread's share of l: fewer than 2^15
+    additions of 2^-23 each, in the sum and in what it is divided by, so 2^-7 of the weights' sum of magnitudes."""
+    d1, reps = 4096, 4096
+    c = mla_case([1], [d1], H=3, block_size=d1, seed=31, causal=False)
+    want, lse, _, A, B = oracle_mla(c)
+    c.table = c.table[:, :1].repeat(1, reps + 1)
+    c.key_length = torch.tensor([d1 * reps])
+    out, ls, st = run_mla(c)
+    assert st == 0
+    u, ds = half_step(c.q_nope.dtype), 2.0 ** -17 * B + 2.0 ** -19   # (a score's error, as in check_mla)
+    assert np.all(np.abs(out - want) <= (2 * ds[..., None] + 2.0 ** -7 + u) * A * (1 + u) + u * np.abs(want))
+    assert np.all(np.abs(ls - lse - np.log(reps)) <= ds + 2.0 ** -8 + 2.0 ** -23 * np.abs(ls))
+    c.key_length = torch.tensor([d1 * reps + 1])
+    out, ls, st = run_mla(c)
+    assert st == N.KVR_DEVERR_KEY_LENGTH and np.all(out == SENTINEL) and np.all(ls == SENTINEL)
