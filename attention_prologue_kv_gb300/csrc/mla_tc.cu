@@ -405,12 +405,14 @@ struct Ctx {
     volatile int* abort;
     bool ok;
 
-    // A wait that gives up (one second) poisons the CTA: the others give up at their first look, and every role
-    // runs its loops to the end without waiting, so that no barrier is left with threads missing.
+    // A wait that gives up (one second) poisons the CTA: the others give up at their first look. The warps that start TMA
+    // copies then stop; every other role runs its loops to the end without waiting, so that no barrier is left with
+    // threads missing.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
         if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort) && ok;
         __syncwarp();
     }
+    __device__ __forceinline__ bool gone() const { return __any_sync(0xFFFFFFFFu, !ok); }
     __device__ __forceinline__ uint32_t stage(int st) const { return base + OFF_K + uint32_t(st) * STAGE_BYTES; }
     // This warp's shared-memory writes are done: tell the MMA warp of the pair.
     __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -445,7 +447,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     Rows rows(p);
     Walk w(p, m);
 #pragma unroll 1
-    while (w.next()) {
+    while (w.next() && !c.gone()) {
         rows.begin(w, lane, lane, halves);
 #pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
@@ -473,6 +475,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                     pend = -1;
                 }
                 c.wait(bar, parity);
+                if (c.gone()) break;
             }
             if (!SWAP) {
                 const uint32_t theirs = __ballot_sync(0xFFFFFFFFu, (mine ? lo : hi) >= 0);
@@ -582,7 +585,7 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
     int j = 0, fixed = 0;
     Walk w(p, m);
 #pragma unroll 1
-    while (w.next()) {
+    while (w.next() && !c.gone()) {
         const int n = w.n, K = w.s.K;
         int base = w.kt0 - 32, own = -1, other = -1;   // first rows of this lane's step, base + lane
 #pragma unroll 1
@@ -599,6 +602,7 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
             const uint32_t stage = c.stage(st);
             if (SWAP) c.wait(&m->s_full[j & 1], (j >> 1) & 1);
             else if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+            if (c.gone()) break;
             if (!SWAP && lane == 0) {
                 m->held[st][mine] = live;
                 m->held[st][mine ^ 1] = row2 < 0 ? 0u : (left2 >= CKEYS ? 0xFFFFFFFFu : (1u << left2) - 1u);
@@ -1263,7 +1267,11 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
             query_warps<CK>(c, tid - 384);
         }
     }
-    if (!c.ok && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
+    if (!c.ok) {
+        if (p.status != nullptr) atomicOr(p.status, KVR_DEVERR_TIMEOUT);
+        const uint64_t t0 = globaltimer_ns();   // copies in flight land in microseconds
+        while (globaltimer_ns() - t0 < 10000000) __nanosleep(1000);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
