@@ -640,13 +640,12 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
 // of 8 rows, so that a warp's stores fill the banks. The next step's loads are in flight meanwhile. Where blocks hold whole
 // groups of 8 keys, lane i looks up a group's first row for step base + i, once for 32 steps.
 struct Group {
-    int64_t first;   // of step base + lane
-    __device__ __forceinline__ void look(const MlaParams& p, int n, int K, int step, int key) { first = key_row(p, n, K, step * KEYS + key); }
-    __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(0xFFFFFFFFu, first, i); }
+    int first;   // of step base + lane
+    __device__ __forceinline__ void look(const MlaParams& p, int n, int K, int step, int key) { first = int(key_row(p, n, K, step * KEYS + key)); }
+    __device__ __forceinline__ int of(int i) const { return __shfl_sync(0xFFFFFFFFu, first, i); }
 };
-// Of 8 keys from `key` on, which exist, given the first one's row.
-__device__ __forceinline__ uint32_t group_bits(int64_t first, int K, int key) {
-    const int left = K - key;
+// Of 8 keys, which exist, given the first one's row and the keys that are left from it on.
+__device__ __forceinline__ uint32_t group_bits(int first, int left) {
     return first < 0 ? 0u : (left >= 8 ? 0xFFu : (1u << max(left, 0)) - 1u);
 }
 
@@ -660,6 +659,10 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
     const int mine = int(c.rank) * CKEYS + wp * 8, theirs = mine ^ CKEYS;   // first keys of the groups
     const int nc = p.Dv / 16, nr = p.k_kind == OUT16 ? p.Dk / 8 : p.Dk / 16, nb = c.nb - half * 4;
     const uint32_t at0 = box_at(0, tk, 2 * c4), at1 = box_at(0, tk, 2 * c4 + 1);   // this lane's places in a box
+    const bool full = half * 16 + 16 <= nc && half * 4 + 4 <= nr;   // all this lane's pieces exist
+    const int kbytes = p.Dk * (p.k_kind == OUT16 ? 2 : 1);
+    const uint8_t* codes = static_cast<const uint8_t*>(p.ckv) + half * 256 + c4 * 16;
+    const uint8_t* ropes = static_cast<const uint8_t*>(p.kc) + (half * 4 + c4) * 16;
     int j = 0;
     Walk w(p, m);
 #pragma unroll 1
@@ -669,7 +672,7 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
         Group own, other;
         struct Load {
             uint4 x[4], rope;
-            uint32_t held;   // the groups' keys that exist: of this CTA (byte 0) and the other (byte 1)
+            uint32_t held;   // which keys of a group exist: of this CTA's (half 0) or of the other's (half 1)
         };
         auto load = [&](int kt, Load& a) {
             int64_t slot;
@@ -677,26 +680,23 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
                 if (kt - base >= 32) {
                     base = kt;
                     own.look(p, n, K, base + lane, mine);
-                    other.look(p, n, K, base + lane, theirs);
+                    if (half) other.look(p, n, K, base + lane, theirs);
                 }
-                const int64_t f = own.of(kt - base), g = other.of(kt - base);
-                a.held = group_bits(f, K, kt * KEYS + mine) | group_bits(g, K, kt * KEYS + theirs) << 8;
-                slot = a.held >> sub & 1 ? f + sub : -1;
+                const int f = own.of(kt - base), left = K - kt * KEYS;
+                if (half) a.held = group_bits(other.of(kt - base), left - theirs);
+                else a.held = group_bits(f, left - mine);
+                slot = f >= 0 && sub < left - mine ? f + sub : -1;
             } else {
                 slot = key_row(p, n, K, kt * KEYS + mine + sub);
-                auto bits = [](uint32_t b) {   // every fourth bit
-                    b &= 0x11111111u;
-                    b = (b | b >> 3) & 0x03030303u;
-                    b = (b | b >> 6) & 0x000F000Fu;
-                    return (b | b >> 12) & 0xFFu;
-                };
-                const uint32_t l = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-                const uint32_t o = __ballot_sync(0xFFFFFFFFu, key_row(p, n, K, kt * KEYS + theirs + sub) >= 0);
-                a.held = bits(l) | bits(o) << 8;
+                // Every fourth bit.
+                uint32_t b = __ballot_sync(0xFFFFFFFFu, (half ? key_row(p, n, K, kt * KEYS + theirs + sub) : slot) >= 0) & 0x11111111u;
+                b = (b | b >> 3) & 0x03030303u;
+                b = (b | b >> 6) & 0x000F000Fu;
+                a.held = (b | b >> 12) & 0xFFu;
             }
-            const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + slot * p.Dv + half * 256 + c4 * 16;
-            const uint8_t* k = static_cast<const uint8_t*>(p.kc) + slot * p.Dk * (p.k_kind == OUT16 ? 2 : 1) + (half * 4 + c4) * 16;
-            if (slot >= 0 && half * 16 + 16 <= nc && half * 4 + 4 <= nr) {
+            const uint8_t* src = codes + slot * p.Dv;
+            const uint8_t* k = ropes + slot * kbytes;
+            if (full && slot >= 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a.x[i] = ld_ahead_v4(src + 64 * i);
                 a.rope = ld_ahead_v4(k);
@@ -723,10 +723,7 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
                 st_shared_v4(box + at0, dec8x8<IT>(p.k_kind, a.rope.x, a.rope.y));
                 st_shared_v4(box + at1, dec8x8<IT>(p.k_kind, a.rope.z, a.rope.w));
             }
-            if (lane == 0 && half == 0) {
-                reinterpret_cast<uint8_t*>(&m->held[st][c.rank])[wp] = uint8_t(a.held);
-                reinterpret_cast<uint8_t*>(&m->held[st][c.rank ^ 1])[wp] = uint8_t(a.held >> 8);
-            }
+            if (lane == 0) reinterpret_cast<uint8_t*>(&m->held[st][int(c.rank) ^ half])[wp] = uint8_t(a.held);
             c.arrive(&m->k_full[st]);
             ++j;
         };
@@ -767,7 +764,7 @@ __device__ __forceinline__ void code_swaps(Ctx& c, int v, const Walk& w, int& j)
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int64_t f = group[g].of(kt - base);
+                const int f = group[g].of(kt - base);
                 slot[g] = f >= 0 && kt * KEYS + theirs * CKEYS + g * 8 + sub < K ? f + sub : -1;
             }
         } else {
@@ -1540,8 +1537,8 @@ cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s) {
     Maps maps = {};
     p.box_rows = 0;
     p.runs = p.table == nullptr || p.d1 % CKEYS == 0;
-    p.groups = p.table == nullptr || p.d1 % 8 == 0;
     const int64_t rows = p.d0 * p.d1;
+    p.groups = (p.table == nullptr || p.d1 % 8 == 0) && rows < int64_t(1) << 31;
     if (p.ckv_kind == OUT16 && p.k_kind == OUT16 && p.Dv % 64 == 0 && p.Dk == 64 && rows < (int64_t(1) << 31) - 64) {
         int r = 32;
         while (p.table != nullptr && r > 1 && p.d1 % r != 0) r /= 2;
