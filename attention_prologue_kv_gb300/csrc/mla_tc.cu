@@ -663,7 +663,7 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
     const int kbytes = p.Dk * (p.k_kind == OUT16 ? 2 : 1);
     const uint8_t* codes = static_cast<const uint8_t*>(p.ckv) + half * 256 + c4 * 16;
     const uint8_t* ropes = static_cast<const uint8_t*>(p.kc) + (half * 4 + c4) * 16;
-    int j = 0;
+    int st = 0, turn = 0;
     Walk w(p, m);
 #pragma unroll 1
     while (w.next()) {
@@ -706,17 +706,16 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
                 a.rope = slot >= 0 && half * 4 + c4 < nr ? ld_ahead_v4(k) : make_uint4(0, 0, 0, 0);
             }
         };
-        auto store = [&](int kt, const Load& a) {
-            const int st = j % STAGES;
+        auto store = [&](const Load& a) {
             const uint32_t stage = c.stage(st);
-            if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
+            if (turn > 0) c.wait(&m->empty[st], (turn & 1) ^ 1);
+            const uint32_t to = stage + half * (4 * KBOX), box = stage + 8 * KBOX;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < nb) {
-                    st_shared_v4(stage + (half * 4 + i) * KBOX + at0, codes_to_halves<CK>(a.x[i].x, a.x[i].y));
-                    st_shared_v4(stage + (half * 4 + i) * KBOX + at1, codes_to_halves<CK>(a.x[i].z, a.x[i].w));
+                    st_shared_v4(to + i * KBOX + at0, codes_to_halves<CK>(a.x[i].x, a.x[i].y));
+                    st_shared_v4(to + i * KBOX + at1, codes_to_halves<CK>(a.x[i].z, a.x[i].w));
                 }
-            const uint32_t box = stage + 8 * KBOX;
             if (p.k_kind == OUT16) {   // eight pieces a row: four of each half
                 st_shared_v4(box_at(box, tk, half * 4 + c4), a.rope);
             } else if (half == 0) {    // four pieces a row
@@ -725,17 +724,17 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
             }
             if (lane == 0) reinterpret_cast<uint8_t*>(&m->held[st][int(c.rank) ^ half])[wp] = uint8_t(a.held);
             c.arrive(&m->k_full[st]);
-            ++j;
+            if (++st == STAGES) st = 0, ++turn;
         };
         Load x, y;
         load(kt0, x);
 #pragma unroll 1
         for (int kt = kt0; kt < kt1; kt += 2) {   // two steps a turn: the loads in flight need no copies
             if (kt + 1 < kt1) load(kt + 1, y);
-            store(kt, x);
+            store(x);
             if (kt + 1 == kt1) break;
             if (kt + 2 < kt1) load(kt + 2, x);
-            store(kt + 1, y);
+            store(y);
         }
     }
 }
