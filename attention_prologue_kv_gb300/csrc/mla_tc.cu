@@ -30,6 +30,12 @@
 // CTA pairs, wherever that falls inside an item. A part of an item leaves
 // its O, m and l in the workspace, and a second kernel joins them in a fixed
 // order, so results do not change from run to run.
+//
+// Measured: 512 tokens x 128 heads over 16384 keys 1540 us (1.5 PFLOP/s, 80% of the measured bf16 rate; a step takes
+// 0.85 us, in which the SM's shared memory moves 210 KB); 256 sequences of one token, 128 heads, 1-4095 keys 158 us (4.5 TB/s,
+// 66% of the copy rate; a step 0.89 us, a part's queries and output 5 us); 61 sequences of one token over up to 16384
+// keys in E4M3 168 us; one sequence of 1000 keys, 16 heads 14.7 us. Steps of 128 keys with two of them in flight were
+// slower (1826 us): a stage's load, scores, softmax and second product follow one another.
 #include <mutex>
 #include <type_traits>
 
