@@ -134,3 +134,62 @@ def test_most_keys():
     c.key_length = torch.tensor([d1 * reps + 1])
     out, ls, st = run_mla(c)
     assert st == N.KVR_DEVERR_KEY_LENGTH and np.all(out == SENTINEL) and np.all(ls == SENTINEL)
+
+
+@pytest.mark.parametrize("cache", ["int8", "fp8_e4m3fn"])
+@pytest.mark.parametrize("block_size", [1, 3, 8, 24, 100])
+def test_block_sizes_of_codes(block_size, cache):
+    check(mla_case([3, 1], [401, 130], 8, block_size=block_size, cache=cache, k_cache=cache, seed=block_size))
+
+
+@pytest.mark.parametrize("block_size", [3, 16, 64])
+@pytest.mark.parametrize("k_cache,scale_len", [("int8", 1), ("fp8_e5m2", 0)])
+def test_codes_in_the_rotary_part_alone(k_cache, scale_len, block_size):
+    check(mla_case([3, 1], [401, 130], 8, block_size=block_size, k_cache=k_cache, k_scale_len=scale_len, seed=block_size))
+
+
+@pytest.mark.parametrize("cache", [None, "int8"])
+def test_many_sequences(cache):
+    """More than a warp holds, most of them short, some without new tokens or keys."""
+    new, keys = [(n * 7) % 4 for n in range(700)], [(n * 37) % 90 for n in range(700)]
+    check(mla_case(new, keys, 3, cache=cache, seed=12))
+
+
+@pytest.mark.parametrize("H", [65536, 65537])
+def test_most_heads(H):
+    check(mla_case([2], [70], H, Dv=8, Dk=8, seed=13))
+
+
+def far(t, rows):
+    """The cache `t` [d0, d1, 1, D] as the last blocks of one of `rows` rows that holds nothing else."""
+    d0, d1, _, D = t.shape
+    big = torch.empty(-(-rows // d1), d1, 1, D, dtype=t.dtype, device="cuda")
+    big[-d0:].copy_(t)
+    return big
+
+
+@pytest.mark.parametrize("Dv,Dk,rows,cache", [
+    (512, 64, 9 << 20, None), (512, 64, 9 << 20, "int8"), (8, 8, (1 << 31) + 1000, None), (16, 16, (1 << 31) + 1000, "int8")])
+def test_far_rows(Dv, Dk, rows, cache):
+    """Offsets behind 2^32 elements, row numbers behind 2^31: the same bits as near the cache's begin."""
+    c = mla_case([3, 1], [401, 130], 8, Dv, Dk, block_size=32, cache=cache, k_cache=cache, seed=14)
+    if torch.cuda.mem_get_info()[0] < 2 * rows * (Dv + Dk) * c.ckv.element_size():
+        pytest.skip("not enough memory on this GPU")
+    want = run_mla(c)
+    d0 = c.ckv.shape[0]
+    c.ckv, c.k = far(c.ckv, rows), far(c.k, rows)
+    c.table = torch.where(c.table < 0, c.table, c.table + (c.ckv.shape[0] - d0))
+    got = run_mla(c)
+    assert got[2] == 0
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    index = torch.tensor([rows - 1, rows - 33, -1])
+    out = torch.full((3, Dv + Dk), SENTINEL, device="cuda", dtype=c.q_nope.dtype)
+    kvr.kv_cache_read(c.ckv, c.k, index.cuda(), out, ckv_scale=None if c.ckv_scale is None else c.ckv_scale.cuda(),
+                      k_scale=None if c.k_scale is None else c.k_scale.cuda())
+    near = torch.full_like(out, SENTINEL)
+    kvr.kv_cache_read(c.ckv[-d0:], c.k[-d0:], (index - (c.ckv.shape[0] - d0) * 32).clamp(min=-1).cuda(), near,
+                      ckv_scale=None if c.ckv_scale is None else c.ckv_scale.cuda(),
+                      k_scale=None if c.k_scale is None else c.k_scale.cuda())
+    assert torch.equal(out.view(torch.int16), near.view(torch.int16))
+    c.ckv = c.k = None
+    torch.cuda.empty_cache()   # tens of GB
