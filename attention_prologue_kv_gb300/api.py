@@ -416,6 +416,7 @@ class BoundCall(PreparedCall):
     which need not be the current one when the call is made."""
 
     workspace = None
+    _home = None   # the stream that an own workspace was taken on
 
     def __init__(self, fn, args, name, keep, device):
         super().__init__(fn, args, name, keep)
@@ -424,11 +425,22 @@ class BoundCall(PreparedCall):
 
     def __call__(self, stream=None):
         if stream is None and torch._C._cuda_getDevice() == self._index:   # the serving loop's call, kept short
-            st = self._fn(self._ref, torch._C._cuda_getCurrentRawStream(self._index))
+            raw = torch._C._cuda_getCurrentRawStream(self._index)
+            st = self._fn(self._ref, raw)
             if st != N.KVR_OK:
                 raise KvrError(st, self._name)
         else:
             _launch(self._fn, self._ref, self._name, self._device, stream)
+            raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream(stream)
+        if self._home is not None and raw != self._home:
+            self._used_on(raw)
+
+    def _used_on(self, raw):
+        """An own workspace, used on another stream than it was taken on, must not go to others before that one is done
+        (a graph's captured calls keep this object instead)."""
+        with torch.cuda.device(self._index):
+            if not torch.cuda.is_current_stream_capturing():
+                self.workspace.record_stream(torch.cuda.ExternalStream(raw, device=self._device))
 
 
 def _heads(t, name, dtype, T=None, H=None):
@@ -612,17 +624,19 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
                   block_table=_ptr(block_table, "block_table"), max_blocks=max_blocks, softmax_scale=float(softmax_scale),
                   causal=1 if causal else 0, out=out.data_ptr(), out_token_stride=o_ts, out_head_stride=o_hs,
                   lse=_ptr(lse, "lse"), dev_status=_ptr(dev_status, "dev_status"), **pair)
+    home = None
     with torch.cuda.device(device):
         need = N.lib().kvr_mla_attention_workspace(ctypes.byref(a))
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            home = torch._C._cuda_getCurrentRawStream(device.index)
     if workspace is not None:
         a.workspace = _ptr(workspace, "workspace")
         a.workspace_bytes = workspace.numel() * workspace.element_size()
     keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, ckv_scale, k_scale, lse, workspace,
             dev_status)
     call = BoundCall(N.lib().mla_attention, a, "mla_attention", keep, device)
-    call.workspace = workspace
+    call.workspace, call._home = workspace, home
     return call
 
 
@@ -651,10 +665,6 @@ def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, 
                                  softmax_scale=softmax_scale, cache_mode=cache_mode, causal=causal, ckv_scale=ckv_scale,
                                  k_scale=k_scale, lse=lse, workspace=workspace, dev_status=dev_status)
     call(stream)
-    if workspace is None and stream is not None and call.workspace is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=q_nope.device)
-        call.workspace.record_stream(stream)   # taken on the current stream, used on another
 
 
 def device_copy(dst, src, stream=None):

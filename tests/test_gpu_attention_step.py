@@ -176,6 +176,32 @@ def test_streams():
     assert np.array_equal(got[0], ref[0])
 
 
+def test_own_workspace_outlives_a_call_on_another_stream():
+    """A bound call's own workspace goes to nobody else while a call of it waits or runs on another stream."""
+    c = mla_case([2, 1], [300, 90], 8, block_size=32, seed=22)
+    ref = run_mla(c)
+    args = [t.cuda().contiguous() for t in (c.q_nope, c.q_rope, c.ckv, c.k, c.table, c.query_start, c.key_length)]
+    for given in (True, False):
+        out = torch.zeros_like(args[0])
+        call = kvr.prepare_mla_attention(*args, out, softmax_scale=c.scale)
+        at, size = call.workspace.data_ptr(), call.workspace.numel()
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(100_000_000)   # tens of milliseconds
+            if not given:
+                call()
+        if given:
+            call(st)
+        del call
+        others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert not st.query(), "the stream was done too early for this test"
+        assert all(o.data_ptr() != at for o in others)
+        torch.cuda.synchronize()
+        assert np.array_equal(out.double().cpu().numpy(), ref[0])
+        del others
+
+
 def test_bound_calls_follow_their_buffers():
     g = torch.Generator().manual_seed(5)
     q = torch.randn(4, 8, 64, generator=g).bfloat16().cuda()
