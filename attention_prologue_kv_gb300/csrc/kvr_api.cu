@@ -11,7 +11,7 @@
 
 #include <algorithm>
 
-#include "kvr_internal.cuh"
+#include "attention_step.cuh"
 
 namespace kvr {
 

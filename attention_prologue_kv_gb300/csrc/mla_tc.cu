@@ -328,7 +328,7 @@ template <class IT>
 __device__ __forceinline__ uint4 dec8x8(int kind, uint32_t a, uint32_t b) {
     const uint4 h = kind == OUT_I8 ? codes_to_halves<OUT_I8>(a, b)
                                    : (kind == OUT_E5M2 ? codes_to_halves<OUT_E5M2>(a, b) : codes_to_halves<OUT_E4M3>(a, b));
-    if constexpr (!IT::is_bf16) return h;
+    if constexpr (!is_bf16<IT>) return h;
     return make_uint4(BF16::pack(F16::lo(h.x), F16::hi(h.x)), BF16::pack(F16::lo(h.y), F16::hi(h.y)),
                       BF16::pack(F16::lo(h.z), F16::hi(h.z)), BF16::pack(F16::lo(h.w), F16::hi(h.w)));
 }
@@ -1102,8 +1102,8 @@ __device__ __forceinline__ void mma_warp(Ctx& c) {
     const MlaParams& p = c.p;
     Misc* m = c.m;
     constexpr int STAGES = stages_of<C8>();
-    constexpr bool half = C8 || !IT::is_bf16;   // type of the latent operands
-    constexpr uint32_t id_n = tc_idesc(ROWS, KEYS, !half, false), id_r = tc_idesc(ROWS, KEYS, IT::is_bf16, false),
+    constexpr bool half = C8 || !is_bf16<IT>;   // type of the latent operands
+    constexpr uint32_t id_n = tc_idesc(ROWS, KEYS, !half, false), id_r = tc_idesc(ROWS, KEYS, is_bf16<IT>, false),
                        id_o = tc_idesc(ROWS, 256, !half, true);
     constexpr bool split = C8 || K8;
     const bool leader = elect_one(), two = p.Dv > 256;

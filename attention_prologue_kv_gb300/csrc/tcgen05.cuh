@@ -4,7 +4,7 @@
 
 #include <cuda.h>
 
-#include "kvr_internal.cuh"
+#include "attention_step.cuh"
 
 namespace kvr {
 
