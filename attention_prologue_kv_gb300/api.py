@@ -657,7 +657,9 @@ def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, 
     j of L sees the keys before key_length - L + j + 1. A token that sees no
     key gets zeros and lse -inf; rows outside every sequence stay as they
     were. lse: optional float32 [T, H], the natural logarithm of the sum.
-    8-bit caches take their write scales (code / scale).
+    8-bit caches take their write scales (code / scale). Keys within
+    key_length are taken to be finite: an infinity or NaN may reach every token
+    of its sequence. At most 2^24 keys a sequence.
     `workspace` (optional, device memory of kvr_mla_attention_workspace
     bytes) must not be shared by calls that can run at the same time; without
     it the call takes one from PyTorch's allocator."""
