@@ -68,7 +68,15 @@ def _kv_rows(kv, name="kv"):
     stride = ss if S > 1 else sb
     if B > 1 and S > 0 and sb != S * stride:
         raise ValueError("%s rows must be uniformly strided" % name)
+    _apart(B * S, stride, name)
     return B, S, stride
+
+
+def _apart(rows, stride, name):
+    """Refuse rows that are one row expanded: the library reads a row stride of 0 as dense rows, which such a tensor's
+    storage does not hold."""
+    if rows > 1 and stride == 0:
+        raise ValueError("%s must not be one row expanded: its rows need memory each" % name)
 
 
 def _cache_dims(c, name):
@@ -381,6 +389,7 @@ def dynamic_quant(q_nope, q_out, dequant_scale, *, exact=False, stream=None):
     except RuntimeError:
         raise ValueError("q_nope rows must be uniformly strided")
     stride = q2.stride(0) if rows > 1 else H
+    _apart(rows, stride, "q_nope")
     if q_out.dtype != torch.int8 or q_out.numel() != q_nope.numel():
         raise ValueError("q_out must be int8 with q_nope's number of elements")
     if dequant_scale.dtype != torch.float32 or dequant_scale.numel() != rows:
