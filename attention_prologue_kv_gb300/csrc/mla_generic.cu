@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
                     if (c < p.Dk) s = fmaf(b[j], mla_value<IT>(p.kc, p.k_kind, slot * p.Dk + c), s);
                 }
                 s = warp_sum(s) * p.scale;
-                const float mn = fmaxf(m, s);
-                const float f = mn == -INFINITY ? 1.f : expf(m - mn), e = mn == -INFINITY ? 0.f : expf(s - mn);
+                const float mn = fmaxf(m, s);   // a NaN score leaves m, and makes the weight NaN
+                const float f = m == mn ? 1.f : expf(m - mn), e = s == -INFINITY ? 0.f : expf(s - mn);
                 m = mn;
                 l = l * f + e;
 #pragma unroll
