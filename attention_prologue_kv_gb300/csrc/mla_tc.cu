@@ -969,6 +969,13 @@ __device__ __forceinline__ float row_sum(const float* x, int r) {
     return G == 1 ? v : v + (x[r + 128] + x[r + 192]);
 }
 
+// Octaves by which weights are held above their reference where they are rounded to halves: a half's spacing stops
+// shrinking at 2^-24, so that a weight below 2^-14 of the reference would lose bits and one below 2^-25 be lost from O,
+// while l counts it (an attention sink and 10^5 keys 17 nats below it: the output off by a third). 7 is the most there is
+// room for: weights below 2^(8 + 7), a half ends at 65504. What is lost of a weight then is 2^-32 of the row's largest.
+template <class PT>
+constexpr float LIFT = is_bf16<PT> ? 0.f : 7.f;
+
 // Softmax: thread (row r, half h of the keys, group g: half of that half).
 template <class IT, bool C8, bool K8>
 __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
@@ -1032,15 +1039,14 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             red[tid] = top;
             softmax_sync<C8>();
             top = fmaxf(row_max<G>(red, r), mx);
-            // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^8,
-            // and the 16-bit rounding of a weight is relative.
+            // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^(8 + LIFT).
             const bool grow = top > mx + 8.f;
             const float f = grow ? exp2_approx(mx - top) : 1.f;
             if (grow) {
                 mx = top;
                 sum *= f;
             }
-            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float ref = mx == -INFINITY ? 0.f : mx - LIFT<PT>;
             uint32_t pk[NK / 2];
 #pragma unroll
             for (int i = 0; i < NK / 2; ++i) {
@@ -1075,7 +1081,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         float* red = m->red[j & 1];
         red[tid] = sum;   // the next step's buffer: its own maxima come after the second barrier
         softmax_sync<C8>();
-        const float2 ml = make_float2(mx, row_sum<G>(red, r));
+        const float2 ml = make_float2(mx - LIFT<PT>, row_sum<G>(red, r));   // the exponent that l and O are taken to
         softmax_sync<C8>();
         c.wait(&m->pv_done, (j - 1) & 1);
         tc_fence_after();

@@ -564,7 +564,8 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  * plain kernel that is much slower.
  * Scores, softmax and sums are float32. The tensor-core kernel rounds each
  * probability for the second product, to `dtype`, or to float16 with an 8-bit
- * latent cache, whose products run on float16 (every code is exact there). A
+ * latent cache, whose products run on float16 (every code is exact there); a
+ * float16 weight also loses up to 2^-32 of its row's largest weight. A
  * scale per channel goes into the query: q / scale[c] is rounded once, to
  * float16 for the latent part and to `dtype` for the rotary part, which moves a
  * score by up to one unit in the last place of that type (relative to the

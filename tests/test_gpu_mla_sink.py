@@ -1,0 +1,77 @@
+"""mla_attention where one key has nearly all the weight and many keys far below it carry the output (an attention sink,
+whose value is small): weights that are rounded to halves keep them.
+
+All rows have the same query, so that one row in float64 is the oracle of all; with as many row tiles as CTA pairs, or
+more, each pair goes over all keys of its rows."""
+import math
+
+import pytest
+import torch
+
+import attention_prologue_kv_gb300 as kvr
+from attention_helpers import DTYPES, half_step
+
+pytestmark = pytest.mark.gpu
+
+N, T, H, BS = 1 << 17, 80, 128, 128
+
+
+def sink_case(dtype, cache, octaves, at):
+    """N keys `octaves` below the one at place `at`; the rotary part alone makes the scores. A value's mean is 1/2."""
+    g = torch.Generator("cuda").manual_seed(3)
+    dt = DTYPES[dtype]
+    c = (0.5 + 0.25 * torch.randn(N, 512, generator=g, device="cuda")).clamp(-1, 2)
+    c[at] = 0
+    scale = None
+    if cache == "int8":
+        scale = torch.full((1,), 60.0, device="cuda")
+        c = (c * 60).round()
+    ckv = c.to(DTYPES[cache or dtype]).view(-1, BS, 1, 512)
+    k = torch.zeros(N, 64, device="cuda", dtype=dt)
+    k[:, 0] = -octaves
+    k[at, 0] = 0
+    q_rope = torch.zeros(1, 1, 64, device="cuda", dtype=dt)
+    q_rope[..., 0] = 1
+    table = torch.arange(N // BS, device="cuda").view(1, -1)
+    return dict(q_nope=torch.zeros(1, 1, 512, device="cuda", dtype=dt).expand(T, H, 512), q_rope=q_rope.expand(T, H, 64), ckv=ckv,
+                k=k.view(-1, BS, 1, 64), table=table, scale=scale)
+
+
+def run(c):
+    out = torch.full((T, H, 512), -77.0, device="cuda", dtype=c["q_nope"].dtype)
+    lse = torch.full((T, H), -77.0, device="cuda")
+    kvr.mla_attention(c["q_nope"], c["q_rope"], c["ckv"], c["k"], c["table"], torch.tensor([0, T], device="cuda"),
+                      torch.tensor([N], device="cuda"), out, softmax_scale=math.log(2.0), causal=False, ckv_scale=c["scale"], lse=lse)
+    return out.double(), lse.double()
+
+
+def oracle(c):
+    """(out [512], sum of |weight * value| [512], lse) of the row."""
+    s = float(torch.tensor(math.log(2.0), dtype=torch.float32)) * c["k"].view(N, 64)[:, 0].double()
+    v = c["ckv"].view(N, 512).double()
+    v = v if c["scale"] is None else v / c["scale"].double()
+    p = torch.softmax(s, 0)
+    return p @ v, p @ v.abs(), torch.logsumexp(s, 0)
+
+
+@pytest.mark.parametrize("at", [0, 70000, N - 1])
+@pytest.mark.parametrize("octaves", [18.0, 23.375, 25.25])   # below 2^-14, near the last bit, below the last half
+@pytest.mark.parametrize("dtype,cache", [("f16", None), ("f16", "int8"), ("bf16", "int8"), ("bf16", None)])
+def test_the_keys_below_a_sink(dtype, cache, octaves, at):
+    """To first order, with u = half a step of the weights' type: each weight is off by u of itself and, as a half, by 2^-32
+    of the largest weight (2^-25, half of a half's last step, 7 octaves up), which is at most 1 of the sum; the score of
+    exact products by 2^-21; float32 sums of the output take 16 keys an addition and of the weights 2 keys an addition in
+    four threads, each addition off by at most 2^-23: N (2^-27 + 2^-26); the output is rounded once."""
+    c = sink_case(dtype, cache, octaves, at)
+    out, lse = run(c)
+    want, size, want_lse = oracle(c)
+    halves = dtype == "f16" or cache is not None
+    u_weight = 2.0 ** -11 if halves else 2.0 ** -8
+    u_out = half_step(DTYPES[dtype])
+    mean = c["ckv"].view(N, 512).double().abs().mean(0) / (60.0 if cache else 1.0)
+    tol = u_out * want.abs() + (u_weight + 2.0 ** -20 + N * (2.0 ** -27 + 2.0 ** -26)) * size + (N * 2.0 ** -32 * mean if halves else 0)
+    if dtype == "f16":
+        tol = tol + 2.0 ** -25
+    off = (out - want).abs()
+    assert (off <= tol * (1 + 2.0 ** -6)).all(), "off by up to %.3g of the output" % float((off / want.abs()).max())
+    assert float((lse - want_lse).abs().max()) <= 2.0 ** -20 + N * 2.0 ** -26 + 2.0 ** -24 * abs(float(want_lse))
