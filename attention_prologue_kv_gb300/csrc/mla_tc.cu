@@ -1048,12 +1048,14 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             }
             const float ref = mx == -INFINITY ? 0.f : mx - LIFT<PT>;
             uint32_t pk[NK / 2];
+            float step = 0.f;   // of its own: one addition a step to the long sum, which rounds small weights beside a large one
 #pragma unroll
             for (int i = 0; i < NK / 2; ++i) {
                 const float a = exp2_approx(s[2 * i] - ref), b = exp2_approx(s[2 * i + 1] - ref);
-                sum += a + b;
+                step += a + b;
                 pk[i] = PT::pack(a, b);
             }
+            sum += step;
             // The product before this one is done: P's buffer is free and O at rest.
             if (j > 0) c.wait(&m->pv_done, (j - 1) & 1);
             if (__any_sync(0xFFFFFFFFu, grow) && kt > w.kt0) {

@@ -75,3 +75,14 @@ def test_the_keys_below_a_sink(dtype, cache, octaves, at):
     off = (out - want).abs()
     assert (off <= tol * (1 + 2.0 ** -6)).all(), "off by up to %.3g of the output" % float((off / want.abs()).max())
     assert float((lse - want_lse).abs().max()) <= 2.0 ** -20 + N * 2.0 ** -26 + 2.0 ** -24 * abs(float(want_lse))
+
+
+@pytest.mark.parametrize("octaves", [22.5, 23.375, 24.25])   # about 3, 1.5 and 1 of a float32's last place, two at a time
+@pytest.mark.parametrize("dtype,cache", [("f16", None), ("bf16", "int8"), ("bf16", None)])
+def test_the_sum_beside_a_sink(dtype, cache, octaves):
+    """Equal small weights round to the same side each time they are added to the sink's: a thread adds its part of a step
+    of 64 keys at once, N / 64 additions of 2^-24 of the sum each."""
+    c = sink_case(dtype, cache, octaves, 5)
+    _, lse = run(c)
+    want = float(oracle(c)[2])
+    assert float((lse - want).abs().max()) <= 2.0 ** -20 + N * 2.0 ** -30 + 2.0 ** -24 * abs(want)
