@@ -5,6 +5,8 @@
 // registers (lane l has channels l, l + 32, ...), keys come one after the
 // other, with the running maximum m and sum l of the softmax:
 //   s = scale * <q, key>,  m' = max(m, s),  o = o e^(m - m') + e^(s - m') c.
+// 64 keys are summed on their own (lb, ob) before they join l and o: added one by one beside a key of large weight, many
+// small ones would all round to the same side (131072 equal ones 23.4 octaves below it: off by a third).
 // Every key row is read once per head, from L1 or L2: this is the plain kernel,
 // bound by the loads and the warp sum of each key. Measured: one token of 16 heads over 1000 keys of 512 + 64 channels
 // 1424 us (the tensor-core kernel 14.7).
@@ -12,7 +14,7 @@
 
 namespace kvr {
 
-constexpr int MLA_GEN_THREADS = 128;
+constexpr int MLA_GEN_THREADS = 128, MLA_GEN_BLOCK = 64;
 
 template <class IT>
 __device__ __forceinline__ float mla_value(const void* cache, int kind, int64_t at) {
@@ -47,11 +49,11 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
             int64_t seen = p.causal ? K - (q1 - 1 - t) : K;
             const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + h * p.qn_hs;
             const uint16_t* qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + h * p.qr_hs;
-            float a[NV], b[NK], o[NV];
+            float a[NV], b[NK], o[NV], ob[NV];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = lane + 32 * j;
-                o[j] = 0.f;
+                o[j] = ob[j] = 0.f;
                 a[j] = c < p.Dv ? IT::one(qn[c]) : 0.f;
                 if (p.ckv_kind != OUT16 && c < p.Dv) a[j] /= p.ckv_scale[p.ckv_scale_per_ch ? c : 0];
             }
@@ -61,7 +63,18 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
                 b[j] = c < p.Dk ? IT::one(qr[c]) : 0.f;
                 if (p.k_kind != OUT16 && c < p.Dk) b[j] /= p.k_scale[p.k_scale_per_ch ? c : 0];
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, lb = 0.f;
+            int held = 0;   // keys in lb and ob
+            auto join = [&]() {
+                l += lb;
+                lb = 0.f;
+                held = 0;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    o[j] += ob[j];
+                    ob[j] = 0.f;
+                }
+            };
             for (int64_t i = 0; i < seen; ++i) {
                 int64_t slot = n * p.d1 + i;
                 if (p.table != nullptr) {
@@ -87,12 +100,24 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
                 }
                 s = warp_sum(s) * p.scale;
                 const float mn = fmaxf(m, s);   // a NaN score leaves m, and makes the weight NaN
-                const float f = m == mn ? 1.f : expf(m - mn), e = s == -INFINITY ? 0.f : expf(s - mn);
-                m = mn;
-                l = l * f + e;
+                const float e = s == -INFINITY ? 0.f : expf(s - mn);
+                if (m != mn) {   // (the same in all lanes)
+                    const float f = expf(m - mn);
+                    m = mn;
+                    l *= f;
+                    lb *= f;
 #pragma unroll
-                for (int j = 0; j < NV; ++j) o[j] = fmaf(e, v[j], o[j] * f);
+                    for (int j = 0; j < NV; ++j) {
+                        o[j] *= f;
+                        ob[j] *= f;
+                    }
+                }
+                lb += e;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) ob[j] = fmaf(e, v[j], ob[j]);
+                if (++held == MLA_GEN_BLOCK) join();
             }
+            join();
             uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.o_ts + h * p.o_hs;
             const float inv = l == 0.f ? 0.f : 1.f / l;   // no key: zeros
 #pragma unroll

@@ -86,3 +86,28 @@ def test_the_sum_beside_a_sink(dtype, cache, octaves):
     _, lse = run(c)
     want = float(oracle(c)[2])
     assert float((lse - want).abs().max()) <= 2.0 ** -20 + N * 2.0 ** -30 + 2.0 ** -24 * abs(want)
+
+
+@pytest.mark.parametrize("octaves", [22.5, 23.375, 24.25])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_the_plain_kernel_beside_a_sink(dtype, octaves):
+    """Rows of 10 + 6 channels, a few of them: 64 keys are summed before they join the long sums, N / 64 additions of 2^-24
+    each in the sum of the weights and in the output's, 64 within a block; the sink has a value here too. A weight is
+    2^-20 off (two roundings of its score, expf)."""
+    dt = DTYPES[dtype]
+    c = sink_case(dtype, None, octaves, 5)
+    c["ckv"] = c["ckv"][..., :10].contiguous()
+    c["ckv"].view(N, 10)[5] = 1
+    c["k"] = c["k"][..., :6].contiguous()
+    c["q_nope"], c["q_rope"] = c["q_nope"][:2, :3, :10], c["q_rope"][:2, :3, :6]
+    out, lse = torch.zeros(2, 3, 10, device="cuda", dtype=dt), torch.zeros(2, 3, device="cuda")
+    call = kvr.prepare_mla_attention(c["q_nope"], c["q_rope"], c["ckv"], c["k"], c["table"], torch.tensor([0, 2], device="cuda"),
+                                     torch.tensor([N], device="cuda"), out, softmax_scale=math.log(2.0), causal=False, lse=lse)
+    assert call.workspace is None
+    call()
+    s = float(torch.tensor(math.log(2.0), dtype=torch.float32)) * c["k"].view(N, 6)[:, 0].double()
+    p, v = torch.softmax(s, 0), c["ckv"].view(N, 10).double()
+    want, size, want_lse = p @ v, p @ v.abs(), float(torch.logsumexp(s, 0))
+    rel = 2.0 ** -19 + N * 2.0 ** -30 + 64 * 2.0 ** -24
+    assert ((out.double() - want).abs() <= half_step(dt) * want.abs() * (1 + 2.0 ** -6) + 2 * rel * size).all()
+    assert float((lse.double() - want_lse).abs().max()) <= rel + 2.0 ** -23 * abs(want_lse)
