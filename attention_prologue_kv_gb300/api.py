@@ -420,36 +420,57 @@ def _launch(fn, ref, name, device, stream):
         raise KvrError(st, name)
 
 
+def _torch_stream(raw, device):
+    """The torch stream of a raw handle (0 and 1 are the legacy default stream)."""
+    return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
+
+
 class BoundCall(PreparedCall):
     """PreparedCall of an operator that holds its tensors on one device,
     which need not be the current one when the call is made."""
 
     workspace = None
-    _home = None   # the stream that an own workspace was taken on
+    _home = None    # the stream that an own workspace was taken on
+    _ready = None   # what that stream still does with the workspace's memory, or None if it was capturing
 
     def __init__(self, fn, args, name, keep, device):
         super().__init__(fn, args, name, keep)
         self._device = device
         self._index = device.index
 
+    def own(self, workspace):
+        """Keep a workspace that was just taken on the current stream (of the call's device, which is current)."""
+        self.workspace = workspace
+        self._home = torch._C._cuda_getCurrentRawStream(self._index)
+        if not torch.cuda.is_current_stream_capturing():
+            self._ready = torch.cuda.Event()
+            self._ready.record()
+
     def __call__(self, stream=None):
         if stream is None and torch._C._cuda_getDevice() == self._index:   # the serving loop's call, kept short
             raw = torch._C._cuda_getCurrentRawStream(self._index)
+            if self._home is not None and raw != self._home:
+                self._lend(raw)
             st = self._fn(self._ref, raw)
             if st != N.KVR_OK:
                 raise KvrError(st, self._name)
         else:
-            _launch(self._fn, self._ref, self._name, self._device, stream)
             raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream(stream)
-        if self._home is not None and raw != self._home:
-            self._used_on(raw)
+            if self._home is not None and raw != self._home:
+                self._lend(raw)
+            _launch(self._fn, self._ref, self._name, self._device, raw)
 
-    def _used_on(self, raw):
-        """An own workspace, used on another stream than it was taken on, must not go to others before that one is done
-        (a graph's captured calls keep this object instead)."""
+    def _lend(self, raw):
+        """The own workspace's use on another stream than it was taken on. That stream first waits for what the other one
+        still does with the memory (a captured call cannot: a capture begins behind a synchronisation), and the memory
+        goes to nobody else before it is done (under capture: before the capture ends)."""
         with torch.cuda.device(self._index):
-            if not torch.cuda.is_current_stream_capturing():
-                self.workspace.record_stream(torch.cuda.ExternalStream(raw, device=self._device))
+            stream = _torch_stream(raw, self._device)
+            if self._ready is not None:
+                with torch.cuda.stream(stream):
+                    if not torch.cuda.is_current_stream_capturing():
+                        stream.wait_event(self._ready)
+            self.workspace.record_stream(stream)
 
 
 def _heads(t, name, dtype, T=None, H=None):
@@ -597,7 +618,11 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
     """mla_attention with its arguments bound once (see PreparedCall). Without
     a `workspace` the object keeps one of its own: calls of one object that can
     run at the same time (two streams, two replayed graphs) need an object, or
-    a workspace, each."""
+    a workspace, each. Keep an object whose call was captured as long as the
+    graph: its replays use the workspace. One made during a capture is for
+    that capture, on its stream or on streams forked behind it; one made
+    before is captured once the stream that it was made on has passed it
+    (torch.cuda.graph synchronises)."""
     _cuda(q_nope, "q_nope")
     if q_nope.dtype not in _IN_DTYPES:
         raise ValueError("q_nope must be bfloat16 or float16")
@@ -633,19 +658,18 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
                   block_table=_ptr(block_table, "block_table"), max_blocks=max_blocks, softmax_scale=float(softmax_scale),
                   causal=1 if causal else 0, out=out.data_ptr(), out_token_stride=o_ts, out_head_stride=o_hs,
                   lse=_ptr(lse, "lse"), dev_status=_ptr(dev_status, "dev_status"), **pair)
-    home = None
-    with torch.cuda.device(device):
-        need = N.lib().kvr_mla_attention_workspace(ctypes.byref(a))
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            home = torch._C._cuda_getCurrentRawStream(device.index)
-    if workspace is not None:
-        a.workspace = _ptr(workspace, "workspace")
-        a.workspace_bytes = workspace.numel() * workspace.element_size()
     keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, ckv_scale, k_scale, lse, workspace,
             dev_status)
     call = BoundCall(N.lib().mla_attention, a, "mla_attention", keep, device)
-    call.workspace, call._home = workspace, home
+    with torch.cuda.device(device):
+        need = N.lib().kvr_mla_attention_workspace(ctypes.byref(a))
+        if workspace is None and need:
+            call.own(torch.empty(need, dtype=torch.uint8, device=device))
+        else:
+            call.workspace = workspace
+    if call.workspace is not None:
+        a.workspace = _ptr(call.workspace, "workspace")
+        a.workspace_bytes = call.workspace.numel() * call.workspace.element_size()
     return call
 
 
@@ -671,11 +695,19 @@ def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, 
     of its sequence. At most 2^24 keys a sequence.
     `workspace` (optional, device memory of kvr_mla_attention_workspace
     bytes) must not be shared by calls that can run at the same time; without
-    it the call takes one from PyTorch's allocator."""
-    call = prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out,
-                                 softmax_scale=softmax_scale, cache_mode=cache_mode, causal=causal, ckv_scale=ckv_scale,
-                                 k_scale=k_scale, lse=lse, workspace=workspace, dev_status=dev_status)
-    call(stream)
+    it the call takes one from PyTorch's allocator, on the stream that it is
+    made on."""
+    def prepare():
+        return prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out,
+                                     softmax_scale=softmax_scale, cache_mode=cache_mode, causal=causal, ckv_scale=ckv_scale,
+                                     k_scale=k_scale, lse=lse, workspace=workspace, dev_status=dev_status)
+    if stream is None or workspace is not None:
+        prepare()(stream)
+        return
+    # With that stream current, so that the workspace's memory goes from call to call in its order.
+    device = _cuda(q_nope, "q_nope").device
+    with torch.cuda.device(device), torch.cuda.stream(_torch_stream(_stream(stream), device)):
+        prepare()()
 
 
 def device_copy(dst, src, stream=None):
