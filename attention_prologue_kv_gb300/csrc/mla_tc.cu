@@ -77,6 +77,7 @@ struct Seq {
 
 struct alignas(16) Misc {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t h_full[MAX_STAGES];   // `held` of a stage is written: within the CTA
     uint64_t s_full[2], p_full, pv_done, q_full, q_free, k_fix, v_fix, drain;
     uint32_t tmem;
     int abort, large;
@@ -492,6 +493,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
                 if (lane == 0) {
                     m->held[st][mine] = live;
                     m->held[st][mine ^ 1] = theirs;
+                    mbar_arrive(&m->h_full[st]);
                 }
             }
             if (R > 0) {
@@ -613,10 +615,6 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
             if (SWAP) c.wait(&m->s_full[j & 1], (j >> 1) & 1);
             else if (j >= STAGES) c.wait(&m->empty[st], ((j / STAGES) & 1) ^ 1);
             if (c.gone()) break;
-            if (!SWAP && lane == 0) {
-                m->held[st][mine] = live;
-                m->held[st][mine ^ 1] = row2 < 0 ? 0u : (left2 >= CKEYS ? 0xFFFFFFFFu : (1u << left2) - 1u);
-            }
             if (live == 0xFFFFFFFFu) {
                 if (lane == 0) {
                     mbar_expect_at(&full[st], 0, uint32_t(boxes) * KBOX);
@@ -641,6 +639,11 @@ __device__ __forceinline__ void key_warp_tma(Ctx& c, const Maps& maps) {
                         for (int k = 0; k < 8; ++k) st_shared_v4(box + uint32_t(lane) * 128u + k * 16u, make_uint4(0, 0, 0, 0));
                     }
                 c.arrive(&full[st]);
+            }
+            if (!SWAP && lane == 0) {   // behind the copy, which is what the step waits for
+                m->held[st][mine] = live;
+                m->held[st][mine ^ 1] = row2 < 0 ? 0u : (left2 >= CKEYS ? 0xFFFFFFFFu : (1u << left2) - 1u);
+                mbar_arrive(&m->h_full[st]);
             }
         }
     }
@@ -732,7 +735,10 @@ __device__ __forceinline__ void code_keys(Ctx& c, int v) {
                 st_shared_v4(box + at0, dec8x8<IT>(p.k_kind, a.rope.x, a.rope.y));
                 st_shared_v4(box + at1, dec8x8<IT>(p.k_kind, a.rope.z, a.rope.w));
             }
-            if (lane == 0) reinterpret_cast<uint8_t*>(&m->held[st][int(c.rank) ^ half])[wp] = uint8_t(a.held);
+            if (lane == 0) {
+                reinterpret_cast<uint8_t*>(&m->held[st][int(c.rank) ^ half])[wp] = uint8_t(a.held);
+                mbar_arrive(&m->h_full[st]);
+            }
             c.arrive(&m->k_full[st]);
             if (++st == STAGES) st = 0, ++turn;
         };
@@ -1011,8 +1017,12 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             float* red = m->red[j & 1];
             c.wait(&m->s_full[j & 1], (j >> 1) & 1);
             tc_fence_after();
-            // Keys that exist: bit i for key0 + i.
-            const uint32_t held = m->held[j % stages_of<C8>()][h] >> (g * NK);
+            // Keys that exist: bit i for key0 + i. They come over a barrier of this CTA, as the arrivals that start the
+            // scores order nothing for these warps; it is long complete when the scores are. (The word is written anew
+            // once this step's weights have gone into O, and they depend on it.)
+            constexpr int STAGES = stages_of<C8>();
+            c.wait(&m->h_full[j % STAGES], (j / STAGES) & 1);
+            const uint32_t held = m->held[j % STAGES][h] >> (g * NK);
             float s[NK];
             tmem_ld(lanes + COL_S + uint32_t(j & 1) * 64 + g * NK, s);
             if (split) {
@@ -1212,6 +1222,7 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&m->k_full[s], C8 ? 16 : 2);
             mbar_init(&m->v_full[s], C8 ? 6 : 2);
             mbar_init(&m->empty[s], 1);
+            mbar_init(&m->h_full[s], C8 ? 8 : 1);
         }
         mbar_init(&m->s_full[0], 1);
         mbar_init(&m->s_full[1], 1);

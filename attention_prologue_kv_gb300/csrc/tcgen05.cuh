@@ -20,9 +20,9 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 // Arrive on the barrier at the same place in CTA `rank` of the cluster. What the
 // arrivals of these kernels publish is operands in the arriving CTA's own shared
-// memory, for the tensor core of that CTA (after fence_async_proxy): no data
-// crosses over with them, so CTA scope does (a release at cluster scope cost about
-// 1000 cycles an arrival).
+// memory, for the tensor core of that CTA (after fence_async_proxy): no thread
+// reads them, so CTA scope does (a release at cluster scope cost about 1000 cycles
+// an arrival). What threads read of one another goes over barriers of their own CTA.
 __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
