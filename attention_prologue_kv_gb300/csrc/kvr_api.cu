@@ -666,8 +666,7 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
     p->d1 = a->cache_d1;
     p->max_blocks = a->max_blocks;
     // A table without columns may be NULL, as in Norm mode; it holds 0 keys, so that no key is read.
-    // 2^24 keys at most: a float32 sum of more would stop growing, and a part of an item stays far below the one second
-    // that its queries' warps wait for it (2^24 keys take 0.3 s).
+    // 2^24 keys at most: a float32 sum of more would stop growing.
     p->max_keys = std::min<int64_t>(norm ? a->cache_d1 : a->max_blocks * a->cache_d1, int64_t(1) << 24);
     p->qn_ts = a->q_nope_token_stride;
     p->qn_hs = a->q_nope_head_stride;

@@ -399,9 +399,11 @@ struct Maps {
     CUtensorMap all, two, rope;
 };
 
-// The rest of a wait, out of line: the roles' loops have to stay in the instruction cache.
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_wait(bar, parity, abort)) return true;
+// The rest of a wait, out of line: the roles' loops have to stay in the instruction cache. `more`: seconds beyond the first.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int more) {
+    do {
+        if (mbar_wait(bar, parity, abort)) return true;
+    } while (*abort == 0 && --more >= 0);
     *abort = 1;
     return false;
 }
@@ -416,11 +418,11 @@ struct Ctx {
     volatile int* abort;
     bool ok;
 
-    // A wait that gives up (one second) poisons the CTA: the others give up at their first look. The warps that start TMA
+    // A wait that gives up (after one second, or one and `more`) poisons the CTA: the others give up at their first look. The warps that start TMA
     // copies then stop; every other role runs its loops to the end without waiting, so that no barrier is left with
     // threads missing.
-    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort) && ok;
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int more = 0) {
+        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, more) && ok;
         __syncwarp();
     }
     __device__ __forceinline__ bool gone() const { return __any_sync(0xFFFFFFFFu, !ok); }
@@ -823,7 +825,7 @@ __device__ __forceinline__ void code_swaps(Ctx& c, int v, const Walk& w, int& j)
 
 // The query warps (four; three with codes) bring the queries of a part: lane v & 7 has chunk v & 7 of each box of a row.
 template <bool C8>
-__device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int part) {
+__device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int part, int steps) {
     constexpr int AT_ONCE = C8 ? 12 : 16, TURNS = C8 ? 6 : 4;   // rows of a turn
     const MlaParams& p = c.p;
     Misc* m = c.m;
@@ -846,7 +848,9 @@ __device__ __forceinline__ void load_queries(Ctx& c, int v, const Walk& w, int p
         }
         lives |= uint32_t(live) << i;
     }
-    if (part > 0) c.wait(&m->q_free, (part - 1) & 1);
+    // This wait alone lasts as long as a part, the `steps` of the one before: 2^24 keys take 0.2 s over TMA rows and 1.3 s
+    // where blocks of one key and rotary codes make a step 5.0 us, so it has another second for every 2^16 of them.
+    if (part > 0) c.wait(&m->q_free, (part - 1) & 1, steps >> 16);
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
         const int r = i * AT_ONCE + (v >> 3);
@@ -1107,11 +1111,12 @@ template <int CK>
 __device__ __forceinline__ void query_warps(Ctx& c, int v) {
     constexpr bool C8 = CK != OUT16;
     Walk w(c.p, c.m);
-    int j = 0;
+    int j = 0, steps = 0;
     bool more = w.next();
 #pragma unroll 1
     for (int part = 0; more; ++part) {
-        load_queries<C8>(c, v, w, part);
+        load_queries<C8>(c, v, w, part, steps);
+        steps = w.kt1 - w.kt0;
         if constexpr (C8) code_swaps<CK>(c, v, w, j);
         more = w.next();
         if (!C8 && more) prefetch_queries(c, v, w);   // (with codes they were just written)
