@@ -97,6 +97,7 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool ve
 cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s);
 cudaError_t launch_mla_generic(const MlaParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_mla_tc(MlaParams p, int dtype, cudaStream_t s);
+bool mla_tc_fits(const MlaParams& p);                       // whether its work can be counted in 64 bits
 int64_t mla_tc_workspace(const MlaParams& p, int dtype);   // bytes on the current device
 
 }  // namespace kvr

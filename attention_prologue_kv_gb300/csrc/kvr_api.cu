@@ -683,7 +683,7 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
     p->ckv_scale_per_ch = a->ckv_scale_len == a->Dv && a->Dv > 1;
     p->k_scale_per_ch = a->k_scale_len == a->Dk && a->Dk > 1;
     p->scale = a->softmax_scale;
-    return KVR_OK;
+    return mla_tensor_cores(a) && !mla_tc_fits(*p) ? KVR_ERR_SHAPE : KVR_OK;
 }
 
 }  // namespace

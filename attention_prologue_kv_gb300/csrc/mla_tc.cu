@@ -190,11 +190,12 @@ struct Walk {
     }
 };
 
-// Where share `which` of `active` begins, in cost.
+// Where share `which` of `active` begins, in cost: total * which / active, which the product may not fit.
 __device__ __forceinline__ int64_t share(int64_t total, int which, int active) {
     if (which >= active) return total;
     if (total < (int64_t(1) << 31) / 256) return unsigned(total) * unsigned(which) / unsigned(active);   // 64-bit divisions take about 100 instructions
-    return total * which / active;
+    const int64_t each = total / active;
+    return each * which + unsigned(total - each * active) * unsigned(which) / unsigned(active);
 }
 // Pairs that get work: equal shares, but none below MIN_KEYS.
 __device__ __forceinline__ int active_pairs(const MlaParams& p, int64_t total) {
@@ -1529,6 +1530,13 @@ static int mla_tc_pairs() {
 static bool prepares_nope(const MlaParams& p, int dtype) { return p.ckv_kind != OUT16 && (p.ckv_scale_per_ch || dtype != KVR_F16); }
 static bool prepares_rope(const MlaParams& p) { return p.k_kind != OUT16 && p.k_scale_per_ch; }
 static int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
+
+bool mla_tc_fits(const MlaParams& p) {
+    // cost() of one sequence is at most row tiles * (H * (keys + ITEM_COST) + ROWS / 2 * row tiles), row tiles <= 2^24, and N
+    // of them, which may share rows, are added up in 64 bits.
+    const int64_t tiles = (p.T * p.H + ROWS - 1) / ROWS, each = p.H * (p.max_keys + ITEM_COST) + ROWS / 2 * tiles;
+    return each <= (int64_t(1) << 62) / tiles / p.N;
+}
 
 int64_t mla_tc_workspace(const MlaParams& p, int dtype) {
     int64_t n = round_up(ws_bytes(mla_tc_pairs(), p.Dv));

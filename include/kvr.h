@@ -558,10 +558,12 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *                KVR_DEVERR_TIMEOUT).
  *
  * Limits: T, H, N >= 0; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256; keys of a
- * sequence <= 2^24 (one that has more is left out, KVR_DEVERR_KEY_LENGTH). Rows of at most 512 + 64 channels, both multiples of 8 (of
- * 16 in an 8-bit cache), on 16-byte boundaries (q, out, caches; strides
- * multiples of 8) and with H <= 65536 run on the tensor cores, all others on a
- * plain kernel that is much slower.
+ * sequence <= 2^24 (one that has more is left out, KVR_DEVERR_KEY_LENGTH). Rows of
+ * at most 512 + 64 channels, both multiples of 8 (of 16 in an 8-bit cache), on
+ * 16-byte boundaries (q, out, caches; strides multiples of 8) and with H <= 65536
+ * run on the tensor cores, all others on a plain kernel that is much slower. On the
+ * tensor cores T * H / 128 * N * H * (keys + 1024) < 2^62, with the keys that the
+ * block table (the cache batch in Norm mode) has room for.
  * Scores, softmax and sums are float32. The tensor-core kernel rounds each
  * probability for the second product, to `dtype`, or to float16 with an 8-bit
  * latent cache, whose products run on float16 (every code is exact there); a
