@@ -605,7 +605,7 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
     if (a == nullptr) return KVR_ERR_NULL;
     if (a->mode != KVR_CACHE_NORM && a->mode != KVR_CACHE_PA_BSND && a->mode != KVR_CACHE_PA_BLK_BSND) return KVR_ERR_MODE;
     if (a->T < 0 || a->H < 0 || a->N < 0 || a->Dv < 1 || a->Dv > 1024 || a->Dk < 1 || a->Dk > 256 || a->max_blocks < 0 ||
-        a->H > 0x7FFFFFFF || a->N > 0x7FFFFFFF || !product_fits({a->T, a->H}) || a->T * a->H > 0x7FFFFFFF)
+        a->H > 0x7FFFFFFF || a->N > 0x7FFFFFFF - 512 || !product_fits({a->T, a->H}) || a->T * a->H > 0x7FFFFFFF)
         return KVR_ERR_SHAPE;
     const kvr_status st = check_caches(a->dtype, a->ckv_dtype, a->k_dtype, a->ckv_scale, a->ckv_scale_len, a->k_scale,
                                        a->k_scale_len, a->cache_d0, a->cache_d1, a->Dv, a->Dk);

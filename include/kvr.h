@@ -557,8 +557,8 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *   dev_status   optional int32 device word (the bits above and
  *                KVR_DEVERR_TIMEOUT).
  *
- * Limits: T, H, N >= 0; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256; keys of a
- * sequence <= 2^24 (one that has more is left out, KVR_DEVERR_KEY_LENGTH). Rows of
+ * Limits: T, H >= 0; 0 <= N < 2^31 - 512; T * H < 2^31; 1 <= Dv <= 1024; 1 <= Dk <= 256;
+ * keys of a sequence <= 2^24 (one that has more is left out, KVR_DEVERR_KEY_LENGTH). Rows of
  * at most 512 + 64 channels, both multiples of 8 (of 16 in an 8-bit cache), on
  * 16-byte boundaries (q, out, caches; strides multiples of 8) and with H <= 65536
  * run on the tensor cores, all others on a plain kernel that is much slower. On the

@@ -40,6 +40,12 @@ def test_work_beyond_64_bits_is_refused(lib, T, H, n, keys, fits):
         assert lib.mla_attention(ctypes.byref(a), None) == N.KVR_ERR_SHAPE
 
 
+@pytest.mark.parametrize("n,ok", [((1 << 31) - 513, True), ((1 << 31) - 512, False), ((1 << 31) - 1, False)])
+def test_the_most_sequences(lib, n, ok):
+    """The schedule rounds N up to its threads, 256 a half, in 32 bits."""
+    assert (lib.kvr_mla_attention_workspace(ctypes.byref(narrow(4, 8, N=n, cache_d0=8, cache_d1=16, max_blocks=1))) > 0) == ok
+
+
 def share(total, which, active):
     """Where share `which` begins, in the kernel's steps."""
     each = total // active
