@@ -94,14 +94,6 @@ __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
         : "memory");
 }
-// The same with A in TMEM: lane l of either half of the lanes has row l % 64 of the CTA's 64, 16-bit channels two a column.
-__device__ __forceinline__ void tc_mma_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
-        : "memory");
-}
 // Arrive on the barrier at this place in both CTAs when the MMAs issued so far are done.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
     asm volatile(
@@ -165,12 +157,6 @@ __device__ __forceinline__ uint4 ld_ahead_v4(const void* p) {
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t src) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
-    return v;
 }
 
 }  // namespace kvr
