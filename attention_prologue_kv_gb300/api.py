@@ -442,7 +442,11 @@ class BoundCall(PreparedCall):
         """Keep a workspace that was just taken on the current stream (of the call's device, which is current)."""
         self.workspace = workspace
         self._home = torch._C._cuda_getCurrentRawStream(self._index)
-        if not torch.cuda.is_current_stream_capturing():
+        self._guests = {}   # torch streams of other handles
+
+    def may_travel(self):
+        """Note what that stream still has to do, for calls on others."""
+        if self._home is not None and not torch.cuda.is_current_stream_capturing():
             self._ready = torch.cuda.Event()
             self._ready.record()
 
@@ -464,13 +468,18 @@ class BoundCall(PreparedCall):
         """The own workspace's use on another stream than it was taken on. That stream first waits for what the other one
         still does with the memory (a captured call cannot: a capture begins behind a synchronisation), and the memory
         goes to nobody else before it is done (under capture: before the capture ends)."""
-        with torch.cuda.device(self._index):
-            stream = _torch_stream(raw, self._device)
-            if self._ready is not None:
-                with torch.cuda.stream(stream):
-                    if not torch.cuda.is_current_stream_capturing():
-                        stream.wait_event(self._ready)
-            self.workspace.record_stream(stream)
+        stream = self._guests.get(raw)
+        if stream is None:
+            stream = self._guests[raw] = _torch_stream(raw, self._device)
+        if self._ready is not None and not self._capturing(raw, stream):
+            stream.wait_event(self._ready)
+        self.workspace.record_stream(stream)
+
+    def _capturing(self, raw, stream):
+        if raw == torch._C._cuda_getCurrentRawStream(self._index) and torch._C._cuda_getDevice() == self._index:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.device(self._index), torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
 
 
 def _heads(t, name, dtype, T=None, H=None):
@@ -612,17 +621,8 @@ def kv_cache_read(ckv_cache, k_cache, index, out, *, cache_mode="PA_BSND", ckv_s
                           dev_status=dev_status)(stream)
 
 
-def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
-                          cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None,
-                          dev_status=None):
-    """mla_attention with its arguments bound once (see PreparedCall). Without
-    a `workspace` the object keeps one of its own: calls of one object that can
-    run at the same time (two streams, two replayed graphs) need an object, or
-    a workspace, each. Keep an object whose call was captured as long as the
-    graph: its replays use the workspace. One made during a capture is for
-    that capture, on its stream or on streams forked behind it; one made
-    before is captured once the stream that it was made on has passed it
-    (torch.cuda.graph synchronises)."""
+def _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode,
+                        causal, ckv_scale, k_scale, lse, workspace, dev_status):
     _cuda(q_nope, "q_nope")
     if q_nope.dtype not in _IN_DTYPES:
         raise ValueError("q_nope must be bfloat16 or float16")
@@ -673,6 +673,25 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
     return call
 
 
+def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
+                          cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None,
+                          dev_status=None):
+    """mla_attention with its arguments bound once (see PreparedCall). Without
+    a `workspace` the object keeps one of its own: calls of one object that can
+    run at the same time (two streams, two replayed graphs) need an object, or
+    a workspace, each. Keep an object whose call was captured as long as the
+    graph: its replays use the workspace. One made during a capture is for
+    that capture, on its stream or on streams forked behind it; one made
+    before is captured once the stream that it was made on has passed it
+    (torch.cuda.graph synchronises)."""
+    _cuda(q_nope, "q_nope")
+    call = _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale,
+                               cache_mode, causal, ckv_scale, k_scale, lse, workspace, dev_status)
+    with torch.cuda.device(q_nope.device):
+        call.may_travel()
+    return call
+
+
 def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
                   cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None, dev_status=None,
                   stream=None):
@@ -697,17 +716,15 @@ def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, 
     bytes) must not be shared by calls that can run at the same time; without
     it the call takes one from PyTorch's allocator, on the stream that it is
     made on."""
-    def prepare():
-        return prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out,
-                                     softmax_scale=softmax_scale, cache_mode=cache_mode, causal=causal, ckv_scale=ckv_scale,
-                                     k_scale=k_scale, lse=lse, workspace=workspace, dev_status=dev_status)
+    args = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode, causal,
+            ckv_scale, k_scale, lse, workspace, dev_status)
     if stream is None or workspace is not None:
-        prepare()(stream)
+        _bind_mla_attention(*args)(stream)
         return
     # With that stream current, so that the workspace's memory goes from call to call in its order.
     device = _cuda(q_nope, "q_nope").device
     with torch.cuda.device(device), torch.cuda.stream(_torch_stream(_stream(stream), device)):
-        prepare()()
+        _bind_mla_attention(*args)()
 
 
 def device_copy(dst, src, stream=None):

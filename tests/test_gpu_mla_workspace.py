@@ -18,14 +18,13 @@ def tensors(c):
 @pytest.fixture
 def workspaces(monkeypatch):
     """Addresses of the workspaces that calls take."""
-    found, prepare = [], api.prepare_mla_attention
+    found, launch = [], api.BoundCall.__call__
 
-    def note(*a, **kw):
-        call = prepare(*a, **kw)
+    def note(call, *a, **kw):
         found.append(call.workspace.data_ptr())
-        return call
+        return launch(call, *a, **kw)
 
-    monkeypatch.setattr(api, "prepare_mla_attention", note)
+    monkeypatch.setattr(api.BoundCall, "__call__", note)
     return found
 
 
