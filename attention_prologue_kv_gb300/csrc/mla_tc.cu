@@ -32,10 +32,13 @@
 // order, so results do not change from run to run.
 //
 // Measured: 512 tokens x 128 heads over 16384 keys 1540 us (1.5 PFLOP/s, 80% of the measured bf16 rate; a step takes
-// 0.85 us, in which the SM's shared memory moves 210 KB); 256 sequences of one token, 128 heads, 1-4095 keys 158 us (4.5 TB/s,
-// 66% of the copy rate; a step 0.89 us, a part's queries and output 5 us); 61 sequences of one token over up to 16384
-// keys in E4M3 168 us; one sequence of 1000 keys, 16 heads 14.7 us. Steps of 128 keys with two of them in flight were
-// slower (1826 us): a stage's load, scores, softmax and second product follow one another.
+// 0.82 us; the unit that runs tcgen05 is busy 92% of the time, 68% with the products themselves); 256 sequences of one
+// token, 128 heads, 1-4095 keys 159 us (4.5 TB/s, 66% of the copy rate; a step 0.89 us, a part's queries and output 5 us);
+// 61 sequences of one token over up to 16384 keys in E4M3 168 us (that unit 59%, no counter above: the chain load, decode,
+// scores, swap, softmax, second product of its three steps in flight); one sequence of 1000 keys, 16 heads 15.0 us. Steps
+// of 128 keys with two of them in flight were slower (1826 us): a stage's load, scores, softmax and second product follow
+// one another. Paths without TMA, with codes or with small blocks, at 65536 keys, us a step: blocks of 16 keys 1.8, of
+// 8 2.6, of 100 3.5, of 1 3.9; rotary codes over 16-bit latent rows 4.0 (blocks of 1: 5.0); latent codes 1.2 (blocks of 1: 1.4).
 #include <mutex>
 #include <type_traits>
 
@@ -55,11 +58,15 @@ constexpr int MAX_STAGES = 4;
 template <bool C8>
 constexpr int stages_of() { return C8 ? 3 : 4; }
 constexpr uint32_t TMEM_COLS = 512, COL_S = 256;   // O: columns 0..255, S: two buffers of 32 + 32
-// An item's own cost, in keys (its queries, first scores and output: about 7 steps). Chunks of 33-129 tokens of 8 sequences:
-// 476 us with 192, 405 with 448, 417 with 768.
+// An item's own cost, in keys (its queries, first scores and output: about 7 steps). With 192, 448 and 768: chunks of 33-129
+// tokens of 8 sequences, 128 heads, 292, 268 and 279 us; chunks of 5-17 tokens of 30, 64 heads, 68.3, 63.9 and 64.8; one
+// token of 256 sequences, 1-4095 keys, 164, 154 and 155; of 64, 300-900 keys, 40.1, 37.4 and 37.4; 1-7 tokens of 33, 20
+// heads, 35.9, 35.5 and 35.2.
 constexpr int64_t ITEM_COST = 448;
-// Least work of a pair, in keys: the join of more parts costs more than they save. One token, 16 heads, 1000 keys: 15.4 us with
-// 192, 14.9 with 320, 16.2 with 384; calls that fill the grid do not depend on it.
+// Least work of a pair, in keys: the join of more parts costs more than they save. One token, 16 heads, with 192, 320, 512
+// and 768: 300 keys 13.0, 13.5, 14.6 and 14.6 us; 1000 keys 15.3, 14.9, 17.9 and 23.9; 2300 keys 15.3, 15.3, 16.7 and 19.8;
+// 4000 keys 20.1, 18.8, 20.0 and 22.9; 9000 keys 28.2, 23.6, 22.5 and 23.9; 20000 keys 39.3, 34.8, 31.8 and 29.9 (where
+// fewer parts to join would be better). Calls that fill the grid do not depend on it. (Both sweeps with the caches in L2.)
 constexpr int64_t MIN_KEYS = 320;
 
 struct Bound {
@@ -190,12 +197,16 @@ struct Walk {
     }
 };
 
-// Where share `which` of `active` begins, in cost: total * which / active, which the product may not fit.
-__device__ __forceinline__ int64_t share(int64_t total, int which, int active) {
-    if (which >= active) return total;
-    if (total < (int64_t(1) << 31) / 256) return unsigned(total) * unsigned(which) / unsigned(active);   // 64-bit divisions take about 100 instructions
+// Where share `which` of `active` begins, in cost: total * which / active, which the product may not fit. Out of line where
+// it takes 64-bit divisions of about 100 instructions each: in line they moved the loops and cost a long chunk 1%.
+__device__ __noinline__ int64_t long_share(int64_t total, int which, int active) {
     const int64_t each = total / active;
     return each * which + unsigned(total - each * active) * unsigned(which) / unsigned(active);
+}
+__device__ __forceinline__ int64_t share(int64_t total, int which, int active) {
+    if (which >= active) return total;
+    if (total < (int64_t(1) << 31) / 256) return unsigned(total) * unsigned(which) / unsigned(active);
+    return long_share(total, which, active);
 }
 // Pairs that get work: equal shares, but none below MIN_KEYS.
 __device__ __forceinline__ int active_pairs(const MlaParams& p, int64_t total) {
@@ -1020,14 +1031,14 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int key0 = kt * KEYS + h * CKEYS + g * NK;
             float* red = m->red[j & 1];
-            c.wait(&m->s_full[j & 1], (j >> 1) & 1);
-            tc_fence_after();
             // Keys that exist: bit i for key0 + i. They come over a barrier of this CTA, as the arrivals that start the
-            // scores order nothing for these warps; it is long complete when the scores are. (The word is written anew
-            // once this step's weights have gone into O, and they depend on it.)
+            // scores order nothing for these warps. (The word is written anew once this step's weights have gone into O,
+            // and they depend on it.)
             constexpr int STAGES = stages_of<C8>();
             c.wait(&m->h_full[j % STAGES], (j / STAGES) & 1);
             const uint32_t held = m->held[j % STAGES][h] >> (g * NK);
+            c.wait(&m->s_full[j & 1], (j >> 1) & 1);
+            tc_fence_after();
             float s[NK];
             tmem_ld(lanes + COL_S + uint32_t(j & 1) * 64 + g * NK, s);
             if (split) {
@@ -1315,7 +1326,9 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
 // keep that rounding small (the products with the codes, exact as halves, then run on halves whatever q's type). A power
 // of two per row, put back into its scores, keeps q / scale below 2^14: it comes from the row's largest |q| and the largest
 // 1 / scale, and float16's range then reaches 2^-38 below. The rotary part keeps q's type, with the scale per channel
-// over a power of two of the largest 1 / scale. One warp a row.
+// over a power of two of the largest 1 / scale: that is 8 bits in bf16, as its own rounding was, and no more accurate than
+// that. 4 tokens of 32 heads over 900 keys, bf16: root-mean-square error of the output 0.0023 with a rotary scale per channel,
+// 0.0022 with one scale, lse off by 6e-4 and 2e-6. One warp a row.
 template <class IT>
 __global__ void __launch_bounds__(256) mla_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn_out, float* mul_out, uint16_t* qr_out) {
     __shared__ float inv[512], invk[64], most[2];
