@@ -103,11 +103,14 @@ typedef enum kvr_status {
 } kvr_status;
 
 /* Bits OR-ed into *dev_status by the kernels. */
-#define KVR_DEVERR_INDEX 0x1       /* kv: an index entry outside {-1} U [0, range) */
-#define KVR_DEVERR_KEY_LENGTH 0x2  /* qsa: key_length[n] < L (the past length would be negative) */
+#define KVR_DEVERR_INDEX 0x1       /* kv, read: an index entry outside {-1} U [0, range); attention: such
+                                      an entry of the block table that a token sees */
+#define KVR_DEVERR_KEY_LENGTH 0x2  /* qsa: key_length[n] < L (the past length would be negative);
+                                      attention: key_length[n] negative or beyond its keys */
 #define KVR_DEVERR_BLOCK_CAP 0x4   /* qsa: a completed block's number is >= Bcap */
-#define KVR_DEVERR_TIMEOUT 0x8     /* a pipeline wait inside a kernel exceeded its limit
-                                      (one second); that CTA stopped early, output incomplete */
+#define KVR_DEVERR_TIMEOUT 0x8     /* a pipeline wait inside a kernel exceeded its limit (one second, in
+                                      mla_attention and one more for 2^22 keys of a part before); that
+                                      CTA stopped early, output incomplete */
 #define KVR_DEVERR_PAST_BLOCKS 0x10 /* qsa, concat-output form: past_block_index_keys holds
                                       fewer than floor(P/kbs) rows for a sequence */
 #define KVR_DEVERR_QUERY 0x20      /* attention: query_start decreases or leaves [0, T] at a sequence */
@@ -572,6 +575,9 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  * float16 for the latent part and to `dtype` for the rotary part, which moves a
  * score by up to one unit in the last place of that type (relative to the
  * terms' size) and lse with it; one scale for all channels rounds nothing more.
+ * The output's sum on the tensor cores takes 16 keys an addition and cuts it off:
+ * up to keys * 2^-27 of the terms' size where one CTA pair goes over all keys
+ * (measured: 2^-10 of the output at 2^20 keys).
  * out, lse and workspace must not overlap an input or one another. The result
  * of a call does not change from run to run on one GPU.
  */
