@@ -413,10 +413,10 @@ struct Maps {
 
 // The rest of a wait, out of line: the roles' loops have to stay in the instruction cache. `more`: seconds beyond the first.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int more) {
-    do {
+    while (*abort == 0) {
         if (mbar_wait(bar, parity, abort)) return true;
-    } while (*abort == 0 && --more >= 0);
-    *abort = 1;
+        if (--more < 0) *abort = 1;
+    }
     return false;
 }
 
