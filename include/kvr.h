@@ -550,8 +550,9 @@ kvr_status kv_cache_read(const kvr_read_args* args, cudaStream_t stream);
  *   ckv_dtype, k_dtype, ckv_scale, k_scale  as in kvr_kv_args; an 8-bit code
  *                stands for code / scale[c].
  *   out          [T, H, Dv] `dtype`, strides as for q. A token that sees no key
- *                gets zeros. A query row that holds a NaN gives NaN in its
- *                output row and lse, and in no other.
+ *                gets zeros, and so does one whose every score is -inf. A query
+ *                row that holds a NaN gives NaN in its output row and lse, and
+ *                in no other.
  *   lse          optional out float32 [T, H]: log(sum_i exp(s[i])), -inf for a
  *                token that sees no key.
  *   workspace    device memory of kvr_mla_attention_workspace(args) bytes,

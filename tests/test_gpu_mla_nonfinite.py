@@ -56,6 +56,20 @@ def test_a_nan_query_that_sees_no_key_or_one(Dv, Dk):
     assert np.isfinite(got[0][1, 0]).all() and np.isfinite(got[1][1, 0])
 
 
+@pytest.mark.parametrize("Dv,Dk", [(512, 64), (10, 6)])
+def test_scores_of_minus_infinity(Dv, Dk):
+    """An infinite query over keys of one sign: every score is -inf, and the row as one that sees no key."""
+    c = case(Dv, Dk)
+    for t in (c.ckv, c.k):
+        t.view(-1, t.shape[-1])[:, -1] = t.view(-1, t.shape[-1])[:, -1].abs() + 0.5
+    want = run_mla(c)
+    got = run_mla(spoiled(c, "q_rope", [(1, 3)], float("-inf")))
+    assert (got[0][1, 3] == 0).all() and np.isneginf(got[1][1, 3])
+    rest = np.ones(want[1].shape, bool)
+    rest[1, 3] = False
+    assert np.array_equal(got[0][rest], want[0][rest]) and np.array_equal(got[1][rest], want[1][rest])
+
+
 @pytest.mark.parametrize("key", [0, 63, 149])
 @pytest.mark.parametrize("part", ["ckv", "k"])
 @pytest.mark.parametrize("Dv,Dk,cache", [(512, 64, None), (512, 64, "fp8_e4m3fn"), (10, 6, None), (10, 6, "fp8_e4m3fn")])
