@@ -430,9 +430,9 @@ struct Ctx {
     volatile int* abort;
     bool ok;
 
-    // A wait that gives up (after one second, or one and `more`) poisons the CTA: the others give up at their first look. The warps that start TMA
-    // copies then stop; every other role runs its loops to the end without waiting, so that no barrier is left with
-    // threads missing.
+    // A wait that gives up (after one second, or one and `more`) poisons the CTA: the others give up at their first look.
+    // The warps that start TMA copies then stop; every other role runs its loops to the end without waiting, so that no
+    // barrier is left with threads missing.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int more = 0) {
         if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, more) && ok;
         __syncwarp();
@@ -997,6 +997,14 @@ __device__ __forceinline__ float row_sum(const float* x, int r) {
 // room for: weights below 2^(8 + 7), a half ends at 65504. What is lost of a weight then is 2^-32 of the row's largest.
 template <class PT>
 constexpr float LIFT = is_bf16<PT> ? 0.f : 7.f;
+// The exponent that weights are taken to. Where scores are so large (2^24) that a float cannot be 7 lower, it may not be
+// more than 7 lower either, or weights would overflow.
+template <class PT>
+__device__ __forceinline__ float reference(float mx) {
+    if (LIFT<PT> == 0.f) return mx;
+    const float r = mx - LIFT<PT>;
+    return mx - r <= LIFT<PT> ? r : mx;   // (infinities stay)
+}
 
 // Softmax: thread (row r, half h of the keys, group g: half of that half).
 template <class IT, bool C8, bool K8>
@@ -1026,7 +1034,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             fn = l2 * (p.ckv_scale_per_ch ? 1.f : c.sc->inv_v[0]);
             if (p.row_mul != nullptr && live) fn *= p.row_mul[(w.s.q0 + row / unsigned(p.H)) * p.H + row % unsigned(p.H)];
         }
-        float mx = -INFINITY, sum = 0.f;
+        float mx = -INFINITY, at = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int key0 = kt * KEYS + h * CKEYS + g * NK;
@@ -1066,13 +1074,16 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
             softmax_sync<C8>();
             top = fmaxf(row_max<G>(red, r), mx);
             // The sum is rescaled only when the maximum grows by more than 2^8: weights then stay below 2^(8 + LIFT).
-            const bool grow = top > mx + 8.f;
-            const float f = grow ? exp2_approx(mx - top) : 1.f;
+            const bool grow = top - mx > 8.f;
+            float f = 1.f;
             if (grow) {
+                const float next = reference<PT>(top);
+                f = exp2_approx(at - next);
                 mx = top;
+                at = next;
                 sum *= f;
             }
-            const float ref = mx == -INFINITY ? 0.f : mx - LIFT<PT>;
+            const float ref = mx == -INFINITY ? 0.f : at;
             uint32_t pk[NK / 2];
             float step = 0.f;   // of its own: one addition a step to the long sum, which rounds small weights beside a large one
 #pragma unroll
@@ -1109,7 +1120,7 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         float* red = m->red[j & 1];
         red[tid] = sum;   // the next step's buffer: its own maxima come after the second barrier
         softmax_sync<C8>();
-        const float2 ml = make_float2(mx - LIFT<PT>, row_sum<G>(red, r));   // the exponent that l and O are taken to
+        const float2 ml = make_float2(at, row_sum<G>(red, r));   // the exponent that l and O are taken to
         softmax_sync<C8>();
         c.wait(&m->pv_done, (j - 1) & 1);
         tc_fence_after();

@@ -111,3 +111,46 @@ def test_the_plain_kernel_beside_a_sink(dtype, octaves):
     rel = 2.0 ** -19 + N * 2.0 ** -30 + 64 * 2.0 ** -24
     assert ((out.double() - want).abs() <= half_step(dt) * want.abs() * (1 + 2.0 ** -6) + 2 * rel * size).all()
     assert float((lse.double() - want_lse).abs().max()) <= rel + 2.0 ** -23 * abs(want_lse)
+
+
+def unit_scale():
+    """The softmax scale whose float32 product with log2(e) is 1: scores in octaves are the products themselves."""
+    log2e = torch.tensor(1.4426950408889634, dtype=torch.float32)
+    x = torch.tensor(math.log(2.0), dtype=torch.float32)
+    near = [torch.nextafter(x, x - 1), x, torch.nextafter(x, x + 1)]
+    return next(float(v) for v in near if float(v * log2e) == 1.0)
+
+
+@pytest.mark.parametrize("base", [10, 23, 24, 25, 26, 28])
+@pytest.mark.parametrize("dtype,cache", [("f16", None), ("f16", "int8"), ("bf16", "int8"), ("bf16", None)])
+def test_scores_that_a_float_holds_coarsely(dtype, cache, base):
+    """Scores of 2^base octaves and 0 to 12 above, in multiples of what a float32 of that size can tell apart: the first step's
+    keys set the reference, later ones are up to 8 octaves above it and then more."""
+    unit, n = 2.0 ** max(base - 23, 0), 512
+    dt = DTYPES[dtype]
+    g = torch.Generator().manual_seed(base)
+    above = torch.zeros(n)
+    above[64:128] = (torch.randint(0, 9, (64,), generator=g) / unit).floor() * unit
+    above[128:] = (torch.randint(0, 13, (n - 128,), generator=g) / unit).floor() * unit
+    k = torch.zeros(n, 64)
+    k[:, 0], k[:, 1] = 2.0 ** (base // 2), above
+    q_rope = torch.zeros(64)
+    q_rope[0], q_rope[1] = 2.0 ** (base - base // 2), 1
+    v = torch.randn(n, 512, generator=g)
+    scale = None
+    if cache:
+        v, scale = (v * 20).round().clamp(-128, 127), torch.full((1,), 20.0, device="cuda")
+    c = dict(ckv=v.to(DTYPES[cache or dtype]).cuda().view(4, 128, 1, 512), k=k.to(dt).cuda().view(4, 128, 1, 64))
+    assert torch.equal(c["k"].float().cpu().view(n, 64), k)
+    rows = 70   # both CTAs of a pair
+    out, lse = torch.zeros(1, rows, 512, device="cuda", dtype=dt), torch.zeros(1, rows, device="cuda")
+    kvr.mla_attention(torch.zeros(1, rows, 512, device="cuda", dtype=dt), q_rope.to(dt).cuda().expand(1, rows, 64).contiguous(), c["ckv"],
+                      c["k"], torch.arange(4, device="cuda").view(1, 4), torch.tensor([0, 1], device="cuda"), torch.tensor([n], device="cuda"),
+                      out, softmax_scale=unit_scale(), ckv_scale=scale, lse=lse)
+    p = torch.softmax(above.double().cuda() * math.log(2.0), 0)
+    value = c["ckv"].view(n, 512).double() / (20.0 if cache else 1.0)
+    want, size = p @ value, p @ value.abs()
+    # Differences of scores are exact and whole, so weights are powers of two and round nowhere; 512 keys in float32.
+    assert ((out.double() - want).abs() <= half_step(dt) * want.abs() * (1 + 2.0 ** -6) + 2.0 ** -14 * size).all()
+    want_lse = (2.0 ** base + torch.logsumexp(above.double() * math.log(2.0), 0) / math.log(2.0)) * math.log(2.0)
+    assert float((lse.double() - float(want_lse)).abs().max()) <= 2.0 ** -22 * float(want_lse)
