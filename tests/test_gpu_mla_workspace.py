@@ -15,6 +15,14 @@ def tensors(c):
     return [d(t) for t in (c.q_nope, c.q_rope, c.ckv, c.k, c.table, c.query_start, c.key_length)]
 
 
+def keep_busy():
+    """The current stream sleeps for some 0.2 s; what follows on it finds its kernels loaded and no free block cached."""
+    torch.empty(8, dtype=torch.uint8, device="cuda").fill_(1)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(400_000_000)
+
+
 @pytest.fixture
 def workspaces(monkeypatch):
     """Addresses of the workspaces that calls take."""
@@ -67,9 +75,8 @@ def test_a_call_on_another_stream_takes_no_memory_that_the_current_one_still_use
     args = tensors(c)
     out = torch.zeros_like(args[0])
     size = kvr.prepare_mla_attention(*args, out, softmax_scale=c.scale).workspace.numel()
-    torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    torch.cuda._sleep(100_000_000)   # tens of milliseconds
+    keep_busy()
     used = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
     at = used.data_ptr()
     del used
@@ -89,10 +96,11 @@ def test_a_bound_call_on_another_stream_waits_for_its_memory(given):
     args = tensors(c)
     out = torch.zeros_like(args[0])
     size = kvr.prepare_mla_attention(*args, out, softmax_scale=c.scale).workspace.numel()
-    torch.cuda.synchronize()
     side, done = torch.cuda.Stream(), torch.cuda.Event()
-    torch.cuda._sleep(100_000_000)
+    keep_busy()
     used = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    filled = torch.cuda.Event()
+    filled.record()
     at = used.data_ptr()
     del used
     call = kvr.prepare_mla_attention(*args, out, softmax_scale=c.scale)
@@ -103,18 +111,11 @@ def test_a_bound_call_on_another_stream_waits_for_its_memory(given):
         with torch.cuda.stream(side):
             call()
     done.record(side)
-    torch.cuda._sleep(1000)
-    while not done.query():   # the call came after the fill: the current stream has at most its last, short sleep left
+    while not done.query():
         pass
-    assert torch.cuda.current_stream().query() or _soon(torch.cuda.current_stream())
+    assert filled.query(), "the call did not wait for what the current stream did to its memory"
     torch.cuda.synchronize()
     assert np.array_equal(out.double().cpu().numpy(), ref[0])
-
-
-def _soon(stream):
-    import time
-    time.sleep(0.005)
-    return stream.query()
 
 
 def test_calls_on_the_default_stream_by_its_handle():
