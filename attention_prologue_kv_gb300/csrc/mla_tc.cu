@@ -34,8 +34,8 @@
 // Measured: 512 tokens x 128 heads over 16384 keys 1540 us (1.5 PFLOP/s, 80% of the measured bf16 rate; a step takes
 // 0.82 us; the unit that runs tcgen05 is busy 92% of the time, 68% with the products themselves); 256 sequences of one
 // token, 128 heads, 1-4095 keys 159 us (4.5 TB/s, 66% of the copy rate; a step 0.89 us, a part's queries and output 5 us);
-// 61 sequences of one token over up to 16384 keys in E4M3 168 us (that unit 59%, no counter above: the chain load, decode,
-// scores, swap, softmax, second product of its three steps in flight); one sequence of 1000 keys, 16 heads 15.0 us. Steps
+// 61 sequences of one token over up to 16384 keys in E4M3 170 us (that unit 59%, no counter above: the chain load, decode,
+// scores, swap, softmax, second product of its three steps in flight); one sequence of 1000 keys, 16 heads 14.9 us. Steps
 // of 128 keys with two of them in flight were slower (1826 us): a stage's load, scores, softmax and second product follow
 // one another. Paths without TMA, with codes or with small blocks, at 65536 keys, us a step: blocks of 16 keys 1.8, of
 // 8 2.6, of 100 3.5, of 1 3.9; rotary codes over 16-bit latent rows 4.0 (blocks of 1: 5.0); latent codes 1.2 (blocks of 1: 1.4).
