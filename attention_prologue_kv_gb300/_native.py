@@ -107,9 +107,45 @@ class MlaArgs(ctypes.Structure):
     ]
 
 
+class TreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", _i64), ("N", _i64), ("query_start", _vp), ("parent", _vp), ("position_start", _vp),
+        ("tree_mask", _vp), ("mask_words", _i64), ("positions", _vp), ("dev_status", _vp),
+    ]
+
+
+class MlaTreeArgs(ctypes.Structure):
+    _fields_ = [("attention", MlaArgs), ("tree_mask", _vp), ("mask_words", _i64)]
+
+
+class KeyWeightArgs(ctypes.Structure):
+    _fields_ = [
+        ("step", MlaArgs), ("weight", _vp), ("weight_stride", _i64), ("weight_len", _i64),
+        ("past", _vp), ("past_stride", _i64), ("decay", _f32),
+    ]
+
+
+class SelectArgs(ctypes.Structure):
+    _fields_ = [
+        ("weight", _vp), ("weight_stride", _i64), ("weight_len", _i64), ("N", _i64), ("key_length", _vp),
+        ("keep", _i64), ("sink", _i64), ("recent", _i64), ("kept", _vp), ("kept_length", _vp),
+        ("kept_weight", _vp), ("kept_weight_stride", _i64), ("kept_weight_len", _i64), ("dev_status", _vp),
+    ]
+
+
+class CompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("ckv_cache", _vp), ("ckv_dtype", _int), ("k_cache", _vp), ("k_dtype", _int),
+        ("mode", _int), ("cache_d0", _i64), ("cache_d1", _i64), ("block_table", _vp), ("max_blocks", _i64),
+        ("N", _i64), ("Dv", _i64), ("Dk", _i64), ("kept", _vp), ("kept_len", _i64), ("kept_length", _vp), ("start", _vp),
+        ("dev_status", _vp),
+    ]
+
+
 EXPORTS = ("kv_rmsnorm_rope_cache", "kv_rmsnorm_rope_cache_staged", "kv_rmsnorm_rope_cache_staged_static",
            "qsa_prepare", "dynamic_quant", "query_rope", "kv_cache_read", "mla_attention",
-           "kvr_mla_attention_workspace", "kvr_device_copy",
+           "kvr_mla_attention_workspace", "draft_tree", "mla_tree_attention", "mla_key_weight",
+           "kvr_mla_key_weight_workspace", "kv_cache_select", "kv_cache_compact", "kvr_device_copy",
            "kvr_check_bounded_wait", "kvr_store_after_delay", "kvr_set_debug_validate",
            "kvr_status_string", "kvr_abi_version")
 
@@ -147,6 +183,13 @@ def lib():
     L.mla_attention.restype = _int
     L.kvr_mla_attention_workspace.argtypes = [ctypes.POINTER(MlaArgs)]
     L.kvr_mla_attention_workspace.restype = _i64
+    for name, args in (("draft_tree", TreeArgs), ("mla_tree_attention", MlaTreeArgs), ("mla_key_weight", KeyWeightArgs),
+                       ("kv_cache_select", SelectArgs), ("kv_cache_compact", CompactArgs)):
+        fn = getattr(L, name)
+        fn.argtypes = [ctypes.POINTER(args), _vp]
+        fn.restype = _int
+    L.kvr_mla_key_weight_workspace.argtypes = [ctypes.POINTER(KeyWeightArgs)]
+    L.kvr_mla_key_weight_workspace.restype = _i64
     L.kvr_check_bounded_wait.argtypes = [_vp, _i64, _i64, _vp]
     L.kvr_check_bounded_wait.restype = _int
     L.kvr_store_after_delay.argtypes = [_vp, _vp, _i64, _i64, _vp]

@@ -621,8 +621,9 @@ def kv_cache_read(ckv_cache, k_cache, index, out, *, cache_mode="PA_BSND", ckv_s
                           dev_status=dev_status)(stream)
 
 
-def _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode,
-                        causal, ckv_scale, k_scale, lse, workspace, dev_status):
+def _step_args(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode, causal,
+               ckv_scale, k_scale, lse, workspace, dev_status):
+    """MlaArgs of a step without its workspace; out None: a call that has none."""
     _cuda(q_nope, "q_nope")
     if q_nope.dtype not in _IN_DTYPES:
         raise ValueError("q_nope must be bfloat16 or float16")
@@ -633,7 +634,7 @@ def _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_s
     pair = _cache_pair(ckv_cache, k_cache, ckv_scale, k_scale, cache_mode, dtype)
     T, H, Dv, n_ts, n_hs = _heads(q_nope, "q_nope", dtype)
     _, _, Dk, r_ts, r_hs = _heads(q_rope, "q_rope", dtype, T, H)
-    _, _, Do, o_ts, o_hs = _heads(out, "out", dtype, T, H)
+    _, _, Do, o_ts, o_hs = (T, H, Dv, 0, 0) if out is None else _heads(out, "out", dtype, T, H)
     if (Dv, Dk, Do) != (pair["Dv"], pair["Dk"], pair["Dv"]):
         raise ValueError("q_nope and out must be as wide as ckv_cache (%d), q_rope as k_cache (%d)" % (pair["Dv"], pair["Dk"]))
     if key_length.dim() != 1:
@@ -656,26 +657,49 @@ def _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_s
                   q_nope_token_stride=n_ts, q_nope_head_stride=n_hs, q_rope_token_stride=r_ts, q_rope_head_stride=r_hs,
                   N=Nn, query_start=query_start.data_ptr(), key_length=key_length.data_ptr(),
                   block_table=_ptr(block_table, "block_table"), max_blocks=max_blocks, softmax_scale=float(softmax_scale),
-                  causal=1 if causal else 0, out=out.data_ptr(), out_token_stride=o_ts, out_head_stride=o_hs,
+                  causal=1 if causal else 0, out=None if out is None else out.data_ptr(), out_token_stride=o_ts, out_head_stride=o_hs,
                   lse=_ptr(lse, "lse"), dev_status=_ptr(dev_status, "dev_status"), **pair)
-    keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, ckv_scale, k_scale, lse, workspace,
-            dev_status)
-    call = BoundCall(N.lib().mla_attention, a, "mla_attention", keep, device)
+    return a
+
+
+def _take_workspace(call, step, need_of, args, workspace, device):
+    """Give a bound call its workspace, an own one where it needs one and got none; `step`: the MlaArgs that names it."""
     with torch.cuda.device(device):
-        need = N.lib().kvr_mla_attention_workspace(ctypes.byref(a))
+        need = need_of(ctypes.byref(args))
         if workspace is None and need:
             call.own(torch.empty(need, dtype=torch.uint8, device=device))
         else:
             call.workspace = workspace
     if call.workspace is not None:
-        a.workspace = _ptr(call.workspace, "workspace")
-        a.workspace_bytes = call.workspace.numel() * call.workspace.element_size()
+        step.workspace = _ptr(call.workspace, "workspace")
+        step.workspace_bytes = call.workspace.numel() * call.workspace.element_size()
     return call
+
+
+def _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode,
+                        causal, ckv_scale, k_scale, lse, workspace, dev_status, tree_mask=None):
+    _cuda(out, "out")
+    a = _step_args(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode, causal,
+                   ckv_scale, k_scale, lse, workspace, dev_status)
+    device = q_nope.device
+    keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, ckv_scale, k_scale, lse, workspace,
+            dev_status, tree_mask)
+    if tree_mask is None:
+        call = BoundCall(N.lib().mla_attention, a, "mla_attention", keep, device)
+        return _take_workspace(call, a, N.lib().kvr_mla_attention_workspace, a, workspace, device)
+    _one_device(device, dict(tree_mask=tree_mask))
+    if tree_mask.dim() != 2 or tree_mask.shape[1] < 1:
+        raise ValueError("tree_mask must be [T, words]")
+    _dense(tree_mask, "tree_mask", torch.int64, (q_nope.shape[0], tree_mask.shape[1]))
+    # (the structure holds a copy of `a`, which the workspace has to go to)
+    tree = N.MlaTreeArgs(attention=a, tree_mask=tree_mask.data_ptr(), mask_words=tree_mask.shape[1])
+    call = BoundCall(N.lib().mla_tree_attention, tree, "mla_attention", keep, device)
+    return _take_workspace(call, tree.attention, N.lib().kvr_mla_attention_workspace, tree.attention, workspace, device)
 
 
 def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
                           cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None,
-                          dev_status=None):
+                          dev_status=None, tree_mask=None):
     """mla_attention with its arguments bound once (see PreparedCall). Without
     a `workspace` the object keeps one of its own: calls of one object that can
     run at the same time (two streams, two replayed graphs) need an object, or
@@ -686,7 +710,7 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
     (torch.cuda.graph synchronises)."""
     _cuda(q_nope, "q_nope")
     call = _bind_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale,
-                               cache_mode, causal, ckv_scale, k_scale, lse, workspace, dev_status)
+                               cache_mode, causal, ckv_scale, k_scale, lse, workspace, dev_status, tree_mask)
     with torch.cuda.device(q_nope.device):
         call.may_travel()
     return call
@@ -694,7 +718,7 @@ def prepare_mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query
 
 def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, *, softmax_scale,
                   cache_mode="PA_BSND", causal=True, ckv_scale=None, k_scale=None, lse=None, workspace=None, dev_status=None,
-                  stream=None):
+                  tree_mask=None, stream=None):
     """Latent attention of new tokens over the caches of kv_rmsnorm_rope_cache:
     out[t, h] = sum_i softmax_i(softmax_scale * (q_nope[t, h] . c[i] +
     q_rope[t, h] . k[i])) c[i], the key row shared by all heads.
@@ -712,19 +736,216 @@ def mla_attention(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, 
     8-bit caches take their write scales (code / scale). Keys within
     key_length are taken to be finite: an infinity or NaN may reach every token
     of its sequence. At most 2^24 keys a sequence.
+    tree_mask int64 [T, words], in place of `causal`: token j of L sees the keys
+    before key_length - L and, for each bit b of its words (bit b % 64 of word
+    b // 64), new token b of its sequence: the ancestors of a drafted token,
+    itself among them, as draft_tree gives them. A sequence with more than
+    64 * words tokens is left out.
     `workspace` (optional, device memory of kvr_mla_attention_workspace
     bytes) must not be shared by calls that can run at the same time; without
     it the call takes one from PyTorch's allocator, on the stream that it is
     made on."""
     args = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, out, softmax_scale, cache_mode, causal,
-            ckv_scale, k_scale, lse, workspace, dev_status)
+            ckv_scale, k_scale, lse, workspace, dev_status, tree_mask)
+    _bind_and_call(_bind_mla_attention, args, q_nope, workspace, stream)
+
+
+def _bind_and_call(bind, args, q_nope, workspace, stream):
     if stream is None or workspace is not None:
-        _bind_mla_attention(*args)(stream)
+        bind(*args)(stream)
         return
     # With that stream current, so that the workspace's memory goes from call to call in its order.
     device = _cuda(q_nope, "q_nope").device
     with torch.cuda.device(device), torch.cuda.stream(_torch_stream(_stream(stream), device)):
-        _bind_mla_attention(*args)()
+        bind(*args)()
+
+
+def prepare_draft_tree(parent, query_start, tree_mask, *, position_start=None, positions=None, dev_status=None):
+    """draft_tree with its arguments bound once (see PreparedCall)."""
+    _cuda(parent, "parent")
+    if parent.dim() != 1:
+        raise ValueError("parent must be [T]")
+    T = parent.shape[0]
+    _one_device(parent.device, dict(query_start=query_start, tree_mask=tree_mask, position_start=position_start,
+                                    positions=positions, dev_status=dev_status))
+    if query_start.dim() != 1 or query_start.shape[0] < 1:
+        raise ValueError("query_start must be [N + 1]")
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [T, words]")
+    Nn, words = query_start.shape[0] - 1, tree_mask.shape[1]
+    for t, name, shape in ((parent, "parent", (T,)), (query_start, "query_start", (Nn + 1,)), (tree_mask, "tree_mask", (T, words)),
+                           (position_start, "position_start", (Nn,)), (positions, "positions", (T,))):
+        _dense(t, name, torch.int64, shape)
+    if positions is not None and position_start is None:
+        raise ValueError("positions need position_start")
+    _status_word(dev_status)
+    a = N.TreeArgs(T=T, N=Nn, query_start=query_start.data_ptr(), parent=parent.data_ptr(),
+                   position_start=_ptr(position_start, "position_start"), tree_mask=tree_mask.data_ptr(), mask_words=words,
+                   positions=_ptr(positions, "positions"), dev_status=_ptr(dev_status, "dev_status"))
+    return BoundCall(N.lib().draft_tree, a, "draft_tree", (parent, query_start, tree_mask, position_start, positions, dev_status),
+                     parent.device)
+
+
+def draft_tree(parent, query_start, tree_mask, *, position_start=None, positions=None, dev_status=None, stream=None):
+    """The ancestors of drafted tokens: parent int64 [T] names, for each token of a
+    sequence (rows [query_start[n], query_start[n + 1])), the place in its sequence
+    of the token before it that it continues, -1 where it continues the context.
+    tree_mask int64 [T, words] receives bit b % 64 of word b // 64 where token b is
+    the token itself or an ancestor, as mla_attention takes it; positions
+    (optional int64 [T]) position_start[n] + the number of its ancestors, as
+    query_rope takes them. Any other parent counts as -1 (KVR_DEVERR_INDEX);
+    sequences of more than 64 * words tokens are left out (KVR_DEVERR_QUERY);
+    rows outside every sequence stay as they were. 1 to 64 words."""
+    prepare_draft_tree(parent, query_start, tree_mask, position_start=position_start, positions=positions,
+                       dev_status=dev_status)(stream)
+
+
+def _rows_of(t, name, n=None):
+    """(N, width, row stride) of float32 [N, width] rows with a dense last axis."""
+    _cuda(t, name)
+    if t.dim() != 2 or t.dtype != torch.float32 or (t.shape[1] > 1 and t.stride(1) != 1) or (n is not None and t.shape[0] != n):
+        raise ValueError("%s must be float32 %s, dense along its last dimension" % (name, "[N, width]" if n is None else "[%d, width]" % n))
+    if t.shape[0] <= 1 or t.shape[1] == 0:
+        return t.shape[0], t.shape[1], t.shape[1]
+    _apart(t.shape[0], t.stride(0), name)
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _bind_mla_key_weight(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight, softmax_scale,
+                         cache_mode, causal, past, decay, ckv_scale, k_scale, workspace, dev_status):
+    if lse is None:
+        raise ValueError("lse must be float32 [T, H], as mla_attention writes it")
+    a = _step_args(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, None, softmax_scale, cache_mode, causal,
+                   ckv_scale, k_scale, lse, workspace, dev_status)
+    device, n = q_nope.device, key_length.shape[0]
+    _one_device(device, dict(weight=weight, past=past))
+    _, width, stride = _rows_of(weight, "weight", n)
+    past_stride = 0
+    if past is not None:
+        _, past_width, past_stride = _rows_of(past, "past", n)
+        if past_width != width:
+            raise ValueError("past must have weight's shape")
+    w = N.KeyWeightArgs(step=a, weight=weight.data_ptr(), weight_stride=stride, weight_len=width,
+                        past=None if past is None else past.data_ptr(), past_stride=past_stride, decay=float(decay))
+    keep = (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight, past, ckv_scale, k_scale,
+            workspace, dev_status)
+    call = BoundCall(N.lib().mla_key_weight, w, "mla_key_weight", keep, device)
+    return _take_workspace(call, w.step, N.lib().kvr_mla_key_weight_workspace, w, workspace, device)
+
+
+def prepare_mla_key_weight(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight, *, softmax_scale,
+                           cache_mode="PA_BSND", causal=True, past=None, decay=1.0, ckv_scale=None, k_scale=None, workspace=None,
+                           dev_status=None):
+    """mla_key_weight with its arguments bound once (see PreparedCall); its
+    workspace is kept as prepare_mla_attention's is."""
+    _cuda(q_nope, "q_nope")
+    call = _bind_mla_key_weight(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight,
+                                softmax_scale, cache_mode, causal, past, decay, ckv_scale, k_scale, workspace, dev_status)
+    with torch.cuda.device(q_nope.device):
+        call.may_travel()
+    return call
+
+
+def mla_key_weight(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight, *, softmax_scale,
+                   cache_mode="PA_BSND", causal=True, past=None, decay=1.0, ckv_scale=None, k_scale=None, workspace=None,
+                   dev_status=None, stream=None):
+    """The attention weight that each key receives: weight[n, i] = decay *
+    past[n, i] + the sum over sequence n's tokens and heads of exp(score - lse)
+    for key i, scores and arguments as in mla_attention, lse float32 [T, H] as it
+    writes it. weight float32 [N, width] (rows may be strided) for sequences of
+    up to `width` keys; entries behind a sequence's last key, and rows of
+    sequences without tokens, stay as they were. past: None (nothing is taken
+    up), `weight` itself to add up in place, or another tensor of its shape.
+    Keys of blocks that the table leaves out receive nothing. After a drafted
+    tree, call it for the accepted tokens over the compacted cache: there they
+    are a causal chain."""
+    _bind_and_call(_bind_mla_key_weight, (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight,
+                                          softmax_scale, cache_mode, causal, past, decay, ckv_scale, k_scale, workspace,
+                                          dev_status), q_nope, workspace, stream)
+
+
+def prepare_kv_cache_select(weight, key_length, kept, kept_length, *, sink=0, recent=0, kept_weight=None, dev_status=None):
+    """kv_cache_select with its arguments bound once (see PreparedCall)."""
+    n, width, stride = _rows_of(weight, "weight")
+    _one_device(weight.device, dict(key_length=key_length, kept=kept, kept_length=kept_length, kept_weight=kept_weight,
+                                    dev_status=dev_status))
+    if kept.dim() != 2:
+        raise ValueError("kept must be [N, keep]")
+    keep = kept.shape[1]
+    for t, name, shape in ((key_length, "key_length", (n,)), (kept_length, "kept_length", (n,)), (kept, "kept", (n, keep))):
+        _dense(t, name, torch.int64, shape)
+    carried, carried_width, carried_stride = None, 0, 0
+    if kept_weight is not None:
+        _, carried_width, carried_stride = _rows_of(kept_weight, "kept_weight", n)
+        carried = kept_weight.data_ptr()
+    _status_word(dev_status)
+    a = N.SelectArgs(weight=weight.data_ptr(), weight_stride=stride, weight_len=width, N=n, key_length=key_length.data_ptr(),
+                     keep=keep, sink=int(sink), recent=int(recent), kept=kept.data_ptr(), kept_length=kept_length.data_ptr(),
+                     kept_weight=carried, kept_weight_stride=carried_stride, kept_weight_len=carried_width,
+                     dev_status=_ptr(dev_status, "dev_status"))
+    return BoundCall(N.lib().kv_cache_select, a, "kv_cache_select", (weight, key_length, kept, kept_length, kept_weight, dev_status),
+                     weight.device)
+
+
+def kv_cache_select(weight, key_length, kept, kept_length, *, sink=0, recent=0, kept_weight=None, dev_status=None, stream=None):
+    """Which keys to keep: of the key_length[n] (int64 [N]) keys with weight float32
+    [N, width] (rows may be strided), as mla_key_weight adds them up, at most
+    keep = kept.shape[1]: the first `sink`, the last `recent` and, of those
+    between, the ones of largest weight, the earlier of equal ones (NaN above
+    every number). kept int64 [N, keep] receives their positions, ascending, then
+    -1; kept_length int64 [N] their count; kept_weight (optional float32
+    [N, >= keep]) their weights in that order, then zeros. sink + recent <= keep."""
+    prepare_kv_cache_select(weight, key_length, kept, kept_length, sink=sink, recent=recent, kept_weight=kept_weight,
+                            dev_status=dev_status)(stream)
+
+
+def prepare_kv_cache_compact(ckv_cache, k_cache, block_table, kept, kept_length, *, start=None, cache_mode="PA_BSND",
+                             dev_status=None):
+    """kv_cache_compact with its arguments bound once (see PreparedCall)."""
+    if cache_mode not in N.CACHE_MODES:
+        raise ValueError("cache_mode must be one of %s" % list(N.CACHE_MODES))
+    d0, d1, Dv = _cache_dims(ckv_cache, "ckv_cache")
+    k0, k1, Dk = _cache_dims(k_cache, "k_cache")
+    if (k0, k1) != (d0, d1):
+        raise ValueError("ckv_cache and k_cache must share their leading dims")
+    _one_device(ckv_cache.device, dict(k_cache=k_cache, block_table=block_table, kept=kept, kept_length=kept_length, start=start,
+                                       dev_status=dev_status))
+    if kept.dim() != 2:
+        raise ValueError("kept must be [N, kept]")
+    n, most = kept.shape
+    max_blocks = 0
+    if cache_mode == "Norm":
+        if block_table is not None:
+            raise ValueError("Norm mode takes no block_table")
+    else:
+        if block_table is None or block_table.dim() != 2:
+            raise ValueError("block_table must be [N, max_blocks] in the paged modes")
+        max_blocks = block_table.shape[1]
+        _dense(block_table, "block_table", torch.int64, (n, max_blocks))
+    for t, name, shape in ((kept, "kept", (n, most)), (kept_length, "kept_length", (n,)), (start, "start", (n,))):
+        _dense(t, name, torch.int64, shape)
+    _status_word(dev_status)
+    a = N.CompactArgs(ckv_cache=ckv_cache.data_ptr(), ckv_dtype=_CACHE_DTYPES[ckv_cache.dtype], k_cache=k_cache.data_ptr(),
+                      k_dtype=_CACHE_DTYPES[k_cache.dtype], mode=N.CACHE_MODES[cache_mode], cache_d0=d0, cache_d1=d1,
+                      block_table=_ptr(block_table, "block_table"), max_blocks=max_blocks, N=n, Dv=Dv, Dk=Dk, kept=kept.data_ptr(),
+                      kept_len=most, kept_length=kept_length.data_ptr(), start=_ptr(start, "start"),
+                      dev_status=_ptr(dev_status, "dev_status"))
+    return BoundCall(N.lib().kv_cache_compact, a, "kv_cache_compact",
+                     (ckv_cache, k_cache, block_table, kept, kept_length, start, dev_status), ckv_cache.device)
+
+
+def kv_cache_compact(ckv_cache, k_cache, block_table, kept, kept_length, *, start=None, cache_mode="PA_BSND", dev_status=None,
+                     stream=None):
+    """Rows of each sequence moved together in place, in both caches: key start[n] + i
+    becomes what key kept[n, i] was, for i < kept_length[n]; kept int64 [N, most]
+    ascending with kept[n, i] >= start[n] + i, as kv_cache_select gives it (start
+    None: 0), or the places of an accepted branch of a drafted tree (start int64
+    [N]: the keys before the tree). Caches of any two types and the block table as
+    mla_attention takes them; rows move as they are. Rows that stay are not
+    touched; blocks that sequences share have to lie within those. An entry out
+    of order or that names no row is not moved (KVR_DEVERR_INDEX)."""
+    prepare_kv_cache_compact(ckv_cache, k_cache, block_table, kept, kept_length, start=start, cache_mode=cache_mode,
+                             dev_status=dev_status)(stream)
 
 
 def device_copy(dst, src, stream=None):

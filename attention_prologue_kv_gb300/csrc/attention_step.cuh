@@ -91,7 +91,20 @@ struct MlaParams {
     const float* row_mul;       // power of two per row that its prepared queries lack, or NULL
     int runs, groups;           // its blocks hold whole halves of a step, whole groups of 8 keys
     int box_rows;               // its TMA boxes' rows (0: none)
+    const int64_t* tree;        // [T, words] words of the new tokens that each token sees, or NULL
+    int64_t words;
+    int64_t max_new;            // new tokens of a sequence: T, or what the words have bits for
 };
+
+// Which of the 32 keys from key0 on a token sees by its words: all before the new ones, the first of which is key `first`.
+__device__ __forceinline__ uint32_t tree_bits(const int64_t* words, int64_t count, int first, int key0) {
+    const int off = key0 - first;   // bit of key0
+    if (off <= -32) return 0xFFFFFFFFu;
+    const int w = off >> 6, s = off & 63;   // (off < 0: the word -1 that comes before is all ones)
+    const uint64_t a = w < 0 ? ~uint64_t(0) : (w < count ? uint64_t(words[w]) : 0);
+    if (s <= 32) return uint32_t(a >> s);
+    return uint32_t(a >> s) | uint32_t((w + 1 < count ? uint64_t(words[w + 1]) : 0) << (64 - s));
+}
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool half_pairs, bool vec, cudaStream_t s);
 cudaError_t launch_read(const ReadParams& p, int out_dtype, bool vec, cudaStream_t s);

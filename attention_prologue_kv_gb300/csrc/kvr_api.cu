@@ -11,7 +11,7 @@
 
 #include <algorithm>
 
-#include "attention_step.cuh"
+#include "cache_ops.cuh"
 
 namespace kvr {
 
@@ -599,8 +599,16 @@ bool mla_tensor_cores(const kvr_mla_args* a) {
            aligned(a->q_rope, 16) && aligned(a->out, 16) && aligned(a->ckv_cache, 16) && aligned(a->k_cache, 16);
 }
 
-// Validate the arguments of mla_attention. `*empty`: nothing to launch.
-kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
+struct Region {
+    const void* p;
+    int64_t n;   // bytes
+};
+
+// Validate the arguments of mla_attention, or of a call that has its `step` and other outputs (wants_out: 0; lse is then
+// read), and fill what the kernels take of them. more_in, more_out: what the call has beside them. `*empty`: nothing to
+// launch.
+kvr_status step_plan(const kvr_mla_args* a, bool wants_out, std::initializer_list<Region> more_in,
+                     std::initializer_list<Region> more_out, MlaParams* p, bool* empty) {
     *empty = false;
     if (a == nullptr) return KVR_ERR_NULL;
     if (a->mode != KVR_CACHE_NORM && a->mode != KVR_CACHE_PA_BSND && a->mode != KVR_CACHE_PA_BLK_BSND) return KVR_ERR_MODE;
@@ -619,30 +627,33 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
         *empty = true;
         return KVR_OK;
     }
-    if (a->q_nope == nullptr || a->q_rope == nullptr || a->out == nullptr || a->query_start == nullptr ||
-        a->key_length == nullptr || a->ckv_cache == nullptr || a->k_cache == nullptr ||
+    if (a->q_nope == nullptr || a->q_rope == nullptr || (wants_out ? a->out == nullptr : a->lse == nullptr) ||
+        a->query_start == nullptr || a->key_length == nullptr || a->ckv_cache == nullptr || a->k_cache == nullptr ||
         (!norm && a->max_blocks > 0 && a->block_table == nullptr))
         return KVR_ERR_NULL;
-    if (!aligned(a->q_nope, 2) || !aligned(a->q_rope, 2) || !aligned(a->out, 2) || !aligned(a->query_start, 8) ||
+    if (!aligned(a->q_nope, 2) || !aligned(a->q_rope, 2) || (wants_out && !aligned(a->out, 2)) || !aligned(a->query_start, 8) ||
         !aligned(a->key_length, 8) || !aligned(a->block_table, 8) || !aligned(a->lse, 4) || !aligned(a->dev_status, 4) ||
         (is16(a->ckv_dtype) && !aligned(a->ckv_cache, 2)) || (is16(a->k_dtype) && !aligned(a->k_cache, 2)))
         return KVR_ERR_SHAPE;
     const int64_t qn = span3(a->T, a->H, a->Dv, a->q_nope_token_stride, a->q_nope_head_stride);
     const int64_t qr = span3(a->T, a->H, a->Dk, a->q_rope_token_stride, a->q_rope_head_stride);
-    const int64_t o = span3(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride);
+    const int64_t o = wants_out ? span3(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride) : 0;
     if (qn < 0 || qr < 0 || o < 0) return KVR_ERR_SHAPE;
-    if (!rows_apart(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride)) return KVR_ERR_ALIAS;
+    if (wants_out && !rows_apart(a->T, a->H, a->Dv, a->out_token_stride, a->out_head_stride)) return KVR_ERR_ALIAS;
     const int64_t rows = a->cache_d0 * a->cache_d1;
-    const struct { const void* p; int64_t n; } in[] = {
+    Region in[16] = {
         {a->q_nope, qn * 2}, {a->q_rope, qr * 2}, {a->query_start, (a->N + 1) * 8}, {a->key_length, a->N * 8},
         {norm ? nullptr : a->block_table, a->N * a->max_blocks * 8},
         {a->ckv_cache, rows * a->Dv * (is16(a->ckv_dtype) ? 2 : 1)}, {a->k_cache, rows * a->Dk * (is16(a->k_dtype) ? 2 : 1)},
         {a->ckv_scale, a->ckv_scale_len * 4}, {a->k_scale, a->k_scale_len * 4}};
-    const struct { const void* p; int64_t n; } outs[] = {
-        {a->out, o * 2}, {a->lse, a->T * a->H * 4}, {a->workspace, a->workspace_bytes}, {a->dev_status, 4}};
-    for (int i = 0; i < 4; ++i) {
-        for (const auto& x : in)
-            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+    Region outs[8] = {{a->workspace, a->workspace_bytes}, {a->dev_status, 4}, {wants_out ? a->out : nullptr, o * 2}};
+    int ins = 9, n_outs = 3;
+    (wants_out ? outs[n_outs++] : in[ins++]) = {a->lse, a->T * a->H * 4};
+    for (const Region& x : more_in) in[ins++] = x;
+    for (const Region& x : more_out) outs[n_outs++] = x;
+    for (int i = 0; i < n_outs; ++i) {
+        for (int j = 0; j < ins; ++j)
+            if (overlap(outs[i].p, outs[i].n, in[j].p, in[j].n)) return KVR_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
     }
@@ -683,7 +694,48 @@ kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty) {
     p->ckv_scale_per_ch = a->ckv_scale_len == a->Dv && a->Dv > 1;
     p->k_scale_per_ch = a->k_scale_len == a->Dk && a->Dk > 1;
     p->scale = a->softmax_scale;
+    p->max_new = a->T;
+    return KVR_OK;
+}
+
+kvr_status mla_plan(const kvr_mla_args* a, MlaParams* p, bool* empty, std::initializer_list<Region> more_in = {}) {
+    const kvr_status st = step_plan(a, true, more_in, {}, p, empty);
+    if (st != KVR_OK || *empty) return st;
     return mla_tensor_cores(a) && !mla_tc_fits(*p) ? KVR_ERR_SHAPE : KVR_OK;
+}
+
+kvr_status launch_attention(const kvr_mla_args* a, const MlaParams& p, cudaStream_t stream) {
+    const bool tc = mla_tensor_cores(a);
+    if (tc) {
+        if (a->workspace == nullptr) return KVR_ERR_NULL;
+        if (!aligned(a->workspace, 32) || a->workspace_bytes < mla_tc_workspace(p, a->dtype)) return KVR_ERR_SHAPE;
+    }
+    (void)cudaGetLastError();
+    return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));
+}
+
+kvr_status key_weight_plan(const kvr_key_weight_args* a, KeyWeightParams* p, bool* empty) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    const kvr_mla_args& s = a->step;
+    if (a->weight_len < 0 || a->weight_stride < a->weight_len || (a->past != nullptr && a->past_stride < a->weight_len) ||
+        !product_fits({s.N < 0 ? 0 : s.N, a->weight_stride, 4}) ||
+        (a->past != nullptr && !product_fits({s.N < 0 ? 0 : s.N, a->past_stride, 4})) || !(a->decay == a->decay))
+        return KVR_ERR_SHAPE;
+    if (!aligned(a->weight, 4) || !aligned(a->past, 4)) return KVR_ERR_SHAPE;
+    const bool in_place = a->past == a->weight;
+    if (in_place && a->past_stride != a->weight_stride && s.N > 1) return KVR_ERR_ALIAS;
+    const int64_t wb = s.N > 0 ? ((s.N - 1) * a->weight_stride + a->weight_len) * 4 : 0;
+    const int64_t pb = s.N > 0 ? ((s.N - 1) * a->past_stride + a->weight_len) * 4 : 0;
+    const kvr_status st = step_plan(&s, false, {{in_place ? nullptr : a->past, pb}}, {{a->weight, wb}}, &p->m, empty);
+    if (st != KVR_OK || *empty) return st;
+    if (a->weight == nullptr && a->weight_len > 0) return KVR_ERR_NULL;
+    p->m.max_keys = std::min(p->m.max_keys, a->weight_len);
+    p->weight = a->weight;
+    p->past = a->past;
+    p->weight_stride = a->weight_stride;
+    p->past_stride = a->past_stride;
+    p->decay = a->decay;
+    return KVR_OK;
 }
 
 }  // namespace
@@ -702,13 +754,144 @@ kvr_status mla_attention(const kvr_mla_args* a, cudaStream_t stream) {
     bool empty;
     const kvr_status st = mla_plan(a, &p, &empty);
     if (st != KVR_OK || empty) return st;
-    const bool tc = mla_tensor_cores(a);
-    if (tc) {
-        if (a->workspace == nullptr) return KVR_ERR_NULL;
-        if (!aligned(a->workspace, 32) || a->workspace_bytes < mla_tc_workspace(p, a->dtype)) return KVR_ERR_SHAPE;
-    }
+    return launch_attention(a, p, stream);
+}
+
+kvr_status mla_tree_attention(const kvr_mla_tree_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    const kvr_mla_args& s = a->attention;
+    if (a->mask_words < 1 || !product_fits({s.T < 0 ? 0 : s.T, a->mask_words, 64}) || !aligned(a->tree_mask, 8)) return KVR_ERR_SHAPE;
+    MlaParams p;
+    bool empty;
+    const kvr_status st = mla_plan(&s, &p, &empty, {{a->tree_mask, s.T * a->mask_words * 8}});
+    if (st != KVR_OK || empty) return st;
+    if (a->tree_mask == nullptr) return KVR_ERR_NULL;
+    p.causal = 0;
+    p.tree = a->tree_mask;
+    p.words = a->mask_words;
+    p.max_new = std::min(p.T, a->mask_words * 64);
+    return launch_attention(&s, p, stream);
+}
+
+int64_t kvr_mla_key_weight_workspace(const kvr_key_weight_args* a) {
+    (void)a;
+    return 0;
+}
+
+kvr_status mla_key_weight(const kvr_key_weight_args* a, cudaStream_t stream) {
+    KeyWeightParams p = {};
+    bool empty;
+    const kvr_status st = key_weight_plan(a, &p, &empty);
+    if (st != KVR_OK || empty) return st;
     (void)cudaGetLastError();
-    return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));
+    return cuda_status(launch_key_weight_generic(p, a->step.dtype, stream));
+}
+
+kvr_status draft_tree(const kvr_tree_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (a->T < 0 || a->N < 0 || a->N > 0x7FFFFFFF || a->mask_words < 1 || a->mask_words > 64 || !product_fits({a->T, a->mask_words, 8}))
+        return KVR_ERR_SHAPE;
+    if (a->T == 0 || a->N == 0) return KVR_OK;
+    if (a->query_start == nullptr || a->parent == nullptr || a->tree_mask == nullptr ||
+        (a->positions != nullptr && a->position_start == nullptr))
+        return KVR_ERR_NULL;
+    const Region in[] = {{a->query_start, (a->N + 1) * 8}, {a->parent, a->T * 8}, {a->positions == nullptr ? nullptr : a->position_start, a->N * 8}};
+    const Region outs[] = {{a->tree_mask, a->T * a->mask_words * 8}, {a->positions, a->T * 8}, {a->dev_status, 4}};
+    for (const auto& x : in)
+        if (!aligned(x.p, 8)) return KVR_ERR_SHAPE;
+    if (!aligned(a->tree_mask, 8) || !aligned(a->positions, 8) || !aligned(a->dev_status, 4)) return KVR_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
+    }
+    const TreeParams p = {a->query_start, a->parent, a->position_start, a->tree_mask, a->positions, a->dev_status, a->T, a->N,
+                          int(a->mask_words)};
+    (void)cudaGetLastError();
+    return cuda_status(launch_tree(p, stream));
+}
+
+kvr_status kv_cache_select(const kvr_select_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (a->N < 0 || a->N >= (int64_t(1) << 27) || a->weight_len < 0 || a->weight_len > 0x7FFFFFFF || a->weight_stride < a->weight_len ||
+        a->keep < 1 || a->keep > 0x7FFFFFFF || a->sink < 0 || a->recent < 0 || a->sink > a->keep || a->recent > a->keep - a->sink ||
+        !product_fits({a->N, a->weight_stride, 4}) || !product_fits({a->N, a->keep, 8}))
+        return KVR_ERR_SHAPE;
+    if (a->kept_weight != nullptr && (a->kept_weight_len < a->keep || a->kept_weight_stride < a->kept_weight_len ||
+                                      !product_fits({a->N, a->kept_weight_stride, 4})))
+        return KVR_ERR_SHAPE;
+    if (a->N == 0) return KVR_OK;
+    if ((a->weight == nullptr && a->weight_len > 0) || a->key_length == nullptr || a->kept == nullptr || a->kept_length == nullptr)
+        return KVR_ERR_NULL;
+    if (!aligned(a->weight, 4) || !aligned(a->key_length, 8) || !aligned(a->kept, 8) || !aligned(a->kept_length, 8) ||
+        !aligned(a->kept_weight, 4) || !aligned(a->dev_status, 4))
+        return KVR_ERR_SHAPE;
+    const Region in[] = {{a->weight, ((a->N - 1) * a->weight_stride + a->weight_len) * 4}, {a->key_length, a->N * 8}};
+    const Region outs[] = {{a->kept, a->N * a->keep * 8}, {a->kept_length, a->N * 8},
+                           {a->kept_weight, ((a->N - 1) * a->kept_weight_stride + a->kept_weight_len) * 4}, {a->dev_status, 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (const auto& x : in)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
+    }
+    const SelectParams p = {a->weight, a->key_length, a->kept, a->kept_length, a->kept_weight, a->dev_status, a->weight_stride,
+                            a->weight_len, a->kept_weight_stride, a->kept_weight_len, int(a->N), int(a->keep), int(a->sink),
+                            int(a->recent), 0};
+    (void)cudaGetLastError();
+    return cuda_status(launch_select(p, stream));
+}
+
+kvr_status kv_cache_compact(const kvr_compact_args* a, cudaStream_t stream) {
+    if (a == nullptr) return KVR_ERR_NULL;
+    if (a->mode != KVR_CACHE_NORM && a->mode != KVR_CACHE_PA_BSND && a->mode != KVR_CACHE_PA_BLK_BSND) return KVR_ERR_MODE;
+    if (!(is16(a->ckv_dtype) || is8(a->ckv_dtype)) || (a->Dk > 0 && !(is16(a->k_dtype) || is8(a->k_dtype)))) return KVR_ERR_DTYPE;
+    const bool norm = a->mode == KVR_CACHE_NORM;
+    if (a->N < 0 || a->N > 0x7FFFFFFF || a->Dv < 1 || a->Dv > (int64_t(1) << 28) || a->Dk < 0 || a->Dk > (int64_t(1) << 28) ||
+        a->kept_len < 0 || a->max_blocks < 0 || a->cache_d0 < 1 || a->cache_d1 < 1 ||
+        !product_fits({a->cache_d0, a->cache_d1, a->Dv + a->Dk, 2}) || !product_fits({a->N, a->kept_len, 8}) ||
+        !product_fits({a->max_blocks, a->cache_d1, 8}) || !product_fits({a->N, a->max_blocks, 8}) || (norm && a->cache_d0 < a->N))
+        return KVR_ERR_SHAPE;
+    if (a->N == 0 || a->kept_len == 0) return KVR_OK;
+    if (a->ckv_cache == nullptr || (a->Dk > 0 && a->k_cache == nullptr) || a->kept == nullptr || a->kept_length == nullptr ||
+        (!norm && a->max_blocks > 0 && a->block_table == nullptr))
+        return KVR_ERR_NULL;
+    const int64_t vb = a->Dv * (is16(a->ckv_dtype) ? 2 : 1), kb = a->Dk == 0 ? 0 : a->Dk * (is16(a->k_dtype) ? 2 : 1);
+    if (!aligned(a->kept, 8) || !aligned(a->kept_length, 8) || !aligned(a->start, 8) || !aligned(a->block_table, 8) ||
+        !aligned(a->dev_status, 4) || (is16(a->ckv_dtype) && !aligned(a->ckv_cache, 2)) ||
+        (kb > 0 && is16(a->k_dtype) && !aligned(a->k_cache, 2)))
+        return KVR_ERR_SHAPE;
+    const int64_t rows = a->cache_d0 * a->cache_d1;
+    void* kc = kb > 0 ? a->k_cache : nullptr;
+    const Region in[] = {{a->kept, a->N * a->kept_len * 8}, {a->kept_length, a->N * 8}, {a->start, a->N * 8},
+                         {norm ? nullptr : a->block_table, a->N * a->max_blocks * 8}};
+    const Region outs[] = {{a->ckv_cache, rows * vb}, {kc, rows * kb}, {a->dev_status, 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return KVR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVR_ERR_ALIAS;
+    }
+    CompactParams p = {};
+    p.ckv = static_cast<uint8_t*>(a->ckv_cache);
+    p.kc = static_cast<uint8_t*>(kc);
+    p.table = norm ? nullptr : a->block_table;
+    p.kept = a->kept;
+    p.kept_length = a->kept_length;
+    p.start = a->start;
+    p.status = a->dev_status;
+    p.N = a->N;
+    p.d0 = a->cache_d0;
+    p.d1 = a->cache_d1;
+    p.max_blocks = a->max_blocks;
+    p.max_keys = std::min<int64_t>(norm ? a->cache_d1 : a->max_blocks * a->cache_d1, 0x7FFFFFFF);
+    p.M = a->kept_len;
+    const bool vec = vb % 16 == 0 && kb % 16 == 0 && aligned(a->ckv_cache, 16) && aligned(kc, 16);
+    p.cu = int(vec ? vb / 16 : vb);
+    p.ku = int(vec ? kb / 16 : kb);
+    (void)cudaGetLastError();
+    return cuda_status(launch_compact(p, vec, stream));
 }
 
 kvr_status kv_cache_read(const kvr_read_args* a, cudaStream_t stream) {

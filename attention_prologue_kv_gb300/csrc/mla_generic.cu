@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
         for (int64_t n = lane; n < p.N; n += 32) {
             const int64_t a = p.query_start[n], b = p.query_start[n + 1], K = p.key_length[n];
             int bits = 0;
-            if (a < 0 || b < a || b > p.T) bits = KVR_DEVERR_QUERY;
+            if (a < 0 || b < a || b > p.T || b - a > p.max_new) bits = KVR_DEVERR_QUERY;
             else if (a < b && (K < 0 || K > p.max_keys)) bits = KVR_DEVERR_KEY_LENGTH;
             if (bits && p.status != nullptr) atomicOr(p.status, bits);
         }
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
     // leaves the others' ranges as they are.
     for (int64_t n = 0; n < p.N; ++n) {
         const int64_t q0 = p.query_start[n], q1 = p.query_start[n + 1], K = p.key_length[n];
-        if (q0 < 0 || q1 <= q0 || q1 > p.T || K < 0 || K > p.max_keys) continue;
+        if (q0 < 0 || q1 <= q0 || q1 > p.T || q1 - q0 > p.max_new || K < 0 || K > p.max_keys) continue;
         const int64_t rows = (q1 - q0) * p.H;
         for (int64_t r = w0; r < rows; r += warps) {
             const int64_t t = q0 + r / p.H, h = r % p.H;
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(MLA_GEN_THREADS) mla_generic_kernel(const __gr
                 }
             };
             for (int64_t i = 0; i < seen; ++i) {
+                if (p.tree != nullptr && !(tree_bits(p.tree + t * p.words, p.words, int(K - (q1 - q0)), int(i)) & 1)) continue;
                 int64_t slot = n * p.d1 + i;
                 if (p.table != nullptr) {
                     const int64_t q = i / p.d1, e = p.table[n * p.max_blocks + q];

@@ -122,7 +122,7 @@ __device__ __forceinline__ Space ws_space(const MlaParams& p) {
 
 __device__ __forceinline__ Seq load_seq(const MlaParams& p, int n, int* bits = nullptr) {
     const int64_t a = p.query_start[n], b = p.query_start[n + 1], K = p.key_length[n];
-    if (a < 0 || b < a || b > p.T) {
+    if (a < 0 || b < a || b > p.T || b - a > p.max_new) {
         if (bits != nullptr) *bits |= KVR_DEVERR_QUERY;
         return {0, 0, 0};
     }
@@ -1027,7 +1027,8 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
         const bool live = row < unsigned(w.s.L) * unsigned(p.H);
         const int vis = live ? seen(p, w.s.L, w.s.K, int(row / unsigned(p.H))) : 0;
-        int wmin = live ? vis : 0x7FFFFFFF;
+        const int64_t* tree = p.tree == nullptr || !live ? nullptr : p.tree + (w.s.q0 + row / unsigned(p.H)) * p.words;
+        int wmin = live ? (tree != nullptr ? w.s.K - w.s.L : vis) : 0x7FFFFFFF;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
         if (C8) {
@@ -1039,12 +1040,14 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int key0 = kt * KEYS + h * CKEYS + g * NK;
             float* red = m->red[j & 1];
+            uint32_t see = 0xFFFFFFFFu;   // of a tree: only the steps with new tokens look
+            if (tree != nullptr && key0 + NK > w.s.K - w.s.L) see = tree_bits(tree, p.words, w.s.K - w.s.L, key0);
             // Keys that exist: bit i for key0 + i. They come over a barrier of this CTA, as the arrivals that start the
             // scores order nothing for these warps. (The word is written anew once this step's weights have gone into O,
             // and they depend on it.)
             constexpr int STAGES = stages_of<C8>();
             c.wait(&m->h_full[j % STAGES], (j / STAGES) & 1);
-            const uint32_t held = m->held[j % STAGES][h] >> (g * NK);
+            const uint32_t held = m->held[j % STAGES][h] >> (g * NK) & see;
             c.wait(&m->s_full[j & 1], (j >> 1) & 1);
             tc_fence_after();
             float s[NK];

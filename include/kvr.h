@@ -36,6 +36,14 @@
  *   kv_cache_read()  the cache rows of an index read back into dense rows,
  *       8-bit codes decoded.
  *
+ *   draft_tree(), mla_tree_attention()  a tree of drafted tokens: the ancestors
+ *       and the positions of its tokens, and mla_attention() where each of them
+ *       sees its ancestors.
+ *
+ *   mla_key_weight(), kv_cache_select(), kv_cache_compact()  caches of bounded
+ *       size: the attention weight that each key receives, the keys to keep by
+ *       it, and kept rows moved together (an accepted branch of a tree too).
+ *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller (the
  *     host-staged entry points also take pinned host buffers); the library
@@ -103,17 +111,21 @@ typedef enum kvr_status {
 } kvr_status;
 
 /* Bits OR-ed into *dev_status by the kernels. */
-#define KVR_DEVERR_INDEX 0x1       /* kv, read: an index entry outside {-1} U [0, range); attention: such
-                                      an entry of the block table that a token sees */
+#define KVR_DEVERR_INDEX 0x1       /* kv, read: an index entry outside {-1} U [0, range); attention, key
+                                      weight: such an entry of the block table that a token sees; tree:
+                                      a parent that does not come before; compact: a kept entry out of
+                                      order or a row that cannot be moved */
 #define KVR_DEVERR_KEY_LENGTH 0x2  /* qsa: key_length[n] < L (the past length would be negative);
-                                      attention: key_length[n] negative or beyond its keys */
+                                      attention, key weight, select, compact: a length that is negative
+                                      or beyond what there is room for */
 #define KVR_DEVERR_BLOCK_CAP 0x4   /* qsa: a completed block's number is >= Bcap */
 #define KVR_DEVERR_TIMEOUT 0x8     /* a pipeline wait inside a kernel exceeded its limit (one second, in
                                       mla_attention and one more for 2^22 keys of a part before); that
                                       CTA stopped early, output incomplete */
 #define KVR_DEVERR_PAST_BLOCKS 0x10 /* qsa, concat-output form: past_block_index_keys holds
                                       fewer than floor(P/kbs) rows for a sequence */
-#define KVR_DEVERR_QUERY 0x20      /* attention: query_start decreases or leaves [0, T] at a sequence */
+#define KVR_DEVERR_QUERY 0x20      /* attention, key weight, tree: query_start decreases or leaves [0, T]
+                                      at a sequence, or it has more tokens than tree_mask has bits */
 
 typedef enum kvr_dtype {
     KVR_BF16 = 0,
@@ -621,6 +633,192 @@ kvr_status mla_attention(const kvr_mla_args* args, cudaStream_t stream);
  * widths, types, scale lengths, strides and alignments in *args, not on what
  * the device arrays hold; `workspace` itself is not looked at. */
 int64_t kvr_mla_attention_workspace(const kvr_mla_args* args);
+
+/*
+ * Arguments of draft_tree(): the tokens that a draft proposes for a sequence form
+ * a tree (or several) that continues its context.
+ *
+ *   query_start  int64 [N + 1]: the drafted tokens of sequence n are rows
+ *                [query_start[n], query_start[n + 1]), as in mla_attention.
+ *   parent       int64 [T]: the place, in its sequence, of the token that this one
+ *                continues, before its own; -1: it continues the context. Any
+ *                other entry counts as -1 and raises KVR_DEVERR_INDEX.
+ *   tree_mask    out int64 [T, mask_words]: bit b % 64 of word b / 64 is set where
+ *                token b of the sequence is the token itself or an ancestor.
+ *   positions    optional out int64 [T]: position_start[n] + the number of
+ *                ancestors, as query_rope and the prologue's tables take it.
+ *   position_start  int64 [N], needed with positions.
+ *   dev_status   optional int32 device word.
+ *
+ * A sequence where query_start decreases or leaves [0, T], or with more than
+ * 64 mask_words tokens, is left out (KVR_DEVERR_QUERY). Rows of such a sequence
+ * and rows outside every sequence are left as they were; rows that two of the
+ * others then share get words of either. Limits: T >= 0,
+ * 0 <= N < 2^31, 1 <= mask_words <= 64. The outputs must not overlap an input or
+ * one another.
+ */
+typedef struct kvr_tree_args {
+    int64_t T, N;
+    const int64_t* query_start;
+    const int64_t* parent;
+    const int64_t* position_start;
+    int64_t* tree_mask;
+    int64_t mask_words;
+    int64_t* positions;
+    int32_t* dev_status;
+} kvr_tree_args;
+
+kvr_status draft_tree(const kvr_tree_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of mla_tree_attention(): mla_attention() where token j of a sequence
+ * with L new tokens and K keys sees the keys [0, K - L) and, for each bit b < L of
+ * its words, key K - L + b (where that is not negative). Its own bit counts like
+ * any other.
+ *
+ *   attention    as for mla_attention; `causal` is not looked at.
+ *   tree_mask    int64 [T, mask_words], rows as those of q; must not overlap an
+ *                output. A sequence with more than 64 mask_words tokens is left
+ *                out (KVR_DEVERR_QUERY).
+ *
+ * Limits and workspace are those of mla_attention; mask_words >= 1.
+ */
+typedef struct kvr_mla_tree_args {
+    kvr_mla_args attention;
+    const int64_t* tree_mask;
+    int64_t mask_words;
+} kvr_mla_tree_args;
+
+kvr_status mla_tree_attention(const kvr_mla_tree_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of mla_key_weight(): the attention weight that each key of a sequence
+ * receives from the sequence's tokens t and heads h,
+ *
+ *   weight[n, i] = decay * past[n, i] + sum_{t, h} exp(s[t, h, i] - lse[t, h])
+ *
+ * over the tokens that see key i, s as in mla_attention.
+ *
+ *   step         as for mla_attention, but `out` is not used and `lse` is read
+ *                (float32 [T, H], needed): what mla_attention wrote for these queries,
+ *                or any other logarithms. A row of -inf adds nothing.
+ *   weight       out float32: key i of sequence n at n * weight_stride + i, room
+ *                for weight_len keys a sequence. Entries behind a sequence's last
+ *                key, and those of sequences without tokens, are left as they were.
+ *                A sequence with more than weight_len keys is left out
+ *                (KVR_DEVERR_KEY_LENGTH). Keys of blocks that the table leaves
+ *                out receive nothing: they get decay * past.
+ *   past         float32, laid out with past_stride, read for the same keys: `weight`
+ *                itself (with the same stride) to add up in place, another array that
+ *                does not overlap it, or NULL: nothing is read.
+ *   decay        factor of past.
+ *
+ * Limits are those of mla_attention (without its limit on work), weight_len >= 0,
+ * strides >= weight_len; `weight` must not overlap an input, the workspace or
+ * dev_status. Rows of at most 512 + 64 channels, both multiples of 8 (of 16 in an
+ * 8-bit cache), on 16-byte boundaries (q and the caches; strides multiples of 8)
+ * and with H <= 65536 run on the tensor cores, all others on a plain kernel that
+ * is much slower. Scores and sums are float32; keys within key_length are taken
+ * to be finite, but a key that is not changes no weight but its own. The result
+ * of a call does not change from run to run on one GPU.
+ */
+typedef struct kvr_key_weight_args {
+    kvr_mla_args step;
+    float* weight;
+    int64_t weight_stride, weight_len;
+    const float* past;
+    int64_t past_stride;
+    float decay;
+} kvr_key_weight_args;
+
+kvr_status mla_key_weight(const kvr_key_weight_args* args, cudaStream_t stream);
+
+/* Bytes of workspace that mla_key_weight(args) needs on the current device (0
+ * where it needs none, or where args are not valid), as
+ * kvr_mla_attention_workspace. */
+int64_t kvr_mla_key_weight_workspace(const kvr_key_weight_args* args);
+
+/*
+ * Arguments of kv_cache_select(): of the key_length[n] keys of a sequence, the
+ * `keep` to keep. All, where they are no more than that; else the first `sink`,
+ * the last `recent` and, of those between, the ones of largest weight: of equal
+ * weights (-0 equals 0) the earlier, NaN above every number.
+ *
+ *   weight       float32: key i of sequence n at n * weight_stride + i, room for
+ *                weight_len keys a sequence.
+ *   key_length   int64 [N]. A negative one or one beyond weight_len: the sequence
+ *                is left out (KVR_DEVERR_KEY_LENGTH), as if it had no keys.
+ *   kept         out int64 [N, keep]: positions of the kept keys, ascending, then -1.
+ *   kept_length  out int64 [N]: how many they are.
+ *   kept_weight  optional out float32, row n at n * kept_weight_stride: the kept
+ *                keys' weights in that order, then zeros up to kept_weight_len
+ *                (>= keep).
+ *   dev_status   optional int32 device word.
+ *
+ * Limits: 0 <= N < 2^27, weight_len < 2^31, keep >= 1, sink, recent >= 0,
+ * sink + recent <= keep < 2^31. The outputs must not overlap an input or one
+ * another.
+ */
+typedef struct kvr_select_args {
+    const float* weight;
+    int64_t weight_stride, weight_len;
+    int64_t N;
+    const int64_t* key_length;
+    int64_t keep, sink, recent;
+    int64_t* kept;
+    int64_t* kept_length;
+    float* kept_weight;
+    int64_t kept_weight_stride, kept_weight_len;
+    int32_t* dev_status;
+} kvr_select_args;
+
+kvr_status kv_cache_select(const kvr_select_args* args, cudaStream_t stream);
+
+/*
+ * Arguments of kv_cache_compact(): rows of a sequence moved together in place, in
+ * both caches: key start[n] + i becomes what key kept[n, i] was, for
+ * i < kept_length[n].
+ *
+ *   ckv_cache, k_cache, ckv_dtype, k_dtype, mode, cache_d0, cache_d1,
+ *   block_table, max_blocks  the caches as in mla_attention, any two types; rows
+ *                move as they are, so scales are not needed. Dk >= 0 (0: no k part;
+ *                k_cache may then be NULL).
+ *   kept         int64 [N, kept_len], ascending in each row, kept[n, i] >=
+ *                start[n] + i, as kv_cache_select gives it (start 0) or as the
+ *                places of an accepted branch of a drafted tree (start: the keys
+ *                before the tree). An entry that is not, or that lies behind the block
+ *                table's keys, and a row whose block the table does not name:
+ *                that row is not written (KVR_DEVERR_INDEX), and where the order is
+ *                broken the sequence's other rows get an unspecified mix of rows.
+ *                A row with kept[n, i] = start[n] + i is not touched.
+ *   kept_length  int64 [N], at most kept_len.
+ *   start        int64 [N], or NULL for 0. A negative start or kept_length, or one
+ *                too large: the sequence is left out (KVR_DEVERR_KEY_LENGTH).
+ *   dev_status   optional int32 device word.
+ *
+ * A row that moves must be of one sequence alone: blocks that sequences share have
+ * to lie within keys that stay. Limits: 0 <= N < 2^31, Dv >= 1, kept_len >= 0,
+ * block-table keys < 2^31. kept, kept_length, start and the table must not overlap
+ * the caches, nor the caches one another.
+ */
+typedef struct kvr_compact_args {
+    void* ckv_cache;
+    kvr_dtype ckv_dtype;
+    void* k_cache;
+    kvr_dtype k_dtype;
+    kvr_cache_mode mode;
+    int64_t cache_d0, cache_d1;
+    const int64_t* block_table;
+    int64_t max_blocks;
+    int64_t N, Dv, Dk;
+    const int64_t* kept;
+    int64_t kept_len;
+    const int64_t* kept_length;
+    const int64_t* start;
+    int32_t* dev_status;
+} kvr_compact_args;
+
+kvr_status kv_cache_compact(const kvr_compact_args* args, cudaStream_t stream);
 
 /* Measurement helper (no counterpart on the pages): a 16-byte vectorised
  * device-to-device copy of `bytes` bytes (a multiple of 16, both pointers

@@ -13,6 +13,7 @@ Modules:
   qsa_prepare            QSA block-key prepare with carry across calls
   dynamic_quant          DynamicQuant of q^N: per-row RowMax/127 scale, int8 codes
   attention_step         query RoPE with several axes, cache rows read back, latent attention
+  cache_ops              drafted trees, the attention weight of keys, which to keep, rows moved together
 
 Every function is pinned by `-m "not gpu"` tests to closed forms, invariants,
 hand-worked toys (tests/golden) or library routines; no part is
@@ -27,10 +28,13 @@ from .qsa_prepare import (ROPE_LAYOUTS, STATUS_BLOCK_CAP, STATUS_KEY_LENGTH,
                           STATUS_PAST_BLOCKS, ref_qsa_prepare, rotate_half_rope)
 from .dynamic_quant import ref_dynamic_quant
 from .attention_step import ref_kv_cache_read, ref_mla_attention, ref_query_rope
+from .cache_ops import (ref_draft_tree, ref_kv_cache_compact, ref_kv_cache_select, ref_mla_key_weight,
+                        ref_mla_tree_attention)
 
 __all__ = [
     "encoders", "NORM", "PA_BSND", "PA_BLK_BSND", "STATUS_INDEX", "STATUS_KEY_LENGTH",
     "STATUS_BLOCK_CAP", "STATUS_PAST_BLOCKS", "ROPE_LAYOUTS", "rotate_half_rope", "cache_slot", "interleave_rope", "kv_values", "quantise", "rms_norm",
     "ref_kv_rmsnorm_rope_cache", "ref_kv_rmsnorm_rope_cache_loop", "ref_qsa_prepare",
     "ref_dynamic_quant", "ref_query_rope", "ref_kv_cache_read", "ref_mla_attention",
+    "ref_draft_tree", "ref_mla_tree_attention", "ref_mla_key_weight", "ref_kv_cache_select", "ref_kv_cache_compact",
 ]
