@@ -714,6 +714,15 @@ kvr_status launch_attention(const kvr_mla_args* a, const MlaParams& p, cudaStrea
     return cuda_status(tc ? launch_mla_tc(p, a->dtype, stream) : launch_mla_generic(p, a->dtype, stream));
 }
 
+// The same of mla_key_weight, which has no `out`.
+bool key_weight_tensor_cores(const kvr_mla_args* a) {
+    const int64_t dv = is8(a->ckv_dtype) ? 16 : 8, dk = is8(a->k_dtype) ? 16 : 8;
+    for (const int64_t s : {a->q_nope_token_stride, a->q_nope_head_stride, a->q_rope_token_stride, a->q_rope_head_stride})
+        if (s % 8 != 0) return false;
+    return a->Dv <= 512 && a->Dk <= 64 && a->Dv % dv == 0 && a->Dk % dk == 0 && a->H <= 65536 && aligned(a->q_nope, 16) &&
+           aligned(a->q_rope, 16) && aligned(a->ckv_cache, 16) && aligned(a->k_cache, 16);
+}
+
 kvr_status key_weight_plan(const kvr_key_weight_args* a, KeyWeightParams* p, bool* empty) {
     if (a == nullptr) return KVR_ERR_NULL;
     const kvr_mla_args& s = a->step;
@@ -774,8 +783,10 @@ kvr_status mla_tree_attention(const kvr_mla_tree_args* a, cudaStream_t stream) {
 }
 
 int64_t kvr_mla_key_weight_workspace(const kvr_key_weight_args* a) {
-    (void)a;
-    return 0;
+    KeyWeightParams p = {};
+    bool empty;
+    if (key_weight_plan(a, &p, &empty) != KVR_OK || empty || !key_weight_tensor_cores(&a->step)) return 0;
+    return key_weight_tc_workspace(p);
 }
 
 kvr_status mla_key_weight(const kvr_key_weight_args* a, cudaStream_t stream) {
@@ -783,8 +794,13 @@ kvr_status mla_key_weight(const kvr_key_weight_args* a, cudaStream_t stream) {
     bool empty;
     const kvr_status st = key_weight_plan(a, &p, &empty);
     if (st != KVR_OK || empty) return st;
+    const bool tc = key_weight_tensor_cores(&a->step);
+    if (tc) {
+        if (a->step.workspace == nullptr) return KVR_ERR_NULL;
+        if (!aligned(a->step.workspace, 32) || a->step.workspace_bytes < key_weight_tc_workspace(p)) return KVR_ERR_SHAPE;
+    }
     (void)cudaGetLastError();
-    return cuda_status(launch_key_weight_generic(p, a->step.dtype, stream));
+    return cuda_status(tc ? launch_key_weight_tc(p, a->step.dtype, stream) : launch_key_weight_generic(p, a->step.dtype, stream));
 }
 
 kvr_status draft_tree(const kvr_tree_args* a, cudaStream_t stream) {
