@@ -1,5 +1,5 @@
-// How the work of mla_key_weight is cut: (sequence, block of key tiles, group of rows, key tile) in that order, into equal
-// shares by cost. Plain arithmetic, on the device and, for its tests, on the host.
+// How the work of mla_key_weight is cut: (sequence, key tile, group of rows) in that order, into equal shares by cost. Plain
+// arithmetic, on the device and, for its tests, on the host.
 #pragma once
 
 #include <stdint.h>
@@ -13,149 +13,115 @@
 namespace kvr {
 
 constexpr int KW_KEYS = 256;    // keys of a tile
-constexpr int KW_BLOCK = 24;    // tiles of a block: its sums stay in shared memory while the groups pass
-// What a group costs beside its tiles, in tiles: its queries.
-constexpr double KW_GROUP_COST = 0.5;
+// What a tile costs beside its groups, in groups: bringing its keys.
+constexpr double KW_TILE_COST = 1.0;
 
 struct KwPos {
-    int n, kb, g, kt;   // sequence, block, group, tile of the block
+    int n, kt, g;   // sequence, tile, group
+    int cut;        // whether groups of the tile come before it
 };
 
-// A sequence's rows in groups of `rows`, its keys in tiles and blocks.
+// A sequence's rows in groups of `rows`, its keys in tiles.
 struct KwShape {
     int L, K, H, rows;
     bool causal;
 
     KVR_HD int groups() const { return int((unsigned(L) * unsigned(H) + unsigned(rows) - 1u) / unsigned(rows)); }
     KVR_HD int tiles() const { return (K + KW_KEYS - 1) / KW_KEYS; }
-    KVR_HD int blocks() const { return (tiles() + KW_BLOCK - 1) / KW_BLOCK; }
-    KVR_HD int block_tiles(int kb) const {
-        const int left = tiles() - kb * KW_BLOCK;
-        return left < KW_BLOCK ? left : KW_BLOCK;
+    // The first group with a row that sees a key of the tile.
+    KVR_HD int first_group(int kt) const {
+        if (!causal) return 0;
+        const int64_t token = int64_t(kt) * KW_KEYS - (int64_t(K) - L);
+        return token <= 0 ? 0 : int(token * H / rows);
     }
-    // Tiles of a block that the group's last row sees.
-    KVR_HD int seen_tiles(int kb, int g) const {
-        const int most = block_tiles(kb);
-        if (!causal) return most;
-        const unsigned last = unsigned(g) * unsigned(rows) + unsigned(rows) - 1u;
-        const int t = int(last / unsigned(H)) < L - 1 ? int(last / unsigned(H)) : L - 1;
-        const int64_t see = int64_t(K) - L + t + 1, before = int64_t(kb) * (KW_BLOCK * KW_KEYS);
-        if (see <= before) return 0;
-        const int64_t n = (see - before + KW_KEYS - 1) / KW_KEYS;
-        return n < most ? int(n) : most;
-    }
-    // Whether every group sees all tiles (but for a fraction of the last ones).
     KVR_HD bool even() const { return !causal || groups() == 1; }
-    // Cost of a block's first x groups: x grows by KW_GROUP_COST at least from group to group. Where the rows see more and
-    // more keys, the integral over the groups of what their ends see, and half a tile, as tiles are whole.
-    KVR_HD double cost(int kb, int x) const {
-        const double most = block_tiles(kb);
-        if (even()) return x * (most + KW_GROUP_COST);
-        const double step = double(rows) / (double(H) * KW_KEYS), first = (double(K) - L) / KW_KEYS + step + 0.5 - double(kb) * KW_BLOCK;
-        double x1 = -first / step, x2 = (most - first) / step;   // where it leaves 0, where it reaches `most`
-        x1 = x1 < 0 ? 0 : (x1 > x ? x : x1);
-        x2 = x2 < x1 ? x1 : (x2 > x ? x : x2);
-        return (x2 - x1) * (first + step * (x1 + x2) * 0.5) + (x - x2) * most + x * KW_GROUP_COST;
+    // Cost of the first x tiles, which grows by KW_TILE_COST at least from tile to tile: where tiles lie behind the first
+    // token's keys, fewer and fewer groups see them.
+    KVR_HD double cost(int x) const {
+        const double all = x * (groups() + KW_TILE_COST);
+        if (even()) return all;
+        const double y = x - 1 - (double(K) - L) / KW_KEYS;
+        return y <= 0 ? all : all - 0.5 * y * y * (double(KW_KEYS) * H / rows);
     }
-    KVR_HD double cost() const {
-        if (L == 0 || K == 0) return 0;
-        if (even()) return groups() * (tiles() + KW_GROUP_COST * blocks());
-        double sum = 0;
-        for (int kb = 0; kb < blocks(); ++kb) sum += cost(kb, groups());
-        return sum;
-    }
+    KVR_HD double cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }
     // Where the share that begins at `off` of the sequence's cost begins. Grows with `off`: shares neither overlap nor leave gaps.
     KVR_HD KwPos locate(int n, double off) const {
-        const int G = groups(), B = blocks();
-        int kb = 0;
+        const int G = groups(), T = tiles();
+        if (G == 1) {   // whole tiles
+            const double x = off / (1 + KW_TILE_COST) + 0.5;
+            return {n, x < T ? int(x) : T, 0, 0};
+        }
+        int lo = 0, hi = T - 1;
         if (even()) {
-            const double each = G * (KW_BLOCK + KW_GROUP_COST);
-            const double at = off / each;
-            kb = at < B - 1 ? int(at) : B - 1;
-            off -= kb * each;
+            const double x = off / (G + KW_TILE_COST);
+            lo = x < T ? int(x) : T - 1;
         } else {
-            for (; kb < B - 1; ++kb) {
-                const double each = cost(kb, G);
-                if (off < each) break;
-                off -= each;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (cost(mid) <= off) lo = mid;
+                else hi = mid - 1;
             }
         }
-        if (off < 0) off = 0;
-        int lo = 0, hi = G - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (cost(kb, mid) <= off) lo = mid;
-            else hi = mid - 1;
-        }
-        const double c0 = cost(kb, lo), c1 = cost(kb, lo + 1);
-        const int kn = seen_tiles(kb, lo);
-        const double f = (off - c0) / (c1 - c0) * kn + 0.5;
-        const int kt = f < 0 ? 0 : (f < kn ? int(f) : kn);
-        return {n, kb, lo, kt};
+        const double c0 = cost(lo), c1 = cost(lo + 1);
+        const int g0 = first_group(lo), count = G - g0;
+        const double f = (off - c0) / (c1 - c0) * count + 0.5;
+        const int g = f < 0 ? 0 : (f < count ? int(f) : count);
+        return {n, lo, g0 + g, g > 0};
     }
 };
 
-// Whether a position lies inside a block, behind its begin.
-KVR_HD bool kw_inside(const KwPos& p) { return p.g > 0 || p.kt > 0; }
-KVR_HD bool kw_same_block(const KwPos& a, const KwPos& b) { return a.n == b.n && a.kb == b.kb; }
-KVR_HD bool kw_same(const KwPos& a, const KwPos& b) { return kw_same_block(a, b) && a.g == b.g && a.kt == b.kt; }
+KVR_HD bool kw_same_tile(const KwPos& a, const KwPos& b) { return a.n == b.n && a.kt == b.kt; }
+KVR_HD bool kw_same(const KwPos& a, const KwPos& b) { return kw_same_tile(a, b) && a.g == b.g; }
 
-// CTA pairs that get work: at most one a tile and a half, so that a pair has more to do than to begin.
+// CTA pairs that get work: none less than a tile of one group.
 KVR_HD int kw_active(double total, int pairs) {
-    const double most = total / 1.5;
+    const double most = total / (1 + KW_TILE_COST);
     return most < 1 ? 1 : (most < pairs ? int(most) : pairs);
 }
 
-// The parts of a share, block by block. `shape(n)` gives a sequence's KwShape.
+// The runs of a share: some tiles of a sequence with one group, or the groups [ga, gb) of one tile.
 template <class Shapes>
 struct KwWalk {
     Shapes shapes;
     KwPos at, end;
-    int N;
-    // the current block
+    int N, loaded = -1;
     KwShape s;
-    int n, kb, tiles;
-    int g_at, g_end, kt_first, kt_last;   // groups left; tiles of the first and of the last one where the share cuts it
-    // the current part
-    int g, kt0, kt1;
-    bool begun = false;
+    // the current run
+    int n, kt0, kt1, ga, gb;
+    bool whole;   // the share has all groups that see its tiles
 
     KVR_HD KwWalk(const Shapes& sh, const KwPos& a, const KwPos& e, int count) : shapes(sh), at(a), end(e), N(count) {}
-    KVR_HD bool next_block() {
-        if (begun) at = {n, kb + 1, 0, 0};
+    KVR_HD bool next() {
         for (;;) {
-            if (at.n >= N || at.n > end.n || (at.n == end.n && (at.kb > end.kb || (at.kb == end.kb && (at.g > end.g || (at.g == end.g && at.kt >= end.kt)))))) return false;
-            if (!begun || at.n != n) s = shapes(at.n);
-            begun = true;
-            n = at.n;
-            if (s.L == 0 || at.kb >= s.blocks()) {
-                at = {n + 1, 0, 0, 0};
+            if (at.n >= N || at.n > end.n ||
+                (at.n == end.n && (at.kt > end.kt || (at.kt == end.kt && (at.cut ? at.g >= end.g : !end.cut)))))
+                return false;
+            if (loaded != at.n) {
+                s = shapes(at.n);
+                loaded = at.n;
+            }
+            const int T = s.L == 0 ? 0 : s.tiles();
+            if (at.kt >= T) {
+                at = {at.n + 1, 0, 0, 0};
                 continue;
             }
-            kb = at.kb;
-            tiles = s.block_tiles(kb);
-            const bool last = end.n == n && end.kb == kb;
-            g_at = at.g;
-            kt_first = at.kt;
-            g_end = last ? (end.kt > 0 ? end.g + 1 : end.g) : s.groups();
-            kt_last = last && end.kt > 0 ? end.kt : KW_BLOCK;
+            n = at.n;
+            kt0 = at.kt;
+            if (s.groups() == 1) {
+                kt1 = end.n == n && end.kt < T ? end.kt : T;
+                ga = 0;
+                gb = 1;
+                whole = true;
+            } else {
+                kt1 = kt0 + 1;
+                ga = at.cut ? at.g : s.first_group(kt0);
+                const bool last = end.n == n && end.kt == kt0;
+                gb = last ? end.g : s.groups();
+                whole = !at.cut && !last;
+            }
+            at = {n, kt1, 0, 0};
             return true;
         }
-    }
-    KVR_HD bool next_part() {
-        while (g_at < g_end) {
-            g = g_at++;
-            kt0 = kt_first;
-            kt_first = 0;
-            kt1 = s.seen_tiles(kb, g);
-            if (g_at == g_end && kt1 > kt_last) kt1 = kt_last;
-            if (kt0 < kt1) return true;
-        }
-        return false;
-    }
-    // Whether the share has all of the block.
-    KVR_HD bool whole(const KwPos& begin) const {
-        return !(begin.n == n && begin.kb == kb && kw_inside(begin)) && !(end.n == n && end.kb == kb);
     }
 };
 

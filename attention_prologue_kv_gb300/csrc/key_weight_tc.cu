@@ -5,21 +5,20 @@
 // f = scale log2 e and l_r = lse_r log2 e. The logarithms are given, so that no pass over the keys has to come first.
 //
 // Keys are the product's first operand: a key's scores then lie in one TMEM lane, and the sum over rows is a sum within a
-// thread: no shuffles, no atomics, one number a key and group of rows. What is not a key (a hole, the end of a block)
+// thread: no shuffles, no atomics, one number a key and share of the work. What is not a key (a hole, the end of a block)
 // only spoils its own lane, which is left out at the end.
 //
-// Tiling: a CTA pair (cta_group::2, M = 256) has 256 keys a step, 128 in each CTA, and a group of up to 256 rows, half of
-// them in each CTA's shared memory, where they stay while the tiles of a block pass. Keys come in boxes of 128 keys x 64
-// channels through a ring of 4 (8 where the queries leave room), so that a box is reused for all rows of the group and
-// nothing of a tile has to wait for the rest. Scores take turns over two halves of TMEM: the exponentials of a tile run
-// beside the products of the next one. The sums of a block's tiles stay in shared memory while the sequence's groups
-// pass; with one group (a decode step) they go straight to the weights.
+// Tiling: a CTA pair (cta_group::2, M = 256) has 256 keys, 128 in each CTA, in 9 boxes of 64 channels that stay in shared
+// memory while the sequence's rows pass in groups of up to 256, half of them through each CTA, box by box through a ring.
+// A box of keys is brought, and codes are decoded, once for all rows. It is free, and the next tile's box on its way, once the
+// last group's product with it is done. Where a sequence has one group (a decode step) whose boxes fit the ring, its
+// queries stay there for all its tiles. Scores take turns over two halves of TMEM: the exponentials of a group run beside
+// the products of the next one.
 //
 // Caches of codes: eight warps decode them into halves (every code is exact there). The queries are divided by the scales
 // before and held as the sum of two halves each, 22 bits, as a weight is a float32: one half alone was off by 2e-4 of it.
-// The second product of the same keys costs tensor-core time, which such a call has to spare while it decodes.
 //
-// Work is cut into equal shares by cost over the pairs (key_weight_plan.cuh). A block that the cut goes through leaves its
+// Work is cut into equal shares by cost over the pairs (key_weight_plan.cuh). A tile that the cut goes through leaves its
 // sums in the workspace, and a second kernel adds them up in a fixed order.
 #include <mutex>
 
@@ -33,43 +32,42 @@ namespace {
 
 constexpr int CKEYS = KW_KEYS / 2;   // keys of a CTA
 constexpr uint32_t BOX = CKEYS * 128;
-constexpr int MAX_STAGES = 8;
-constexpr uint32_t TMEM_COLS = 512, COL_D = 256;   // a tile's scores: 256 columns at most
-constexpr int LSE_SLOTS = 4;   // groups whose logarithms are in shared memory: those of the three tiles at work, and the next
-constexpr uint32_t ACC_BYTES = KW_BLOCK * CKEYS * 4, LSE_BYTES = LSE_SLOTS * 1024;
+constexpr int KBOXES = 9, ROPE = 8;   // boxes of a tile; the rotary part's
+constexpr uint32_t OFF_Q = KBOXES * BOX, Q_BYTES = 73728, OFF_LSE = OFF_Q + Q_BYTES;   // the queries' ring
+constexpr int MAX_SLOTS = 18;        // of that ring: all boxes of a row in two halves
+constexpr int LSE_SLOTS = 4;         // groups whose logarithms are in shared memory
+constexpr uint32_t LSE_SLOT = 2048, OFF_MISC = OFF_LSE + LSE_SLOTS * LSE_SLOT;
+constexpr uint32_t TMEM_COLS = 512, COL_D = 256;   // a group's scores: 256 columns at most
 
 struct alignas(16) Misc {
-    uint64_t k_full[MAX_STAGES], k_empty[MAX_STAGES];
-    uint64_t q_full, q_free, d_full[2], d_free[2], lse_full[LSE_SLOTS], drain;
+    uint64_t k_full[KBOXES], k_empty[KBOXES], q_full[MAX_SLOTS], q_empty[MAX_SLOTS];
+    uint64_t d_full[2], d_free[2], lse_full[LSE_SLOTS], lse_free[LSE_SLOTS], drain;
     uint32_t tmem;
     int abort;
     KwPos begin, end;
     double wsum[32];
+    float other[2][CKEYS];   // sums of the second half of the sum warps
 };
+constexpr uint32_t SMEM = OFF_MISC + uint32_t(sizeof(Misc));
+static_assert(SMEM <= 232448, "shared memory of a CTA");
 
 struct Tc {
-    KeyWeightParams w;
-    const uint16_t* qn_lo;   // lower halves of the queries of codes, or NULL
-    const uint16_t* qr_lo;
-    const float* row_mul;    // power of two per row that prepared queries lack
-    int pairs, rows, stages, box_rows;
+    KeyWeightParams w;       // its queries: row t * H + h at that times qn_hs, qr_hs (those of codes prepared)
+    const float* row_mul;    // power of two per row that prepared queries lack, or NULL
+    int pairs, rows, slots, box_rows;
+    int lo_n, lo_r;          // the latent, the rotary part's queries have a second half
+};
+struct Maps {
+    CUtensorMap qn, qr, qn_lo, qr_lo, latent, rope;
 };
 
-// Shared memory: queries [boxes][rows / 2], ring, sums, logarithms, barriers.
-__host__ __device__ inline uint32_t q_bytes(int rows, bool codes) { return uint32_t(rows) * 64u * (codes ? 18u : 9u); }
-__host__ __device__ inline uint32_t smem_of(int rows, bool codes, int stages) {
-    return q_bytes(rows, codes) + uint32_t(stages) * BOX + ACC_BYTES + LSE_BYTES + uint32_t(sizeof(Misc));
-}
-static_assert(256 * 64 * 9 + 4 * BOX + ACC_BYTES + LSE_BYTES + sizeof(Misc) <= 232448, "shared memory of a CTA");
-static_assert(128 * 64 * 9 + 8 * BOX + ACC_BYTES + LSE_BYTES + sizeof(Misc) <= 232448, "shared memory of a CTA");
-
-// Workspace: header, the pairs' begins, sums of two blocks a pair.
+// Workspace: header, the pairs' begins, sums of two tiles a pair.
 struct alignas(16) Start {
     KwPos at;
     int L, K, pad[2];
 };
 __host__ __device__ inline int64_t ws_sums(int pairs) { return 256 + (int64_t(pairs) * int64_t(sizeof(Start)) + 255) / 256 * 256; }
-__host__ __device__ inline int64_t ws_bytes(int pairs) { return ws_sums(pairs) + int64_t(pairs) * 2 * KW_BLOCK * KW_KEYS * 4; }
+__host__ __device__ inline int64_t ws_bytes(int pairs) { return ws_sums(pairs) + int64_t(pairs) * 2 * KW_KEYS * 4; }
 struct Space {
     int32_t* active;
     Start* starts;
@@ -150,22 +148,21 @@ __device__ void schedule(const Tc& p, Misc* m, int pair) {
 struct Ctx {
     const Tc& p;
     Misc* m;
-    uint32_t base, ring, tmem, rank;
+    uint32_t base, tmem, rank;
     int lane, nb;   // nb: 64-channel boxes of the latent part
-    float* acc;
     float* lse;
     volatile int* abort;
     bool ok;
 
-    // As in the attention kernel: a wait that gives up poisons the CTA; the warp that starts TMA copies then stops, the others run
+    // As in the attention kernel: a wait that gives up poisons the CTA; the warps that start TMA copies then stop, the others run
     // their loops to the end without waiting.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
         if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0) && ok;
         __syncwarp();
     }
     __device__ __forceinline__ bool gone() const { return __any_sync(0xFFFFFFFFu, !ok); }
-    __device__ __forceinline__ uint32_t stage(int st) const { return ring + uint32_t(st) * BOX; }
-    __device__ __forceinline__ uint32_t q_box(int b) const { return base + uint32_t(b) * uint32_t(p.rows) * 64u; }
+    __device__ __forceinline__ uint32_t k_box(int b) const { return base + uint32_t(b) * BOX; }
+    __device__ __forceinline__ uint32_t q_slot(int s) const { return base + OFF_Q + uint32_t(s) * uint32_t(p.rows) * 64u; }
     // This warp's shared-memory writes are done: tell the MMA warp of the pair.
     __device__ __forceinline__ void arrive(uint64_t* bar) {
         fence_async_proxy();
@@ -173,9 +170,19 @@ struct Ctx {
         if (lane == 0) mbar_arrive_at(bar, 0);
     }
     __device__ __forceinline__ Walk walk() const { return Walk(Shapes{p}, m->begin, m->end, int(p.w.m.N)); }
+    __device__ __forceinline__ int q_boxes() const { return (nb << p.lo_n) + (1 << p.lo_r); }
+    // Whether a run's queries stay in the ring for its tiles.
+    __device__ __forceinline__ bool stays(const Walk& w) const { return w.kt1 - w.kt0 > 1 && q_boxes() <= p.slots; }
 };
 
-constexpr int ROPE_BOX = 8, LO_BOX = 9, ROPE_LO_BOX = 17;   // boxes of the queries
+// A place in the queries' ring, and how often it went round.
+struct Ring {
+    int slot = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) slot = 0, ++turn;
+    }
+};
 
 // A key's row, looked up in two steps: the load of the block table, and what needs it.
 struct Look {
@@ -203,59 +210,137 @@ struct Look {
 };
 
 // One warp brings the CTA's 16-bit keys through TMA: a box is 128 / R copies of R rows, R what divides the cache's blocks.
-__device__ __forceinline__ void tma_warp(Ctx& c, const CUtensorMap* latent, const CUtensorMap* rope) {
+__device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     const MlaParams& p = c.p.w.m;
-    const int R = c.p.box_rows, copies = CKEYS / R, mask = c.p.stages - 1, log = c.p.stages == 8 ? 3 : 2;
-    int j = 0;
+    const int R = c.p.box_rows, copies = CKEYS / R;
+    int tile = 0;
     Walk w = c.walk();
-    while (w.next_block())
-        while (w.next_part()) {
-            Look next;
-            auto look = [&](int kt) {   // (a lane without a copy, and what lies behind the part, has no key)
-                const int key = (w.kb * KW_BLOCK + kt) * KW_KEYS + int(c.rank) * CKEYS + c.lane * R;
-                next.begin(p, w.n, c.lane < copies && kt < w.kt1 ? w.s.K : 0, key);
-            };
-            look(w.kt0);
+    while (w.next()) {
+        if (w.ga >= w.gb) continue;
+        Look next;
+        auto look = [&](int kt) {   // (a lane without a copy, and what lies behind the run, has no key)
+            next.begin(p, w.n, c.lane < copies && kt < w.kt1 ? w.s.K : 0, kt * KW_KEYS + int(c.rank) * CKEYS + c.lane * R);
+        };
+        look(w.kt0);
 #pragma unroll 1
-            for (int kt = w.kt0; kt < w.kt1; ++kt) {
-                const int row = int(next.row(p));
-                look(kt + 1);
-                const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, row >= 0))) * uint32_t(R) * 128u;
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++tile) {
+            const int row = int(next.row(p));
+            look(kt + 1);
+            const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, row >= 0))) * uint32_t(R) * 128u;
 #pragma unroll 1
-                for (int b = 0; b <= c.nb; ++b, ++j) {
-                    const int st = j & mask;
-                    if (j > mask) c.wait(&c.m->k_empty[st], ((j >> log) & 1) ^ 1);
-                    if (c.gone()) return;
-                    if (c.lane == 0) mbar_expect_at(&c.m->k_full[st], 0, bytes);
-                    __syncwarp();
-                    if (row >= 0)
-                        tma_box_at(c.stage(st) + uint32_t(c.lane * R) * 128u, b < c.nb ? latent : rope, 0, row, b < c.nb ? b : 0,
-                                   &c.m->k_full[st], 0);
-                }
+            for (int b = 0; b <= c.nb; ++b) {
+                const int at = b < c.nb ? b : ROPE;
+                if (tile > 0) c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
+                if (c.gone()) return;
+                if (c.lane == 0) mbar_expect_at(&c.m->k_full[at], 0, bytes);
+                __syncwarp();
+                if (row >= 0)
+                    tma_tile_at(c.k_box(at) + uint32_t(c.lane * R) * 128u, b < c.nb ? &maps.latent : &maps.rope, b < c.nb ? b * 64 : 0,
+                                row, &c.m->k_full[at], 0);
             }
         }
+    }
+}
+
+// One warp brings the queries, half of a group's rows, box by box in the order of the products. Rows behind the sequence's last
+// one are another's, or none: their columns are left out of the sums.
+__device__ __forceinline__ void query_warp(Ctx& c, const Maps& maps) {
+    const Tc& p = c.p;
+    const MlaParams& a = p.w.m;
+    const int half = p.rows / 2;
+    const int64_t all = a.T * a.H;
+    Ring ring;
+    Walk w = c.walk();
+    while (w.next()) {
+        const int64_t first = a.query_start[w.n] * a.H + int64_t(c.rank) * half;
+        const int turns = c.stays(w) ? 1 : w.kt1 - w.kt0;
+#pragma unroll 1
+        for (int turn = 0; turn < turns; ++turn)
+#pragma unroll 1
+            for (int g = w.ga; g < w.gb; ++g) {
+                const int64_t at = first + int64_t(g) * p.rows;
+                const int row = int(at < all ? at : all);
+#pragma unroll 1
+                for (int b = 0; b <= c.nb; ++b) {
+                    const bool rope = b == c.nb;
+#pragma unroll 1
+                    for (int lo = 0; lo <= (rope ? p.lo_r : p.lo_n); ++lo) {
+                        if (ring.turn > 0) c.wait(&c.m->q_empty[ring.slot], (ring.turn & 1) ^ 1);
+                        if (c.gone()) return;
+                        if (c.lane == 0) {
+                            mbar_expect_at(&c.m->q_full[ring.slot], 0, uint32_t(half) * 128u);
+                            tma_tile_at(c.q_slot(ring.slot), rope ? (lo ? &maps.qr_lo : &maps.qr) : (lo ? &maps.qn_lo : &maps.qn),
+                                        rope ? 0 : b * 64, row, &c.m->q_full[ring.slot], 0);
+                        }
+                        __syncwarp();
+                        ring.next(p.slots);
+                    }
+                }
+            }
+    }
+}
+
+// One warp brings the groups' logarithms, times log2 e and negative, as they are added; -inf (a row that saw nothing) as
+// -inf, so that the row adds 2^-inf. With prepared queries each row's factor stands beside.
+template <bool PREP>
+__device__ __forceinline__ void lse_warp(Ctx& c) {
+    const MlaParams& p = c.p.w.m;
+    const int rows = c.p.rows;
+    constexpr float LOG2E = 1.4426950408889634f;
+    int item = 0;
+    Walk w = c.walk();
+    while (w.next()) {
+        const int64_t first = p.query_start[w.n] * p.H;
+        const unsigned all = unsigned(w.s.L) * unsigned(p.H);
+        for (int kt = w.kt0; kt < w.kt1; ++kt)
+#pragma unroll 1
+            for (int g = w.ga; g < w.gb; ++g, ++item) {
+                const int slot = item % LSE_SLOTS;
+                float l[8], f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = k * 32 + c.lane;
+                    const unsigned row = unsigned(g) * unsigned(rows) + i;
+                    const bool live = i < rows && row < all;
+                    l[k] = live ? p.lse[first + row] : 0.f;
+                    f[k] = PREP && live ? c.p.row_mul[first + row] * (p.scale * LOG2E) : 0.f;
+                }
+                if (item >= LSE_SLOTS) c.wait(&c.m->lse_free[slot], ((item / LSE_SLOTS) & 1) ^ 1);
+                float* lse = c.lse + slot * (LSE_SLOT / 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = k * 32 + c.lane;
+                    if (i >= rows) break;
+                    const float x = l[k] == -INFINITY ? -INFINITY : -l[k] * LOG2E;
+                    if (PREP) *reinterpret_cast<float2*>(lse + 2 * i) = make_float2(f[k], x);
+                    else lse[i] = x;
+                }
+                __syncwarp();
+                if (c.lane == 0) mbar_arrive(&c.m->lse_full[slot]);
+            }
+    }
 }
 
 // The tiles of a share as the loading warps go over them: a thread has rows v >> 2 and 64 + v >> 2 of each tile.
 struct Tiles {
     const Ctx& c;
     Walk w;
-    int kt, r0;
+    int kt = 0, r0;
     bool in = false;
     Look look[2];
     int64_t slot[2];
-    __device__ __forceinline__ Tiles(const Ctx& x, int v) : c(x), w(x.walk()), kt(0), r0(v >> 2) {}
+    __device__ __forceinline__ Tiles(const Ctx& x, int v) : c(x), w(x.walk()), r0(v >> 2) {}
     __device__ __forceinline__ void begin(int t) {
-        const int key = (w.kb * KW_BLOCK + t) * KW_KEYS + int(c.rank) * CKEYS + r0;
+        const int key = t * KW_KEYS + int(c.rank) * CKEYS + r0;
         look[0].begin(c.p.w.m, w.n, w.s.K, key);
         look[1].begin(c.p.w.m, w.n, w.s.K, key + 64);
     }
     __device__ __forceinline__ bool next() {
         if (!in || ++kt >= w.kt1) {
-            while (!(in && w.next_part())) {
-                if (!w.next_block()) return false;
-                in = true;
-            }
+            do {
+                if (!w.next()) return false;
+            } while (w.ga >= w.gb);
+            in = true;
             kt = w.kt0;
             begin(kt);
         }
@@ -266,27 +351,27 @@ struct Tiles {
     }
 };
 
-// Eight warps bring 16-bit latent rows that TMA does not take (small blocks, narrow rows, rotary codes): 16-byte copies, three
-// boxes in flight. A thread has pieces c4 and c4 + 4 of its rows; odd rows take them the other way round, so that eight
+// Eight warps bring 16-bit latent rows that TMA does not take (blocks that no 8 keys divide, rotary codes): 16-byte copies,
+// three boxes in flight. A thread has pieces c4 and c4 + 4 of its rows; odd rows take them the other way round, so that eight
 // lanes write to all banks.
 __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
-    const int c4 = v & 3, r0 = v >> 2, mask = c.p.stages - 1, log = c.p.stages == 8 ? 3 : 2, nc = p.Dv / 8, nr = p.Dk / 8;
+    const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 8, nr = p.Dk / 8;
     const bool k8 = p.k_kind != OUT16;
-    int j = 0;
+    int tile = 0;
     Tiles t(c, v);
-    while (t.next()) {
+    for (; t.next(); ++tile) {
         uint4 codes[2];
         if (k8)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 codes[h] = t.slot[h] >= 0 && c4 < p.Dk / 16 ? ld_ahead_v4(static_cast<const uint8_t*>(p.kc) + t.slot[h] * p.Dk + c4 * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-        for (int b = 0; b <= c.nb; ++b, ++j) {
-            const int st = j & mask;
-            if (j > mask) c.wait(&c.m->k_empty[st], ((j >> log) & 1) ^ 1);
-            const uint32_t box = c.stage(st);
+        for (int b = 0; b <= c.nb; ++b) {
             const bool rope = b == c.nb;
+            const int at = rope ? ROPE : b;
+            if (tile > 0) c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
+            const uint32_t box = c.k_box(at);
             if (rope && k8) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -306,24 +391,25 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
                     }
             }
             cp_async_commit();
-            if (j >= 3) {
+            if (b >= 3) {
                 cp_async_wait<3>();
-                c.arrive(&c.m->k_full[(j - 3) & mask]);
+                c.arrive(&c.m->k_full[b - 3]);
             }
         }
+        // The tile's last boxes: the next one's first is free only when the products have had all of this one.
+        cp_async_wait<0>();
+        for (int b = max(0, c.nb - 2); b <= c.nb; ++b) c.arrive(&c.m->k_full[b < c.nb ? b : ROPE]);
     }
-    cp_async_wait<0>();
-    for (int i = max(0, j - 3); i < j; ++i) c.arrive(&c.m->k_full[i & mask]);
 }
 
 // Eight warps decode a cache of codes, half a tile's channels at a time, the next half's loads in flight meanwhile.
 template <int CK>
 __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
-    const int c4 = v & 3, r0 = v >> 2, mask = c.p.stages - 1, log = c.p.stages == 8 ? 3 : 2, nc = p.Dv / 16;
+    const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 16;
     const bool k8 = p.k_kind != OUT16;
     const int nr = k8 ? p.Dk / 16 : p.Dk / 8;
-    int j = 0, unit = 2;   // units of a tile: boxes 0-3, boxes 4-7, the rotary part
+    int tile = 0, unit = 2;   // units of a tile: boxes 0-3, boxes 4-7, the rotary part
     Tiles t(c, v);
     auto advance = [&]() {
         if (++unit == 1 && c.nb <= 4) ++unit;
@@ -353,9 +439,9 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= boxes) break;
-            const int st = j & mask;
-            if (j > mask) c.wait(&c.m->k_empty[st], ((j >> log) & 1) ^ 1);
-            const uint32_t box = c.stage(st);
+            const int at = u == 2 ? ROPE : u * 4 + i;
+            if (tile > 0) c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
+            const uint32_t box = c.k_box(at);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = r0 + 64 * h;
@@ -371,9 +457,9 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v) {
                     st_shared_v4(box_at(box, r, c4 + 4), x[h * 4 + 1]);
                 }
             }
-            c.arrive(&c.m->k_full[st]);
-            ++j;
+            c.arrive(&c.m->k_full[at]);
         }
+        if (u == 2) ++tile;
     };
     uint4 x[8], y[8];
     bool more = advance();
@@ -392,121 +478,57 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     }
 }
 
-// QW warps bring a group's queries, half of its rows, and the logarithms of all: times log2 e, negative, as they are added;
-// -inf (a row that saw nothing) and rows behind the last one as -inf, so that the row adds 2^-inf. With prepared queries each
-// row's factor stands beside.
-template <bool PREP, int QW>
-__device__ __forceinline__ void query_warps(Ctx& c, int v) {
-    const MlaParams& p = c.p.w.m;
-    const int rows = c.p.rows, half = rows / 2, ch = v & 7, r0 = v >> 3, nc = p.Dv / 8, nr = p.Dk / 8;
-    constexpr float LOG2E = 1.4426950408889634f;
-    int group = 0;
-    Walk w = c.walk();
-    while (w.next_block()) {
-        const int64_t q0 = p.query_start[w.n];
-        const unsigned all = unsigned(w.s.L) * unsigned(p.H);
-        while (w.next_part()) {
-            if (group > 0) c.wait(&c.m->q_free, (group - 1) & 1);
-            const unsigned first = unsigned(w.g) * unsigned(rows);
-#pragma unroll 2
-            for (int r = r0; r < half; r += 4 * QW) {
-                const unsigned row = first + c.rank * half + r;
-                const bool live = row < all;
-                const int64_t t = live ? q0 + row / unsigned(p.H) : 0, head = live ? row % unsigned(p.H) : 0;
-                const uint16_t* qn = static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs;
-                const uint16_t* qr = static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const bool in = live && b * 8 + ch < nc;
-                    if (b < c.nb) cp_async16(box_at(c.q_box(b), r, ch), in ? qn + (b * 8 + ch) * 8 : qn, in);
-                }
-                cp_async16(box_at(c.q_box(ROPE_BOX), r, ch), live && ch < nr ? qr + ch * 8 : qr, live && ch < nr);
-                if (PREP) {
-                    const int64_t at = t * p.H + head;
-                    if (c.p.qn_lo != nullptr) {
-                        const uint16_t* lo = c.p.qn_lo + at * p.Dv;
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const bool in = live && b * 8 + ch < nc;
-                            if (b < c.nb) cp_async16(box_at(c.q_box(LO_BOX + b), r, ch), in ? lo + (b * 8 + ch) * 8 : lo, in);
-                        }
-                    }
-                    if (c.p.qr_lo != nullptr) {
-                        const uint16_t* lo = c.p.qr_lo + at * p.Dk;
-                        cp_async16(box_at(c.q_box(ROPE_LO_BOX), r, ch), live && ch < nr ? lo + ch * 8 : lo, live && ch < nr);
-                    }
-                }
-            }
-            cp_async_commit();
-            float* lse = c.lse + (group % LSE_SLOTS) * 256;
-            for (int i = v; i < rows; i += 32 * QW) {
-                const bool live = first + i < all;
-                const int64_t at = live ? q0 * p.H + first + i : 0;
-                const float l = live ? p.lse[at] : -INFINITY, x = l == -INFINITY ? -INFINITY : -l * LOG2E;
-                if (PREP) {
-                    lse[2 * i] = live ? c.p.row_mul[at] * (p.scale * LOG2E) : 0.f;
-                    lse[2 * i + 1] = x;
-                } else {
-                    lse[i] = x;
-                }
-            }
-            __syncwarp();
-            if (c.lane == 0) mbar_arrive(&c.m->lse_full[group % LSE_SLOTS]);
-            cp_async_wait<0>();
-            c.arrive(&c.m->q_full);
-            ++group;
-        }
-    }
-}
-
-// The MMA warp of CTA 0. C8, K8: which operands are halves with a second part.
+// The MMA warp of CTA 0.
 template <class IT, bool C8>
 __device__ __forceinline__ void mma_warp(Ctx& c) {
     const Tc& p = c.p;
     Misc* m = c.m;
-    const bool k8 = p.w.m.k_kind != OUT16;
     const uint32_t id_it = tc_idesc(KW_KEYS, p.rows, is_bf16<IT>, false), id_half = tc_idesc(KW_KEYS, p.rows, false, false);
-    const uint32_t id_n = C8 ? id_half : id_it, id_r = k8 ? id_half : id_it;
-    const int mask = p.stages - 1, log = p.stages == 8 ? 3 : 2;
+    const uint32_t id_n = C8 ? id_half : id_it, id_r = p.w.m.k_kind != OUT16 ? id_half : id_it;
     const bool leader = elect_one();
-    int j = 0, group = 0, used[2] = {0, 0};
+    int tile = 0, item = 0;
+    Ring ring;
     Walk w = c.walk();
-    while (w.next_block())
-        while (w.next_part()) {
-            c.wait(&m->q_full, group & 1);
+    while (w.next()) {
+        if (w.ga >= w.gb) continue;
+        const bool stay = c.stays(w);
+        const Ring first = ring;
 #pragma unroll 1
-            for (int kt = w.kt0; kt < w.kt1; ++kt) {
-                const int h = kt & 1;
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++tile) {
+            if (stay) ring = first;
+            const bool fresh = !stay || kt == w.kt0, free = !stay || kt + 1 == w.kt1;   // the queries come, and go
+#pragma unroll 1
+            for (int g = w.ga; g < w.gb; ++g, ++item) {
+                const int h = item & 1;
                 const uint32_t d = c.tmem + uint32_t(h) * COL_D;
-                if (used[h] > 0) c.wait(&m->d_free[h], (used[h] - 1) & 1);
-                ++used[h];
+                if (item > 1) c.wait(&m->d_free[h], ((item >> 1) & 1) ^ 1);
 #pragma unroll 1
-                for (int b = 0; b <= c.nb; ++b, ++j) {
-                    const int st = j & mask;
+                for (int b = 0; b <= c.nb; ++b) {
                     const bool rope = b == c.nb;
-                    c.wait(&m->k_full[st], (j >> log) & 1);
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t kd = tc_desc(c.stage(st), 16, 1024), qd = tc_desc(c.q_box(rope ? ROPE_BOX : b), 16, 1024);
+                    const int at = rope ? ROPE : b;
+                    if (g == w.ga) c.wait(&m->k_full[at], tile & 1);
+                    const uint64_t kd = tc_desc(c.k_box(at), 16, 1024);
+#pragma unroll 1
+                    for (int lo = 0; lo <= (rope ? p.lo_r : p.lo_n); ++lo) {
+                        if (fresh) c.wait(&m->q_full[ring.slot], ring.turn & 1);
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t qd = tc_desc(c.q_slot(ring.slot), 16, 1024);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) tc_mma_pair(d, kd + s * 2, qd + s * 2, rope ? id_r : id_n, b > 0 || s > 0);
-                        if (rope ? k8 : C8) {
-                            const uint64_t lo = tc_desc(c.q_box(rope ? ROPE_LO_BOX : LO_BOX + b), 16, 1024);
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) tc_mma_pair(d, kd + s * 2, lo + s * 2, rope ? id_r : id_n, true);
+                            for (int s = 0; s < 4; ++s) tc_mma_pair(d, kd + s * 2, qd + s * 2, rope ? id_r : id_n, b > 0 || lo > 0 || s > 0);
+                            if (free) tc_commit_pair(&m->q_empty[ring.slot]);
                         }
-                        tc_commit_pair(&m->k_empty[st]);
+                        __syncwarp();
+                        ring.next(p.slots);
                     }
+                    if (g + 1 == w.gb && leader) tc_commit_pair(&m->k_empty[at]);
                     __syncwarp();
                 }
-                if (leader) {
-                    tc_commit_pair(&m->d_full[h]);
-                    if (kt + 1 == w.kt1) tc_commit_pair(&m->q_free);
-                }
+                if (leader) tc_commit_pair(&m->d_full[h]);
                 __syncwarp();
             }
-            ++group;
         }
+    }
     if (!c.ok) {   // let what was issued finish before TMEM goes
         if (leader) {
             tc_commit_pair(&m->drain);
@@ -536,14 +558,15 @@ __device__ __forceinline__ float2 column_sum(const float (&s)[32], const float* 
     }
     return sum;
 }
-// The same where causal masking may hide the key from rows: `sees` keys of the token that the column belongs to, as its
-// head `head`; the next token sees one more.
+// The same where causal masking may hide the key from rows (`sees` keys of the token that the column belongs to, as its head
+// `head`; the next token sees one more), or where columns are no rows of the sequence (`left` are).
 template <bool PREP>
-__device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* lse, float f, float2 sum, int key, int H, int& sees, int& head) {
+__device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* lse, float f, float2 sum, int key, int H, int& sees, int& head,
+                                             int left) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float x = PREP ? fmaf(s[i], lse[2 * i], lse[2 * i + 1]) : fmaf(s[i], f, lse[i]);
-        if (key < sees) sum.x += exp2_approx(x);
+        if (key < sees && i < left) sum.x += exp2_approx(x);
         if (++head == H) {
             head = 0;
             ++sees;
@@ -561,96 +584,93 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
     const int mine = EG == 2 ? tid >> 7 : 0, r = tid & 127, rows = p.rows;
     const uint32_t lanes = c.tmem + (uint32_t(tid >> 5 & 3) << 21);
     const float f = a.scale * 1.4426950408889634f;
-    float* acc = c.acc + r;
-    int group = 0, used[2] = {0, 0};
+    int item = 0, joined = 0;
     Walk w = c.walk();
-    while (w.next_block()) {
-        for (int kt = mine; kt < w.tiles; kt += EG) acc[kt * CKEYS] = 0.f;
-        int from = KW_BLOCK, upto = 0;   // tiles with sums
-        const int key0 = w.kb * (KW_BLOCK * KW_KEYS) + int(c.rank) * CKEYS;
-        while (w.next_part()) {
-            const float* lse = c.lse + (group % LSE_SLOTS) * 256;
-            c.wait(&m->lse_full[group % LSE_SLOTS], (group / LSE_SLOTS) & 1);
-            ++group;
-            from = min(from, w.kt0);
-            upto = max(upto, w.kt1);
-            const unsigned first = unsigned(w.g) * unsigned(rows);
-            const int t0 = int(first / unsigned(a.H)), h0 = int(first % unsigned(a.H));
-            const int sees0 = a.causal ? w.s.K - w.s.L + t0 + 1 : w.s.K;
+    while (w.next()) {
+        const unsigned all = unsigned(w.s.L) * unsigned(a.H);
+        const int slot = pair * 2 + (m->begin.n == w.n && m->begin.kt == w.kt0 ? 0 : 1);
+        const float* past = p.w.past == nullptr ? nullptr : p.w.past + w.n * p.w.past_stride;
+        float* weight = p.w.weight + w.n * p.w.weight_stride;
 #pragma unroll 1
-            for (int kt = w.kt0; kt < w.kt1; ++kt) {
-                const int h = kt & 1;
+        for (int kt = w.kt0; kt < w.kt1; ++kt) {
+            const int key0 = kt * KW_KEYS + int(c.rank) * CKEYS, key = key0 + r;
+            const bool writes = EG == 1 || (w.gb - w.ga == 1 ? (item & 1) == mine : mine == 0);
+            float old = 0.f, total = 0.f;
+            if (writes && w.whole && past != nullptr && key < w.s.K) old = past[key];
+            const bool held = writes && key_row(a, w.n, w.s.K, key) >= 0;
+#pragma unroll 1
+            for (int g = w.ga; g < w.gb; ++g, ++item) {
+                const int h = item & 1, ls = item % LSE_SLOTS;
                 if (EG == 2 && h != mine) continue;
-                c.wait(&m->d_full[h], used[h] & 1);
-                ++used[h];
+                const unsigned first = unsigned(g) * unsigned(rows);
+                const int t0 = int(first / unsigned(a.H)), h0 = int(first % unsigned(a.H));
+                const int sees0 = a.causal ? w.s.K - w.s.L + t0 + 1 : w.s.K, left = int(min(all - first, unsigned(rows)));
+                const bool masked = (a.causal && key0 + CKEYS > sees0) || left < rows;
+                const float* lse = c.lse + ls * (LSE_SLOT / 4);
+                c.wait(&m->lse_full[ls], (item / LSE_SLOTS) & 1);
+                c.wait(&m->d_full[h], (item >> 1) & 1);
                 tc_fence_after();
                 const uint32_t d = lanes + uint32_t(h) * COL_D;
-                const int key = key0 + kt * KW_KEYS + r;
-                const bool masked = key0 + kt * KW_KEYS + CKEYS > sees0 && a.causal;
                 float2 sum = make_float2(0.f, 0.f);
                 int sees = sees0, head = h0;
+                // (a key behind the last is a lane without a meaning; without causal masking every row sees `key`)
+                if (!a.causal) sees = 0x7FFFFFFF - rows;
                 float x[32], y[32];
                 tmem_ld32(d, x);
 #pragma unroll 1
                 for (int q = 0; q < rows; q += 64) {
                     tmem_wait_ld();
                     if (q + 32 < rows) tmem_ld32(d + q + 32, y);
-                    if (masked) sum = masked_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum, key, a.H, sees, head);
+                    if (masked) sum = masked_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum, key, a.H, sees, head, left - q);
                     else sum = column_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum);
                     if (q + 32 >= rows) break;
                     tmem_wait_ld();
                     if (q + 64 < rows) tmem_ld32(d + q + 64, x);
-                    if (masked) sum = masked_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum, key, a.H, sees, head);
+                    if (masked) sum = masked_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum, key, a.H, sees, head, left - q - 32);
                     else sum = column_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (c.lane == 0) mbar_arrive_at(&m->d_free[h], 0);
-                acc[kt * CKEYS] += sum.x + sum.y;
+                if (c.lane == 0) {
+                    mbar_arrive_at(&m->d_free[h], 0);
+                    mbar_arrive(&m->lse_free[ls]);
+                }
+                total += sum.x + sum.y;
             }
-        }
-        // Out: to the weights where the share has all that adds to them, else to the workspace.
-        const bool direct = w.s.groups() == 1 || w.whole(m->begin);
-        const bool only = w.s.groups() == 1;   // its tiles alone: others may be another pair's
-        const int slot = pair * 2 + (m->begin.n == w.n && m->begin.kb == w.kb ? 0 : 1);
-        float* sums = ws_space(p).sums + int64_t(slot) * (KW_BLOCK * KW_KEYS) + int(c.rank) * CKEYS + r;
-        const float* past = p.w.past == nullptr ? nullptr : p.w.past + w.n * p.w.past_stride;
-        float* weight = p.w.weight + w.n * p.w.weight_stride;
-        for (int kt = mine; kt < w.tiles; kt += EG) {
-            if (only && (kt < from || kt >= upto)) continue;
-            const int key = key0 + kt * KW_KEYS + r;
-            float v = acc[kt * CKEYS];
-            if (key_row(a, w.n, w.s.K, key) < 0) v = 0.f;   // whatever lay in its place
-            if (!direct) {
-                sums[kt * KW_KEYS] = v;
-            } else if (key < w.s.K) {
-                weight[key] = past == nullptr ? v : fmaf(p.w.decay, past[key], v);
+            if (EG == 2 && w.gb - w.ga > 1) {
+                float* other = &m->other[joined & 1][r];
+                ++joined;
+                if (mine == 1) *other = total;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (mine == 0) total += *other;
             }
+            if (!writes) continue;
+            if (!held) total = 0.f;   // whatever lay in its place
+            if (!w.whole) ws_space(p).sums[int64_t(slot) * KW_KEYS + int(c.rank) * CKEYS + r] = total;
+            else if (key < w.s.K) weight[key] = past == nullptr ? total : fmaf(p.w.decay, old, total);
         }
     }
 }
 
-// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then QW queries, 1 MMA, and 1 for TMA or 8 that load and
-// decode; at most 16, so that each thread may have 128 registers.
+// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then MMA, queries, logarithms, and 1 for TMA or 8 that load
+// and decode; at most 16, so that each thread may have 128 registers.
 template <bool TMA>
 struct Roles {
-    static constexpr int EG = TMA ? 2 : 1, QW = TMA ? 4 : 2;
-    static constexpr int QUERY = 4 * EG, MMA = QUERY + QW, LOAD = MMA + 1, LOADERS = TMA ? 1 : 8;
+    static constexpr int EG = TMA ? 2 : 1;
+    static constexpr int MMA = 4 * EG, QUERY = MMA + 1, LSE = MMA + 2, LOAD = MMA + 3, LOADERS = TMA ? 1 : 8;
     static constexpr int THREADS = (LOAD + LOADERS) * 32;
 };
 
+// CK: OutKind of the latent rows.
 template <class IT, int CK, bool TMA>
 __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1, 1)
-    key_weight_tc_kernel(const __grid_constant__ Tc p, const __grid_constant__ CUtensorMap latent, const __grid_constant__ CUtensorMap rope) {
+    key_weight_tc_kernel(const __grid_constant__ Tc p, const __grid_constant__ Maps maps) {
     using R = Roles<TMA>;
     constexpr bool C8 = CK != OUT16;
-    const bool prep = p.row_mul != nullptr;
     extern __shared__ __align__(1024) uint8_t smem_raw[];   // the swizzle repeats every 1024 bytes
-    const uint32_t base = smem_u32(smem_raw), qb = q_bytes(p.rows, prep);
-    uint8_t* at = smem_raw + qb + uint32_t(p.stages) * BOX;
-    float* acc = reinterpret_cast<float*>(at);
-    float* lse = reinterpret_cast<float*>(at + ACC_BYTES);
-    Misc* m = reinterpret_cast<Misc*>(at + ACC_BYTES + LSE_BYTES);
+    const uint32_t base = smem_u32(smem_raw);
+    float* lse = reinterpret_cast<float*>(smem_raw + OFF_LSE);
+    Misc* m = reinterpret_cast<Misc*>(smem_raw + OFF_MISC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = blockIdx.x >> 1;
     const uint32_t rank = cluster_rank();
     if (base % 1024 != 0) {   // the declaration's alignment was not kept: nothing below would be right
@@ -658,17 +678,22 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
         return;
     }
     if (tid == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&m->k_full[s], 2 * R::LOADERS);
-            mbar_init(&m->k_empty[s], 1);
+        for (int b = 0; b < KBOXES; ++b) {
+            mbar_init(&m->k_full[b], 2 * R::LOADERS);
+            mbar_init(&m->k_empty[b], 1);
         }
-        mbar_init(&m->q_full, 2 * R::QW);
-        mbar_init(&m->q_free, 1);
+        for (int s = 0; s < MAX_SLOTS; ++s) {
+            mbar_init(&m->q_full[s], 2);
+            mbar_init(&m->q_empty[s], 1);
+        }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&m->d_full[h], 1);
             mbar_init(&m->d_free[h], 8);
         }
-        for (int s = 0; s < LSE_SLOTS; ++s) mbar_init(&m->lse_full[s], R::QW);
+        for (int s = 0; s < LSE_SLOTS; ++s) {
+            mbar_init(&m->lse_full[s], 1);
+            mbar_init(&m->lse_free[s], 4);
+        }
         mbar_init(&m->drain, 1);
         m->abort = 0;
         fence_mbar_init();
@@ -689,17 +714,20 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
     cluster_wait();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    Ctx c{p, m, base, base + qb, tmem, rank, lane, (p.w.m.Dv + 63) / 64, acc, lse, &m->abort, true};
-    if (warp < R::QUERY) {
-        if (C8 || (!TMA && prep)) sum_warps<true, R::EG>(c, tid, pair);
+    Ctx c{p, m, base, tmem, rank, lane, (p.w.m.Dv + 63) / 64, lse, &m->abort, true};
+    const bool prep = C8 || (!TMA && p.row_mul != nullptr);   // (rotary codes alone come without TMA)
+    if (warp < R::MMA) {
+        if (prep) sum_warps<true, R::EG>(c, tid, pair);
         else if (!C8) sum_warps<false, R::EG>(c, tid, pair);
-    } else if (warp < R::MMA) {
-        if (C8 || (!TMA && prep)) query_warps<true, R::QW>(c, tid - R::QUERY * 32);
-        else if (!C8) query_warps<false, R::QW>(c, tid - R::QUERY * 32);
     } else if (warp == R::MMA) {
         if (rank == 0) mma_warp<IT, C8>(c);
+    } else if (warp == R::QUERY) {
+        query_warp(c, maps);
+    } else if (warp == R::LSE) {
+        if (prep) lse_warp<true>(c);
+        else if (!C8) lse_warp<false>(c);
     } else if constexpr (TMA) {
-        tma_warp(c, &latent, &rope);
+        key_warp(c, maps);
     } else if constexpr (C8) {
         code_warps<CK>(c, tid - R::LOAD * 32);
     } else {
@@ -720,7 +748,8 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
 
 // Queries for a cache of codes: z = q / scale (q itself for a part that is 16-bit), over a power of two per row that keeps all
 // of the row's z below 2^14, as halves hi = half(z) and lo = half(z - hi): 22 bits of z, or of 2^-24 where z is smaller.
-// The 16-bit part keeps its type, over the same power. One warp a row.
+// The 16-bit part keeps its type, over the same power. Without `mul` the rows are laid out densely as they are, for queries
+// whose rows lie unevenly over tokens and heads (TMA takes them by rows). One warp a row.
 template <class IT>
 __global__ void __launch_bounds__(256) key_weight_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn, uint16_t* qn_lo, uint16_t* qr,
                                                                  uint16_t* qr_lo, float* mul) {
@@ -753,9 +782,9 @@ __global__ void __launch_bounds__(256) key_weight_queries_kernel(const __grid_co
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e = top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) - 13, -113), 113) : 0;
+        const int e = mul != nullptr && top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) - 13, -113), 113) : 0;
         const float g = ldexpf(1.f, -e);
-        if (lane == 0) mul[row] = ldexpf(1.f, e);
+        if (lane == 0 && mul != nullptr) mul[row] = ldexpf(1.f, e);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const int ch = (k < 2 ? k * 32 + lane : lane) * 8, width = k < 2 ? p.Dv : p.Dk;
@@ -779,13 +808,11 @@ __global__ void __launch_bounds__(256) key_weight_queries_kernel(const __grid_co
     }
 }
 
-// Adds up the sums of a block that the cut goes through, in the pairs' order: blocks x take the one that the begin of pair
-// x + 1 is in, if that is the first inside it. A thread has four keys.
-constexpr int JOIN_THREADS = 256;
-__global__ void __launch_bounds__(JOIN_THREADS) key_weight_join_kernel(const __grid_constant__ Tc p) {
+// Adds up the sums of a tile that the cut goes through, in the pairs' order: block x takes the one that the begin of pair
+// x + 1 is in, if that is the first inside it. A thread has a key.
+__global__ void __launch_bounds__(KW_KEYS) key_weight_join_kernel(const __grid_constant__ Tc p) {
     const Space ws = ws_space(p);
-    const int lane = threadIdx.x & 31, b = blockIdx.x + 1;
-    const int i = (blockIdx.y * JOIN_THREADS + threadIdx.x) * 4;   // of the block's keys
+    const int lane = threadIdx.x & 31, b = blockIdx.x + 1, i = threadIdx.x;
     auto start = [&](int q) {
         Start v = {{-1, 0, 0, 0}, 0, 0, {0, 0}};
         if (q < p.pairs) v = ws.starts[q];
@@ -794,29 +821,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) key_weight_join_kernel(const __g
     pdl_wait();
     pdl_launch_dependents();
     const int active = *ws.active;
-    if (b >= active) return;
     const Start here = start(b), before = start(b - 1);
-    if (here.at.n >= p.w.m.N || !kw_inside(here.at)) return;
-    const KwShape s = {here.L, here.K, p.w.m.H, p.rows, p.w.m.causal != 0};
-    const bool same = kw_same_block(before.at, here.at);
-    if (s.groups() == 1 || (same && kw_inside(before.at))) return;
-    const int key = here.at.kb * (KW_BLOCK * KW_KEYS) + i;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* sums = ws.sums + i;
-    auto add = [&](int slot) {
-        const float4 v = *reinterpret_cast<const float4*>(sums + int64_t(slot) * (KW_BLOCK * KW_KEYS));
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-    };
-    // The last block of pair b - 1, then the first of each pair that begins inside; none of a pair without work.
+    if (b >= active || here.at.n >= p.w.m.N || !here.at.cut) return;
+    const bool same = kw_same_tile(before.at, here.at);
+    if (same && before.at.cut) return;
+    const int n = here.at.n, key = here.at.kt * KW_KEYS + i;
+    float sum = 0.f;
+    auto add = [&](int slot) { sum += ws.sums[int64_t(slot) * KW_KEYS + i]; };
+    // The last tile of pair b - 1, then the first of each pair that begins inside; none of a pair without work.
     if (!kw_same(before.at, here.at)) add((b - 1) * 2 + (same ? 0 : 1));
     for (int at = b;; at += 31) {
         const Start x = start(at + lane);   // lane i has pair at + i; its end is lane i + 1's begin
-        const KwPos y = {__shfl_down_sync(0xFFFFFFFFu, x.at.n, 1), __shfl_down_sync(0xFFFFFFFFu, x.at.kb, 1),
-                         __shfl_down_sync(0xFFFFFFFFu, x.at.g, 1), __shfl_down_sync(0xFFFFFFFFu, x.at.kt, 1)};
-        const bool in = at + lane < active && kw_same_block(x.at, here.at);
+        const KwPos y = {__shfl_down_sync(0xFFFFFFFFu, x.at.n, 1), __shfl_down_sync(0xFFFFFFFFu, x.at.kt, 1),
+                         __shfl_down_sync(0xFFFFFFFFu, x.at.g, 1), 0};
+        const bool in = at + lane < active && kw_same_tile(x.at, here.at);
         const uint32_t run = __ballot_sync(0xFFFFFFFFu, in), works = __ballot_sync(0xFFFFFFFFu, in && !(at + lane + 1 < active && kw_same(x.at, y)));
         const int count = min(31, run == 0xFFFFFFFFu ? 32 : __ffs(~run) - 1);
 #pragma unroll 4
@@ -824,18 +842,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) key_weight_join_kernel(const __g
             if (works >> q & 1) add((at + q) * 2);
         if (count < 31) break;
     }
-    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-    const int n = here.at.n;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (key + k < here.K) {
-            float* to = p.w.weight + n * p.w.weight_stride + key + k;
-            *to = p.w.past == nullptr ? v[k] : fmaf(p.w.decay, p.w.past[n * p.w.past_stride + key + k], v[k]);
-        }
+    if (key >= here.K) return;
+    float* to = p.w.weight + n * p.w.weight_stride + key;
+    *to = p.w.past == nullptr ? sum : fmaf(p.w.decay, p.w.past[n * p.w.past_stride + key], sum);
 }
-static_assert(KW_BLOCK * KW_KEYS % (JOIN_THREADS * 4) == 0, "whole blocks of threads");
 
-using Kernel = void (*)(Tc, CUtensorMap, CUtensorMap);
+using Kernel = void (*)(Tc, Maps);
 template <class IT>
 Kernel kernel_of_t(int ck, bool tma) {
     switch (ck) {
@@ -847,7 +859,6 @@ Kernel kernel_of_t(int ck, bool tma) {
 }
 Kernel kernel_of(int dtype, int ck, bool tma) { return dtype == KVR_BF16 ? kernel_of_t<BF16>(ck, tma) : kernel_of_t<F16>(ck, tma); }
 int threads_of(bool tma) { return tma ? Roles<true>::THREADS : Roles<false>::THREADS; }
-constexpr int MOST_SMEM = 232448;
 
 // CTA pairs that fit on the current device at once; looked up once per device, as is the shared memory allowed.
 int pairs_of_device() {
@@ -864,7 +875,7 @@ int pairs_of_device() {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(sm_count_current_device()) / 2 * 2);
         cfg.blockDim = dim3(threads_of(true));
-        cfg.dynamicSmemBytes = MOST_SMEM;
+        cfg.dynamicSmemBytes = SMEM;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -876,7 +887,7 @@ int pairs_of_device() {
             for (int ck : {OUT16, OUT_I8, OUT_E4M3, OUT_E5M2})
                 for (bool tma : {false, true})
                     good = good && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_of(dtype, ck, tma)),
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_SMEM) == cudaSuccess;
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM)) == cudaSuccess;
         good = good && cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kernel_of(KVR_BF16, OUT16, true)), &cfg) == cudaSuccess && n > 0;
         if (!good) {
             (void)cudaGetLastError();
@@ -888,13 +899,29 @@ int pairs_of_device() {
 }
 
 int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
+bool codes_in(const MlaParams& p) { return p.ckv_kind != OUT16 || p.k_kind != OUT16; }
+// Whether the queries' rows, (token, head) in order, are evenly spaced, as TMA takes them.
+bool q_flat(const MlaParams& p) {
+    const int64_t far = int64_t(1) << 38;
+    return (p.T == 1 && p.H == 1) || ((p.T == 1 || (p.qn_ts == p.H * p.qn_hs && p.qr_ts == p.H * p.qr_hs)) && p.qn_hs >= p.Dv &&
+                                      p.qr_hs >= p.Dk && p.qn_hs < far && p.qr_hs < far);
+}
+
+// Rows of `width` elements that start `stride` apart, in boxes of 64 channels and box_rows rows; what lies outside is zeros.
+bool encode_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int width, int64_t stride, int box_rows) {
+    const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, one[2] = {1, 1};
+    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+                     strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 
 int64_t key_weight_tc_workspace(const KeyWeightParams& w) {
     const MlaParams& p = w.m;
     int64_t n = round_up(ws_bytes(pairs_of_device()));
-    if (p.ckv_kind == OUT16 && p.k_kind == OUT16) return n;
+    if (!codes_in(p) && q_flat(p)) return n;
     const int64_t rows = p.T * p.H;
     return n + round_up(rows * 4) + round_up(rows * p.Dv * 2) * (p.ckv_kind != OUT16 ? 2 : 1) + round_up(rows * p.Dk * 2) * (p.k_kind != OUT16 ? 2 : 1);
 }
@@ -904,24 +931,26 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
     p.w = w;
     MlaParams& a = p.w.m;
     p.pairs = pairs_of_device();
-    const bool codes = a.ckv_kind != OUT16 || a.k_kind != OUT16;
-    // Rows of a group: what a sequence has on average, up to 256 (128 where queries are held twice).
-    const int64_t each = (a.T * a.H + a.N - 1) / a.N, most = codes ? 128 : 256;
+    const bool codes = codes_in(a), bf = dtype == KVR_BF16;
+    if (encoder() == nullptr) return cudaErrorNotSupported;
+    // Rows of a group: what a sequence has on average, up to 256.
+    const int64_t each = (a.T * a.H + a.N - 1) / a.N;
     p.rows = 32;
-    while (p.rows < most && p.rows < each) p.rows *= 2;
-    p.stages = smem_of(p.rows, codes, 8) <= uint32_t(MOST_SMEM) ? 8 : 4;
-    const int64_t rows = a.d0 * a.d1;
-    CUtensorMap latent = {}, rope = {};
-    if (!codes && a.Dv % 64 == 0 && a.Dk == 64 && rows < (int64_t(1) << 31) - CKEYS) {
+    while (p.rows < 256 && p.rows < each) p.rows *= 2;
+    p.slots = int(Q_BYTES) / (p.rows * 64);
+    if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
+    p.lo_n = a.ckv_kind != OUT16;
+    p.lo_r = a.k_kind != OUT16;
+    const int64_t rows = a.d0 * a.d1, n = a.T * a.H;
+    Maps maps = {};
+    if (!codes && rows < (int64_t(1) << 31) - CKEYS) {
         int r = CKEYS;
         while (a.table != nullptr && r > 1 && a.d1 % r != 0) r /= 2;
-        const bool bf = dtype == KVR_BF16;
-        if (r >= 8 && encoder() != nullptr && encode_rows(&latent, a.ckv, bf, rows, a.Dv, r, 1) && encode_rows(&rope, a.kc, bf, rows, a.Dk, r, 1))
-            p.box_rows = r;
+        if (r >= 8 && encode_2d(&maps.latent, a.ckv, bf, rows, a.Dv, a.Dv, r) && encode_2d(&maps.rope, a.kc, bf, rows, a.Dk, a.Dk, r)) p.box_rows = r;
     }
-    if (codes) {
+    uint16_t *qn_lo = nullptr, *qr_lo = nullptr;
+    if (codes || !q_flat(a)) {
         char* at = static_cast<char*>(a.workspace) + round_up(ws_bytes(p.pairs));
-        const int64_t n = a.T * a.H;
         auto take = [&](int64_t bytes) {
             char* got = at;
             at += round_up(bytes);
@@ -929,30 +958,31 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
         };
         float* mul = reinterpret_cast<float*>(take(n * 4));
         uint16_t* qn = reinterpret_cast<uint16_t*>(take(n * a.Dv * 2));
-        uint16_t* qn_lo = a.ckv_kind != OUT16 ? reinterpret_cast<uint16_t*>(take(n * a.Dv * 2)) : nullptr;
+        if (p.lo_n) qn_lo = reinterpret_cast<uint16_t*>(take(n * a.Dv * 2));
         uint16_t* qr = reinterpret_cast<uint16_t*>(take(n * a.Dk * 2));
-        uint16_t* qr_lo = a.k_kind != OUT16 ? reinterpret_cast<uint16_t*>(take(n * a.Dk * 2)) : nullptr;
+        if (p.lo_r) qr_lo = reinterpret_cast<uint16_t*>(take(n * a.Dk * 2));
+        if (!codes) mul = nullptr;
         const int64_t cap = int64_t(sm_count_current_device()) * 8, need = (n + 7) / 8;
         const dim3 grid(unsigned(need < cap ? need : cap));
-        const cudaError_t e = dtype == KVR_BF16 ? launch_pdl(key_weight_queries_kernel<BF16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul)
-                                                : launch_pdl(key_weight_queries_kernel<F16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul);
+        const cudaError_t e = bf ? launch_pdl(key_weight_queries_kernel<BF16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul)
+                                 : launch_pdl(key_weight_queries_kernel<F16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul);
         if (e != cudaSuccess) return e;
         p.row_mul = mul;
-        p.qn_lo = qn_lo;
-        p.qr_lo = qr_lo;
         a.qn = qn;
-        a.qn_ts = int64_t(a.H) * a.Dv;
         a.qn_hs = a.Dv;
         a.qr = qr;
-        a.qr_ts = int64_t(a.H) * a.Dk;
         a.qr_hs = a.Dk;
     }
+    // A part whose cache is codes has halves, the other one q's type.
+    const int64_t n_stride = a.T == 1 && a.H == 1 ? a.Dv : a.qn_hs, r_stride = a.T == 1 && a.H == 1 ? a.Dk : a.qr_hs;
+    if (!encode_2d(&maps.qn, a.qn, bf && !p.lo_n, n, a.Dv, n_stride, p.rows / 2) || !encode_2d(&maps.qr, a.qr, bf && !p.lo_r, n, a.Dk, r_stride, p.rows / 2) ||
+        (p.lo_n && !encode_2d(&maps.qn_lo, qn_lo, false, n, a.Dv, a.Dv, p.rows / 2)) || (p.lo_r && !encode_2d(&maps.qr_lo, qr_lo, false, n, a.Dk, a.Dk, p.rows / 2)))
+        return cudaErrorInvalidValue;
     const bool tma = p.box_rows > 0;
-    const cudaError_t e = launch_pdl(kernel_of(dtype, a.ckv_kind, tma), dim3(unsigned(p.pairs * 2)), dim3(threads_of(tma)),
-                                     smem_of(p.rows, codes, p.stages), s, p, latent, rope);
+    const cudaError_t e = launch_pdl(kernel_of(dtype, a.ckv_kind, tma), dim3(unsigned(p.pairs * 2)), dim3(threads_of(tma)), SMEM, s, p, maps);
     // Where no sequence can have two groups, nothing is cut that would have to be joined.
-    if (e != cudaSuccess || p.pairs == 1 || a.T * a.H <= p.rows) return e;
-    return launch_pdl(key_weight_join_kernel, dim3(unsigned(p.pairs - 1), KW_BLOCK * KW_KEYS / (JOIN_THREADS * 4)), dim3(JOIN_THREADS), 0, s, p);
+    if (e != cudaSuccess || p.pairs == 1 || n <= p.rows) return e;
+    return launch_pdl(key_weight_join_kernel, dim3(unsigned(p.pairs - 1)), dim3(KW_KEYS), 0, s, p);
 }
 
 }  // namespace kvr

@@ -51,6 +51,15 @@ __device__ __forceinline__ void tma_box_at(uint32_t dst, const CUtensorMap* map,
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "r"(rank)
         : "memory");
 }
+// The same of a 2-D tensor.
+__device__ __forceinline__ void tma_tile_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [a];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(rank)
+        : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));

@@ -186,3 +186,40 @@ def test_refusals():
     two = torch.zeros(1, 40, device="cuda")
     with pytest.raises(kvr.KvrError):
         kvr.mla_key_weight(*args, lse.cuda(), two[:, :24], past=two[:, 8:32], **ok)
+
+
+@pytest.mark.parametrize("kw", [dict(H=16), dict(H=40), dict(H=16, cache="int8"), dict(H=40, dtype="f16", cache="fp8_e4m3fn", scale_len=512),
+                                dict(H=16, block_size=100), dict(H=3, Dv=70, Dk=6)])
+def test_rows_of_others_do_not_matter(kw):
+    """Queries of another sequence, and rows outside every sequence, share a group's products: NaN there stays there."""
+    c = mla_case([3, 2, 7], [300, 500, 90], seed=14, gap=5, **dict(dict(block_size=64), **kw))
+    lse, width = row_lse(c), width_of(c)
+    want = run_weight(c, lse, width)[0]
+    c.q_nope[12:] = float("nan")
+    c.q_rope[12:] = float("inf")
+    c.q_nope[3:5] = float("nan")
+    got = run_weight(c, lse, width)[0]
+    assert np.array_equal(got[[0, 2]], want[[0, 2]]) and np.isnan(got[1, :499]).all()
+
+
+@pytest.mark.parametrize("new,keys,H", [([90], [100], 128), ([70, 3], [5000, 6000], 64), ([9] * 30, [700] * 30, 128),
+                                        ([1] * 3, [9000, 20, 12000], 32), ([2] * 5, [3000] * 5, 128)])
+def test_tiles_cut_over_many_ctas(new, keys, H):
+    c = mla_case(new, keys, H=H, block_size=128, seed=15)
+    check(c, past=torch.rand(len(new), width_of(c), generator=torch.Generator().manual_seed(5)))
+
+
+def test_heads_that_share_a_query_and_strided_ones():
+    """Expanded heads (stride 0), heads outside tokens, and rows with a gap between tokens."""
+    c = mla_case([5, 30], [300, 200], H=8, block_size=64, seed=16)
+    g = torch.Generator().manual_seed(1)
+    for make in (lambda d: torch.randn(35, 1, d, generator=g).bfloat16().expand(35, 8, d),
+                 lambda d: torch.randn(8, 35, d, generator=g).bfloat16().transpose(0, 1),
+                 lambda d: torch.randn(35, 9, d, generator=g).bfloat16()[:, 1:]):
+        qn, qr = make(512), make(64)
+        c.q_nope, c.q_rope = qn.contiguous(), qr.contiguous()
+        lse, w = row_lse(c), torch.full((2, 303), SENTINEL, device="cuda")
+        on = lambda t: t._base.cuda().as_strided(t.shape, t.stride(), t.storage_offset())  # noqa: E731
+        kvr.mla_key_weight(on(qn), on(qr), cuda(c.ckv), cuda(c.k), cuda(c.table), cuda(c.query_start), cuda(c.key_length), lse.cuda(), w,
+                           softmax_scale=c.scale)
+        check_weight(c, (f64(w), 0), oracle_weight(c, lse, 303))
