@@ -402,79 +402,91 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
     }
 }
 
-// Eight warps decode a cache of codes, half a tile's channels at a time, the next half's loads in flight meanwhile.
+// Eight warps decode a cache of codes, two boxes of a tile at a time (the rotary part for itself), the loads of the next three
+// such units in flight meanwhile.
 template <int CK>
 __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
-    const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 16;
+    const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 16, units = (c.nb + 1) / 2;
     const bool k8 = p.k_kind != OUT16;
     const int nr = k8 ? p.Dk / 16 : p.Dk / 8;
-    int tile = 0, unit = 2;   // units of a tile: boxes 0-3, boxes 4-7, the rotary part
+    int tile = 0, unit = units;   // (unit `units` is the rotary part)
     Tiles t(c, v);
     auto advance = [&]() {
-        if (++unit == 1 && c.nb <= 4) ++unit;
-        if (unit < 3) return true;
+        if (++unit <= units) return true;
         unit = 0;
         return t.next();
     };
-    auto load = [&](uint4 (&x)[8]) {
+    auto load = [&](uint4 (&x)[4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t row = t.slot[h];
-            if (unit < 2) {
-                const uint8_t* src = static_cast<const uint8_t*>(p.ckv) + row * p.Dv + unit * 256 + c4 * 16;
+            const bool rope = unit == units;
+            const uint8_t* src = rope ? static_cast<const uint8_t*>(p.kc) + row * p.Dk * (k8 ? 1 : 2) : static_cast<const uint8_t*>(p.ckv) + row * p.Dv;
+            const int first = rope ? c4 : unit * 8 + c4, count = rope ? nr : nc;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[h * 4 + i] = row >= 0 && unit * 16 + i * 4 + c4 < nc ? ld_ahead_v4(src + i * 64) : make_uint4(0, 0, 0, 0);
-            } else {
-                const uint8_t* src = static_cast<const uint8_t*>(p.kc) + row * p.Dk * (k8 ? 1 : 2) + c4 * 16;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    x[h * 4 + i] = row >= 0 && i * 4 + c4 < nr ? ld_ahead_v4(src + i * 64) : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < 2; ++i)
+                x[h * 2 + i] = row >= 0 && first + i * 4 < count ? ld_ahead_v4(src + (first + i * 4) * 16) : make_uint4(0, 0, 0, 0);
         }
     };
-    auto put = [&](int u, const uint4 (&x)[8]) {
-        const int boxes = u == 2 ? 1 : min(4, c.nb - u * 4);
+    auto put = [&](int u, const uint4 (&x)[4]) {
+        const bool rope = u == units, two = !rope && u * 2 + 1 < c.nb;
+        const int at = rope ? ROPE : u * 2;
+        if (tile > 0) {
+            c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
+            if (two) c.wait(&c.m->k_empty[at + 1], (tile & 1) ^ 1);
+        }
+        const uint32_t box = c.k_box(at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= boxes) break;
-            const int at = u == 2 ? ROPE : u * 4 + i;
-            if (tile > 0) c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
-            const uint32_t box = c.k_box(at);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = r0 + 64 * h;
-                const uint4 y = x[h * 4 + i];
-                if (u < 2) {
-                    st_shared_v4(box_at(box, r, 2 * c4), codes_to_halves<CK>(y.x, y.y));
-                    st_shared_v4(box_at(box, r, 2 * c4 + 1), codes_to_halves<CK>(y.z, y.w));
-                } else if (k8) {
-                    st_shared_v4(box_at(box, r, 2 * c4), dec8x8<F16>(p.k_kind, y.x, y.y));
-                    st_shared_v4(box_at(box, r, 2 * c4 + 1), dec8x8<F16>(p.k_kind, y.z, y.w));
-                } else {
-                    st_shared_v4(box_at(box, r, c4), y);
-                    st_shared_v4(box_at(box, r, c4 + 4), x[h * 4 + 1]);
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 64 * h;
+            const uint4 y = x[h * 2], z = x[h * 2 + 1];
+            if (!rope) {
+                st_shared_v4(box_at(box, r, 2 * c4), codes_to_halves<CK>(y.x, y.y));
+                st_shared_v4(box_at(box, r, 2 * c4 + 1), codes_to_halves<CK>(y.z, y.w));
+                if (two) {
+                    st_shared_v4(box_at(box + BOX, r, 2 * c4), codes_to_halves<CK>(z.x, z.y));
+                    st_shared_v4(box_at(box + BOX, r, 2 * c4 + 1), codes_to_halves<CK>(z.z, z.w));
                 }
+            } else if (k8) {
+                st_shared_v4(box_at(box, r, 2 * c4), dec8x8<F16>(p.k_kind, y.x, y.y));
+                st_shared_v4(box_at(box, r, 2 * c4 + 1), dec8x8<F16>(p.k_kind, y.z, y.w));
+            } else {
+                st_shared_v4(box_at(box, r, c4), y);
+                st_shared_v4(box_at(box, r, c4 + 4), z);
             }
-            c.arrive(&c.m->k_full[at]);
         }
-        if (u == 2) ++tile;
+        fence_async_proxy();
+        __syncwarp();
+        if (c.lane == 0) {
+            mbar_arrive_at(&c.m->k_full[at], 0);
+            if (two) mbar_arrive_at(&c.m->k_full[at + 1], 0);
+        }
+        if (rope) ++tile;
     };
-    uint4 x[8], y[8];
-    bool more = advance();
-    int ux = unit, uy = 0;
-    if (more) load(x);
-    while (more) {   // two units a turn: the loads in flight need no copies
-        more = advance();
-        uy = unit;
-        if (more) load(y);
-        put(ux, x);
-        if (!more) break;
-        more = advance();
-        ux = unit;
-        if (more) load(x);
-        put(uy, y);
+    uint4 x[4][4];
+    int u[4];
+    bool more = true;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = -1;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        more = more && advance();
+        if (more) {
+            u[k] = unit;
+            load(x[k]);
+        }
+    }
+    for (;;) {   // four units a turn: the loads in flight need no copies
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (u[k] < 0) return;
+            const int then = (k + 3) & 3;
+            more = more && advance();
+            u[then] = more ? unit : -1;
+            if (more) load(x[then]);
+            put(u[k], x[k]);
+        }
     }
 }
 
@@ -558,19 +570,19 @@ __device__ __forceinline__ float2 column_sum(const float (&s)[32], const float* 
     }
     return sum;
 }
-// The same where causal masking may hide the key from rows (`sees` keys of the token that the column belongs to, as its head
-// `head`; the next token sees one more), or where columns are no rows of the sequence (`left` are).
+// The same over the columns [from, upto) alone.
 template <bool PREP>
-__device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* lse, float f, float2 sum, int key, int H, int& sees, int& head,
-                                             int left) {
+__device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* lse, float f, float2 sum, int from, int upto) {
+    uint32_t see = from <= 0 ? 0xFFFFFFFFu : (from < 32 ? 0xFFFFFFFFu << from : 0u);
+    if (upto < 32) see &= upto <= 0 ? 0u : (1u << upto) - 1u;
+    if (__all_sync(0xFFFFFFFFu, see == 0u)) return sum;
+    if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) return column_sum<PREP>(s, lse, f, sum);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float x = PREP ? fmaf(s[i], lse[2 * i], lse[2 * i + 1]) : fmaf(s[i], f, lse[i]);
-        if (key < sees && i < left) sum.x += exp2_approx(x);
-        if (++head == H) {
-            head = 0;
-            ++sees;
-        }
+    for (int i = 0; i < 32; i += 2) {
+        const float a = exp2_approx(PREP ? fmaf(s[i], lse[2 * i], lse[2 * i + 1]) : fmaf(s[i], f, lse[i]));
+        const float b = exp2_approx(PREP ? fmaf(s[i + 1], lse[2 * i + 2], lse[2 * i + 3]) : fmaf(s[i + 1], f, lse[i + 1]));
+        sum.x += see >> i & 1 ? a : 0.f;
+        sum.y += see >> (i + 1) & 1 ? b : 0.f;
     }
     return sum;
 }
@@ -594,6 +606,7 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
 #pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt) {
             const int key0 = kt * KW_KEYS + int(c.rank) * CKEYS, key = key0 + r;
+            const int old_keys = a.causal ? w.s.K - w.s.L : 0x40000000, own = min(key - old_keys, w.s.L);
             const bool writes = EG == 1 || (w.gb - w.ga == 1 ? (item & 1) == mine : mine == 0);
             float old = 0.f, total = 0.f;
             if (writes && w.whole && past != nullptr && key < w.s.K) old = past[key];
@@ -602,31 +615,29 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
             for (int g = w.ga; g < w.gb; ++g, ++item) {
                 const int h = item & 1, ls = item % LSE_SLOTS;
                 if (EG == 2 && h != mine) continue;
+                // Columns [from, left) are rows that see the key: those of its own token, where it is a new one, and behind.
                 const unsigned first = unsigned(g) * unsigned(rows);
-                const int t0 = int(first / unsigned(a.H)), h0 = int(first % unsigned(a.H));
-                const int sees0 = a.causal ? w.s.K - w.s.L + t0 + 1 : w.s.K, left = int(min(all - first, unsigned(rows)));
-                const bool masked = (a.causal && key0 + CKEYS > sees0) || left < rows;
+                const int left = int(min(all - first, unsigned(rows)));
+                const int from = own <= 0 ? 0 : int(min(int64_t(own) * a.H - first, int64_t(rows)));
+                const bool masked = (key0 + CKEYS - 1 - old_keys) > 0 || left < rows;
                 const float* lse = c.lse + ls * (LSE_SLOT / 4);
                 c.wait(&m->lse_full[ls], (item / LSE_SLOTS) & 1);
                 c.wait(&m->d_full[h], (item >> 1) & 1);
                 tc_fence_after();
                 const uint32_t d = lanes + uint32_t(h) * COL_D;
                 float2 sum = make_float2(0.f, 0.f);
-                int sees = sees0, head = h0;
-                // (a key behind the last is a lane without a meaning; without causal masking every row sees `key`)
-                if (!a.causal) sees = 0x7FFFFFFF - rows;
                 float x[32], y[32];
                 tmem_ld32(d, x);
 #pragma unroll 1
                 for (int q = 0; q < rows; q += 64) {
                     tmem_wait_ld();
                     if (q + 32 < rows) tmem_ld32(d + q + 32, y);
-                    if (masked) sum = masked_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum, key, a.H, sees, head, left - q);
+                    if (masked) sum = masked_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum, from - q, left - q);
                     else sum = column_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum);
                     if (q + 32 >= rows) break;
                     tmem_wait_ld();
                     if (q + 64 < rows) tmem_ld32(d + q + 64, x);
-                    if (masked) sum = masked_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum, key, a.H, sees, head, left - q - 32);
+                    if (masked) sum = masked_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum, from - q - 32, left - q - 32);
                     else sum = column_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum);
                 }
                 tc_fence_before();
