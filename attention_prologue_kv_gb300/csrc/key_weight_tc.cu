@@ -160,6 +160,9 @@ struct Ctx {
         if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0) && ok;
         __syncwarp();
     }
+    __device__ __forceinline__ void wait_alone(uint64_t* bar, uint32_t parity) {   // by one thread of a warp
+        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0) && ok;
+    }
     __device__ __forceinline__ bool gone() const { return __any_sync(0xFFFFFFFFu, !ok); }
     __device__ __forceinline__ uint32_t k_box(int b) const { return base + uint32_t(b) * BOX; }
     __device__ __forceinline__ uint32_t q_slot(int s) const { return base + OFF_Q + uint32_t(s) * uint32_t(p.rows) * 64u; }
@@ -173,15 +176,6 @@ struct Ctx {
     __device__ __forceinline__ int q_boxes() const { return (nb << p.lo_n) + (1 << p.lo_r); }
     // Whether a run's queries stay in the ring for its tiles.
     __device__ __forceinline__ bool stays(const Walk& w) const { return w.kt1 - w.kt0 > 1 && q_boxes() <= p.slots; }
-};
-
-// A place in the queries' ring, and how often it went round.
-struct Ring {
-    int slot = 0;
-    uint32_t turn = 0;
-    __device__ __forceinline__ void next(int slots) {
-        if (++slot == slots) slot = 0, ++turn;
-    }
 };
 
 // A key's row, looked up in two steps: the load of the block table, and what needs it.
@@ -242,40 +236,41 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
     }
 }
 
-// One warp brings the queries, half of a group's rows, box by box in the order of the products. Rows behind the sequence's last
-// one are another's, or none: their columns are left out of the sums.
-__device__ __forceinline__ void query_warp(Ctx& c, const Maps& maps) {
+// One thread brings the queries, half of a group's rows, box by box in the order of the products. Rows behind the sequence's
+// last one are another's, or none: their columns are left out of the sums.
+__device__ __forceinline__ void query_thread(Ctx& c, const Maps& maps) {
     const Tc& p = c.p;
     const MlaParams& a = p.w.m;
-    const int half = p.rows / 2;
+    const int half = p.rows / 2, slots = p.slots;
+    const uint32_t bytes = uint32_t(half) * 128u;
     const int64_t all = a.T * a.H;
-    Ring ring;
+    int slot = 0;
+    uint32_t turn = 0;
     Walk w = c.walk();
     while (w.next()) {
         const int64_t first = a.query_start[w.n] * a.H + int64_t(c.rank) * half;
         const int turns = c.stays(w) ? 1 : w.kt1 - w.kt0;
 #pragma unroll 1
-        for (int turn = 0; turn < turns; ++turn)
+        for (int t = 0; t < turns; ++t)
 #pragma unroll 1
             for (int g = w.ga; g < w.gb; ++g) {
                 const int64_t at = first + int64_t(g) * p.rows;
                 const int row = int(at < all ? at : all);
+                auto box = [&](const CUtensorMap* map, int x) {
+                    if (turn > 0) c.wait_alone(&c.m->q_empty[slot], (turn & 1) ^ 1);
+                    if (!c.ok) return;
+                    mbar_expect_at(&c.m->q_full[slot], 0, bytes);
+                    tma_tile_at(c.q_slot(slot), map, x, row, &c.m->q_full[slot], 0);
+                    if (++slot == slots) slot = 0, ++turn;
+                };
 #pragma unroll 1
-                for (int b = 0; b <= c.nb; ++b) {
-                    const bool rope = b == c.nb;
-#pragma unroll 1
-                    for (int lo = 0; lo <= (rope ? p.lo_r : p.lo_n); ++lo) {
-                        if (ring.turn > 0) c.wait(&c.m->q_empty[ring.slot], (ring.turn & 1) ^ 1);
-                        if (c.gone()) return;
-                        if (c.lane == 0) {
-                            mbar_expect_at(&c.m->q_full[ring.slot], 0, uint32_t(half) * 128u);
-                            tma_tile_at(c.q_slot(ring.slot), rope ? (lo ? &maps.qr_lo : &maps.qr) : (lo ? &maps.qn_lo : &maps.qn),
-                                        rope ? 0 : b * 64, row, &c.m->q_full[ring.slot], 0);
-                        }
-                        __syncwarp();
-                        ring.next(p.slots);
-                    }
+                for (int b = 0; b < c.nb; ++b) {
+                    box(&maps.qn, b * 64);
+                    if (p.lo_n) box(&maps.qn_lo, b * 64);
                 }
+                box(&maps.qr, 0);
+                if (p.lo_r) box(&maps.qr_lo, 0);
+                if (!c.ok) return;
             }
     }
 }
@@ -402,151 +397,148 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
     }
 }
 
-// Eight warps decode a cache of codes, two boxes of a tile at a time (the rotary part for itself), the loads of the next three
-// such units in flight meanwhile.
+// Eight warps decode a cache of codes, a quarter of a tile at a time: two latent boxes, with the last two the rotary one, the
+// loads of the next three quarters in flight meanwhile. The barrier of a quarter's first box stands for all of it. What a
+// warp has to do sets the time of a tile (a scheduler has two of them, and a lone warp goes at about 5 cycles an
+// instruction): quarters are unrolled, a tile's places worked out once. With units found at run time and a barrier a box a
+// tile took 6.6 us.
+constexpr int QUARTERS = 4;
 template <int CK>
 __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
-    const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 16, units = (c.nb + 1) / 2;
+    const int c4 = v & 3, r0 = v >> 2;
     const bool k8 = p.k_kind != OUT16;
-    const int nr = k8 ? p.Dk / 16 : p.Dk / 8;
-    int tile = 0, unit = units;   // (unit `units` is the rotary part)
+    const uint32_t at0 = box_at(c.base, r0, 2 * c4), at1 = box_at(c.base, r0, 2 * c4 + 1);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint32_t pieces = 0;   // of a row that exist: bit b for box b, bits 8 and 9 for the rotary part
+    for (int b = 0; b < 8; ++b) pieces |= uint32_t(b * 4 + c4 < p.Dv / 16) << b;
+    for (int i = 0; i < 2; ++i) pieces |= uint32_t(i * 4 + c4 < p.Dk / (k8 ? 16 : 8)) << (8 + i);
+    int tile = 0;
     Tiles t(c, v);
-    auto advance = [&]() {
-        if (++unit <= units) return true;
-        unit = 0;
-        return t.next();
-    };
-    auto load = [&](uint4 (&x)[4]) {
+    const uint8_t *src[2], *rot[2];
+    uint32_t live[2];   // (of the tile whose loads are on their way)
+    auto next = [&]() {
+        if (!t.next()) return false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t row = t.slot[h];
-            const bool rope = unit == units;
-            const uint8_t* src = rope ? static_cast<const uint8_t*>(p.kc) + row * p.Dk * (k8 ? 1 : 2) : static_cast<const uint8_t*>(p.ckv) + row * p.Dv;
-            const int first = rope ? c4 : unit * 8 + c4, count = rope ? nr : nc;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                x[h * 2 + i] = row >= 0 && first + i * 4 < count ? ld_ahead_v4(src + (first + i * 4) * 16) : make_uint4(0, 0, 0, 0);
+            live[h] = t.slot[h] >= 0 ? pieces : 0u;
+            src[h] = static_cast<const uint8_t*>(p.ckv) + t.slot[h] * p.Dv + c4 * 16;
+            rot[h] = static_cast<const uint8_t*>(p.kc) + t.slot[h] * (p.Dk * (k8 ? 1 : 2)) + c4 * 16;
         }
+        return true;
+    };
+    auto load = [&](int u, uint4 (&x)[4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[h * 2 + i] = live[h] >> (2 * u + i) & 1 ? ld_ahead_v4(src[h] + (2 * u + i) * 64) : none;
+    };
+    uint4 q[QUARTERS][4], rope[4];
+    auto load_rope = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) rope[h * 2 + i] = live[h] >> (8 + i) & 1 ? ld_ahead_v4(rot[h] + i * 64) : none;
     };
     auto put = [&](int u, const uint4 (&x)[4]) {
-        const bool rope = u == units, two = !rope && u * 2 + 1 < c.nb;
-        const int at = rope ? ROPE : u * 2;
-        if (tile > 0) {
-            c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
-            if (two) c.wait(&c.m->k_empty[at + 1], (tile & 1) ^ 1);
-        }
-        const uint32_t box = c.k_box(at);
+        // (the products have had a tile's boxes in order: the last one's barrier stands for all of the quarter)
+        if (tile > 0) c.wait(&c.m->k_empty[u + 1 == QUARTERS ? ROPE : min(2 * u + 1, c.nb - 1)], (tile & 1) ^ 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = r0 + 64 * h;
-            const uint4 y = x[h * 2], z = x[h * 2 + 1];
-            if (!rope) {
-                st_shared_v4(box_at(box, r, 2 * c4), codes_to_halves<CK>(y.x, y.y));
-                st_shared_v4(box_at(box, r, 2 * c4 + 1), codes_to_halves<CK>(y.z, y.w));
-                if (two) {
-                    st_shared_v4(box_at(box + BOX, r, 2 * c4), codes_to_halves<CK>(z.x, z.y));
-                    st_shared_v4(box_at(box + BOX, r, 2 * c4 + 1), codes_to_halves<CK>(z.z, z.w));
+        for (int i = 0; i < 2; ++i)
+            if (2 * u + i < c.nb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t to = uint32_t(2 * u + i) * BOX + uint32_t(h) * (64 * 128);
+                    st_shared_v4(at0 + to, codes_to_halves<CK>(x[h * 2 + i].x, x[h * 2 + i].y));
+                    st_shared_v4(at1 + to, codes_to_halves<CK>(x[h * 2 + i].z, x[h * 2 + i].w));
                 }
-            } else if (k8) {
-                st_shared_v4(box_at(box, r, 2 * c4), dec8x8<F16>(p.k_kind, y.x, y.y));
-                st_shared_v4(box_at(box, r, 2 * c4 + 1), dec8x8<F16>(p.k_kind, y.z, y.w));
-            } else {
-                st_shared_v4(box_at(box, r, c4), y);
-                st_shared_v4(box_at(box, r, c4 + 4), z);
+        if (u + 1 == QUARTERS) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (k8) {
+                    st_shared_v4(at0 + ROPE * BOX + h * (64 * 128), dec8x8<F16>(p.k_kind, rope[h * 2].x, rope[h * 2].y));
+                    st_shared_v4(at1 + ROPE * BOX + h * (64 * 128), dec8x8<F16>(p.k_kind, rope[h * 2].z, rope[h * 2].w));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) st_shared_v4(box_at(c.k_box(ROPE), r0 + 64 * h, c4 + 4 * i), rope[h * 2 + i]);
+                }
             }
         }
-        fence_async_proxy();
-        __syncwarp();
-        if (c.lane == 0) {
-            mbar_arrive_at(&c.m->k_full[at], 0);
-            if (two) mbar_arrive_at(&c.m->k_full[at + 1], 0);
-        }
-        if (rope) ++tile;
+        c.arrive(&c.m->k_full[2 * u]);
     };
-    uint4 x[4][4];
-    int u[4];
-    bool more = true;
+    bool more = next();
+    if (!more) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) u[k] = -1;
+    for (int u = 0; u + 1 < QUARTERS; ++u) load(u, q[u]);
+    for (; more; ++tile) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        more = more && advance();
-        if (more) {
-            u[k] = unit;
-            load(x[k]);
-        }
-    }
-    for (;;) {   // four units a turn: the loads in flight need no copies
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (u[k] < 0) return;
-            const int then = (k + 3) & 3;
-            more = more && advance();
-            u[then] = more ? unit : -1;
-            if (more) load(x[then]);
-            put(u[k], x[k]);
+        for (int u = 0; u < QUARTERS; ++u) {
+            const int then = (u + QUARTERS - 1) % QUARTERS;
+            if (u == 0) load_rope();
+            if (u == 1) more = next();
+            if (u == 0 || more) load(then, q[then]);
+            put(u, q[u]);
         }
     }
 }
 
-// The MMA warp of CTA 0.
+// The MMA warp of CTA 0: one thread goes over the boxes. It has about 250 cycles for each (64 channels of 128 rows), at about 5
+// an instruction: nothing is worked out in the loop that need not be, and no other lane is waited for.
 template <class IT, bool C8>
-__device__ __forceinline__ void mma_warp(Ctx& c) {
+__device__ __forceinline__ void mma_thread(Ctx& c) {
     const Tc& p = c.p;
     Misc* m = c.m;
     const uint32_t id_it = tc_idesc(KW_KEYS, p.rows, is_bf16<IT>, false), id_half = tc_idesc(KW_KEYS, p.rows, false, false);
     const uint32_t id_n = C8 ? id_half : id_it, id_r = p.w.m.k_kind != OUT16 ? id_half : id_it;
-    const bool leader = elect_one();
-    int tile = 0, item = 0;
-    Ring ring;
+    const uint64_t keys = tc_desc(c.base, 16, 1024), queries = tc_desc(c.q_slot(0), 16, 1024);
+    const uint32_t q_step = uint32_t(p.rows) * 64u / 16u;
+    int tile = 0, item = 0, slot = 0, slots = p.slots, nb = c.nb;
+    uint32_t turn = 0;
     Walk w = c.walk();
     while (w.next()) {
         if (w.ga >= w.gb) continue;
         const bool stay = c.stays(w);
-        const Ring first = ring;
+        const int slot0 = slot;
+        const uint32_t turn0 = turn;
 #pragma unroll 1
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++tile) {
-            if (stay) ring = first;
+            if (stay) slot = slot0, turn = turn0;
             const bool fresh = !stay || kt == w.kt0, free = !stay || kt + 1 == w.kt1;   // the queries come, and go
 #pragma unroll 1
             for (int g = w.ga; g < w.gb; ++g, ++item) {
                 const int h = item & 1;
                 const uint32_t d = c.tmem + uint32_t(h) * COL_D;
-                if (item > 1) c.wait(&m->d_free[h], ((item >> 1) & 1) ^ 1);
-#pragma unroll 1
-                for (int b = 0; b <= c.nb; ++b) {
-                    const bool rope = b == c.nb;
-                    const int at = rope ? ROPE : b;
-                    if (g == w.ga) c.wait(&m->k_full[at], tile & 1);
-                    const uint64_t kd = tc_desc(c.k_box(at), 16, 1024);
-#pragma unroll 1
-                    for (int lo = 0; lo <= (rope ? p.lo_r : p.lo_n); ++lo) {
-                        if (fresh) c.wait(&m->q_full[ring.slot], ring.turn & 1);
-                        tc_fence_after();
-                        if (leader) {
-                            const uint64_t qd = tc_desc(c.q_slot(ring.slot), 16, 1024);
+                const bool first = g == w.ga, last = g + 1 == w.gb;
+                if (item > 1) c.wait_alone(&m->d_free[h], ((item >> 1) & 1) ^ 1);
+                auto box = [&](int at, uint32_t id, bool accumulate) {   // one box of queries with the keys' box `at`
+                    if (fresh) c.wait_alone(&m->q_full[slot], turn & 1);
+                    tc_fence_after();
+                    const uint64_t kd = keys + uint32_t(at) * (BOX / 16), qd = queries + uint32_t(slot) * q_step;
+                    tc_mma_pair(d, kd, qd, id, accumulate);
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) tc_mma_pair(d, kd + s * 2, qd + s * 2, rope ? id_r : id_n, b > 0 || lo > 0 || s > 0);
-                            if (free) tc_commit_pair(&m->q_empty[ring.slot]);
-                        }
-                        __syncwarp();
-                        ring.next(p.slots);
-                    }
-                    if (g + 1 == w.gb && leader) tc_commit_pair(&m->k_empty[at]);
-                    __syncwarp();
+                    for (int s = 1; s < 4; ++s) tc_mma_pair(d, kd + s * 2, qd + s * 2, id, true);
+                    if (free) tc_commit_pair(&m->q_empty[slot]);
+                    if (++slot == slots) slot = 0, ++turn;
+                };
+#pragma unroll 1
+                for (int b = 0; b < nb; ++b) {
+                    if (first && (!C8 || b % 2 == 0)) c.wait_alone(&m->k_full[b], tile & 1);   // (codes: a barrier for two boxes)
+                    box(b, id_n, b > 0);
+                    if (C8) box(b, id_n, true);
+                    if (last) tc_commit_pair(&m->k_empty[b]);
                 }
-                if (leader) tc_commit_pair(&m->d_full[h]);
-                __syncwarp();
+                // (codes: the rotary box comes with the last quarter)
+                if (first) c.wait_alone(&m->k_full[C8 ? 2 * (QUARTERS - 1) : ROPE], tile & 1);
+#pragma unroll 1
+                for (int lo = 0; lo <= p.lo_r; ++lo) box(ROPE, id_r, true);
+                if (last) tc_commit_pair(&m->k_empty[ROPE]);
+                tc_commit_pair(&m->d_full[h]);
             }
         }
     }
     if (!c.ok) {   // let what was issued finish before TMEM goes
-        if (leader) {
-            tc_commit_pair(&m->drain);
-            mbar_wait(&m->drain, 0, nullptr);
-        }
-        __syncwarp();
+        tc_commit_pair(&m->drain);
+        mbar_wait(&m->drain, 0, nullptr);
     }
 }
 
@@ -731,9 +723,9 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
         if (prep) sum_warps<true, R::EG>(c, tid, pair);
         else if (!C8) sum_warps<false, R::EG>(c, tid, pair);
     } else if (warp == R::MMA) {
-        if (rank == 0) mma_warp<IT, C8>(c);
+        if (rank == 0 && elect_one()) mma_thread<IT, C8>(c);
     } else if (warp == R::QUERY) {
-        query_warp(c, maps);
+        if (elect_one()) query_thread(c, maps);
     } else if (warp == R::LSE) {
         if (prep) lse_warp<true>(c);
         else if (!C8) lse_warp<false>(c);
