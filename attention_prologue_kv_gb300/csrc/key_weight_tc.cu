@@ -316,19 +316,20 @@ __device__ __forceinline__ void lse_warp(Ctx& c) {
     }
 }
 
-// The tiles of a share as the loading warps go over them: a thread has rows v >> 2 and 64 + v >> 2 of each tile.
+// The tiles of a share as the loading warps go over them: a thread looks up NL rows of each, `step` apart.
+template <int NL>
 struct Tiles {
     const Ctx& c;
     Walk w;
-    int kt = 0, r0;
+    int kt = 0, r0, step;
     bool in = false;
-    Look look[2];
-    int64_t slot[2];
-    __device__ __forceinline__ Tiles(const Ctx& x, int v) : c(x), w(x.walk()), r0(v >> 2) {}
+    Look look[NL];
+    int64_t slot[NL];
+    __device__ __forceinline__ Tiles(const Ctx& x, int first, int apart) : c(x), w(x.walk()), r0(first), step(apart) {}
     __device__ __forceinline__ void begin(int t) {
         const int key = t * KW_KEYS + int(c.rank) * CKEYS + r0;
-        look[0].begin(c.p.w.m, w.n, w.s.K, key);
-        look[1].begin(c.p.w.m, w.n, w.s.K, key + 64);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) look[i].begin(c.p.w.m, w.n, w.s.K, key + i * step);
     }
     __device__ __forceinline__ bool next() {
         if (!in || ++kt >= w.kt1) {
@@ -339,8 +340,8 @@ struct Tiles {
             kt = w.kt0;
             begin(kt);
         }
-        slot[0] = look[0].row(c.p.w.m);
-        slot[1] = look[1].row(c.p.w.m);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) slot[i] = look[i].row(c.p.w.m);
         if (kt + 1 < w.kt1) begin(kt + 1);   // one tile ahead
         return true;
     }
@@ -354,7 +355,7 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
     const int c4 = v & 3, r0 = v >> 2, nc = p.Dv / 8, nr = p.Dk / 8;
     const bool k8 = p.k_kind != OUT16;
     int tile = 0;
-    Tiles t(c, v);
+    Tiles<2> t(c, r0, 64);
     for (; t.next(); ++tile) {
         uint4 codes[2];
         if (k8)
@@ -397,88 +398,112 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
     }
 }
 
-// Eight warps decode a cache of codes, a quarter of a tile at a time: two latent boxes, with the last two the rotary one, the
-// loads of the next three quarters in flight meanwhile. The barrier of a quarter's first box stands for all of it. What a
-// warp has to do sets the time of a tile (a scheduler has two of them, and a lone warp goes at about 5 cycles an
-// instruction): quarters are unrolled, a tile's places worked out once. With units found at run time and a barrier a box a
-// tile took 6.6 us.
-constexpr int QUARTERS = 4;
+// Eight warps decode a cache of codes: two have two of a tile's latent boxes, 64 rows each, a lane 16 pieces of 16 codes. Each
+// half's next loads start as soon as it is stored, so that they have a tile's time. 64 sequences of 8192 keys in int8 take 145
+// to 151 us with 16 heads, 4.5 us a tile, the same from L2 as from DRAM; without any load 85. Tried: all eight warps at each
+// pair of boxes in turn, four arrivals a tile 162; sixteen warps of half the rows 136, but 190 instead of 155 with 128 heads;
+// half of the codes decoded ahead of the wait 189; the next rows prefetched into L2 164; whole lines a load 178.
 template <int CK>
 __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
-    const int c4 = v & 3, r0 = v >> 2;
-    const bool k8 = p.k_kind != OUT16;
-    const uint32_t at0 = box_at(c.base, r0, 2 * c4), at1 = box_at(c.base, r0, 2 * c4 + 1);
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    uint32_t pieces = 0;   // of a row that exist: bit b for box b, bits 8 and 9 for the rotary part
-    for (int b = 0; b < 8; ++b) pieces |= uint32_t(b * 4 + c4 < p.Dv / 16) << b;
-    for (int i = 0; i < 2; ++i) pieces |= uint32_t(i * 4 + c4 < p.Dk / (k8 ? 16 : 8)) << (8 + i);
+    const int lane = c.lane, c4 = lane & 3, r = lane >> 2, u = v >> 6, row0 = (v >> 5 & 1) * 64;
+    if (2 * u >= c.nb) return;
+    const uint32_t box = c.k_box(2 * u) + uint32_t(row0) * 128u, at0 = box_at(box, r, 2 * c4), at1 = box_at(box, r, 2 * c4 + 1);
+    const int first = u * 8 + c4, nc = p.Dv / 16, done = min(2 * u + 1, c.nb - 1);
+    const bool in0 = first < nc, in1 = first + 4 < nc, two = 2 * u + 1 < c.nb;
+    const uint8_t* base = static_cast<const uint8_t*>(p.ckv) + (in0 ? first : 0) * 16;
+    const bool whole = u * 8 + 8 <= nc;   // (the same in all lanes)
     int tile = 0;
-    Tiles t(c, v);
-    const uint8_t *src[2], *rot[2];
-    uint32_t live[2];   // (of the tile whose loads are on their way)
-    auto next = [&]() {
-        if (!t.next()) return false;
+    Tiles<2> t(c, row0 + lane, 32);
+    // Rows half * 32 + 8 k + r. In the place of a key that does not exist, row 0: what it holds spoils that key's sums alone, which
+    // are left out, and a branch a load took 250 cycles each. Channels that do not exist are zeros.
+    auto load = [&](int half, uint4 (&x)[8]) {
+        const uint8_t* src[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            live[h] = t.slot[h] >= 0 ? pieces : 0u;
-            src[h] = static_cast<const uint8_t*>(p.ckv) + t.slot[h] * p.Dv + c4 * 16;
-            rot[h] = static_cast<const uint8_t*>(p.kc) + t.slot[h] * (p.Dk * (k8 ? 1 : 2)) + c4 * 16;
+        for (int k = 0; k < 4; ++k) src[k] = base + max(__shfl_sync(0xFFFFFFFFu, t.slot[half], 8 * k + r), int64_t(0)) * p.Dv;
+        if (whole) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = ld_ahead_v4(src[k]);
+                x[2 * k + 1] = ld_ahead_v4(src[k] + 64);
+            }
+        } else {
+            const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = in0 ? ld_ahead_v4(src[k]) : none;
+                x[2 * k + 1] = in1 ? ld_ahead_v4(src[k] + 64) : none;
+            }
         }
-        return true;
     };
-    auto load = [&](int u, uint4 (&x)[4]) {
+    auto store = [&](int half, const uint4 (&x)[8]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) x[h * 2 + i] = live[h] >> (2 * u + i) & 1 ? ld_ahead_v4(src[h] + (2 * u + i) * 64) : none;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t to = uint32_t(half * 32 + 8 * k) * 128u;
+            st_shared_v4(at0 + to, codes_to_halves<CK>(x[2 * k].x, x[2 * k].y));
+            st_shared_v4(at1 + to, codes_to_halves<CK>(x[2 * k].z, x[2 * k].w));
+            if (two) {
+                st_shared_v4(at0 + to + BOX, codes_to_halves<CK>(x[2 * k + 1].x, x[2 * k + 1].y));
+                st_shared_v4(at1 + to + BOX, codes_to_halves<CK>(x[2 * k + 1].z, x[2 * k + 1].w));
+            }
+        }
     };
-    uint4 q[QUARTERS][4], rope[4];
-    auto load_rope = [&]() {
+    uint4 x[8], y[8];
+    bool more = t.next();
+    if (!more) return;
+    load(0, x);
+    load(1, y);
+    for (; more; ++tile) {
+        // (the products have had a tile's boxes in order)
+        more = t.next();
+        if (tile > 0) c.wait(&c.m->k_empty[done], (tile & 1) ^ 1);
+        store(0, x);
+        if (more) load(0, x);
+        store(1, y);
+        if (more) load(1, y);
+        c.arrive(&c.m->k_full[2 * u]);
+    }
+}
+
+// Beside them, one warp brings the rotary part: 16-bit rows by 16-byte copies, codes decoded.
+__device__ __forceinline__ void rope_warp(Ctx& c) {
+    const MlaParams& p = c.p.w.m;
+    const bool k8 = p.k_kind != OUT16;
+    const int lane = c.lane, per = k8 ? 4 : 8, ch = lane & (per - 1), r = lane / per;   // lanes a row
+    const bool in = ch < p.Dk / (k8 ? 16 : 8);
+    const uint8_t* base = static_cast<const uint8_t*>(p.kc) + ch * 16;
+    const int bytes = p.Dk * (k8 ? 1 : 2);
+    const uint32_t box = c.k_box(ROPE);
+    int tile = 0;
+    Tiles<4> t(c, lane, 32);
+    for (; t.next(); ++tile) {
+        if (tile > 0) c.wait(&c.m->k_empty[ROPE], (tile & 1) ^ 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < 4; ++q) {   // 32 rows
+            if (k8) {
+                uint4 x[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) rope[h * 2 + i] = live[h] >> (8 + i) & 1 ? ld_ahead_v4(rot[h] + i * 64) : none;
-    };
-    auto put = [&](int u, const uint4 (&x)[4]) {
-        // (the products have had a tile's boxes in order: the last one's barrier stands for all of the quarter)
-        if (tile > 0) c.wait(&c.m->k_empty[u + 1 == QUARTERS ? ROPE : min(2 * u + 1, c.nb - 1)], (tile & 1) ^ 1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (2 * u + i < c.nb)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t to = uint32_t(2 * u + i) * BOX + uint32_t(h) * (64 * 128);
-                    st_shared_v4(at0 + to, codes_to_halves<CK>(x[h * 2 + i].x, x[h * 2 + i].y));
-                    st_shared_v4(at1 + to, codes_to_halves<CK>(x[h * 2 + i].z, x[h * 2 + i].w));
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, t.slot[q], 8 * k + r);
+                    x[k] = row >= 0 && in ? ld_ahead_v4(base + row * bytes) : make_uint4(0, 0, 0, 0);
                 }
-        if (u + 1 == QUARTERS) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (k8) {
-                    st_shared_v4(at0 + ROPE * BOX + h * (64 * 128), dec8x8<F16>(p.k_kind, rope[h * 2].x, rope[h * 2].y));
-                    st_shared_v4(at1 + ROPE * BOX + h * (64 * 128), dec8x8<F16>(p.k_kind, rope[h * 2].z, rope[h * 2].w));
-                } else {
+                for (int k = 0; k < 4; ++k) {
+                    st_shared_v4(box_at(box, 32 * q + 8 * k + r, 2 * ch), dec8x8<F16>(p.k_kind, x[k].x, x[k].y));
+                    st_shared_v4(box_at(box, 32 * q + 8 * k + r, 2 * ch + 1), dec8x8<F16>(p.k_kind, x[k].z, x[k].w));
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) st_shared_v4(box_at(c.k_box(ROPE), r0 + 64 * h, c4 + 4 * i), rope[h * 2 + i]);
+                for (int k = 0; k < 8; ++k) {
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, t.slot[q], 4 * k + r);
+                    const bool ok = row >= 0 && in;
+                    cp_async16(box_at(box, 32 * q + 4 * k + r, ch), ok ? base + row * bytes : base, ok);
                 }
             }
         }
-        c.arrive(&c.m->k_full[2 * u]);
-    };
-    bool more = next();
-    if (!more) return;
-#pragma unroll
-    for (int u = 0; u + 1 < QUARTERS; ++u) load(u, q[u]);
-    for (; more; ++tile) {
-#pragma unroll
-        for (int u = 0; u < QUARTERS; ++u) {
-            const int then = (u + QUARTERS - 1) % QUARTERS;
-            if (u == 0) load_rope();
-            if (u == 1) more = next();
-            if (u == 0 || more) load(then, q[then]);
-            put(u, q[u]);
-        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        c.arrive(&c.m->k_full[ROPE]);
     }
 }
 
@@ -527,8 +552,7 @@ __device__ __forceinline__ void mma_thread(Ctx& c) {
                     if (C8) box(b, id_n, true);
                     if (last) tc_commit_pair(&m->k_empty[b]);
                 }
-                // (codes: the rotary box comes with the last quarter)
-                if (first) c.wait_alone(&m->k_full[C8 ? 2 * (QUARTERS - 1) : ROPE], tile & 1);
+                if (first) c.wait_alone(&m->k_full[ROPE], tile & 1);
 #pragma unroll 1
                 for (int lo = 0; lo <= p.lo_r; ++lo) box(ROPE, id_r, true);
                 if (last) tc_commit_pair(&m->k_empty[ROPE]);
@@ -655,12 +679,12 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
     }
 }
 
-// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then MMA, queries, logarithms, and 1 for TMA or 8 that load
-// and decode; at most 16, so that each thread may have 128 registers.
+// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then MMA, queries, logarithms, and 1 for TMA, 8 that copy, or
+// 8 that decode and 1 for the rotary part; at most 16, so that each thread may have 128 registers.
 template <bool TMA>
 struct Roles {
     static constexpr int EG = TMA ? 2 : 1;
-    static constexpr int MMA = 4 * EG, QUERY = MMA + 1, LSE = MMA + 2, LOAD = MMA + 3, LOADERS = TMA ? 1 : 8;
+    static constexpr int MMA = 4 * EG, QUERY = MMA + 1, LSE = MMA + 2, LOAD = MMA + 3, LOADERS = TMA ? 1 : 9;
     static constexpr int THREADS = (LOAD + LOADERS) * 32;
 };
 
@@ -682,7 +706,7 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
     }
     if (tid == 0) {
         for (int b = 0; b < KBOXES; ++b) {
-            mbar_init(&m->k_full[b], 2 * R::LOADERS);
+            mbar_init(&m->k_full[b], TMA ? 2 : (C8 ? (b == ROPE ? 2 : 4) : 16));
             mbar_init(&m->k_empty[b], 1);
         }
         for (int s = 0; s < MAX_SLOTS; ++s) {
@@ -732,9 +756,10 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
     } else if constexpr (TMA) {
         key_warp(c, maps);
     } else if constexpr (C8) {
-        code_warps<CK>(c, tid - R::LOAD * 32);
+        if (warp < R::LOAD + 8) code_warps<CK>(c, tid - R::LOAD * 32);
+        else rope_warp(c);
     } else {
-        copy_warps(c, tid - R::LOAD * 32);
+        if (warp < R::LOAD + 8) copy_warps(c, tid - R::LOAD * 32);
     }
     if (!c.ok) {
         if (p.w.m.status != nullptr) atomicOr(p.w.m.status, KVR_DEVERR_TIMEOUT);
