@@ -33,7 +33,6 @@ struct SelectParams {
     int32_t* status;
     int64_t weight_stride, weight_len, kept_weight_stride, kept_weight_len;
     int N, keep, sink, recent;
-    int share;            // weights of a CTA that shared memory has room for
 };
 
 struct CompactParams {

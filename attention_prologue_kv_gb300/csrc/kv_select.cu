@@ -1,15 +1,16 @@
 // Which keys of a sequence to keep: the `keep` of largest rank, in order of their positions.
 //
-// A weight's rank is its bits, made to order as unsigned numbers (NaN above every number, protected keys above all). The
-// keep-th largest rank t is found digit by digit from the top (11, 11 and 10 bits): count the ranks of each digit among
-// those that agree so far, walk down to the digit that holds the wanted one. Of the keys equal to t the earliest fill up:
-// with G(i), E(i) the keys before i of rank above t and equal to t, key i is kept if it is above t, or equal and E(i) is
-// below what is missing, and its place is G(i) + min(E(i), missing). Counts are whole numbers: the order in which they are
-// added changes nothing.
+// A weight's rank is its bits, made to order as unsigned numbers (NaN above every number). Keys that stay anyway, the first
+// `sink` and the last `recent`, stand above all and are left out of the search. The rank t that divides the others is found
+// between the least and the greatest one by counting: their range is cut into at most 2048 bins, the ranks of each counted,
+// the bin walked down to that holds the wanted one, and so on inside it, until all of a bin is wanted or a bin is one rank.
+// Of the keys equal to t the earliest fill up: with G(i), E(i) the keys before i of rank above t and equal to t, key i stays
+// if it is above t, or equal and E(i) is below what is missing, and its place is G(i) + min(E(i), missing). Counts are whole
+// numbers: the order in which they are added changes nothing.
 //
-// A cluster of CTAs has one sequence, a run of its keys in each CTA's shared memory, so that weights are read once (a
-// share beyond that is read again, from L2). The CTAs read one another's counts: a barrier of the cluster a digit, and one
-// for the keys before a CTA's own.
+// A cluster of CTAs has one sequence, each a run of its keys in registers, so that weights are read once (beyond 16384 keys a
+// CTA they are read anew, from L2). The CTAs read one another's counts: a barrier of the cluster for the range, one a round of
+// counting (two as a rule: bits of floats spread weights by their logarithm) and one for the keys before a CTA's own.
 #include "cache_ops.cuh"
 #include "tcgen05.cuh"
 
@@ -17,187 +18,233 @@ namespace kvr {
 
 namespace {
 
-constexpr int NT = 512, WARPS = NT / 32, BINS = 2048;
+constexpr int NT = 1024, WARPS = NT / 32, BINS = 2048;
 constexpr int MAX_CTAS = 8;
-constexpr int ROOM = 49152;   // weights a CTA's shared memory takes at most
 
 __device__ __forceinline__ uint32_t rank_of(float w) {
     if (w != w) return 0xFFFFFFFEu;
     const uint32_t b = __float_as_uint(w + 0.f);   // -0 becomes 0
     return b >> 31 ? ~b : b | 0x80000000u;
 }
+constexpr uint32_t STAYS = 0xFFFFFFFFu, NONE = 0u;   // (no number's rank)
+
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
     return r;
 }
-// A word at this place in CTA `rank` of the cluster.
-__device__ __forceinline__ int peer_load(const int* at, uint32_t rank) {
-    int v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.b32 %0, [a];\n\t}"
-                 : "=r"(v)
+// Two words at this place in CTA `rank` of the cluster.
+__device__ __forceinline__ int2 peer_load(const int2* at, uint32_t rank) {
+    int2 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.b32 {%0, %1}, [a];\n\t}"
+                 : "=r"(v.x), "=r"(v.y)
                  : "r"(smem_u32(at)), "r"(rank)
                  : "memory");
     return v;
 }
 
 struct Shared {
-    int hist[2][BINS];    // of a digit; the next one's meanwhile
-    int warp_sum[WARPS];
-    int found[2];         // the digit, and what is wanted of it
-    int above[WARPS], equal[WARPS];
-    int total[2];         // this CTA's keys above and equal
+    int2 hist[2][BINS / 2];   // of a round; the next one's meanwhile
+    int2 range, total;        // this CTA's least and greatest rank; its keys above and equal
+    int2 part[WARPS];
+    int sums[WARPS];
+    int found[3];             // the bin, what is wanted of it, what it has
 };
 
+// VPT: keys of a thread, 0: as many as there are, read when they are looked at. Key j of a lane is the warp's first + 32 j + lane.
+template <int VPT>
 __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ SelectParams p) {
-    extern __shared__ float held[];
     __shared__ Shared m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const int n = int(blockIdx.x / size);
-    for (int i = tid; i < BINS; i += NT) m.hist[0][i] = 0;
+    auto sync = [&]() {
+        if (size > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+    m.hist[0][tid] = make_int2(0, 0);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t length = p.key_length[n];
     const bool good = length >= 0 && length <= p.weight_len;
     if (!good && rank == 0 && tid == 0 && p.status != nullptr) atomicOr(p.status, KVR_DEVERR_KEY_LENGTH);
     const int K = good ? int(length) : 0;
-    const float* weight = p.weight + n * p.weight_stride;
-    // This CTA's keys: [first, first + mine).
-    const int share = (K + int(size) - 1) / int(size), first = min(K, int(rank) * share), mine = min(share, K - first);
-    const int cached = min(mine, p.share);
     const bool all = K <= p.keep;
-    for (int i = tid; i < cached; i += NT) held[i] = weight[first + i];
-    auto value = [&](int i) { return i < cached ? held[i] : weight[first + i]; };
-    const int last = K - p.recent;   // (only where K > keep >= recent)
-    auto rank_at = [&](int i) {
-        const int at = first + i;
-        return at < p.sink || at >= last ? 0xFFFFFFFFu : rank_of(value(i));
+    // This CTA's keys are [first, first + mine), this warp's [at, end).
+    const int share = (K + int(size) - 1) / int(size), first = min(K, int(rank) * share), mine = min(share, K - first);
+    const int run = VPT > 0 ? 32 * VPT : ((mine + WARPS - 1) / WARPS + 31) / 32 * 32;
+    const int at = first + min(mine, warp * run), end = min(first + mine, at + run);
+    const float* weight = p.weight + n * p.weight_stride;
+    const int last = K - p.recent;
+    auto rank_at = [&](int i, float w) { return i >= end ? NONE : (all || i < p.sink || i >= last ? STAYS : rank_of(w)); };
+    float value[VPT > 0 ? VPT : 1];
+    uint32_t ranks[VPT > 0 ? VPT : 1];
+    if (VPT > 0) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = at + 32 * j + lane;
+            value[j] = i < end ? weight[i] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) ranks[j] = rank_at(at + 32 * j + lane, value[j]);
+    }
+    // For each of this lane's keys, warp after warp the same number of times.
+    auto each = [&](auto&& f) {
+        if constexpr (VPT > 0) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) f(at + 32 * j + lane, ranks[j], value[j]);
+        } else {
+#pragma unroll 4
+            for (int i = at + lane; i < at + run; i += 32) {
+                const float w = i < end ? weight[i] : 0.f;
+                f(i, rank_at(i, w), w);
+            }
+        }
     };
-    __syncthreads();
-    uint32_t t = 0;
+    uint32_t t = NONE;
     int missing = 0;
     if (!all) {   // (the same in all CTAs of the cluster)
-        int want = p.keep;
-        uint32_t prefix = 0;
+        uint32_t lo = STAYS, hi = NONE;
+        each([&](int, uint32_t r, float) {
+            if (r != NONE && r != STAYS) {
+                lo = min(lo, r);
+                hi = max(hi, r);
+            }
+        });
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+        if (lane == 0) m.part[warp] = make_int2(int(lo), int(hi));
+        __syncthreads();
+        if (warp == 0) {
+            const int2 v = m.part[lane];
+            lo = __reduce_min_sync(0xFFFFFFFFu, uint32_t(v.x));
+            hi = __reduce_max_sync(0xFFFFFFFFu, uint32_t(v.y));
+            if (lane == 0) m.range = make_int2(int(lo), int(hi));
+        }
+        sync();
+        lo = STAYS;
+        hi = NONE;
+        for (uint32_t q = 0; q < size; ++q) {
+            const int2 v = peer_load(&m.range, q);
+            lo = min(lo, uint32_t(v.x));
+            hi = max(hi, uint32_t(v.y));
+        }
+        int want = p.keep - p.sink - p.recent;   // of the others: less than there are
+        t = STAYS - 1;                           // where none is wanted
 #pragma unroll 1
-        for (int digit = 0; digit < 3; ++digit) {
-            const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0), bits = digit == 2 ? 10 : 11, bins = 1 << bits;
-            int* hist = m.hist[digit & 1];
-#pragma unroll 4
-            for (int i = tid; i < mine; i += NT) {
-                const uint32_t r = rank_at(i);
-                if (digit == 0 || r >> (shift + bits) == prefix) atomicAdd(&hist[r >> shift & (bins - 1)], 1);
-            }
-            for (int i = tid; i < BINS; i += NT) m.hist[(digit & 1) ^ 1][i] = 0;
-            cluster_sync_all();
-            // Thread i has the bins 4 i .. 4 i + 3 counted from the top.
-            int c[4], sum = 0;
-            const int top = bins - 1 - 4 * tid;
+        for (int round = 0; want > 0; ++round) {
+            const uint32_t range = hi - lo;
+            const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
+            int* hist = reinterpret_cast<int*>(m.hist[round & 1]);
+            each([&](int, uint32_t r, float) {
+                if (r >= lo && r <= hi) atomicAdd(&hist[(r - lo) >> shift], 1);
+            });
+            sync();
+            // (everyone has read the round before's counts)
+            m.hist[(round & 1) ^ 1][tid] = make_int2(0, 0);
+            // Thread i has the bins 2 i and 2 i + 1 counted from the top, which are the words of one pair.
+            int2 c = make_int2(0, 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                c[k] = 0;
-                if (top - k >= 0)
-                    for (uint32_t q = 0; q < size; ++q) c[k] += peer_load(&hist[top - k], q);
-                sum += c[k];
-            }
+            for (uint32_t q = 0; q < MAX_CTAS; ++q)
+                if (q < size) {
+                    const int2 v = peer_load(&m.hist[round & 1][BINS / 2 - 1 - tid], q);
+                    c.x += v.y;
+                    c.y += v.x;
+                }
+            const int sum = c.x + c.y;
             int scan = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
                 if (lane >= o) scan += v;
             }
-            if (lane == 31) m.warp_sum[warp] = scan;
+            if (lane == 31) m.sums[warp] = scan;
             __syncthreads();
-            int before = scan - sum;
-            for (int q = 0; q < warp; ++q) before += m.warp_sum[q];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (before < want && want <= before + c[k]) {
-                    m.found[0] = top - k;
-                    m.found[1] = want - before;
-                }
-                before += c[k];
+            int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? m.sums[lane] : 0) + scan - sum;
+            if (before < want && want <= before + sum) {
+                const bool second = want > before + c.x;
+                m.found[0] = BINS - 1 - 2 * tid - (second ? 1 : 0);
+                m.found[1] = want - before - (second ? c.x : 0);
+                m.found[2] = second ? c.y : c.x;
             }
             __syncthreads();
-            prefix = prefix << bits | uint32_t(m.found[0]);
+            lo += uint32_t(m.found[0]) << shift;
+            hi = min(hi, lo + ((1u << shift) - 1));
             want = m.found[1];
-            // (the next digit's counts go to the other array, which the CTAs have cleared behind the barrier above)
-            cluster_sync_all();
+            if (want == m.found[2]) {   // all of it
+                t = lo - 1;
+                break;
+            }
+            if (shift == 0) {
+                t = lo;
+                missing = want;
+                break;
+            }
         }
-        t = prefix;
-        missing = want;
     }
     // Keys above and equal in each warp's run.
-    const int run = ((mine + WARPS - 1) / WARPS + 31) / 32 * 32, r0 = min(mine, warp * run), r1 = min(mine, r0 + run);
     int above = 0, equal = 0;
-    for (int i = r0; i < r1; i += 32) {
-        const uint32_t r = i + lane < r1 ? (all ? 1u : rank_at(i + lane)) : 0u;
-        above += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < r1 && r > t));
-        equal += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < r1 && r == t));
-    }
-    if (lane == 0) {
-        m.above[warp] = above;
-        m.equal[warp] = equal;
-    }
+    each([&](int, uint32_t r, float) {
+        above += r > t;
+        equal += r == t && r != NONE;
+    });
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+    if (lane == 0) m.part[warp] = make_int2(above, equal);
     __syncthreads();
-    if (tid == 0) {
-        int a = 0, e = 0;
-        for (int q = 0; q < WARPS; ++q) {
-            a += m.above[q];
-            e += m.equal[q];
+    const int2 of = m.part[lane];
+    int G = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of.x : 0), E = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of.y : 0);
+    if (warp == WARPS - 1 && lane == 0) m.total = make_int2(G + above, E + equal);
+    if (size > 1) {
+        cluster_sync_all();
+        for (uint32_t q = 0; q < rank; ++q) {
+            const int2 v = peer_load(&m.total, q);
+            G += v.x;
+            E += v.y;
         }
-        m.total[0] = a;
-        m.total[1] = e;
+        cluster_arrive();   // a CTA stays until the others have its counts
     }
-    cluster_sync_all();
-    int G = 0, E = 0;
-    for (uint32_t q = 0; q < rank; ++q) {
-        G += peer_load(&m.total[0], q);
-        E += peer_load(&m.total[1], q);
-    }
-    for (int q = 0; q < warp; ++q) {
-        G += m.above[q];
-        E += m.equal[q];
-    }
-    cluster_arrive();   // a CTA stays until the others have its counts
     int64_t* kept = p.kept + int64_t(n) * p.keep;
     float* carried = p.kept_weight == nullptr ? nullptr : p.kept_weight + n * p.kept_weight_stride;
     const uint32_t below = (1u << lane) - 1;
-    for (int i = r0; i < r1; i += 32) {
-        const bool in = i + lane < r1;
-        const uint32_t r = in ? (all ? 1u : rank_at(i + lane)) : 0u;
-        const uint32_t up = __ballot_sync(0xFFFFFFFFu, in && r > t), same = __ballot_sync(0xFFFFFFFFu, in && r == t);
+    each([&](int i, uint32_t r, float w) {
+        const uint32_t up = __ballot_sync(0xFFFFFFFFu, r > t), same = __ballot_sync(0xFFFFFFFFu, r == t && r != NONE);
         const int e = E + __popc(same & below);
-        if (in && (r > t || (r == t && e < missing))) {
-            const int at = G + __popc(up & below) + min(e, missing);
-            kept[at] = first + i + lane;
-            if (carried != nullptr) carried[at] = value(i + lane);
+        if (r > t || (same >> lane & 1 && e < missing)) {
+            const int to = G + __popc(up & below) + min(e, missing);
+            kept[to] = i;
+            if (carried != nullptr) carried[to] = w;
         }
         G += __popc(up);
         E += __popc(same);
-    }
+    });
     const int count = all ? K : p.keep;
     const int64_t step = int64_t(size) * NT, begin = count + int64_t(rank) * NT + tid;
     for (int64_t i = begin; i < p.keep; i += step) kept[i] = -1;
     if (carried != nullptr)
         for (int64_t i = begin; i < p.kept_weight_len; i += step) carried[i] = 0.f;
     if (rank == 0 && tid == 0) p.kept_length[n] = count;
-    cluster_wait();
+    if (size > 1) cluster_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_select(SelectParams p, cudaStream_t s) {
+    // CTAs of a sequence: as many as the registers need, and while the SMs are not filled and a CTA has 4096 keys or more.
     int ctas = 1;
-    while (ctas < MAX_CTAS && p.weight_len > int64_t(ctas) * 2048 && int64_t(p.N) * ctas * 2 <= 2 * sm_count_current_device()) ctas *= 2;
-    while (ctas < MAX_CTAS && p.weight_len > int64_t(ctas) * ROOM) ctas *= 2;
-    const int64_t share = (p.weight_len + ctas - 1) / ctas;
-    p.share = int(share < ROOM ? share : ROOM);
+    while (ctas < MAX_CTAS && (p.weight_len > int64_t(ctas) * NT * 16 ||
+                               (p.weight_len >= int64_t(ctas) * 4096 && int64_t(p.N) * ctas * 2 <= sm_count_current_device())))
+        ctas *= 2;
+    const int64_t each = (p.weight_len + ctas - 1) / ctas;
+    void (*kernel)(SelectParams) = each <= NT       ? kv_select_kernel<1>
+                                   : each <= NT * 2 ? kv_select_kernel<2>
+                                   : each <= NT * 4 ? kv_select_kernel<4>
+                                   : each <= NT * 8 ? kv_select_kernel<8>
+                                   : each <= NT * 16 ? kv_select_kernel<16>
+                                                     : kv_select_kernel<0>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.N) * unsigned(ctas));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = size_t(p.share) * sizeof(float);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -207,12 +254,7 @@ cudaError_t launch_select(SelectParams p, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cfg.dynamicSmemBytes + sizeof(Shared) > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_select_kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, ROOM * int(sizeof(float)));
-        if (e != cudaSuccess) return e;
-    }
-    return cudaLaunchKernelEx(&cfg, kv_select_kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace kvr

@@ -854,7 +854,7 @@ kvr_status kv_cache_select(const kvr_select_args* a, cudaStream_t stream) {
     }
     const SelectParams p = {a->weight, a->key_length, a->kept, a->kept_length, a->kept_weight, a->dev_status, a->weight_stride,
                             a->weight_len, a->kept_weight_stride, a->kept_weight_len, int(a->N), int(a->keep), int(a->sink),
-                            int(a->recent), 0};
+                            int(a->recent)};
     (void)cudaGetLastError();
     return cuda_status(launch_select(p, stream));
 }
