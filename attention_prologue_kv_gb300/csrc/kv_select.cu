@@ -2,13 +2,13 @@
 //
 // A weight's rank is its bits, made to order as unsigned numbers (NaN above every number). Keys that stay anyway, the first
 // `sink` and the last `recent`, stand above all and are left out of the search. The rank t that divides the others is found
-// between the least and the greatest one by counting: their range is cut into at most 2048 bins, the ranks of each counted,
+// between the least and the greatest one by counting: their range is cut into at most 1024 bins, the ranks of each counted,
 // the bin walked down to that holds the wanted one, and so on inside it, until all of a bin is wanted or a bin is one rank.
 // Of the keys equal to t the earliest fill up: with G(i), E(i) the keys before i of rank above t and equal to t, key i stays
 // if it is above t, or equal and E(i) is below what is missing, and its place is G(i) + min(E(i), missing). Counts are whole
 // numbers: the order in which they are added changes nothing.
 //
-// A cluster of CTAs has one sequence, each a run of its keys in registers, so that weights are read once (beyond 16384 keys a
+// A cluster of CTAs has one sequence, each a run of its keys in registers, so that weights are read once (beyond 32768 keys a
 // CTA they are read anew, from L2). The CTAs read one another's counts: a barrier of the cluster for the range, one a round of
 // counting (two as a rule: bits of floats spread weights by their logarithm) and one for the keys before a CTA's own.
 #include "cache_ops.cuh"
@@ -18,8 +18,9 @@ namespace kvr {
 
 namespace {
 
-constexpr int NT = 1024, WARPS = NT / 32, BINS = 2048;
-constexpr int MAX_CTAS = 8;
+// Bins: one a thread. With 2048, which all CTAs read of one another too, 131000 keys took 19.8 us instead of 15.9.
+constexpr int NT = 1024, WARPS = NT / 32, BINS = NT;
+constexpr int MAX_CTAS = 16;   // beyond 8, where the device has to be asked, for what 8 have no registers for
 
 __device__ __forceinline__ uint32_t rank_of(float w) {
     if (w != w) return 0xFFFFFFFEu;
@@ -33,7 +34,15 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
     return r;
 }
-// Two words at this place in CTA `rank` of the cluster.
+// What is at this place in CTA `rank` of the cluster.
+__device__ __forceinline__ int peer_load(const int* at, uint32_t rank) {
+    int v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.b32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(smem_u32(at)), "r"(rank)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ int2 peer_load(const int2* at, uint32_t rank) {
     int2 v;
     asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.b32 {%0, %1}, [a];\n\t}"
@@ -44,7 +53,7 @@ __device__ __forceinline__ int2 peer_load(const int2* at, uint32_t rank) {
 }
 
 struct Shared {
-    int2 hist[2][BINS / 2];   // of a round; the next one's meanwhile
+    int hist[2][BINS];   // of a round; the next one's meanwhile
     int2 range, total;        // this CTA's least and greatest rank; its keys above and equal
     int2 part[WARPS];
     int sums[WARPS];
@@ -62,7 +71,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         if (size > 1) cluster_sync_all();
         else __syncthreads();
     };
-    m.hist[0][tid] = make_int2(0, 0);
+    m.hist[0][tid] = 0;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t length = p.key_length[n];
@@ -77,6 +86,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
     const float* weight = p.weight + n * p.weight_stride;
     const int last = K - p.recent;
     auto rank_at = [&](int i, float w) { return i >= end ? NONE : (all || i < p.sink || i >= last ? STAYS : rank_of(w)); };
+    constexpr bool HOLDS = VPT <= 16;   // the weights too; else those that stay are read again
     float value[VPT > 0 ? VPT : 1];
     uint32_t ranks[VPT > 0 ? VPT : 1];
     if (VPT > 0) {
@@ -92,7 +102,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
     auto each = [&](auto&& f) {
         if constexpr (VPT > 0) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) f(at + 32 * j + lane, ranks[j], value[j]);
+            for (int j = 0; j < VPT; ++j) f(at + 32 * j + lane, ranks[j], HOLDS ? value[j] : 0.f);
         } else {
 #pragma unroll 4
             for (int i = at + lane; i < at + run; i += 32) {
@@ -134,24 +144,19 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
 #pragma unroll 1
         for (int round = 0; want > 0; ++round) {
             const uint32_t range = hi - lo;
-            const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
-            int* hist = reinterpret_cast<int*>(m.hist[round & 1]);
+            const int bits = 32 - __clz(range), shift = bits > 10 ? bits - 10 : 0;
+            int* hist = m.hist[round & 1];
             each([&](int, uint32_t r, float) {
                 if (r >= lo && r <= hi) atomicAdd(&hist[(r - lo) >> shift], 1);
             });
             sync();
             // (everyone has read the round before's counts)
-            m.hist[(round & 1) ^ 1][tid] = make_int2(0, 0);
-            // Thread i has the bins 2 i and 2 i + 1 counted from the top, which are the words of one pair.
-            int2 c = make_int2(0, 0);
+            m.hist[(round & 1) ^ 1][tid] = 0;
+            // Thread i has the i-th bin from the top.
+            int sum = 0;
 #pragma unroll
             for (uint32_t q = 0; q < MAX_CTAS; ++q)
-                if (q < size) {
-                    const int2 v = peer_load(&m.hist[round & 1][BINS / 2 - 1 - tid], q);
-                    c.x += v.y;
-                    c.y += v.x;
-                }
-            const int sum = c.x + c.y;
+                if (q < size) sum += peer_load(&m.hist[round & 1][BINS - 1 - tid], q);
             int scan = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -162,10 +167,9 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
             __syncthreads();
             int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? m.sums[lane] : 0) + scan - sum;
             if (before < want && want <= before + sum) {
-                const bool second = want > before + c.x;
-                m.found[0] = BINS - 1 - 2 * tid - (second ? 1 : 0);
-                m.found[1] = want - before - (second ? c.x : 0);
-                m.found[2] = second ? c.y : c.x;
+                m.found[0] = BINS - 1 - tid;
+                m.found[1] = want - before;
+                m.found[2] = sum;
             }
             __syncthreads();
             lo += uint32_t(m.found[0]) << shift;
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         if (r > t || (same >> lane & 1 && e < missing)) {
             const int to = G + __popc(up & below) + min(e, missing);
             kept[to] = i;
-            if (carried != nullptr) carried[to] = w;
+            if (carried != nullptr) carried[to] = HOLDS ? w : weight[i];
         }
         G += __popc(up);
         E += __popc(same);
@@ -230,10 +234,11 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
 }  // namespace
 
 cudaError_t launch_select(SelectParams p, cudaStream_t s) {
-    // CTAs of a sequence: as many as the registers need, and while the SMs are not filled and a CTA has 4096 keys or more.
+    // CTAs of a sequence: as many as the registers need, and up to 8 while the SMs are not filled and a CTA has 4096 keys or more.
+    // (Of one sequence of 131000 keys 8 take 15.9 us and 16 more, whose counts every CTA reads; of 500000 keys 85 and 51.)
     int ctas = 1;
     while (ctas < MAX_CTAS && (p.weight_len > int64_t(ctas) * NT * 16 ||
-                               (p.weight_len >= int64_t(ctas) * 4096 && int64_t(p.N) * ctas * 2 <= sm_count_current_device())))
+                               (ctas < 8 && p.weight_len >= int64_t(ctas) * 4096 && int64_t(p.N) * ctas * 2 <= sm_count_current_device())))
         ctas *= 2;
     const int64_t each = (p.weight_len + ctas - 1) / ctas;
     void (*kernel)(SelectParams) = each <= NT       ? kv_select_kernel<1>
@@ -241,7 +246,12 @@ cudaError_t launch_select(SelectParams p, cudaStream_t s) {
                                    : each <= NT * 4 ? kv_select_kernel<4>
                                    : each <= NT * 8 ? kv_select_kernel<8>
                                    : each <= NT * 16 ? kv_select_kernel<16>
+                                   : each <= NT * 32 ? kv_select_kernel<32>
                                                      : kv_select_kernel<0>;
+    if (ctas > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.N) * unsigned(ctas));
     cfg.blockDim = dim3(NT);
