@@ -13,9 +13,6 @@
 namespace kvr {
 
 constexpr int KW_KEYS = 256;    // keys of a tile
-// What a tile costs beside its groups, in groups: bringing its keys.
-constexpr double KW_TILE_COST = 1.0;
-
 struct KwPos {
     int n, kt, g;   // sequence, tile, group
     int cut;        // whether groups of the tile come before it
@@ -35,25 +32,26 @@ struct KwShape {
         return token <= 0 ? 0 : int(token * H / rows);
     }
     KVR_HD bool even() const { return !causal || groups() == 1; }
-    // Cost of the first x tiles, which grows by KW_TILE_COST at least from tile to tile: where tiles lie behind the first
-    // token's keys, fewer and fewer groups see them.
-    KVR_HD double cost(int x) const {
-        const double all = x * (groups() + KW_TILE_COST);
+    // Cost of the first x tiles, in groups; a tile costs one more, for bringing its keys, so that this grows by one at least
+    // from tile to tile. Where tiles lie behind the first token's keys, fewer and fewer groups see them. (Whole numbers: an
+    // SM has few units for doubles, and a call's first microseconds count.)
+    KVR_HD int64_t cost(int x) const {
+        const int64_t all = int64_t(x) * (groups() + 1);
         if (even()) return all;
         const double y = x - 1 - (double(K) - L) / KW_KEYS;
-        return y <= 0 ? all : all - 0.5 * y * y * (double(KW_KEYS) * H / rows);
+        return y <= 0 ? all : all - int64_t(0.5 * y * y * (double(KW_KEYS) * H / rows));
     }
-    KVR_HD double cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }
+    KVR_HD int64_t cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }
     // Where the share that begins at `off` of the sequence's cost begins. Grows with `off`: shares neither overlap nor leave gaps.
-    KVR_HD KwPos locate(int n, double off) const {
+    KVR_HD KwPos locate(int n, int64_t off) const {
         const int G = groups(), T = tiles();
-        if (G == 1) {   // whole tiles
-            const double x = off / (1 + KW_TILE_COST) + 0.5;
+        if (G == 1) {   // whole tiles, of cost 2
+            const int64_t x = (off + 1) / 2;
             return {n, x < T ? int(x) : T, 0, 0};
         }
         int lo = 0, hi = T - 1;
         if (even()) {
-            const double x = off / (G + KW_TILE_COST);
+            const int64_t x = off >> 31 == 0 ? int64_t(unsigned(off) / unsigned(G + 1)) : off / (G + 1);
             lo = x < T ? int(x) : T - 1;
         } else {
             while (lo < hi) {
@@ -62,22 +60,27 @@ struct KwShape {
                 else hi = mid - 1;
             }
         }
-        const double c0 = cost(lo), c1 = cost(lo + 1);
+        const int64_t c0 = cost(lo), c1 = cost(lo + 1);
         const int g0 = first_group(lo), count = G - g0;
-        const double f = (off - c0) / (c1 - c0) * count + 0.5;
-        const int g = f < 0 ? 0 : (f < count ? int(f) : count);
+        const float f = float(off - c0) / float(c1 - c0) * float(count) + 0.5f;
+        const int g = f < 0 ? 0 : (f < float(count) ? int(f) : count);
         return {n, lo, g0 + g, g > 0};
     }
 };
+
+// Where share `which` of `active` begins.
+KVR_HD int64_t kw_share(int64_t total, int which, int active) {
+    if (which >= active) return total;
+    if (total < (int64_t(1) << 31) / 256) return unsigned(total) * unsigned(which) / unsigned(active);
+    const int64_t each = total / active;
+    return each * which + (total - each * active) * which / active;
+}
 
 KVR_HD bool kw_same_tile(const KwPos& a, const KwPos& b) { return a.n == b.n && a.kt == b.kt; }
 KVR_HD bool kw_same(const KwPos& a, const KwPos& b) { return kw_same_tile(a, b) && a.g == b.g; }
 
 // CTA pairs that get work: none less than a tile of one group.
-KVR_HD int kw_active(double total, int pairs) {
-    const double most = total / (1 + KW_TILE_COST);
-    return most < 1 ? 1 : (most < pairs ? int(most) : pairs);
-}
+KVR_HD int kw_active(int64_t total, int pairs) { return total < 2 ? 1 : (total / 2 < pairs ? int(total / 2) : pairs); }
 
 // The runs of a share: some tiles of a sequence with one group, or the groups [ga, gb) of one tile.
 template <class Shapes>

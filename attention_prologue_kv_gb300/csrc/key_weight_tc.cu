@@ -45,7 +45,7 @@ struct alignas(16) Misc {
     uint32_t tmem;
     int abort;
     KwPos begin, end;
-    double wsum[32];
+    int64_t wsum[32];
     float other[2][CKEYS];   // sums of the second half of the sum warps
 };
 constexpr uint32_t SMEM = OFF_MISC + uint32_t(sizeof(Misc));
@@ -80,8 +80,8 @@ __device__ __forceinline__ Space ws_space(const Tc& p) {
 
 struct Shapes {
     const Tc& p;
-    __device__ __forceinline__ KwShape operator()(int n) const {
-        const Seq s = load_seq(p.w.m, n);
+    __device__ __forceinline__ KwShape operator()(int n, int* bits = nullptr) const {
+        const Seq s = load_seq(p.w.m, n, bits);
         return {s.L, s.K, p.w.m.H, p.rows, p.w.m.causal != 0};
     }
 };
@@ -94,52 +94,45 @@ __device__ void schedule(const Tc& p, Misc* m, int pair) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = int(p.w.m.N);
     const int per = (N - 1) / THREADS + 1, n0 = min(int64_t(tid) * per, int64_t(N)), n1 = min(int64_t(n0) + per, int64_t(N));
     const Shapes shapes{p};
-    double sum = 0;
+    int64_t sum = 0;
     int bits = 0;
+    KwShape s = {0, 0, 1, 32, false};
     for (int n = n0; n < n1; ++n) {
-        (void)load_seq(p.w.m, n, &bits);
-        sum += shapes(n).cost();
+        s = shapes(n, &bits);
+        sum += s.cost();
     }
     if (bits != 0 && blockIdx.x == 0 && p.w.m.status != nullptr) atomicOr(p.w.m.status, bits);
-    double scan = sum;
+    int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += v;
     }
     if (lane == 31) m->wsum[warp] = scan;
     if (tid == 0) m->begin = m->end = {N, 0, 0, 0};
     __syncthreads();
-    double before = 0, total = 0;
+    int64_t before = 0, total = 0;
+#pragma unroll
     for (int q = 0; q < WARPS; ++q) {
-        if (q == warp) before = total;
-        total += m->wsum[q];
+        const int64_t v = m->wsum[q];
+        if (q < warp) before += v;
+        total += v;
     }
-    // (a thread's sequences begin where its predecessor's end, to the bit: both are the same sum)
-    double base = __shfl_up_sync(0xFFFFFFFFu, scan, 1);
-    base = before + (lane == 0 ? 0 : base);
-    const double upto = before + scan;
+    const int64_t upto = before + scan, base = upto - sum;
     const int active = kw_active(total, p.pairs);
-    const double u[2] = {pair >= active ? total : total * pair / active, pair + 1 >= active ? total : total * (pair + 1) / active};
-    if ((u[0] >= base && u[0] < upto) || (u[1] >= base && u[1] < upto)) {
-        double at[2] = {u[0] - base, u[1] - base};
-        bool found[2] = {!(u[0] >= base && u[0] < upto), !(u[1] >= base && u[1] < upto)};
-        for (int n = n0; n < n1; ++n) {
-            const KwShape s = shapes(n);
-            const double c = s.cost();
-            for (int h = 0; h < 2; ++h) {
-                if (found[h]) continue;
-                // (the last one with work takes what rounding leaves over)
-                if (c > 0 && (at[h] < c || n + 1 == n1)) {
-                    (h ? m->end : m->begin) = s.locate(n, at[h]);
-                    found[h] = true;
-                } else {
-                    at[h] -= c;
-                }
+    for (int h = 0; h < 2; ++h) {
+        int64_t at = kw_share(total, pair + h, active);
+        if (at < base || at >= upto) continue;
+        at -= base;
+        for (int n = n0;; ++n) {   // (one of them holds it)
+            if (per > 1) s = shapes(n);
+            const int64_t c = s.cost();
+            if (at < c) {
+                (h ? m->end : m->begin) = s.locate(n, at);
+                break;
             }
+            at -= c;
         }
-        for (int h = 0; h < 2; ++h)
-            if (!found[h]) (h ? m->end : m->begin) = {n1, 0, 0, 0};
     }
     if (tid == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
 }
@@ -945,6 +938,12 @@ bool encode_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int 
 }
 
 }  // namespace
+
+bool key_weight_tc_fits(const KeyWeightParams& w) {
+    // cost() of one sequence is at most tiles * (groups + 1), and N of them, which may share rows, are added up.
+    const MlaParams& p = w.m;
+    return ((p.T * p.H + 31) / 32 + 1) * ((p.max_keys + KW_KEYS - 1) / KW_KEYS + 1) <= (int64_t(1) << 62) / p.N;
+}
 
 int64_t key_weight_tc_workspace(const KeyWeightParams& w) {
     const MlaParams& p = w.m;

@@ -739,6 +739,7 @@ kvr_status key_weight_plan(const kvr_key_weight_args* a, KeyWeightParams* p, boo
     if (st != KVR_OK || *empty) return st;
     if (a->weight == nullptr && a->weight_len > 0) return KVR_ERR_NULL;
     p->m.max_keys = std::min(p->m.max_keys, a->weight_len);
+    if (key_weight_tensor_cores(&s) && !key_weight_tc_fits(*p)) return KVR_ERR_SHAPE;
     p->weight = a->weight;
     p->past = a->past;
     p->weight_stride = a->weight_stride;

@@ -713,14 +713,16 @@ kvr_status mla_tree_attention(const kvr_mla_tree_args* args, cudaStream_t stream
  *                does not overlap it, or NULL: nothing is read.
  *   decay        factor of past.
  *
- * Limits are those of mla_attention (without its limit on work), weight_len >= 0,
- * strides >= weight_len; `weight` must not overlap an input, the workspace or
- * dev_status. Rows of at most 512 + 64 channels, both multiples of 8 (of 16 in an
- * 8-bit cache), on 16-byte boundaries (q and the caches; strides multiples of 8)
- * and with H <= 65536 run on the tensor cores, all others on a plain kernel that
- * is much slower. Scores and sums are float32; keys within key_length are taken
- * to be finite, but a key that is not changes no weight but its own. The result
- * of a call does not change from run to run on one GPU.
+ * Limits are those of mla_attention, weight_len >= 0, strides >= weight_len;
+ * `weight` must not overlap an input, the workspace or dev_status. Rows of at
+ * most 512 + 64 channels, both multiples of 8 (of 16 in an 8-bit cache), on
+ * 16-byte boundaries (q and the caches; strides multiples of 8) and with H <=
+ * 65536 run on the tensor cores, all others on a plain kernel that is much
+ * slower; the limit on work is there (T * H / 32 + 2) * (keys / 256 + 2) * N <
+ * 2^62. Scores and sums are float32. A query for a cache of codes is divided by
+ * the scales and held in 22 bits there. Keys within key_length need not be
+ * finite: one that is not changes no weight but its own. The result of a call
+ * does not change from run to run on one GPU.
  */
 typedef struct kvr_key_weight_args {
     kvr_mla_args step;

@@ -99,6 +99,17 @@ def test_key_weight_refusals(lib, step_kw, kw, want):
     assert lib.mla_key_weight(ctypes.byref(weight(step_kw, **kw)), None) == want
 
 
+def test_key_weight_refuses_work_that_64_bits_cannot_count(lib):
+    kw = dict(T=1 << 30, H=1, q_nope_token_stride=512, q_rope_token_stride=64, q_nope_head_stride=512, q_rope_head_stride=64, mode=1,
+              cache_d0=1, cache_d1=1 << 24, max_blocks=1, q_nope=0, workspace=0)
+    far = dict(q_nope=1 << 50, q_rope=1 << 51, query_start=1 << 52, key_length=3 << 51, block_table=1 << 53, ckv_cache=3 << 52,
+               k_cache=1 << 54, lse=3 << 53)
+    out = dict(weight=1 << 55, weight_len=1 << 24, weight_stride=1 << 24, past=0)
+    # (2^30 / 32 + 1) * (2^16 + 1) * N against 2^62: N = 2^21 is too many, 2^21 - 2^16 would be launched, had it a workspace
+    for n, want in ((1 << 21, N.KVR_ERR_SHAPE), ((1 << 21) - (1 << 16), N.KVR_ERR_NULL)):
+        assert lib.mla_key_weight(ctypes.byref(weight(dict(kw, N=n, **far), **out)), None) == want
+
+
 def select(**kw):
     a = dict(weight=M, weight_stride=100, weight_len=100, N=3, key_length=2 * M, keep=20, sink=2, recent=5, kept=3 * M,
              kept_length=4 * M, kept_weight=5 * M, kept_weight_stride=20, kept_weight_len=20)
