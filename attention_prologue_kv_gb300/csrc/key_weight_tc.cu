@@ -147,14 +147,14 @@ struct Ctx {
     volatile int* abort;
     bool ok;
 
-    // As in the attention kernel: a wait that gives up poisons the CTA; the warps that start TMA copies then stop, the others run
+    // As in the attention kernel: a wait that gives up poisons the CTA; the roles that start TMA copies then stop, the others run
     // their loops to the end without waiting.
-    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
-        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0) && ok;
-        __syncwarp();
-    }
     __device__ __forceinline__ void wait_alone(uint64_t* bar, uint32_t parity) {   // by one thread of a warp
-        if (!mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0) && ok;
+        if (ok && !mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0);
+    }
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+        wait_alone(bar, parity);
+        __syncwarp();
     }
     __device__ __forceinline__ bool gone() const { return __any_sync(0xFFFFFFFFu, !ok); }
     __device__ __forceinline__ uint32_t k_box(int b) const { return base + uint32_t(b) * BOX; }

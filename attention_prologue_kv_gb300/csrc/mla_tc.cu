@@ -923,8 +923,9 @@ __device__ __forceinline__ float reference(float mx) {
     return mx - r <= LIFT<PT> ? r : mx;   // (infinities stay)
 }
 
-// Softmax: thread (row r, half h of the keys, group g: half of that half).
-template <class IT, bool C8, bool K8>
+// Softmax: thread (row r, half h of the keys, group g: half of that half). TREE: the new tokens see one another by words; a loop of
+// its own, as the look at them cost the other calls 1% (with codes 3%).
+template <class IT, bool C8, bool K8, bool TREE>
 __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
     using PT = typename std::conditional<C8, F16, IT>::type;   // type of the weights and the decoded codes
     constexpr int G = groups_of<C8>(), NK = CKEYS / G;          // keys of a thread
@@ -944,8 +945,8 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         const unsigned row = unsigned(w.i) * ROWS + c.rank * CROWS + r;
         const bool live = row < unsigned(w.s.L) * unsigned(p.H);
         const int vis = live ? seen(p, w.s.L, w.s.K, int(row / unsigned(p.H))) : 0;
-        const int64_t* tree = p.tree == nullptr || !live ? nullptr : p.tree + (w.s.q0 + row / unsigned(p.H)) * p.words;
-        int wmin = live ? (tree != nullptr ? w.s.K - w.s.L : vis) : 0x7FFFFFFF;
+        const int64_t* tree = TREE && live ? p.tree + (w.s.q0 + row / unsigned(p.H)) * p.words : nullptr;
+        int wmin = live ? (TREE ? w.s.K - w.s.L : vis) : 0x7FFFFFFF;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
         if (C8) {
@@ -957,8 +958,8 @@ __device__ __forceinline__ void softmax_warps(Ctx& c, int tid, int pair) {
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++j) {
             const int key0 = kt * KEYS + h * CKEYS + g * NK;
             float* red = m->red[j & 1];
-            uint32_t see = 0xFFFFFFFFu;   // of a tree: only the steps with new tokens look
-            if (tree != nullptr && key0 + NK > w.s.K - w.s.L) see = tree_bits(tree, p.words, w.s.K - w.s.L, key0);
+            uint32_t see = 0xFFFFFFFFu;
+            if (TREE && live && key0 + NK > w.s.K - w.s.L) see = tree_bits(tree, p.words, w.s.K - w.s.L, key0);   // (few steps do)
             // Keys that exist: bit i for key0 + i. They come over a barrier of this CTA, as the arrivals that start the
             // scores order nothing for these warps. (The word is written anew once this step's weights have gone into O,
             // and they depend on it.)
@@ -1223,7 +1224,8 @@ __global__ void __launch_bounds__(NT, 1) __cluster_dims__(2, 1, 1)
     Ctx c{p, m, sc, base, tmem, rank, lane, (p.Dv + 63) / 64, &m->abort, true};
 
     if (warp < 4 * groups_of<C8>()) {
-        softmax_warps<IT, C8, K8>(c, tid, pair);
+        if (p.tree == nullptr) softmax_warps<IT, C8, K8, false>(c, tid, pair);
+        else softmax_warps<IT, C8, K8, true>(c, tid, pair);
     } else if (warp == MMA_WARP) {
         if (rank == 0) mma_warp<IT, C8, K8>(c);
     } else if constexpr (C8) {

@@ -223,3 +223,38 @@ def test_heads_that_share_a_query_and_strided_ones():
         kvr.mla_key_weight(on(qn), on(qr), cuda(c.ckv), cuda(c.k), cuda(c.table), cuda(c.query_start), cuda(c.key_length), lse.cuda(), w,
                            softmax_scale=c.scale)
         check_weight(c, (f64(w), 0), oracle_weight(c, lse, 303))
+
+
+@pytest.mark.parametrize("kw", [dict(Dv=8, Dk=8), dict(Dv=8, Dk=8, block_size=4), dict(Dv=16, Dk=16, cache="int8", k_cache="int8"),
+                                dict(Dv=16, Dk=8, cache="fp8_e5m2", block_size=16), dict(Dv=72, Dk=64, dtype="f16", mode="Norm"),
+                                dict(Dv=136, Dk=24), dict(Dv=1, Dk=2), dict(Dv=336, Dk=64, cache="fp8_e4m3fn", scale_len=336)])
+def test_narrow_rows(kw):
+    check(mla_case([3, 20], [300, 77], H=11, scale=0.3, seed=17, **dict(dict(block_size=32), **kw)))
+
+
+def test_more_heads_than_a_group():
+    for H, new, keys in ((300, [1, 2], [513, 90]), (1000, [3], [700])):
+        check(mla_case(new, keys, H=H, block_size=64, seed=18))
+
+
+def test_two_calls_captured_on_branches_of_a_graph():
+    both = [mla_case([3, 1], [900, 1500], H=24, block_size=64, seed=20), mla_case([40] * 3, [700] * 3, H=16, block_size=64, seed=21)]
+    lses = [row_lse(c).cuda() for c in both]
+    want = [run_weight(c, lse.cpu(), width_of(c))[0] for c, lse in zip(both, lses)]
+    args = [[*queries(c), cuda(c.ckv), cuda(c.k), cuda(c.table), cuda(c.query_start), cuda(c.key_length)] for c in both]
+    outs = [torch.full((len(c.key_length), width_of(c)), SENTINEL, device="cuda") for c in both]
+    sides = [torch.cuda.Stream() for _ in both]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for side in sides:
+            side.wait_stream(main)
+        for a, lse, out, c, side in zip(args, lses, outs, both, sides):
+            kvr.mla_key_weight(*a, lse, out, softmax_scale=c.scale, stream=side)
+        for side in sides:
+            main.wait_stream(side)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert np.array_equal(f64(out), w)

@@ -138,3 +138,7 @@ def test_refusals():
             kvr.kv_cache_compact(*bad)
     with pytest.raises(ValueError):
         kvr.kv_cache_compact(ckv, k, table, i(2, 4), i(2), cache_mode="Norm")
+
+
+def test_no_rotary_part():
+    assert run(case([300, 44], 16, Dk=0, seed=12), chosen([300, 44], [100, 40], 13), [100, 40]) == 0
