@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         int want = p.keep - p.sink - p.recent;   // of the others: less than there are
         t = STAYS - 1;                           // where none is wanted
 #pragma unroll 1
-        for (int round = 0; want > 0; ++round) {
+        for (int round = 0; want > 0 && round < 4; ++round) {   // (32 bits, 10 a round: also where weights change while they are read)
             const uint32_t range = hi - lo;
             const int bits = 32 - __clz(range), shift = bits > 10 ? bits - 10 : 0;
             int* hist = m.hist[round & 1];
@@ -152,6 +152,10 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
             sync();
             // (everyone has read the round before's counts)
             m.hist[(round & 1) ^ 1][tid] = 0;
+            if (tid == 0) {   // (what stands if no bin is found, in all CTAs alike: only where weights change meanwhile)
+                m.found[0] = 0;
+                m.found[1] = m.found[2] = want;
+            }
             // Thread i has the i-th bin from the top.
             int sum = 0;
 #pragma unroll
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
             }
             __syncthreads();
             lo += uint32_t(m.found[0]) << shift;
-            hi = min(hi, lo + ((1u << shift) - 1));
+            hi = lo + min(hi - lo, (1u << shift) - 1);   // (lo + 2^shift may not fit)
             want = m.found[1];
             if (want == m.found[2]) {   // all of it
                 t = lo - 1;
@@ -214,8 +218,8 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
     each([&](int i, uint32_t r, float w) {
         const uint32_t up = __ballot_sync(0xFFFFFFFFu, r > t), same = __ballot_sync(0xFFFFFFFFu, r == t && r != NONE);
         const int e = E + __popc(same & below);
-        if (r > t || (same >> lane & 1 && e < missing)) {
-            const int to = G + __popc(up & below) + min(e, missing);
+        const int to = G + __popc(up & below) + min(e, missing);
+        if ((r > t || (same >> lane & 1 && e < missing)) && to < p.keep) {
             kept[to] = i;
             if (carried != nullptr) carried[to] = HOLDS ? w : weight[i];
         }

@@ -73,6 +73,14 @@ def test_one_long_sequence(width):
     run(weights(1, width, 4, "few"), [width], width // 3, 0, 0)
 
 
+@pytest.mark.parametrize("least", [-1.01, -2.0, -3.7, -1e30, -np.inf])
+def test_ranges_up_to_the_last_rank(least):
+    """NaN, the highest rank, above a negative least weight: the bin that ends the range reaches beyond 32 bits."""
+    w = np.array([[least] + [np.nan] * 5 + [1.0, 2.0, 1.0, 0.5, -0.25, np.inf, 3.0]], dtype=np.float32)
+    for keep in range(1, 13):
+        run(w, [13], keep)
+
+
 def test_many_sequences():
     run(weights(1000, 40, 5, "few"), [int(x) for x in np.random.default_rng(1).integers(0, 41, 1000)], 16, 2, 3)
 
