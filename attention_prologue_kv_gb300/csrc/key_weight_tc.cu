@@ -772,55 +772,64 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
 // The 16-bit part keeps its type, over the same power. Without `mul` the rows are laid out densely as they are, for queries
 // whose rows lie unevenly over tokens and heads (TMA takes them by rows). One warp a row.
 template <class IT>
-__global__ void __launch_bounds__(256) key_weight_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn, uint16_t* qn_lo, uint16_t* qr,
+__global__ void __launch_bounds__(256, 6) key_weight_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn, uint16_t* qn_lo, uint16_t* qr,
                                                                  uint16_t* qr_lo, float* mul) {
-    __shared__ float inv[512], invk[64];
+    __shared__ __align__(16) float inv[512], invk[64];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int c = threadIdx.x; c < p.Dv; c += 256) inv[c] = qn_lo == nullptr ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? c : 0];
-    if (threadIdx.x < p.Dk) invk[threadIdx.x] = qr_lo == nullptr ? 1.f : 1.f / p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0];
+    for (int c = threadIdx.x; c < 512; c += 256) inv[c] = qn_lo == nullptr || c >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? c : 0];
+    if (threadIdx.x < 64)
+        invk[threadIdx.x] = qr_lo == nullptr || threadIdx.x >= p.Dk ? 1.f : 1.f / p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0];
     __syncthreads();
     const int64_t rows = p.T * p.H;
     for (int64_t row = int64_t(blockIdx.x) * 8 + warp; row < rows; row += int64_t(gridDim.x) * 8) {
         const int64_t t = row / p.H, head = row - t * p.H;
-        float z[3][8], top = 0.f;   // two pieces of the latent part, one of the rotary part
+        const uint16_t* from[2] = {static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs,
+                                   static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs};
+        uint4 x[3];   // two pieces of the latent part, one of the rotary part
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const int ch = (k < 2 ? k * 32 + lane : lane) * 8;
-            const bool in = ch < (k < 2 ? p.Dv : p.Dk);
-            const uint16_t* q = k < 2 ? static_cast<const uint16_t*>(p.qn) + t * p.qn_ts + head * p.qn_hs
-                                      : static_cast<const uint16_t*>(p.qr) + t * p.qr_ts + head * p.qr_hs;
-            const uint4 x = in ? ld_stream_v4(q + ch) : make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            const float* by = k < 2 ? inv : invk;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[k][2 * i] = in ? IT::lo(u[i]) * by[ch + 2 * i] : 0.f;
-                z[k][2 * i + 1] = in ? IT::hi(u[i]) * by[ch + 2 * i + 1] : 0.f;
-                top = fmaxf(top, fmaxf(fabsf(z[k][2 * i]), fabsf(z[k][2 * i + 1])));
-            }
+            const int ch = (k == 1 ? 32 + lane : lane) * 8;
+            x[k] = ch < (k < 2 ? p.Dv : p.Dk) ? ld_stream_v4(from[k >> 1] + ch) : make_uint4(0, 0, 0, 0);
         }
+        // z of a word's two channels.
+        auto pair = [&](int k, int i) {
+            const float* by = (k < 2 ? inv : invk) + (k == 1 ? 32 + lane : lane & (k < 2 ? 31 : 7)) * 8 + 2 * i;
+            const uint32_t u = i == 0 ? x[k].x : (i == 1 ? x[k].y : (i == 2 ? x[k].z : x[k].w));
+            const float2 b = *reinterpret_cast<const float2*>(by);
+            return make_float2(IT::lo(u) * b.x, IT::hi(u) * b.y);
+        };
+        float top = 0.f;
+        if (mul != nullptr) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e = mul != nullptr && top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) - 13, -113), 113) : 0;
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 z = pair(k, i);
+                    top = fmaxf(top, fmaxf(fabsf(z.x), fabsf(z.y)));
+                }
+            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));   // (not negative: ordered as its bits)
+        }
+        const int e = top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) - 13, -113), 113) : 0;
         const float g = ldexpf(1.f, -e);
         if (lane == 0 && mul != nullptr) mul[row] = ldexpf(1.f, e);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const int ch = (k < 2 ? k * 32 + lane : lane) * 8, width = k < 2 ? p.Dv : p.Dk;
+            const int ch = (k == 1 ? 32 + lane : lane) * 8, width = k < 2 ? p.Dv : p.Dk;
             if (ch >= width) continue;
             uint16_t* hi = (k < 2 ? qn : qr) + row * width + ch;
             uint16_t* lo = k < 2 ? qn_lo : qr_lo;
             uint32_t a[4], b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = z[k][2 * i] * g, y = z[k][2 * i + 1] * g;
+                const float2 z = pair(k, i);
+                const float u = z.x * g, v = z.y * g;
                 if (lo == nullptr) {
-                    a[i] = IT::pack(x, y);
+                    a[i] = IT::pack(u, v);
                 } else {
-                    a[i] = F16::pack(x, y);
-                    b[i] = F16::pack(x - F16::lo(a[i]), y - F16::hi(a[i]));
+                    a[i] = F16::pack(u, v);
+                    b[i] = F16::pack(u - F16::lo(a[i]), v - F16::hi(a[i]));
                 }
             }
             *reinterpret_cast<uint4*>(hi) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -989,7 +998,7 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
         uint16_t* qr = reinterpret_cast<uint16_t*>(take(n * a.Dk * 2));
         if (p.lo_r) qr_lo = reinterpret_cast<uint16_t*>(take(n * a.Dk * 2));
         if (!codes) mul = nullptr;
-        const int64_t cap = int64_t(sm_count_current_device()) * 8, need = (n + 7) / 8;
+        const int64_t cap = int64_t(sm_count_current_device()) * 6, need = (n + 7) / 8;
         const dim3 grid(unsigned(need < cap ? need : cap));
         const cudaError_t e = bf ? launch_pdl(key_weight_queries_kernel<BF16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul)
                                  : launch_pdl(key_weight_queries_kernel<F16>, grid, dim3(256), 0, s, a, qn, qn_lo, qr, qr_lo, mul);
