@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         int want = p.keep - p.sink - p.recent;   // of the others: less than there are
         t = STAYS - 1;                           // where none is wanted
 #pragma unroll 1
-        for (int round = 0; want > 0 && round < 4; ++round) {   // (32 bits, 10 a round: also where weights change while they are read)
+        for (int round = 0; want > 0 && round < 4; ++round) {   // (32 bits, 10 a round)
             const uint32_t range = hi - lo;
             const int bits = 32 - __clz(range), shift = bits > 10 ? bits - 10 : 0;
             int* hist = m.hist[round & 1];
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
             sync();
             // (everyone has read the round before's counts)
             m.hist[(round & 1) ^ 1][tid] = 0;
-            if (tid == 0) {   // (what stands if no bin is found, in all CTAs alike: only where weights change meanwhile)
+            if (VPT == 0 && tid == 0) {   // what stands if no bin is found, in all CTAs alike: weights may change between two readings
                 m.found[0] = 0;
                 m.found[1] = m.found[2] = want;
             }
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         const uint32_t up = __ballot_sync(0xFFFFFFFFu, r > t), same = __ballot_sync(0xFFFFFFFFu, r == t && r != NONE);
         const int e = E + __popc(same & below);
         const int to = G + __popc(up & below) + min(e, missing);
-        if ((r > t || (same >> lane & 1 && e < missing)) && to < p.keep) {
+        if ((r > t || (same >> lane & 1 && e < missing)) && (VPT > 0 || to < p.keep)) {
             kept[to] = i;
             if (carried != nullptr) carried[to] = HOLDS ? w : weight[i];
         }
