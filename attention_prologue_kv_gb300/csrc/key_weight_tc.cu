@@ -20,6 +20,13 @@
 //
 // Work is cut into equal shares by cost over the pairs (key_weight_plan.cuh). A tile that the cut goes through leaves its
 // sums in the workspace, and a second kernel adds them up in a fixed order.
+//
+// What bounds it: below about 100 rows a key the cache's bytes, above the tensor cores. Measured: 256 sequences of one token, 128
+// heads, 1-4095 keys 112 us (6.0 TB/s, 88% of the copy rate); 512 tokens x 128 heads over 16384 keys 640 us alone (1.9 PFLOP/s,
+// all of the measured bf16 rate) and 700 in a long run at the power limit; windows of 17-32 tokens, 8 sequences of 3000-8192
+// keys in E4M3, 171 us (twice the latent products, for the second halves); one token of 16 heads over 1000 keys 10.1 us.
+// The sums on the tensor cores are cut off at each addition of 16 products: a weight is 1.4e-6 of itself too small in bf16, 2.6e-6
+// over codes.
 #include <mutex>
 
 #include "cache_ops.cuh"

