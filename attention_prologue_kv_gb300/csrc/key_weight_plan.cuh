@@ -18,18 +18,18 @@ struct KwPos {
     int cut;        // whether groups of the tile come before it
 };
 
-// A sequence's rows in groups of `rows`, its keys in tiles.
+// A sequence's rows in groups of 2^shift, its keys in tiles.
 struct KwShape {
-    int L, K, H, rows;
+    int L, K, H, shift;
     bool causal;
 
-    KVR_HD int groups() const { return int((unsigned(L) * unsigned(H) + unsigned(rows) - 1u) / unsigned(rows)); }
+    KVR_HD int groups() const { return int((unsigned(L) * unsigned(H) + (1u << shift) - 1u) >> shift); }
     KVR_HD int tiles() const { return (K + KW_KEYS - 1) / KW_KEYS; }
     // The first group with a row that sees a key of the tile.
     KVR_HD int first_group(int kt) const {
         if (!causal) return 0;
         const int64_t token = int64_t(kt) * KW_KEYS - (int64_t(K) - L);
-        return token <= 0 ? 0 : int(token * H / rows);
+        return token <= 0 ? 0 : int(token * H >> shift);
     }
     KVR_HD bool even() const { return !causal || groups() == 1; }
     // Cost of the first x tiles, in groups; a tile costs one more, for bringing its keys, so that this grows by one at least
@@ -39,7 +39,7 @@ struct KwShape {
         const int64_t all = int64_t(x) * (groups() + 1);
         if (even()) return all;
         const double y = x - 1 - (double(K) - L) / KW_KEYS;
-        return y <= 0 ? all : all - int64_t(0.5 * y * y * (double(KW_KEYS) * H / rows));
+        return y <= 0 ? all : all - int64_t(0.5 * y * y * (double(KW_KEYS) * H / double(1 << shift)));
     }
     KVR_HD int64_t cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }
     // Where the share that begins at `off` of the sequence's cost begins. Grows with `off`: shares neither overlap nor leave gaps.

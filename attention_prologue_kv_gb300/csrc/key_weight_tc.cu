@@ -61,7 +61,7 @@ static_assert(SMEM <= 232448, "shared memory of a CTA");
 struct Tc {
     KeyWeightParams w;       // its queries: row t * H + h at that times qn_hs, qr_hs (those of codes prepared)
     const float* row_mul;    // power of two per row that prepared queries lack, or NULL
-    int pairs, rows, slots, box_rows;
+    int pairs, rows, shift, slots, box_rows;   // rows = 2^shift
     int lo_n, lo_r;          // the latent, the rotary part's queries have a second half
 };
 struct Maps {
@@ -89,7 +89,7 @@ struct Shapes {
     const Tc& p;
     __device__ __forceinline__ KwShape operator()(int n, int* bits = nullptr) const {
         const Seq s = load_seq(p.w.m, n, bits);
-        return {s.L, s.K, p.w.m.H, p.rows, p.w.m.causal != 0};
+        return {s.L, s.K, p.w.m.H, p.shift, p.w.m.causal != 0};
     }
 };
 using Walk = KwWalk<Shapes>;
@@ -103,7 +103,7 @@ __device__ void schedule(const Tc& p, Misc* m, int pair) {
     const Shapes shapes{p};
     int64_t sum = 0;
     int bits = 0;
-    KwShape s = {0, 0, 1, 32, false};
+    KwShape s = {0, 0, 1, 5, false};
     for (int n = n0; n < n1; ++n) {
         s = shapes(n, &bits);
         sum += s.cost();
@@ -413,6 +413,7 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const bool in0 = first < nc, in1 = first + 4 < nc, two = 2 * u + 1 < c.nb;
     const uint8_t* base = static_cast<const uint8_t*>(p.ckv) + (in0 ? first : 0) * 16;
     const bool whole = u * 8 + 8 <= nc;   // (the same in all lanes)
+    const int second = in1 ? 64 : 0;
     int tile = 0;
     Tiles<2> t(c, row0 + lane, 32);
     // Rows half * 32 + 8 k + r. In the place of a key that does not exist, row 0: what it holds spoils that key's sums alone, which
@@ -421,19 +422,16 @@ __device__ __forceinline__ void code_warps(Ctx& c, int v) {
         const uint8_t* src[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) src[k] = base + max(__shfl_sync(0xFFFFFFFFu, t.slot[half], 8 * k + r), int64_t(0)) * p.Dv;
-        if (whole) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = ld_ahead_v4(src[k]);
-                x[2 * k + 1] = ld_ahead_v4(src[k] + 64);
-            }
-        } else {
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = ld_ahead_v4(src[k]);
+            x[2 * k + 1] = ld_ahead_v4(src[k] + second);
+        }
+        if (!whole) {
             const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = in0 ? ld_ahead_v4(src[k]) : none;
-                x[2 * k + 1] = in1 ? ld_ahead_v4(src[k] + 64) : none;
-            }
+            for (int k = 0; k < 8; ++k)
+                if (!(k & 1 ? in1 : in0)) x[k] = none;
         }
     };
     auto store = [&](int half, const uint4 (&x)[8]) {
@@ -591,8 +589,6 @@ template <bool PREP>
 __device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* lse, float f, float2 sum, int from, int upto) {
     uint32_t see = from <= 0 ? 0xFFFFFFFFu : (from < 32 ? 0xFFFFFFFFu << from : 0u);
     if (upto < 32) see &= upto <= 0 ? 0u : (1u << upto) - 1u;
-    if (__all_sync(0xFFFFFFFFu, see == 0u)) return sum;
-    if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) return column_sum<PREP>(s, lse, f, sum);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
         const float a = exp2_approx(PREP ? fmaf(s[i], lse[2 * i], lse[2 * i + 1]) : fmaf(s[i], f, lse[i]));
@@ -643,18 +639,16 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
                 const uint32_t d = lanes + uint32_t(h) * COL_D;
                 float2 sum = make_float2(0.f, 0.f);
                 float x[32], y[32];
-                tmem_ld32(d, x);
+                tmem_ld32(d, y);
 #pragma unroll 1
-                for (int q = 0; q < rows; q += 64) {
+                for (int q = 0; q < rows; q += 32) {   // (once in the code: instructions come from far)
                     tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = y[i];
                     if (q + 32 < rows) tmem_ld32(d + q + 32, y);
-                    if (masked) sum = masked_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum, from - q, left - q);
-                    else sum = column_sum<PREP>(x, lse + q * (PREP ? 2 : 1), f, sum);
-                    if (q + 32 >= rows) break;
-                    tmem_wait_ld();
-                    if (q + 64 < rows) tmem_ld32(d + q + 64, x);
-                    if (masked) sum = masked_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum, from - q - 32, left - q - 32);
-                    else sum = column_sum<PREP>(y, lse + (q + 32) * (PREP ? 2 : 1), f, sum);
+                    const float* l = lse + q * (PREP ? 2 : 1);
+                    if (masked && !__all_sync(0xFFFFFFFFu, from <= q && left >= q + 32)) sum = masked_sum<PREP>(x, l, f, sum, from - q, left - q);
+                    else sum = column_sum<PREP>(x, l, f, sum);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -978,8 +972,9 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
     if (encoder() == nullptr) return cudaErrorNotSupported;
     // Rows of a group: what a sequence has on average, up to 256.
     const int64_t each = (a.T * a.H + a.N - 1) / a.N;
-    p.rows = 32;
-    while (p.rows < 256 && p.rows < each) p.rows *= 2;
+    p.shift = 5;
+    while (p.shift < 8 && int64_t(1) << p.shift < each) ++p.shift;
+    p.rows = 1 << p.shift;
     p.slots = int(Q_BYTES) / (p.rows * 64);
     if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
     p.lo_n = a.ckv_kind != OUT16;

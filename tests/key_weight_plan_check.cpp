@@ -26,12 +26,12 @@ int main() {
     std::mt19937 r(1);
     double worst = 0;
     for (int batch = 0; batch < 3000; ++batch) {
-        const int N = 1 + r() % 12, H = 1 + r() % 130, rows = 32 << (r() % 4), pairs = 1 + r() % 76;
+        const int N = 1 + r() % 12, H = 1 + r() % 130, shift = 5 + r() % 4, rows = 1 << shift, pairs = 1 + r() % 76;
         const bool causal = r() % 3;
         std::vector<KwShape> v;
         for (int n = 0; n < N; ++n) {
             const int L = r() % 4 ? 1 + r() % (r() % 2 ? 3 : 200) : 0, K = r() % 7 == 0 ? r() % 5 : r() % (r() % 2 ? 600 : 20000);
-            v.push_back({L, K, H, rows, causal});
+            v.push_back({L, K, H, shift, causal});
         }
         int64_t total = 0;
         std::vector<int64_t> base;
