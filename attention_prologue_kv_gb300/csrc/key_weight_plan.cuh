@@ -31,15 +31,13 @@ struct KwShape {
         const int64_t token = int64_t(kt) * KW_KEYS - (int64_t(K) - L);
         return token <= 0 ? 0 : int(token * H >> shift);
     }
-    KVR_HD bool even() const { return !causal || groups() == 1; }
     // Cost of the first x tiles, in groups; a tile costs one more, for bringing its keys, so that this grows by one at least
-    // from tile to tile. Where tiles lie behind the first token's keys, fewer and fewer groups see them. (Whole numbers: an
-    // SM has few units for doubles, and a call's first microseconds count.)
+    // from tile to tile. Where tiles lie behind the first token's keys, fewer and fewer groups see them: with the last tile's
+    // first key d tokens behind, d H / 2^shift of its groups do not, and the integral over d is taken off. (d < L, so that d^2 H
+    // < 2^62. Whole numbers: an SM has few units for doubles, and a call's first microseconds count.)
     KVR_HD int64_t cost(int x) const {
-        const int64_t all = int64_t(x) * (groups() + 1);
-        if (even()) return all;
-        const double y = x - 1 - (double(K) - L) / KW_KEYS;
-        return y <= 0 ? all : all - int64_t(0.5 * y * y * (double(KW_KEYS) * H / double(1 << shift)));
+        const int64_t all = int64_t(x) * (groups() + 1), d = int64_t(x - 1) * KW_KEYS - (int64_t(K) - L);
+        return !causal || d <= 0 ? all : all - (d * d * H >> (9 + shift));
     }
     KVR_HD int64_t cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }
     // Where the share that begins at `off` of the sequence's cost begins. Grows with `off`: shares neither overlap nor leave gaps.
@@ -50,15 +48,10 @@ struct KwShape {
             return {n, x < T ? int(x) : T, 0, 0};
         }
         int lo = 0, hi = T - 1;
-        if (even()) {
-            const int64_t x = off >> 31 == 0 ? int64_t(unsigned(off) / unsigned(G + 1)) : off / (G + 1);
-            lo = x < T ? int(x) : T - 1;
-        } else {
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (cost(mid) <= off) lo = mid;
-                else hi = mid - 1;
-            }
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (cost(mid) <= off) lo = mid;
+            else hi = mid - 1;
         }
         const int64_t c0 = cost(lo), c1 = cost(lo + 1);
         const int g0 = first_group(lo), count = G - g0;

@@ -144,6 +144,32 @@ __device__ void schedule(const Tc& p, Misc* m, int pair) {
     if (tid == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
 }
 
+// The same where a lane can have a sequence each (a few conversations: latency counts): one warp for the share's begin, one for its
+// end, without a word between warps.
+__device__ __forceinline__ void schedule_small(const Tc& p, Misc* m, int pair) {
+    const int lane = threadIdx.x & 31, half = threadIdx.x >> 5, N = int(p.w.m.N);
+    int bits = 0;
+    KwShape s = {0, 0, 1, 5, false};
+    if (lane < N) s = Shapes{p}(lane, &bits);
+    const int64_t mine = s.cost();
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, scan, 31);
+    const int active = kw_active(total, p.pairs);
+    const int64_t at = kw_share(total, pair + half, active);
+    KwPos* to = half ? &m->end : &m->begin;
+    if (at >= scan - mine && at < scan) *to = s.locate(lane, at - (scan - mine));
+    if (at == total && lane == 0) *to = {N, 0, 0, 0};
+    if (half == 0) {
+        if (bits != 0 && blockIdx.x == 0 && p.w.m.status != nullptr) atomicOr(p.w.m.status, bits);
+        if (lane == 0 && pair == 0 && cluster_rank() == 0) *ws_space(p).active = active;
+    }
+}
+
 // What every role has.
 struct Ctx {
     const Tc& p;
@@ -725,7 +751,8 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
     cluster_arrive();   // barriers and TMEM are set up; the other half is below, behind the schedule
     pdl_wait();
     pdl_launch_dependents();
-    schedule<R::THREADS>(p, m, pair);
+    if (p.w.m.N > 32) schedule<R::THREADS>(p, m, pair);
+    else if (warp < 2) schedule_small(p, m, pair);
     __syncthreads();
     if (tid == 0 && rank == 0) {
         Seq s = {0, 0, 0};
