@@ -8,8 +8,8 @@
 // if it is above t, or equal and E(i) is below what is missing, and its place is G(i) + min(E(i), missing). Counts are whole
 // numbers: the order in which they are added changes nothing.
 //
-// A cluster of CTAs has one sequence, each a run of its keys in registers, so that weights are read once (beyond 32768 keys a
-// CTA they are read anew, from L2). The CTAs read one another's counts: a barrier of the cluster for the range, one a round of
+// A cluster of CTAs has one sequence, each a run of its keys in registers, so that weights are read once (beyond 16384 keys a
+// CTA their ranks are in shared memory, beyond 49152 they are read anew, from L2). The CTAs read one another's counts: a barrier of the cluster for the range, one a round of
 // counting (two or three: bits of floats spread weights by their logarithm) and one for the keys before a CTA's own.
 //
 // Latency is what it costs. Measured: 32768 of one sequence's 131000 keys 17 us (3.6 to load and rank, 3 for the range, 3 a round,
@@ -63,10 +63,14 @@ struct Shared {
     int found[3];             // the bin, what is wanted of it, what it has
 };
 
-// VPT: keys of a thread, 0: as many as there are, read when they are looked at. Key j of a lane is the warp's first + 32 j + lane.
+// VPT: keys of a thread in registers; SHARED: as many as there are, their ranks in shared memory; AGAIN: read whenever they are
+// looked at. Key j of a lane is the warp's first + 32 j + lane.
+constexpr int SHARED = -1, AGAIN = 0;
+constexpr int64_t ROOM = 49152;   // ranks that shared memory takes
 template <int VPT>
 __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ SelectParams p) {
     __shared__ Shared m;
+    extern __shared__ uint32_t held[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const int n = int(blockIdx.x / size);
@@ -89,7 +93,6 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
     const float* weight = p.weight + n * p.weight_stride;
     const int last = K - p.recent;
     auto rank_at = [&](int i, float w) { return i >= end ? NONE : (all || i < p.sink || i >= last ? STAYS : rank_of(w)); };
-    constexpr bool HOLDS = VPT <= 16;   // the weights too; else those that stay are read again
     float value[VPT > 0 ? VPT : 1];
     uint32_t ranks[VPT > 0 ? VPT : 1];
     if (VPT > 0) {
@@ -100,12 +103,18 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) ranks[j] = rank_at(at + 32 * j + lane, value[j]);
+    } else if (VPT == SHARED) {
+#pragma unroll 8
+        for (int i = at + lane; i < end; i += 32) held[i - first] = rank_at(i, weight[i]);
     }
     // For each of this lane's keys, warp after warp the same number of times.
     auto each = [&](auto&& f) {
         if constexpr (VPT > 0) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) f(at + 32 * j + lane, ranks[j], HOLDS ? value[j] : 0.f);
+            for (int j = 0; j < VPT; ++j) f(at + 32 * j + lane, ranks[j], value[j]);
+        } else if constexpr (VPT == SHARED) {
+#pragma unroll 4
+            for (int i = at + lane; i < at + run; i += 32) f(i, i < end ? held[i - first] : NONE, 0.f);
         } else {
 #pragma unroll 4
             for (int i = at + lane; i < at + run; i += 32) {
@@ -155,7 +164,7 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
             sync();
             // (everyone has read the round before's counts)
             m.hist[(round & 1) ^ 1][tid] = 0;
-            if (VPT == 0 && tid == 0) {   // what stands if no bin is found, in all CTAs alike: weights may change between two readings
+            if (VPT == AGAIN && tid == 0) {   // what stands if no bin is found, in all CTAs alike: weights may change between two readings
                 m.found[0] = 0;
                 m.found[1] = m.found[2] = want;
             }
@@ -222,9 +231,9 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
         const uint32_t up = __ballot_sync(0xFFFFFFFFu, r > t), same = __ballot_sync(0xFFFFFFFFu, r == t && r != NONE);
         const int e = E + __popc(same & below);
         const int to = G + __popc(up & below) + min(e, missing);
-        if ((r > t || (same >> lane & 1 && e < missing)) && (VPT > 0 || to < p.keep)) {
+        if ((r > t || (same >> lane & 1 && e < missing)) && (VPT != AGAIN || to < p.keep)) {
             kept[to] = i;
-            if (carried != nullptr) carried[to] = HOLDS ? w : weight[i];
+            if (carried != nullptr) carried[to] = VPT == SHARED ? weight[i] : w;
         }
         G += __popc(up);
         E += __popc(same);
@@ -241,20 +250,26 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
 }  // namespace
 
 cudaError_t launch_select(SelectParams p, cudaStream_t s) {
-    // CTAs of a sequence: as many as the registers need, and up to 8 while the SMs are not filled and a CTA has 4096 keys or more.
-    // (Of one sequence of 131000 keys 8 take 15.9 us and 16 more, whose counts every CTA reads; of 500000 keys 85 and 51.)
+    // CTAs of a sequence: as many as registers need, and up to 8 while the SMs are not filled and a CTA has 4096 keys or more. (Of
+    // one sequence of 131000 keys 8 take 17 us and 16 took 20 to 24, whose counts every CTA reads; of 200000 keys 8, with ranks in
+    // shared memory, 26.8 and 16 20.9. 131000 keys with ranks in shared memory: 22.)
     int ctas = 1;
     while (ctas < MAX_CTAS && (p.weight_len > int64_t(ctas) * NT * 16 ||
                                (ctas < 8 && p.weight_len >= int64_t(ctas) * 4096 && int64_t(p.N) * ctas * 2 <= sm_count_current_device())))
         ctas *= 2;
     const int64_t each = (p.weight_len + ctas - 1) / ctas;
-    void (*kernel)(SelectParams) = each <= NT       ? kv_select_kernel<1>
+    void (*kernel)(SelectParams) = each <= NT ? kv_select_kernel<1>
                                    : each <= NT * 2 ? kv_select_kernel<2>
                                    : each <= NT * 4 ? kv_select_kernel<4>
                                    : each <= NT * 8 ? kv_select_kernel<8>
                                    : each <= NT * 16 ? kv_select_kernel<16>
-                                   : each <= NT * 32 ? kv_select_kernel<32>
-                                                     : kv_select_kernel<0>;
+                                   : each <= ROOM ? kv_select_kernel<SHARED>
+                                                  : kv_select_kernel<AGAIN>;
+    const size_t smem = each <= NT * 16 || each > ROOM ? 0 : size_t(each) * sizeof(uint32_t);
+    if (smem + sizeof(Shared) > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ROOM * sizeof(uint32_t)));
+        if (e != cudaSuccess) return e;
+    }
     if (ctas > 8) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
@@ -262,6 +277,7 @@ cudaError_t launch_select(SelectParams p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.N) * unsigned(ctas));
     cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

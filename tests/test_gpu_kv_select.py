@@ -73,6 +73,12 @@ def test_one_long_sequence(width):
     run(weights(1, width, 4, "few"), [width], width // 3, 0, 0)
 
 
+def test_keys_that_are_read_again():
+    """More than registers and shared memory of sixteen CTAs hold."""
+    run(weights(1, 900001, 7), [900001], 3000, 4, 512)
+    run(weights(2, 900001, 8, "odd"), [900000, 850000], 400000, 4, 512, pad=1)
+
+
 @pytest.mark.parametrize("least", [-1.01, -2.0, -3.7, -1e30, -np.inf])
 def test_ranges_up_to_the_last_rank(least):
     """NaN, the highest rank, above a negative least weight: the bin that ends the range reaches beyond 32 bits."""
