@@ -15,8 +15,9 @@
 // queries stay there for all its tiles. Scores take turns over two halves of TMEM: the exponentials of a group run beside
 // the products of the next one.
 //
-// Caches of codes: eight warps decode them into halves (every code is exact there). The queries are divided by the scales
-// before and held as the sum of two halves each, 22 bits, as a weight is a float32: one half alone was off by 2e-4 of it.
+// Caches of codes: eight warps decode them into halves (every code is exact there). The queries are divided by scales per channel
+// before and held as the sum of two halves each, 22 bits, as a weight is a float32: one half alone was off by 2e-4 of it. One
+// scale for all latent channels goes into the row's factor instead.
 //
 // Work is cut into equal shares by cost over the pairs (key_weight_plan.cuh). A tile that the cut goes through leaves its
 // sums in the workspace, and a second kernel adds them up in a fixed order.
@@ -541,6 +542,7 @@ __device__ __forceinline__ void mma_thread(Ctx& c) {
     const uint32_t id_n = C8 ? id_half : id_it, id_r = p.w.m.k_kind != OUT16 ? id_half : id_it;
     const uint64_t keys = tc_desc(c.base, 16, 1024), queries = tc_desc(c.q_slot(0), 16, 1024);
     const uint32_t q_step = uint32_t(p.rows) * 64u / 16u;
+    const bool lo_n = p.lo_n;
     int tile = 0, item = 0, slot = 0, slots = p.slots, nb = c.nb;
     uint32_t turn = 0;
     Walk w = c.walk();
@@ -573,7 +575,7 @@ __device__ __forceinline__ void mma_thread(Ctx& c) {
                 for (int b = 0; b < nb; ++b) {
                     if (first && (!C8 || b % 2 == 0)) c.wait_alone(&m->k_full[b], tile & 1);   // (codes: a barrier for two boxes)
                     box(b, id_n, b > 0);
-                    if (C8) box(b, id_n, true);
+                    if (C8 && lo_n) box(b, id_n, true);
                     if (last) tc_commit_pair(&m->k_empty[b]);
                 }
                 if (first) c.wait_alone(&m->k_full[ROPE], tile & 1);
@@ -797,8 +799,10 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
 
 // Queries for a cache of codes: z = q / scale (q itself for a part that is 16-bit), over a power of two per row that keeps all
 // of the row's z below 2^14, as halves hi = half(z) and lo = half(z - hi): 22 bits of z, or of 2^-24 where z is smaller.
-// The 16-bit part keeps its type, over the same power. Without `mul` the rows are laid out densely as they are, for queries
-// whose rows lie unevenly over tokens and heads (TMA takes them by rows). One warp a row.
+// One scale for all latent channels goes into the row's factor instead: z = q, which a half holds exactly (or to 2^-38 of the
+// row's largest), and the rotary part is multiplied by that scale, in two parts of its cache's type: 9 + 1 box products
+// instead of 16 + 1. A 16-bit part keeps its type, over the same power. Without `mul` the rows are laid out densely as they
+// are, for queries whose rows lie unevenly over tokens and heads (TMA takes them by rows). One warp a row.
 template <class IT>
 __global__ void __launch_bounds__(256, 6) key_weight_queries_kernel(const __grid_constant__ MlaParams p, uint16_t* qn, uint16_t* qn_lo, uint16_t* qr,
                                                                  uint16_t* qr_lo, float* mul) {
@@ -806,9 +810,11 @@ __global__ void __launch_bounds__(256, 6) key_weight_queries_kernel(const __grid
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int c = threadIdx.x; c < 512; c += 256) inv[c] = qn_lo == nullptr || c >= p.Dv ? 1.f : 1.f / p.ckv_scale[p.ckv_scale_per_ch ? c : 0];
+    const bool half_n = p.ckv_kind != OUT16, half_r = p.k_kind != OUT16;
+    const float one = half_n && qn_lo == nullptr ? p.ckv_scale[0] : 1.f;   // the one scale
+    for (int c = threadIdx.x; c < 512; c += 256) inv[c] = qn_lo == nullptr || c >= p.Dv ? 1.f : 1.f / p.ckv_scale[c];
     if (threadIdx.x < 64)
-        invk[threadIdx.x] = qr_lo == nullptr || threadIdx.x >= p.Dk ? 1.f : 1.f / p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0];
+        invk[threadIdx.x] = one * (!half_r || threadIdx.x >= p.Dk ? 1.f : 1.f / p.k_scale[p.k_scale_per_ch ? threadIdx.x : 0]);
     __syncthreads();
     const int64_t rows = p.T * p.H;
     for (int64_t row = int64_t(blockIdx.x) * 8 + warp; row < rows; row += int64_t(gridDim.x) * 8) {
@@ -841,23 +847,25 @@ __global__ void __launch_bounds__(256, 6) key_weight_queries_kernel(const __grid
         }
         const int e = top > 0.f && top <= 3.0e38f ? min(max(ilogbf(top) - 13, -113), 113) : 0;
         const float g = ldexpf(1.f, -e);
-        if (lane == 0 && mul != nullptr) mul[row] = ldexpf(1.f, e);
+        if (lane == 0 && mul != nullptr) mul[row] = ldexpf(1.f, e) / one;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const int ch = (k == 1 ? 32 + lane : lane) * 8, width = k < 2 ? p.Dv : p.Dk;
             if (ch >= width) continue;
             uint16_t* hi = (k < 2 ? qn : qr) + row * width + ch;
             uint16_t* lo = k < 2 ? qn_lo : qr_lo;
+            const bool half = k < 2 ? half_n : half_r;
             uint32_t a[4], b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 z = pair(k, i);
                 const float u = z.x * g, v = z.y * g;
-                if (lo == nullptr) {
-                    a[i] = IT::pack(u, v);
-                } else {
+                if (half) {
                     a[i] = F16::pack(u, v);
                     b[i] = F16::pack(u - F16::lo(a[i]), v - F16::hi(a[i]));
+                } else {
+                    a[i] = IT::pack(u, v);
+                    b[i] = IT::pack(u - IT::lo(a[i]), v - IT::hi(a[i]));
                 }
             }
             *reinterpret_cast<uint4*>(hi) = make_uint4(a[0], a[1], a[2], a[3]);
@@ -957,6 +965,9 @@ int pairs_of_device() {
 }
 
 int64_t round_up(int64_t x) { return (x + 255) / 256 * 256; }
+// Which queries are held in two parts.
+bool two_n(const MlaParams& p) { return p.ckv_kind != OUT16 && p.ckv_scale_per_ch; }
+bool two_r(const MlaParams& p) { return p.k_kind != OUT16 || (p.ckv_kind != OUT16 && !p.ckv_scale_per_ch); }
 bool codes_in(const MlaParams& p) { return p.ckv_kind != OUT16 || p.k_kind != OUT16; }
 // Whether the queries' rows, (token, head) in order, are evenly spaced, as TMA takes them.
 bool q_flat(const MlaParams& p) {
@@ -987,7 +998,7 @@ int64_t key_weight_tc_workspace(const KeyWeightParams& w) {
     int64_t n = round_up(ws_bytes(pairs_of_device()));
     if (!codes_in(p) && q_flat(p)) return n;
     const int64_t rows = p.T * p.H;
-    return n + round_up(rows * 4) + round_up(rows * p.Dv * 2) * (p.ckv_kind != OUT16 ? 2 : 1) + round_up(rows * p.Dk * 2) * (p.k_kind != OUT16 ? 2 : 1);
+    return n + round_up(rows * 4) + round_up(rows * p.Dv * 2) * (two_n(p) ? 2 : 1) + round_up(rows * p.Dk * 2) * (two_r(p) ? 2 : 1);
 }
 
 cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream_t s) {
@@ -1004,8 +1015,8 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
     p.rows = 1 << p.shift;
     p.slots = int(Q_BYTES) / (p.rows * 64);
     if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
-    p.lo_n = a.ckv_kind != OUT16;
-    p.lo_r = a.k_kind != OUT16;
+    p.lo_n = two_n(a);
+    p.lo_r = two_r(a);
     const int64_t rows = a.d0 * a.d1, n = a.T * a.H;
     Maps maps = {};
     if (!codes && rows < (int64_t(1) << 31) - CKEYS) {
@@ -1040,8 +1051,10 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
     }
     // A part whose cache is codes has halves, the other one q's type.
     const int64_t n_stride = a.T == 1 && a.H == 1 ? a.Dv : a.qn_hs, r_stride = a.T == 1 && a.H == 1 ? a.Dk : a.qr_hs;
-    if (!encode_2d(&maps.qn, a.qn, bf && !p.lo_n, n, a.Dv, n_stride, p.rows / 2) || !encode_2d(&maps.qr, a.qr, bf && !p.lo_r, n, a.Dk, r_stride, p.rows / 2) ||
-        (p.lo_n && !encode_2d(&maps.qn_lo, qn_lo, false, n, a.Dv, a.Dv, p.rows / 2)) || (p.lo_r && !encode_2d(&maps.qr_lo, qr_lo, false, n, a.Dk, a.Dk, p.rows / 2)))
+    const bool bf_n = bf && a.ckv_kind == OUT16, bf_r = bf && a.k_kind == OUT16;
+    if (!encode_2d(&maps.qn, a.qn, bf_n, n, a.Dv, n_stride, p.rows / 2) || !encode_2d(&maps.qr, a.qr, bf_r, n, a.Dk, r_stride, p.rows / 2) ||
+        (p.lo_n && !encode_2d(&maps.qn_lo, qn_lo, bf_n, n, a.Dv, a.Dv, p.rows / 2)) ||
+        (p.lo_r && !encode_2d(&maps.qr_lo, qr_lo, bf_r, n, a.Dk, a.Dk, p.rows / 2)))
         return cudaErrorInvalidValue;
     const bool tma = p.box_rows > 0;
     const cudaError_t e = launch_pdl(kernel_of(dtype, a.ckv_kind, tma), dim3(unsigned(p.pairs * 2)), dim3(threads_of(tma)), SMEM, s, p, maps);

@@ -113,7 +113,8 @@ def check_weight(c, gpu, ref, past=None, decay=1.0):
     """Bounds, to first order:
     * a score is a sum of at most 576 + products in float32, at most 64 roundings of 2^-23 of the terms' size B each (16
       products an addition on the tensor cores, 18 chained and 5 butterfly adds on the plain kernel). A query divided by a
-      scale per channel is held as the sum of two halves: 22 bits of it, 2^-22 B more. With lse in the exponent, and its and the
+      scale per channel is held as the sum of two halves: 22 bits of it, 2^-22 B more; the rotary part beside latent codes with
+      one scale as two parts of its type, 2^-18 B more at most (bf16). With lse in the exponent, and its and the
       score's product with log2 e: |d(s - lse)| <= 2^-17 B + 2^-21 (1 + |s| + |lse|) <= 2^-17 (B + 1 + |s| + |lse|);
     * a weight is off by that factor: 2^-17 E; to second order 2^-16 E covers it;
     * the float32 sum over r rows: r 2^-24 of the sum at most, and the exponential itself 2^-21;
