@@ -889,7 +889,7 @@ def prepare_kv_cache_select(weight, key_length, kept, kept_length, *, sink=0, re
 
 def kv_cache_select(weight, key_length, kept, kept_length, *, sink=0, recent=0, kept_weight=None, dev_status=None, stream=None):
     """Which keys to keep: of the key_length[n] (int64 [N]) keys with weight float32
-    [N, width] (rows may be strided), as mla_key_weight adds them up, at most
+    [N, width] (rows may be strided, width <= 2^30), as mla_key_weight adds them up, at most
     keep = kept.shape[1]: the first `sink`, the last `recent` and, of those
     between, the ones of largest weight, the earlier of equal ones (NaN above
     every number). kept int64 [N, keep] receives their positions, ascending, then

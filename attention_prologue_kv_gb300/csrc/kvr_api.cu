@@ -831,7 +831,7 @@ kvr_status draft_tree(const kvr_tree_args* a, cudaStream_t stream) {
 
 kvr_status kv_cache_select(const kvr_select_args* a, cudaStream_t stream) {
     if (a == nullptr) return KVR_ERR_NULL;
-    if (a->N < 0 || a->N >= (int64_t(1) << 27) || a->weight_len < 0 || a->weight_len > 0x7FFFFFFF || a->weight_stride < a->weight_len ||
+    if (a->N < 0 || a->N >= (int64_t(1) << 27) || a->weight_len < 0 || a->weight_len > (int64_t(1) << 30) || a->weight_stride < a->weight_len ||
         a->keep < 1 || a->keep > 0x7FFFFFFF || a->sink < 0 || a->recent < 0 || a->sink > a->keep || a->recent > a->keep - a->sink ||
         !product_fits({a->N, a->weight_stride, 4}) || !product_fits({a->N, a->keep, 8}))
         return KVR_ERR_SHAPE;

@@ -759,7 +759,7 @@ int64_t kvr_mla_key_weight_workspace(const kvr_key_weight_args* args);
  *                (>= keep).
  *   dev_status   optional int32 device word.
  *
- * Limits: 0 <= N < 2^27, weight_len < 2^31, keep >= 1, sink, recent >= 0,
+ * Limits: 0 <= N < 2^27, weight_len <= 2^30, keep >= 1, sink, recent >= 0,
  * sink + recent <= keep < 2^31. The outputs must not overlap an input or one
  * another.
  */

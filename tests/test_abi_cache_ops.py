@@ -131,6 +131,16 @@ def test_select_refusals(lib, kw, want):
     assert lib.kv_cache_select(ctypes.byref(select(**kw)), None) == want
 
 
+# A key's number and the end of its CTA's share, both rounded up, are counted in 31 bits.
+def test_select_longest(lib):
+    far = dict(weight=1 << 50, key_length=1 << 51, kept=1 << 52, kept_weight=0, N=1)
+    for length in ((1 << 30) + 1, (1 << 31) - 1):
+        a = select(weight_len=length, weight_stride=length, kept_length=1 << 53, **far)
+        assert lib.kv_cache_select(ctypes.byref(a), None) == N.KVR_ERR_SHAPE
+    # (as far as a null pointer, which is looked at behind the limits)
+    assert lib.kv_cache_select(ctypes.byref(select(weight_len=1 << 30, weight_stride=1 << 30, kept_length=0, **far)), None) == N.KVR_ERR_NULL
+
+
 def compact(**kw):
     a = dict(ckv_cache=M, ckv_dtype=0, k_cache=3 * M, k_dtype=0, mode=1, cache_d0=8, cache_d1=16, block_table=4 * M, max_blocks=4,
              N=2, Dv=512, Dk=64, kept=5 * M, kept_len=7, kept_length=6 * M, start=7 * M)
