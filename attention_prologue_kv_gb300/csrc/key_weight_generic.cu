@@ -4,8 +4,8 @@
 //
 // One warp per key: the key's channels stay in registers (lane l has channels l, l + 32, ...), the sequence's rows come one
 // after the other. 64 rows are summed on their own before they join the key's sum. This is the plain kernel, bound by the
-// loads and the warp sum of each (row, key). Measured: one token of 16 heads over 1000 keys 17 us (the tensor-core kernel 10),
-// 256 sequences of one token, 128 heads, 1-4095 keys 39.8 ms (112 us).
+// loads and the warp sum of each (row, key). Measured: one token of 16 heads over 1000 keys 17 us (the tensor-core kernel 7),
+// 256 sequences of one token, 128 heads, 1-4095 keys 39.8 ms (110 us).
 #include "cache_ops.cuh"
 
 namespace kvr {
