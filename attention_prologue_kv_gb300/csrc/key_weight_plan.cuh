@@ -33,10 +33,12 @@ struct KwShape {
     }
     // Cost of the first x tiles, in groups; a tile costs one more, for bringing its keys, so that this grows by one at least
     // from tile to tile. Where tiles lie behind the first token's keys, fewer and fewer groups see them: with the last tile's
-    // first key d tokens behind, d H / 2^shift of its groups do not, and the integral over d is taken off. (d < L, so that d^2 H
-    // < 2^62. Whole numbers: an SM has few units for doubles, and a call's first microseconds count.)
+    // first key d tokens behind, d H / 2^shift of its groups do not, and the integral over d is taken off; groups of tokens that
+    // are too many for the keys see no tile. (d < L, so that d^2 H < 2^62. Whole numbers: an SM has few units for doubles, and a
+    // call's first microseconds count.)
     KVR_HD int64_t cost(int x) const {
-        const int64_t all = int64_t(x) * (groups() + 1), d = int64_t(x - 1) * KW_KEYS - (int64_t(K) - L);
+        const int none = causal && L > K ? int(int64_t(L - K) * H >> shift) : 0;
+        const int64_t all = int64_t(x) * (groups() - none + 1), d = int64_t(x - 1) * KW_KEYS - (K > L ? K - L : 0);
         return !causal || d <= 0 ? all : all - (d * d * H >> (9 + shift));
     }
     KVR_HD int64_t cost() const { return L == 0 || K == 0 ? 0 : cost(tiles()); }

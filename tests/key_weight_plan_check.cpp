@@ -1,5 +1,5 @@
 // Random batches: every (sequence, tile, group that sees the tile) is in one share, each tile's sums are written once or left in
-// the slots that the joining kernel reads, and the shares are even.
+// the slots that the joining kernel reads, and the shares are even. With an argument: chunks that may be longer than their keys.
 #include <algorithm>
 #include <cstdio>
 #include <map>
@@ -22,14 +22,20 @@ static int fail(const char* what, int batch) {
     return 1;
 }
 
-int main() {
+int main(int argc, char**) {
+    const bool chunks = argc > 1;
     std::mt19937 r(1);
     double worst = 0;
-    for (int batch = 0; batch < 3000; ++batch) {
+    for (int batch = 0; batch < (chunks ? 150 : 3000); ++batch) {
         const int N = 1 + r() % 12, H = 1 + r() % 130, shift = 5 + r() % 4, rows = 1 << shift, pairs = 1 + r() % 76;
         const bool causal = r() % 3;
         std::vector<KwShape> v;
         for (int n = 0; n < N; ++n) {
+            if (chunks) {
+                const int L = 1 + r() % 6000, K = r() % (r() % 2 ? 40 : (r() % 2 ? 3000 : 9000));
+                v.push_back({L, K, H, shift, causal});
+                continue;
+            }
             const int L = r() % 4 ? 1 + r() % (r() % 2 ? 3 : 200) : 0, K = r() % 7 == 0 ? r() % 5 : r() % (r() % 2 ? 600 : 20000);
             v.push_back({L, K, H, shift, causal});
         }

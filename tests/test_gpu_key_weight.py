@@ -53,6 +53,13 @@ def test_causal_or_not(new, keys, causal):
     check(mla_case(new, keys, H=16, block_size=64, seed=3, causal=causal))
 
 
+# Most tokens of a chunk see no key: the work that is cut is that of the others.
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,keys", [([1500, 700], [10, 300]), ([2100], [1]), ([3, 1300, 1], [40, 257, 5]), ([900, 4], [0, 9])])
+def test_more_tokens_than_keys(new, keys, causal):
+    check(mla_case(new, keys, H=16, block_size=64, seed=4, causal=causal))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("cache,k_cache,scale_len,k_scale_len", [
     ("int8", None, 1, 1), ("int8", None, 512, 1), ("fp8_e4m3fn", None, 512, 1), ("fp8_e5m2", None, 1, 1),
