@@ -856,7 +856,8 @@ def mla_key_weight(q_nope, q_rope, ckv_cache, k_cache, block_table, query_start,
     up to `width` keys; entries behind a sequence's last key, and rows of
     sequences without tokens, stay as they were. past: None (nothing is taken
     up), `weight` itself to add up in place, or another tensor of its shape.
-    Keys of blocks that the table leaves out receive nothing. After a drafted
+    Keys of blocks that the table leaves out receive nothing; a row whose lse is
+    -inf adds nothing, whatever its query holds (padding). After a drafted
     tree, call it for the accepted tokens over the compacted cache: there they
     are a causal chain."""
     _bind_and_call(_bind_mla_key_weight, (q_nope, q_rope, ckv_cache, k_cache, block_table, query_start, key_length, lse, weight,

@@ -230,8 +230,10 @@ struct Look {
     }
 };
 
-// One warp brings the CTA's 16-bit keys through TMA: a box is 128 / R copies of R rows, R what divides the cache's blocks.
-__device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
+// Two warps bring the CTA's 16-bit keys through TMA, every other box each: a box is 128 / R copies of R rows, R what divides the
+// cache's blocks. (One warp: blocks of 16 keys, 64 sequences of 4096, 64 to 69 us, by how its copies were compiled; two 58. Blocks
+// of 128 take 57 with either.)
+__device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps, int which) {
     const MlaParams& p = c.p.w.m;
     const int R = c.p.box_rows, copies = CKEYS / R;
     int tile = 0;
@@ -249,7 +251,7 @@ __device__ __forceinline__ void key_warp(Ctx& c, const Maps& maps) {
             look(kt + 1);
             const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xFFFFFFFFu, row >= 0))) * uint32_t(R) * 128u;
 #pragma unroll 1
-            for (int b = 0; b <= c.nb; ++b) {
+            for (int b = which; b <= c.nb; b += 2) {
                 const int at = b < c.nb ? b : ROPE;
                 if (tile > 0) c.wait(&c.m->k_empty[at], (tile & 1) ^ 1);
                 if (c.gone()) return;
@@ -302,7 +304,7 @@ __device__ __forceinline__ void query_thread(Ctx& c, const Maps& maps) {
     }
 }
 
-// One warp brings the groups' logarithms, times log2 e and negative, as they are added; -inf (a row that saw nothing) as
+// One warp brings the groups' logarithms, times log2 e and negative, as they are added; -inf (a row that saw nothing, or padding) as
 // -inf, so that the row adds 2^-inf. With prepared queries each row's factor stands beside.
 template <bool PREP>
 __device__ __forceinline__ void lse_warp(Ctx& c) {
@@ -627,6 +629,29 @@ __device__ __forceinline__ float2 masked_sum(const float (&s)[32], const float* 
     return sum;
 }
 
+// A group's sum anew, rows of 2^-inf left out: with a score that is not finite (a padded row's query may hold anything) they have
+// made it NaN, the only thing but 0 that they can add. Looked for afterwards and out of line, so that the sums' loop stays as it
+// is: masks of such rows, written and looked at with every group, cost 64 tokens of a chunk 1% and int8 codes 3%. The additions
+// keep their order.
+template <bool PREP>
+__device__ __noinline__ float counted_sum(uint32_t d, const float* lse, float f, int rows, int from, int upto) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int q = 0; q < rows; q += 16) {
+        float s[16];
+        tmem_ld16(d + q, s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float by = PREP ? lse[2 * (q + i)] : f, l = PREP ? lse[2 * (q + i) + 1] : lse[q + i];
+            const float a = l == -INFINITY || q + i < from || q + i >= upto ? 0.f : exp2_approx(fmaf(s[i], by, l));
+            if (i & 1) sum.y += a;
+            else sum.x += a;
+        }
+    }
+    return sum.x + sum.y;
+}
+
 // Four warps a half of TMEM (EG = 2), or four for both: thread r has key r of the CTA's half of a tile.
 template <bool PREP, int EG>
 __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
@@ -678,13 +703,15 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
                     if (masked && !__all_sync(0xFFFFFFFFu, from <= q && left >= q + 32)) sum = masked_sum<PREP>(x, l, f, sum, from - q, left - q);
                     else sum = column_sum<PREP>(x, l, f, sum);
                 }
+                float part = sum.x + sum.y;
+                if (__any_sync(0xFFFFFFFFu, part != part && key < w.s.K)) part = counted_sum<PREP>(d, lse, f, rows, from, left);
                 tc_fence_before();
                 __syncwarp();
                 if (c.lane == 0) {
                     mbar_arrive_at(&m->d_free[h], 0);
                     mbar_arrive(&m->lse_free[ls]);
                 }
-                total += sum.x + sum.y;
+                total += part;
             }
             if (EG == 2 && w.gb - w.ga > 1) {
                 float* other = &m->other[joined & 1][r];
@@ -701,12 +728,12 @@ __device__ __forceinline__ void sum_warps(Ctx& c, int tid, int pair) {
     }
 }
 
-// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then MMA, queries, logarithms, and 1 for TMA, 8 that copy, or
+// TMA: the latent rows come through it. Warps: 0 to 4 EG - 1 sums, then MMA, queries, logarithms, and 2 for TMA, 8 that copy, or
 // 8 that decode and 1 for the rotary part; at most 16, so that each thread may have 128 registers.
 template <bool TMA>
 struct Roles {
     static constexpr int EG = TMA ? 2 : 1;
-    static constexpr int MMA = 4 * EG, QUERY = MMA + 1, LSE = MMA + 2, LOAD = MMA + 3, LOADERS = TMA ? 1 : 9;
+    static constexpr int MMA = 4 * EG, QUERY = MMA + 1, LSE = MMA + 2, LOAD = MMA + 3, LOADERS = TMA ? 2 : 9;
     static constexpr int THREADS = (LOAD + LOADERS) * 32;
 };
 
@@ -777,7 +804,7 @@ __global__ void __launch_bounds__(Roles<TMA>::THREADS, 1) __cluster_dims__(2, 1,
         if (prep) lse_warp<true>(c);
         else if (!C8) lse_warp<false>(c);
     } else if constexpr (TMA) {
-        key_warp(c, maps);
+        key_warp(c, maps, warp - R::LOAD);
     } else if constexpr (C8) {
         if (warp < R::LOAD + 8) code_warps<CK>(c, tid - R::LOAD * 32);
         else rope_warp(c);

@@ -701,7 +701,8 @@ kvr_status mla_tree_attention(const kvr_mla_tree_args* args, cudaStream_t stream
  *
  *   step         as for mla_attention, but `out` is not used and `lse` is read
  *                (float32 [T, H], needed): what mla_attention wrote for these queries,
- *                or any other logarithms. A row of -inf adds nothing.
+ *                or any other logarithms. A row of -inf adds nothing, whatever
+ *                its query holds (padding).
  *   weight       out float32: key i of sequence n at n * weight_stride + i, room
  *                for weight_len keys a sequence. Entries behind a sequence's last
  *                key, and those of sequences without tokens, are left as they were.
