@@ -64,6 +64,7 @@ struct Tc {
     const float* row_mul;    // power of two per row that prepared queries lack, or NULL
     int pairs, rows, shift, slots, box_rows;   // rows = 2^shift
     int lo_n, lo_r;          // the latent, the rotary part's queries have a second half
+    int patience;            // seconds of a wait beyond the first
 };
 struct Maps {
     CUtensorMap qn, qr, qn_lo, qr_lo, latent, rope;
@@ -181,10 +182,10 @@ struct Ctx {
     volatile int* abort;
     bool ok;
 
-    // As in the attention kernel: a wait that gives up poisons the CTA; the roles that start TMA copies then stop, the others run
-    // their loops to the end without waiting.
+    // As in the attention kernel: a wait that gives up (after one second and `patience`) poisons the CTA; the roles that start TMA
+    // copies then stop, the others run their loops to the end without waiting.
     __device__ __forceinline__ void wait_alone(uint64_t* bar, uint32_t parity) {   // by one thread of a warp
-        if (ok && !mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, 0);
+        if (ok && !mbar_try_wait(bar, parity)) ok = wait_on(bar, parity, abort, p.patience);
     }
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
         wait_alone(bar, parity);
@@ -1044,6 +1045,7 @@ cudaError_t launch_key_weight_tc(const KeyWeightParams& w, int dtype, cudaStream
     if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
     p.lo_n = two_n(a);
     p.lo_r = two_r(a);
+    p.patience = kw_patience(a.T * a.H, a.max_keys);
     const int64_t rows = a.d0 * a.d1, n = a.T * a.H;
     Maps maps = {};
     if (!codes && rows < (int64_t(1) << 31) - CKEYS) {

@@ -120,8 +120,9 @@ typedef enum kvr_status {
                                       or beyond what there is room for */
 #define KVR_DEVERR_BLOCK_CAP 0x4   /* qsa: a completed block's number is >= Bcap */
 #define KVR_DEVERR_TIMEOUT 0x8     /* a pipeline wait inside a kernel exceeded its limit (one second, in
-                                      mla_attention and one more for 2^22 keys of a part before); that
-                                      CTA stopped early, output incomplete */
+                                      mla_attention and one more for 2^22 keys of a part before, in
+                                      mla_key_weight for 2^22 rows of queries and for 2^22 keys that
+                                      there is room for); that CTA stopped early, output incomplete */
 #define KVR_DEVERR_PAST_BLOCKS 0x10 /* qsa, concat-output form: past_block_index_keys holds
                                       fewer than floor(P/kbs) rows for a sequence */
 #define KVR_DEVERR_QUERY 0x20      /* attention, key weight, tree: query_start decreases or leaves [0, T]
