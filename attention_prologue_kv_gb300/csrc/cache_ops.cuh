@@ -51,7 +51,7 @@ struct CompactParams {
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_key_weight_generic(const KeyWeightParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_key_weight_tc(const KeyWeightParams& p, int dtype, cudaStream_t s);
-bool key_weight_tc_fits(const KeyWeightParams& p);           // whether its work can be counted in 64 bits
+bool key_weight_tc_fits(const KeyWeightParams& p);           // whether its rows and work can be counted
 int64_t key_weight_tc_workspace(const KeyWeightParams& p);   // bytes on the current device
 cudaError_t launch_select(SelectParams p, cudaStream_t s);
 cudaError_t launch_compact(CompactParams p, bool vec, cudaStream_t s);

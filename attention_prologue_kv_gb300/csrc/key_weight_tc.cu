@@ -1016,9 +1016,10 @@ bool encode_2d(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int 
 }  // namespace
 
 bool key_weight_tc_fits(const KeyWeightParams& w) {
-    // cost() of one sequence is at most tiles * (groups + 1), and N of them, which may share rows, are added up.
+    // cost() of one sequence is at most tiles * (groups + 1), and N of them, which may share rows, are added up. A key's place among
+    // the new tokens' (up to 255 behind the last one) and the rows of a query box (up to 127 behind) are counted in 31 bits.
     const MlaParams& p = w.m;
-    return ((p.T * p.H + 31) / 32 + 1) * ((p.max_keys + KW_KEYS - 1) / KW_KEYS + 1) <= (int64_t(1) << 62) / p.N;
+    return p.T * p.H <= 0x7FFFFFFF - 511 && ((p.T * p.H + 31) / 32 + 1) * ((p.max_keys + KW_KEYS - 1) / KW_KEYS + 1) <= (int64_t(1) << 62) / p.N;
 }
 
 int64_t key_weight_tc_workspace(const KeyWeightParams& w) {

@@ -720,8 +720,8 @@ kvr_status mla_tree_attention(const kvr_mla_tree_args* args, cudaStream_t stream
  * most 512 + 64 channels, both multiples of 8 (of 16 in an 8-bit cache), on
  * 16-byte boundaries (q and the caches; strides multiples of 8) and with H <=
  * 65536 run on the tensor cores, all others on a plain kernel that is much
- * slower; the limit on work is there (T * H / 32 + 2) * (keys / 256 + 2) * N <
- * 2^62. Scores and sums are float32. A query for a cache with scales per
+ * slower; the limits are there T * H <= 2^31 - 512 and, on work, (T * H / 32 + 2) *
+ * (keys / 256 + 2) * N < 2^62. Scores and sums are float32. A query for a cache with scales per
  * channel is divided by them and held in 22 bits there; with one scale for all
  * latent channels the rotary part is multiplied by it and held in 16 bits (of
  * bf16) or 22. Keys within key_length need not be
