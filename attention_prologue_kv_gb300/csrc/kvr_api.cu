@@ -731,7 +731,7 @@ kvr_status key_weight_plan(const kvr_key_weight_args* a, KeyWeightParams* p, boo
         (a->past != nullptr && !product_fits({s.N < 0 ? 0 : s.N, a->past_stride, 4})) || !(a->decay == a->decay))
         return KVR_ERR_SHAPE;
     if (!aligned(a->weight, 4) || !aligned(a->past, 4)) return KVR_ERR_SHAPE;
-    const bool in_place = a->past == a->weight;
+    const bool in_place = a->past != nullptr && a->past == a->weight;
     if (in_place && a->past_stride != a->weight_stride && s.N > 1) return KVR_ERR_ALIAS;
     const int64_t wb = s.N > 0 ? ((s.N - 1) * a->weight_stride + a->weight_len) * 4 : 0;
     const int64_t pb = s.N > 0 ? ((s.N - 1) * a->past_stride + a->weight_len) * 4 : 0;

@@ -23,3 +23,10 @@ def call(lib, T, H, Dv=8, Dk=8, **kw):  # noqa: F811
     ((1 << 24) - 1, 128, N.KVR_ERR_SHAPE), ((1 << 24) - 4, 128, N.KVR_ERR_NULL)])
 def test_most_rows_on_the_tensor_cores(lib, T, H, want):  # noqa: F811
     assert call(lib, T, H) == want   # (KVR_ERR_NULL: as far as the workspace, which is looked at behind the limits)
+
+
+# Without weights to add to, past_stride is not looked at: NULL is no address that `weight` and `past` share.
+@pytest.mark.parametrize("kw", [dict(weight_len=0, weight_stride=8, past_stride=0), dict(weight_len=64, weight_stride=64, past_stride=0)])
+def test_neither_weight_nor_past(lib, kw):  # noqa: F811
+    a = weight(dict(workspace=0), **dict(dict(weight=0, past=0), **kw))
+    assert lib.mla_key_weight(ctypes.byref(a), None) == N.KVR_ERR_NULL   # (the workspace; `weight` where it has room for keys)
