@@ -15,7 +15,10 @@
 //
 // Latency is what it costs. Measured: 32768 of one sequence's 131000 keys 17 us (3.6 to load and rank, 3 for the range, 3 a round,
 // 3.5 to write), 2048 of 4095 keys of 64 sequences 6.5 us, 500 of 1000 keys of 256 sequences 7.6 us.
+#include <mutex>
+
 #include "cache_ops.cuh"
+#include "select_plan.cuh"
 #include "tcgen05.cuh"
 
 namespace kvr {
@@ -23,8 +26,8 @@ namespace kvr {
 namespace {
 
 // Bins: one a thread. With 2048, which all CTAs read of one another too, 131000 keys took 19.8 us instead of 15.9.
-constexpr int NT = 1024, WARPS = NT / 32, BINS = NT;
-constexpr int MAX_CTAS = 16;   // beyond 8, where the device has to be asked, for what 8 have no registers for
+constexpr int NT = SEL_THREADS, WARPS = NT / 32, BINS = NT;
+constexpr int MAX_CTAS = 16;   // beyond 8, where the device is asked, for what 8 have no registers for
 
 __device__ __forceinline__ uint32_t rank_of(float w) {
     if (w != w) return 0xFFFFFFFEu;
@@ -66,8 +69,7 @@ struct Shared {
 
 // VPT: keys of a thread in registers; SHARED: as many as there are, their ranks in shared memory; AGAIN: read whenever they are
 // looked at. Key j of a lane is the warp's first + 32 j + lane.
-constexpr int SHARED = -1, AGAIN = 0;
-constexpr int64_t ROOM = 49152;   // ranks that shared memory takes
+constexpr int SHARED = SEL_SHARED, AGAIN = SEL_AGAIN;
 template <int VPT>
 __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ SelectParams p) {
     __shared__ Shared m;
@@ -248,27 +250,64 @@ __global__ void __launch_bounds__(NT) kv_select_kernel(const __grid_constant__ S
     if (size > 1) cluster_wait();
 }
 
+using Kernel = void (*)(SelectParams);
+Kernel kernel_of(int form) {
+    switch (form) {
+        case 1: return kv_select_kernel<1>;
+        case 2: return kv_select_kernel<2>;
+        case 4: return kv_select_kernel<4>;
+        case 8: return kv_select_kernel<8>;
+        case 16: return kv_select_kernel<16>;
+        case SHARED: return kv_select_kernel<SHARED>;
+        default: return kv_select_kernel<AGAIN>;
+    }
+}
+
+// Whether a cluster of 16 CTAs, each with all that one can have of an SM, fits anywhere on the current device; asked once per
+// device.
+bool wide_clusters() {
+    static std::mutex mu;
+    static int known[64] = {0};   // 1: they do, 2: they do not
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev] == 0) {
+        const void* kernel = reinterpret_cast<const void*>(kernel_of(SHARED));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(MAX_CTAS);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = SEL_ROOM * sizeof(uint32_t);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = MAX_CTAS;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(cfg.dynamicSmemBytes)) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return false;
+        }
+        known[dev] = n > 0 ? 1 : 2;
+    }
+    return known[dev] == 1;
+}
+
 }  // namespace
 
 cudaError_t launch_select(SelectParams p, cudaStream_t s) {
-    // CTAs of a sequence: as many as registers need, and up to 8 while the SMs are not filled and a CTA has 4096 keys or more. (Of
-    // one sequence of 131000 keys 8 take 17 us and 16 took 20 to 24, whose counts every CTA reads; of 200000 keys 8, with ranks in
-    // shared memory, 26.8 and 16 20.9. 131000 keys with ranks in shared memory: 22.)
-    int ctas = 1;
-    while (ctas < MAX_CTAS && (p.weight_len > int64_t(ctas) * NT * 16 ||
-                               (ctas < 8 && p.weight_len >= int64_t(ctas) * 4096 && int64_t(p.N) * ctas * 2 <= sm_count_current_device())))
-        ctas *= 2;
-    const int64_t each = (p.weight_len + ctas - 1) / ctas;
-    void (*kernel)(SelectParams) = each <= NT ? kv_select_kernel<1>
-                                   : each <= NT * 2 ? kv_select_kernel<2>
-                                   : each <= NT * 4 ? kv_select_kernel<4>
-                                   : each <= NT * 8 ? kv_select_kernel<8>
-                                   : each <= NT * 16 ? kv_select_kernel<16>
-                                   : each <= ROOM ? kv_select_kernel<SHARED>
-                                                  : kv_select_kernel<AGAIN>;
-    const size_t smem = each <= NT * 16 || each > ROOM ? 0 : size_t(each) * sizeof(uint32_t);
+    const bool wide = p.weight_len > int64_t(8) * NT * 16 && wide_clusters();
+    const SelectForm f = select_form(p.weight_len, p.N, sm_count_current_device(), wide ? MAX_CTAS : 8);
+    const int ctas = f.ctas;
+    Kernel kernel = kernel_of(f.form);
+    const size_t smem = f.form == SHARED ? size_t(f.each) * sizeof(uint32_t) : 0;
     if (smem + sizeof(Shared) > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ROOM * sizeof(uint32_t)));
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(SEL_ROOM * sizeof(uint32_t)));
         if (e != cudaSuccess) return e;
     }
     if (ctas > 8) {
