@@ -4,7 +4,8 @@
 // One CTA a sequence, its parents in shared memory, one thread a token: it walks up to the context and
 // sets a bit a step. A parent comes before its token, so that the walk goes down through the words: a word is written once,
 // from a register. What it costs is a launch and two dependent loads; a step of the walk is one
-// load from shared memory. Measured: one sequence of 26 tokens 2.9 us, 256 of 9-127 tokens 3.0 us.
+// load from shared memory. Measured: one sequence of 26 tokens 2.8 us, 256 of 9-127 tokens 2.9 to 3.3. What a token
+// costs is its depth, so that chains, which drafts do not have at such lengths, are quadratic: 64 tokens 5.9 us, 512 129, 4096 7100.
 #include "cache_ops.cuh"
 
 namespace kvr {

@@ -13,8 +13,9 @@
 // of the cluster for the range, one a round of counting (two or three: bits of floats spread weights by their logarithm) and one
 // for the keys before a CTA's own.
 //
-// Latency is what it costs. Measured: 32768 of one sequence's 131000 keys 17 us (3.6 to load and rank, 3 for the range, 3 a round,
-// 3.5 to write), 2048 of 4095 keys of 64 sequences 6.5 us, 500 of 1000 keys of 256 sequences 7.6 us.
+// Latency is what it costs. Measured, with the same weights in each call and with others from DRAM: 32768 of one sequence's 131000
+// keys 16.8 us and 17.2 to 19.6 (3.6 to load and rank, 3 for the range, 3 a round, 3.5 to write), 2048 of 4095 keys of 64 sequences
+// 5.9 and 7.1 to 8.2, 500 of 1000 keys of 256 sequences 7.3 and 8.1.
 #include <mutex>
 
 #include "cache_ops.cuh"
