@@ -27,8 +27,8 @@
 // (6.1 TB/s, 90% of the copy rate); 512 tokens x 128 heads over 16384 keys 625 to 640 us alone (1.9 PFLOP/s, the rate of a library
 // product) and 690 to 712 in a long run at the power limit; windows of 17-32 tokens, 8 sequences of 3000-8192 keys in E4M3, 164 to
 // 168 us (twice the latent products, for the second halves; windows of 32 over 4096 keys 190, with one scale 120 to 124); one token
-// of 16 heads over 1000 keys 6.8 us. The sums on the tensor cores are cut off at each addition of 16
-// products: a weight is 1.4e-6 of itself too small in bf16, 2.6e-6 over codes with scales per channel, 0.9e-6 with one.
+// of 16 heads over 1000 keys 6.8 us. The sums on the tensor cores are cut off at each addition of 16 products: a weight is 1.4e-6
+// of itself too small in bf16, 2.6e-6 over codes with scales per channel, 0.9e-6 with one.
 #include <mutex>
 
 #include "cache_ops.cuh"
@@ -432,9 +432,10 @@ __device__ __forceinline__ void copy_warps(Ctx& c, int v) {
 // Eight warps decode a cache of codes: two have two of a tile's latent boxes, 64 rows each, a lane 16 pieces of 16 codes. Each
 // half's next loads start as soon as it is stored, so that they have a tile's time. 64 sequences of 8192 keys in int8 take 139
 // to 142 us with 16 heads (E4M3 with scales per channel and 128 heads: 145 to 149), the same from L2 as from DRAM; without any load
-// 85. Both move by as much as 15% with the order of the roles in the code, which share the instruction cache. Tried, when they took 145 to 151: all eight warps at each
-// pair of boxes in turn, four arrivals a tile 162; sixteen warps of half the rows 136, but 190 instead of 155 with 128 heads;
-// half of the codes decoded ahead of the wait 189; the next rows prefetched into L2 164; whole lines a load 178.
+// 85. Both move by as much as 15% with the order of the roles in the code, which share the instruction cache. Tried, when int8 took
+// 145 to 151: all eight warps at each pair of boxes in turn, four arrivals a tile 162; sixteen warps of half the rows 136, but 190
+// instead of 155 with 128 heads; half of the codes decoded ahead of the wait 189; the next rows prefetched into L2 164; whole
+// lines a load 178.
 template <int CK>
 __device__ __forceinline__ void code_warps(Ctx& c, int v) {
     const MlaParams& p = c.p.w.m;
